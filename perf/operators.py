@@ -31,40 +31,40 @@ _ROW = {"int4": lambda d: d // 2 + 4, "int2": lambda d: d // 4 + 4, "int8": lamb
 def listed():
     return [
         # one chat turn's first tokens, fp32 activations: nothing but latency
-        dict(name="decode, one short sequence", op="decode", batch=1, hq=4, hkv=2, d=64, bs=16, lo=37, hi=37, qtype="f32",
+        dict(name="decode: one short sequence", op="decode", batch=1, hq=4, hkv=2, d=64, bs=16, lo=37, hi=37, qtype="f32",
              headwise=False, window=0, sink=0),
         # a serving batch of ragged contexts, grouped heads 4 : 1, 16-token pages
-        dict(name="decode, 64 ragged sequences", op="decode", batch=64, hq=32, hkv=8, d=128, bs=16, lo=1024, hi=8192,
+        dict(name="decode: 64 ragged sequences", op="decode", batch=64, hq=32, hkv=8, d=128, bs=16, lo=1024, hi=8192,
              qtype="bf16", headwise=False, window=0, sink=0),
         # half of the heads keep a window and sinks, their other pages evicted
-        dict(name="decode, head-wise windows", op="decode", batch=32, hq=40, hkv=8, d=128, bs=64, lo=32768, hi=32768,
+        dict(name="decode: head-wise windows", op="decode", batch=32, hq=40, hkv=8, d=128, bs=64, lo=32768, hi=32768,
              qtype="bf16", headwise=True, window=4096, sink=4),
         # one long document: all of the card for four heads' keys
-        dict(name="decode, one long sequence", op="decode", batch=1, hq=20, hkv=4, d=128, bs=64, lo=131071, hi=131071,
+        dict(name="decode: one long sequence", op="decode", batch=1, hq=20, hkv=4, d=128, bs=64, lo=131071, hi=131071,
              qtype="bf16", headwise=False, window=0, sink=0),
         # a small batch's whole step: the new token's rows written, then read
-        dict(name="step, 7 short sequences", op="step", batch=7, hq=32, hkv=8, d=128, bs=16, lo=1, hi=401, qtype="bf16",
+        dict(name="step: 7 short sequences", op="step", batch=7, hq=32, hkv=8, d=128, bs=16, lo=1, hi=401, qtype="bf16",
              headwise=False, window=0, sink=0),
         # a large batch's step, grouped heads 5 : 1, 64-token pages
-        dict(name="step, 96 ragged sequences", op="step", batch=96, hq=20, hkv=4, d=128, bs=64, lo=512, hi=8192,
+        dict(name="step: 96 ragged sequences", op="step", batch=96, hq=20, hkv=4, d=128, bs=64, lo=512, hi=8192,
              qtype="bf16", headwise=False, window=0, sink=0),
         # one sequence's last page duplicated by a host scheduler
-        dict(name="copy, 3 pages of 2 layers", op="copy", layers=2, mode="int4", hkv=2, d=64, bs=16, blocks=64, pairs=3,
+        dict(name="copy: 3 pages of 2 layers", op="copy", layers=2, mode="int4", hkv=2, d=64, bs=16, blocks=64, pairs=3,
              headwise=False),
         # pages of many sequences moved at once in every layer of a model
-        dict(name="copy, 1200 pages of 32 layers", op="copy", layers=32, mode="int4", hkv=8, d=128, bs=16, blocks=4001,
+        dict(name="copy: 1200 pages of 32 layers", op="copy", layers=32, mode="int4", hkv=8, d=128, bs=16, blocks=4001,
              pairs=1200, headwise=False),
         # one request's four beams
-        dict(name="fork, 4 beams", op="fork", layers=2, mode="int4", hkv=2, d=64, bs=16, groups=1, beams=4, lo=100, hi=100,
+        dict(name="fork: 4 beams", op="fork", layers=2, mode="int4", hkv=2, d=64, bs=16, groups=1, beams=4, lo=100, hi=100,
              new=1, headwise=False),
         # a batch of beam searches, shared prefixes
-        dict(name="fork, 64 searches of 4 beams", op="fork", layers=8, mode="int4", hkv=8, d=128, bs=16, groups=64, beams=4,
+        dict(name="fork: 64 searches of 4 beams", op="fork", layers=8, mode="int4", hkv=8, d=128, bs=16, groups=64, beams=4,
              lo=500, hi=4096, new=1, headwise=False),
         # a small cache after a few requests ended
-        dict(name="compact, 3 sequences", op="compact", layers=2, mode="int2", hkv=4, d=128, bs=64, batch=3, lo=100, hi=900,
+        dict(name="compact: 3 sequences", op="compact", layers=2, mode="int2", hkv=4, d=128, bs=64, batch=3, lo=100, hi=900,
              used=0.4, headwise=False),
         # a fragmented pool of 16-bit pages, half in use
-        dict(name="compact, 96 sequences", op="compact", layers=8, mode="bf16", hkv=4, d=128, bs=16, batch=96, lo=300,
+        dict(name="compact: 96 sequences", op="compact", layers=8, mode="bf16", hkv=4, d=128, bs=16, batch=96, lo=300,
              hi=1500, used=0.5, headwise=False),
     ]
 
