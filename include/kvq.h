@@ -82,14 +82,20 @@ typedef enum {
  *   the optional RHT) one symmetric fp32 scale s = amax / 127 (INT8 codes
  *   clamp(rne(x / s), -127, 127)) or s = amax / 448 (FP8 E4M3 codes: x / s
  *   rounded to nearest even, saturating at 448); s = 0 gives zero codes;
- *   value code * s. */
+ *   value code * s.
+ * BF16_CACHE: nothing is quantised: the row's values as bf16 (fp32 input
+ *   rounds to nearest even), no RHT.  For layers kept in full precision next
+ *   to quantised ones.  kvq_write, kvq_gather(_chunk), the decode calls and
+ *   the page calls take it; kvq_prefill_attn does not (gather the pages and
+ *   call kvq_prefill_dense_attn). */
 typedef enum {
   KVQ_INT4_TOKEN_HEAD = 0,
   KVQ_INT2_TOKEN_HEAD = 1,
   KVQ_INT8_CHANNEL = 2,
   KVQ_INT4_STEGO = 3,
   KVQ_INT8_TOKEN_HEAD = 4,
-  KVQ_FP8_TOKEN_HEAD = 5
+  KVQ_FP8_TOKEN_HEAD = 5,
+  KVQ_BF16_CACHE = 6
 } kvq_mode;
 
 /* Element type of q / k / v inputs. */
@@ -119,13 +125,15 @@ typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1 } kvq_dtype;
  *       INT8: head_dim bytes of two's-complement codes (no pad)
  *       INT8_TOKEN_HEAD / FP8_TOKEN_HEAD: head_dim code bytes (two's
  *             complement / E4M3), then the fp32 scale (little endian)
+ *       BF16_CACHE: head_dim bf16 values (little endian), 2 * head_dim bytes
  *   Both pools must be 16-byte aligned.
  *
  * rht_signs: int8 [head_dim] of +1/-1 (device).  Non-NULL turns the random
  *   Hadamard transform on for INT4/INT2: y = H (signs * x), H the unnormalised
  *   Sylvester Walsh-Hadamard matrix ([vLLM-INT4] 功能与动机, 实现拆解 2); the
  *   same for INT4_STEGO and the INT8 / FP8 token-head modes.  One vector per
- *   layer, shared by K, V and every head.  Must be NULL for INT8_CHANNEL.
+ *   layer, shared by K, V and every head.  Must be NULL for INT8_CHANNEL and
+ *   BF16_CACHE.
  *
  * ch_amax / ch_amax_ready (INT8 only, else NULL):
  *   ch_amax: fp32 [2][num_kv_heads][head_dim] (index 0 = K, 1 = V).  The scale
@@ -282,7 +290,8 @@ kvq_status kvq_decode_attn(const kvq_cache* cache, const kvq_paging* paging,
  * decode steps (a few new tokens per sequence: each (sequence, kv head)
  * writes its rows with one CTA).  KVQ_INT8_CHANNEL is not supported (its
  * first write takes the channel maxima over every token first):
- * KVQ_ERR_UNSUPPORTED. */
+ * KVQ_ERR_UNSUPPORTED.  KVQ_BF16_CACHE has no query preparation: there the
+ * call launches the write, then the decode. */
 kvq_status kvq_write_decode_attn(const kvq_cache* cache, const kvq_paging* paging,
                                  const void* k, const void* v, int32_t kv_dtype,
                                  const int32_t* cu_new_tokens, int32_t num_tokens,

@@ -45,6 +45,7 @@ int sm_count() {
 // Kernel code family of an API mode: the zero-point-in-scale INT4 rows are
 // INT4 rows with another pad (the `stego` flag of the kernel parameters).
 int kernel_mode(int32_t mode) { return mode == KVQ_INT4_STEGO ? kvq::MODE_INT4 : mode; }
+static_assert((int)KVQ_BF16_CACHE == (int)kvq::MODE_DBF16, "16-bit pages and the dense prefill's rows are one kernel mode");
 
 kvq_status check_cache(const kvq_cache* c) {
   if (!c) return fail(KVQ_ERR_INVALID_ARG, "cache is NULL");
@@ -52,12 +53,15 @@ kvq_status check_cache(const kvq_cache* c) {
   if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16))
     return fail(KVQ_ERR_INVALID_ARG, "k_pages / v_pages must be 16-byte aligned");
   if (c->mode != KVQ_INT4_TOKEN_HEAD && c->mode != KVQ_INT2_TOKEN_HEAD && c->mode != KVQ_INT8_CHANNEL &&
-      c->mode != KVQ_INT4_STEGO && c->mode != KVQ_INT8_TOKEN_HEAD && c->mode != KVQ_FP8_TOKEN_HEAD)
+      c->mode != KVQ_INT4_STEGO && c->mode != KVQ_INT8_TOKEN_HEAD && c->mode != KVQ_FP8_TOKEN_HEAD &&
+      c->mode != KVQ_BF16_CACHE)
     return fail(KVQ_ERR_UNSUPPORTED, "unknown mode");
   if (c->head_dim != 64 && c->head_dim != 128) return fail(KVQ_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
   if (c->block_size != 16 && c->block_size != 32 && c->block_size != 64)
     return fail(KVQ_ERR_UNSUPPORTED, "block_size must be 16, 32 or 64");
   if (c->num_blocks <= 0 || c->num_kv_heads <= 0) return fail(KVQ_ERR_INVALID_ARG, "num_blocks / num_kv_heads must be > 0");
+  if (c->mode == KVQ_BF16_CACHE && c->rht_signs)
+    return fail(KVQ_ERR_INVALID_ARG, "a 16-bit cache takes no RHT signs (nothing is quantised)");
   if (c->mode == KVQ_INT8_CHANNEL) {
     if (c->rht_signs) return fail(KVQ_ERR_INVALID_ARG, "INT8 per-channel mode takes no RHT signs");
     if (!c->ch_amax || !c->ch_amax_ready) return fail(KVQ_ERR_INVALID_ARG, "INT8 mode needs ch_amax and ch_amax_ready");
@@ -108,6 +112,35 @@ kvq::AttnParams attn_params(const kvq_cache* c, const kvq_paging* p, const void*
   a.out = out;
   a.dev_error = dev_error;
   return a;
+}
+
+kvq::WriteParams write_params(const kvq_cache* cache, const kvq_paging* paging, const void* k, const void* v,
+                              int32_t dtype, const int32_t* cu_new_tokens, int32_t num_tokens, int32_t* dev_error) {
+  kvq::WriteParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.k_pages = cache->k_pages;
+  P.v_pages = cache->v_pages;
+  P.num_blocks = cache->num_blocks;
+  P.num_kv_heads = cache->num_kv_heads;
+  P.block_size = cache->block_size;
+  P.head_dim = cache->head_dim;
+  P.mode = kernel_mode(cache->mode);
+  P.stego = cache->mode == KVQ_INT4_STEGO;
+  P.signs = cache->mode == KVQ_INT8_CHANNEL ? nullptr : cache->rht_signs;
+  P.ch_amax = cache->ch_amax;
+  P.ch_ready = cache->ch_amax_ready;
+  P.headwise = paging->block_tables_headwise != nullptr;
+  P.table = P.headwise ? paging->block_tables_headwise : paging->block_tables;
+  P.max_blocks = paging->max_blocks;
+  P.batch = paging->batch;
+  P.seq_lens = paging->seq_lens;
+  P.cu_new = cu_new_tokens;
+  P.k = k;
+  P.v = v;
+  P.dtype = dtype;
+  P.num_tokens = num_tokens;
+  P.dev_error = dev_error;
+  return P;
 }
 
 kvq_status check_q(const kvq_cache* c, const void* q, int32_t dtype, int32_t hq, const float* out) {
@@ -170,6 +203,7 @@ int32_t kvq_row_bytes(int32_t mode, int32_t head_dim) {
   if (mode == KVQ_INT2_TOKEN_HEAD) return head_dim / 4 + 4;
   if (mode == KVQ_INT8_CHANNEL) return head_dim;
   if (mode == KVQ_INT8_TOKEN_HEAD || mode == KVQ_FP8_TOKEN_HEAD) return head_dim + 4;
+  if (mode == KVQ_BF16_CACHE) return 2 * head_dim;
   return 0;
 }
 
@@ -201,30 +235,7 @@ kvq_status kvq_write(const kvq_cache* cache, const kvq_paging* paging, const voi
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(KVQ_ERR_INVALID_ARG, "k / v must be 16-byte aligned");
   if ((long long)num_tokens * cache->num_kv_heads * 2 / 8 + 1 > 0x7FFFFFFFLL)
     return fail(KVQ_ERR_UNSUPPORTED, "too many tokens for one call");
-  kvq::WriteParams P;
-  std::memset(&P, 0, sizeof(P));
-  P.k_pages = cache->k_pages;
-  P.v_pages = cache->v_pages;
-  P.num_blocks = cache->num_blocks;
-  P.num_kv_heads = cache->num_kv_heads;
-  P.block_size = cache->block_size;
-  P.head_dim = cache->head_dim;
-  P.mode = kernel_mode(cache->mode);
-  P.stego = cache->mode == KVQ_INT4_STEGO;
-  P.signs = cache->mode == KVQ_INT8_CHANNEL ? nullptr : cache->rht_signs;
-  P.ch_amax = cache->ch_amax;
-  P.ch_ready = cache->ch_amax_ready;
-  P.headwise = paging->block_tables_headwise != nullptr;
-  P.table = P.headwise ? paging->block_tables_headwise : paging->block_tables;
-  P.max_blocks = paging->max_blocks;
-  P.batch = paging->batch;
-  P.seq_lens = paging->seq_lens;
-  P.cu_new = cu_new_tokens;
-  P.k = k;
-  P.v = v;
-  P.dtype = dtype;
-  P.num_tokens = num_tokens;
-  P.dev_error = dev_error;
+  const kvq::WriteParams P = write_params(cache, paging, k, v, dtype, cu_new_tokens, num_tokens, dev_error);
   cudaError_t e = kvq::launch_write(P, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   return KVQ_OK;
@@ -350,6 +361,16 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
         !page_chunk_map(&P.kv_map[1], cache->v_pages, cache->num_blocks, cache->num_kv_heads, cache->block_size, R, rpc))
       return fail(KVQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the K / V pools");
   }
+  if (cache->mode == KVQ_BF16_CACHE) {
+    if ((long long)cache->num_blocks * cache->num_kv_heads * (cache->block_size / 16) > 0x7FFFFFFFLL)
+      return fail(KVQ_ERR_UNSUPPORTED, "pool too large for 32-bit chunk numbers");
+    if (fw.k) {  // 16-bit pages: the step's write is a launch of its own, which the decode's start overlaps
+      const cudaError_t e = kvq::launch_write(
+          write_params(cache, paging, fw.k, fw.v, fw.dtype, fw.cu_new, fw.num_tokens, dev_error),
+          static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(e);
+    }
+  }
   uint8_t* w = static_cast<uint8_t*>(workspace);
   kvq::DecodeWs ws;
   ws.tile_start = reinterpret_cast<int*>(w + L.off_tile_start);
@@ -432,6 +453,8 @@ kvq_status kvq_prefill_attn(const kvq_cache* cache, const kvq_paging* paging, co
   kvq_status st = check_cache(cache);
   if (st != KVQ_OK) return st;
   if ((st = check_paging(paging, cache->num_kv_heads)) != KVQ_OK) return st;
+  if (cache->mode == KVQ_BF16_CACHE)
+    return fail(KVQ_ERR_UNSUPPORTED, "16-bit pages: gather them (kvq_gather) and call kvq_prefill_dense_attn");
   if (total_q < 0 || max_q_per_seq < 0) return fail(KVQ_ERR_INVALID_ARG, "total_q / max_q_per_seq < 0");
   if (paging->batch == 0 || total_q == 0 || max_q_per_seq == 0) return KVQ_OK;
   if ((st = check_q(cache, q, dtype, num_q_heads, out)) != KVQ_OK) return st;

@@ -10,8 +10,8 @@ namespace kvq {
 
 // Kernel code families.  The API's zero-point-in-scale INT4 mode (3) runs as
 // MODE_INT4 with the `stego` flag of the parameters; 4 and 5 are the INT8 /
-// FP8 rows with one fp32 scale per (token, kv head); 6 is the dense prefill's
-// bf16 rows (no codes, no scale).
+// FP8 rows with one fp32 scale per (token, kv head); 6 is bf16 rows (no codes,
+// no scale): the 16-bit pages and the dense prefill's rows.
 enum { MODE_INT4 = 0, MODE_INT2 = 1, MODE_INT8 = 2, MODE_I8T = 4, MODE_F8T = 5, MODE_DBF16 = 6 };
 enum { DT_F32 = 0, DT_BF16 = 1 };
 enum { DEVERR_BLOCK_RANGE = 1, DEVERR_TABLE_RANGE = 2, DEVERR_SEQ_LEN = 4, DEVERR_TIMEOUT = 8, DEVERR_BOUNDS = 16 };

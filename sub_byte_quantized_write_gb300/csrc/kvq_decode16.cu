@@ -1,0 +1,438 @@
+// kvq_decode16.cu -- split-KV decode attention over 16-bit (bf16) pages.
+//
+// For every sequence b and q head: out = sum_j p_j v_j / sum_j p_j with
+// p_j = exp(scale q . k_j) over the visible keys j, K and V rows read as they
+// lie in the pages (no codes, no scale, no rotation).  4 D G flops for the
+// 4 D bytes of one key of one kv head (G q heads share it): bound by memory
+// for every group the library takes.
+//
+// Design.  The unit of work is a chunk of 16 keys (every page holds whole
+// chunks: 16 rows, contiguous).  The concatenated chunk lists of all
+// (sequence, kv head) pairs are cut into one contiguous, equal slice per warp,
+// whatever the context lengths; a warp writes one partial record (running
+// maximum, sum, unnormalised output) each time its slice leaves a pair, and a
+// second kernel joins the records of a pair.
+//  * Chunk look-up is lane-parallel: lane i of a warp finds the pair, the page
+//    and the 16-bit visibility mask of chunk x + i of the slice, 32 chunks at
+//    a time and one such block ahead, so that the table's latency and the
+//    change of pair cost the loop nothing.
+//  * K and V go from global memory straight to the registers of the matrix
+//    instructions (m16n8k16, bf16 x bf16 with fp32 sums): the order of the
+//    dims of a dot product is free, so a lane reads 16 consecutive bytes of a
+//    key row and these are its operand words for two k-steps; the order of the
+//    output dims is free too, so a lane reads 16 bytes (8 dims) of four key
+//    rows and eight byte permutes pair them by key.  No shared memory, no
+//    wait: the loads of chunk x + 1 are in flight while chunk x is computed
+//    (K's from the end of QK^T on, V's from the end of P.V on).
+//  * QK^T has M = 16 keys and N = 8 q heads: exact products of bf16 inputs.
+//    An fp32 q is split into three bf16 terms (24 bits), three instructions
+//    into the same sums.  P.V has M = 16 dims, K = 16 keys, N = 8 heads; the
+//    weights, an 8 x 8 transpose away (movmatrix), are split into three bf16
+//    terms for the same reason: two terms would keep 16 bits, an error of
+//    2e-6 of the output where the fp32 sums themselves are off by 1e-6.
+//  * The maximum is a reference, not the exact one: it moves (and the sums and
+//    outputs are rescaled) only when a logit passes it by 2^8, so most chunks
+//    take one vote and no reduction.  Weights up to 2^8 lose nothing in fp32
+//    or bf16, whose exponents have the range.
+//  * Masked keys: the logit is replaced by -inf and the value row by zeros,
+//    since a stale slot may hold a NaN, which a zero weight would not cancel.
+
+#include <math_constants.h>
+
+#include "kvq_decode.cuh"
+#include "kvq_internal.h"
+
+namespace kvq {
+
+namespace {
+
+constexpr int D16_KEYS = 16;       // keys per chunk
+constexpr int D16_WARPS = 12;      // per CTA, one CTA per SM
+constexpr int D16_RUNS = 2048;     // entries of the prefix sums over the pairs
+constexpr int D16_MIN_CHUNKS = 4;  // per warp, at least
+constexpr float D16_SLACK = 8.0f;  // log2 units a logit may pass the reference maximum by
+
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {  // read once: not kept in L1
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// D = A * B + D, m16n8k16, bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Three bf16 terms whose sum is (lo, hi) to 24 bits each: what is left after
+// a rounding to 8 bits is exact in fp32, so the third term's rounding, 2^-24
+// of the value at most, is all that is lost.
+__device__ __forceinline__ void split3(float lo, float hi, uint32_t (&t)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    t[k] = pack_bf16(lo, hi);
+    if (k < 2) {
+      lo -= __uint_as_float(t[k] << 16);
+      hi -= __uint_as_float(t[k] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 16 ? 0xFFFFu : (1u << n) - 1u); }
+
+// What the loop needs of one chunk.
+struct Chunk {
+  int bh;         // (sequence, kv head) pair
+  int row;        // chunk of 16 rows in the pool, -1: nothing to read
+  uint32_t mask;  // bit k: key k is visible
+};
+
+template <int D, bool Q32>
+__global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnParams P, const DecodeWs ws) {
+  constexpr int NT = D16_WARPS * 32;
+  constexpr int JK = D / 32;  // 16-byte pieces of a key row per lane
+  constexpr int JV = D / 64;  // 16-byte pieces of a value row per lane
+  constexpr int ROW = 2 * D;  // bytes
+  extern __shared__ __align__(16) uint8_t qsm[];  // Q32: the q terms, [warp][3][JK][32 lanes][16 bytes]
+  __shared__ int run_start[D16_RUNS + 1];
+  __shared__ int wtot[D16_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int G = P.group, Hkv = P.num_kv_heads, bs = P.block_size, BH = P.batch * Hkv;
+  const int bs_log2 = __ffs(bs) - 1;
+  allow_dependent_launch();  // the merge kernel may launch; it waits for this grid to finish
+
+  // Prefix sums of the pairs' chunk counts, over runs of `items` pairs; CTA 0
+  // also publishes every pair's first chunk for the merge and reports bad lengths.
+  const int items = (BH + D16_RUNS - 1) / D16_RUNS;
+  const int nruns = (BH + items - 1) / items;
+  const int rpt = (nruns + NT - 1) / NT;  // runs per thread
+  {
+    const int first = min(BH, (int)threadIdx.x * rpt * items), last = min(BH, first + rpt * items);
+    int sum = 0;
+    for (int bh = first; bh < last; ++bh) sum += tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS).n_virt;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) wtot[warp] = incl;
+    __syncthreads();
+    int x = incl - sum;
+    for (int w = 0; w < warp; ++w) x += wtot[w];
+    for (int bh = first; bh < last; ++bh) {
+      if (bh % items == 0) run_start[bh / items] = x;
+      const int n = tile_list(P, bh / Hkv, bh % Hkv, blockIdx.x == 0 && bh % Hkv == 0, D16_KEYS).n_virt;
+      if (blockIdx.x == 0) ws.tile_start[bh] = x;
+      x += n;
+    }
+    if (threadIdx.x == NT - 1) {
+      run_start[nruns] = x;
+      if (blockIdx.x == 0) ws.tile_start[BH] = x;
+    }
+    __syncthreads();
+  }
+  const int T = run_start[nruns];
+  const int nw = stream_workers(T, gridDim.x * D16_WARPS, ws.fixed_workers, D16_MIN_CHUNKS);
+  const int gw = blockIdx.x * D16_WARPS + warp;
+  if (gw >= nw) return;  // whole warp; no CTA-wide barrier follows
+  const int lo = slice_lo(gw, T, nw), hi = slice_lo(gw + 1, T, nw);
+  if (lo >= hi) return;
+
+  int err = 0;
+  auto look_up = [&](int x) -> Chunk {  // of global chunk x; lanes at or past hi get nothing
+    Chunk r;
+    r.bh = -1;
+    r.row = -1;
+    r.mask = 0;
+    if (x >= hi) return r;
+    int a = 0, z = nruns;
+    while (z - a > 1) {
+      const int mid = (a + z) >> 1;
+      if (run_start[mid] <= x) a = mid;
+      else z = mid;
+    }
+    int bh = a * items, start = run_start[a];
+    TileList t = tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
+    while (start + t.n_virt <= x) {  // (items > 1 only)
+      start += t.n_virt;
+      ++bh;
+      t = tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
+    }
+    r.bh = bh;
+    const int key = D16_KEYS * tile_of(t, x - start);
+    r.mask = low_bits(t.Leff - key);
+    if (t.W > 0) {
+      const int before = t.L - t.W - key;  // keys of the chunk before the window
+      r.mask &= ~low_bits(before) | low_bits(P.sink - key);
+    }
+    if (!KVQ_IN_BOUNDS((key >> bs_log2) < P.max_blocks, P.dev_error)) r.mask = 0;
+    if (r.mask) {
+      const int e = __ldg(P.table + (size_t)(P.headwise ? bh : bh / Hkv) * P.max_blocks + (key >> bs_log2));
+      if (e >= P.num_blocks) err |= DEVERR_BLOCK_RANGE;
+      else if (e >= 0) r.row = (e * Hkv + bh % Hkv) * (bs / D16_KEYS) + ((key & (bs - 1)) / D16_KEYS);
+    }
+    return r;
+  };
+
+  uint4 ka[JK], kb[JK], vr[4][JV];
+  auto load_k = [&](int row) {
+    if (row < 0) return;
+    const uint8_t* p = P.k_pages + (size_t)row * (D16_KEYS * ROW) + g * ROW + c * 16;
+#pragma unroll
+    for (int j = 0; j < JK; ++j) {
+      ka[j] = ld_stream(p + 64 * j);
+      kb[j] = ld_stream(p + 8 * ROW + 64 * j);
+    }
+  };
+  auto load_v = [&](int row) {
+    if (row < 0) return;
+    const uint8_t* p = P.v_pages + (size_t)row * (D16_KEYS * ROW) + 2 * c * ROW + g * 16;
+#pragma unroll
+    for (int j = 0; j < JV; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vr[k][j] = ld_stream(p + (8 * (k >> 1) + (k & 1)) * ROW + 128 * j);  // keys 2c, 2c+1, 2c+8, 2c+9
+  };
+
+  uint4 qf[Q32 ? 1 : JK];  // head g's dims 32 j + 8 c .. + 7
+  uint8_t* qw = qsm + (size_t)warp * 3 * JK * 512 + lane * 16;
+  float acc[JV][4][4];     // [.][w]: dims 64 j + 8 g + 2 w, + 1 of heads 2 c, 2 c + 1
+  float m[2], l[2];
+  const float sl = P.softmax_scale * 1.4426950408889634f;
+  auto begin_pair = [&](int bh) {
+    const size_t q0 = ((size_t)(bh / Hkv) * P.num_q_heads + (bh % Hkv) * G + g) * D + 8 * c;
+#pragma unroll
+    for (int j = 0; j < JK; ++j) {
+      if constexpr (Q32) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+        if (g < G) load_row_elems<8>(P.q, DT_F32, q0 + 32 * j, x);
+        uint32_t t[4][3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split3(x[2 * i], x[2 * i + 1], t[i]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(qw + (k * JK + j) * 512) = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
+      } else {
+        qf[j] = g < G ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.q) + 2 * q0) + 4 * j)
+                      : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < JV; ++j)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][w][i] = 0.0f;
+    m[0] = m[1] = -CUDART_INF_F;
+    l[0] = l[1] = 0.0f;
+  };
+  auto end_pair = [&](int bh) {  // the record of (worker gw, pair bh)
+    const int rec = gw + bh;
+    if (!KVQ_IN_BOUNDS(rec < ws.n_partials, P.dev_error)) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+      const int head = 2 * c + i;
+      if (head < G) {
+        if (g == 0) ws.part_ml[(size_t)rec * G + head] = make_float2(m[i], l[i]);
+        float* po = ws.part_o + ((size_t)rec * G + head) * D + 8 * g;
+#pragma unroll
+        for (int j = 0; j < JV; ++j) {
+          *reinterpret_cast<float4*>(po + 64 * j) = make_float4(acc[j][0][i], acc[j][0][2 + i], acc[j][1][i], acc[j][1][2 + i]);
+          *reinterpret_cast<float4*>(po + 64 * j + 4) = make_float4(acc[j][2][i], acc[j][2][2 + i], acc[j][3][i], acc[j][3][2 + i]);
+        }
+      }
+    }
+  };
+
+  Chunk cur = look_up(lo + lane), nxt = look_up(lo + 32 + lane);
+  // The pages: the write of this step's tokens may still run (this grid
+  // starts alongside it).
+  grid_dependency_wait();
+  int row = __shfl_sync(0xffffffffu, cur.row, 0);
+  load_k(row);
+  load_v(row);
+  int bh = __shfl_sync(0xffffffffu, cur.bh, 0);
+  begin_pair(bh);
+#pragma unroll 1
+  for (int x = lo; x < hi; ++x) {
+    const int i = (x - lo) & 31;
+    const uint32_t mask = __shfl_sync(0xffffffffu, cur.mask, i);
+    const int b1 = __shfl_sync(0xffffffffu, cur.bh, i);
+    if (i == 31) {  // the next block of 32 chunks, looked up one block ago
+      cur = nxt;
+      nxt = look_up(x + 33 + lane);
+    }
+    const int row1 = __shfl_sync(0xffffffffu, cur.row, (i + 1) & 31);  // of chunk x + 1
+    if (b1 != bh) {
+      end_pair(bh);
+      bh = b1;
+      begin_pair(bh);
+    }
+    float s[2][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[0][k] = s[1][k] = 0.0f;
+    if (row >= 0) {
+#pragma unroll
+      for (int j = 0; j < JK; ++j) {
+        if constexpr (Q32) {
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint4 q = *reinterpret_cast<const uint4*>(qw + (k * JK + j) * 512);
+            mma_bf16(s[0], ka[j].x, kb[j].x, ka[j].y, kb[j].y, q.x, q.y);
+            mma_bf16(s[1], ka[j].z, kb[j].z, ka[j].w, kb[j].w, q.z, q.w);
+          }
+        } else {
+          mma_bf16(s[0], ka[j].x, kb[j].x, ka[j].y, kb[j].y, qf[j].x, qf[j].y);
+          mma_bf16(s[1], ka[j].z, kb[j].z, ka[j].w, kb[j].w, qf[j].z, qf[j].w);
+        }
+      }
+    }
+    load_k(row1);
+    if (row >= 0) {
+      float y[4];  // (key g, head 2c), (g, 2c+1), (g+8, 2c), (g+8, 2c+1) in log2 units
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = (s[0][k] + s[1][k]) * sl;
+      if (mask != 0xFFFFu) {
+        if (!((mask >> g) & 1)) y[0] = y[1] = -CUDART_INF_F;
+        if (!((mask >> (g + 8)) & 1)) y[2] = y[3] = -CUDART_INF_F;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (!((mask >> (2 * c + 8 * (k >> 1) + (k & 1))) & 1))
+#pragma unroll
+            for (int j = 0; j < JV; ++j) vr[k][j] = make_uint4(0, 0, 0, 0);
+      }
+      const float t0 = fmaxf(y[0], y[2]), t1 = fmaxf(y[1], y[3]);
+      if (__any_sync(0xffffffffu, t0 > m[0] + D16_SLACK || t1 > m[1] + D16_SLACK)) {
+        float t[2] = {t0, t1};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) t[k] = fmaxf(t[k], __shfl_xor_sync(0xffffffffu, t[k], o));
+          const float mn = fmaxf(m[k], t[k]);
+          const float f = m[k] == -CUDART_INF_F ? 0.0f : ex2(m[k] - mn);
+          m[k] = mn;
+          l[k] *= f;
+#pragma unroll
+          for (int j = 0; j < JV; ++j)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              acc[j][w][k] *= f;
+              acc[j][w][2 + k] *= f;
+            }
+        }
+      }
+      const float m0 = m[0] == -CUDART_INF_F ? 0.0f : m[0], m1 = m[1] == -CUDART_INF_F ? 0.0f : m[1];
+      const float p0 = ex2(y[0] - m0), p1 = ex2(y[1] - m1), p2 = ex2(y[2] - m0), p3 = ex2(y[3] - m1);
+      l[0] += p0 + p2;
+      l[1] += p1 + p3;
+      uint32_t b0[3], b1_[3];
+      split3(p0, p1, b0);
+      split3(p2, p3, b1_);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        b0[k] = transpose8x8(b0[k]);
+        b1_[k] = transpose8x8(b1_[k]);
+      }
+#pragma unroll
+      for (int j = 0; j < JV; ++j) {
+        const uint32_t v0[4] = {vr[0][j].x, vr[0][j].y, vr[0][j].z, vr[0][j].w};
+        const uint32_t v1[4] = {vr[1][j].x, vr[1][j].y, vr[1][j].z, vr[1][j].w};
+        const uint32_t v2[4] = {vr[2][j].x, vr[2][j].y, vr[2][j].z, vr[2][j].w};
+        const uint32_t v3[4] = {vr[3][j].x, vr[3][j].y, vr[3][j].z, vr[3][j].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a0 = prmt(v0[w], v1[w], 0x5410), a1 = prmt(v0[w], v1[w], 0x7632);
+          const uint32_t a2 = prmt(v2[w], v3[w], 0x5410), a3 = prmt(v2[w], v3[w], 0x7632);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) mma_bf16(acc[j][w], a0, a1, a2, a3, b0[k], b1_[k]);
+        }
+      }
+    }
+    load_v(row1);
+    row = row1;
+  }
+  end_pair(bh);
+  err = __reduce_or_sync(0xffffffffu, err);
+  if (err && lane == 0) flag_error(P.dev_error, err);
+}
+
+// Joins the records of one (sequence, q head): one warp each.
+template <int D>
+__global__ void __launch_bounds__(256) decode16_merge_kernel(const AttnParams P, const DecodeWs ws) {
+  constexpr int EPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long wid = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int Hq = P.num_q_heads, G = P.group, Hkv = P.num_kv_heads;
+  if (wid >= (long long)P.batch * Hq) return;
+  const int b = (int)(wid / Hq), hq = (int)(wid % Hq);
+  const int bh = b * Hkv + hq / G, BH = P.batch * Hkv;
+  float* out = P.out + (size_t)wid * D;
+  grid_dependency_wait();  // every record is written
+  const int T = ws.tile_start[BH];
+  const int start = ws.tile_start[bh], end = ws.tile_start[bh + 1];
+  if (start >= end || !KVQ_IN_BOUNDS(start >= 0 && end <= T, P.dev_error)) {  // no visible key
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) out[lane + 32 * e] = 0.0f;
+    return;
+  }
+  const int nw = stream_workers(T, ws.nwall, ws.fixed_workers, D16_MIN_CHUNKS);
+  const int w0 = worker_of(start, T, nw), w1 = worker_of(end - 1, T, nw);
+  const float no_signs[EPL] = {};
+  merge_records<D>(P, ws, bh, hq % G, w0, w1 - w0 + 1, no_signs, out, lane);
+}
+
+template <int D, bool Q32>
+cudaError_t launch_decode16_t(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
+  const size_t smem = Q32 ? (size_t)D16_WARPS * 3 * (D / 32) * 512 : 0;
+  if (smem > 0) {
+    // the opt-in shared-memory size is set once per device (not inside later
+    // calls, which may be captured into a CUDA graph)
+    static bool attr_set[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+      e = cudaFuncSetAttribute(decode16_kernel<D, Q32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+  }
+  cudaError_t e = launch_dependent(decode16_kernel<D, Q32>, dim3(grid), dim3(D16_WARPS * 32), smem, stream, P, ws);
+  if (e != cudaSuccess) return e;
+  const long long warps = (long long)P.batch * P.num_q_heads;
+  return launch_dependent(decode16_merge_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P, ws);
+}
+
+}  // namespace
+
+DecodeShape decode16_shape() { return {1, D16_WARPS}; }
+
+cudaError_t launch_decode16(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
+  const bool f32 = P.dtype == DT_F32;
+  if (P.head_dim == 128)
+    return f32 ? launch_decode16_t<128, true>(P, ws, grid, stream) : launch_decode16_t<128, false>(P, ws, grid, stream);
+  return f32 ? launch_decode16_t<64, true>(P, ws, grid, stream) : launch_decode16_t<64, false>(P, ws, grid, stream);
+}
+
+}  // namespace kvq

@@ -129,7 +129,7 @@ inline DecodeLayout decode_ws_layout(int batch, int num_kv_heads, int group, int
 
 DecodeShape decode_shape(int mode, int head_dim, int group);
 // Key rows per page chunk that the decode's tensor copies move (16 or 8), or 0
-// when the configuration copies its pages with cp.async (INT8 per channel).
+// when the configuration reads its pages another way (INT8 per channel, bf16).
 // The caller's tensor maps kv_map[0 | 1] view the K / V pool as 2-D tensors
 // of such chunks: row (block * Hkv + head) * (block_size / rows) + chunk.
 int decode_chunk_rows(int mode, int head_dim, int group);
@@ -137,6 +137,10 @@ int decode_chunk_rows(int mode, int head_dim, int group);
 cudaError_t launch_write(const WriteParams& P, cudaStream_t stream);
 cudaError_t launch_gather(const WriteParams& P, cudaStream_t stream);
 cudaError_t launch_decode(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream);
+// the decode over 16-bit pages (kvq_decode16.cu), which launch_decode and
+// decode_shape hand to
+DecodeShape decode16_shape();
+cudaError_t launch_decode16(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream);
 cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream);
 
 // The prefill grid: x = query tiles of the longest chunk (PREFILL_ROWS_PER_CTA

@@ -14,6 +14,7 @@
 // INT8 / FP8 per (token, kv_head): the same vLLM page, 功能与动机 and 关联脉络
 // (the per-token-head INT8 / FP8 modes the INT4 mode builds on): one
 // symmetric fp32 scale per row, stored after the D code bytes.
+// 16-bit rows: the values as bf16, a copy (fp32 input rounds to nearest even).
 // Scatter through a uniform or head-wise block table with -1 sentinels:
 // FastDeploy PR #7718 "Optimize AppendAttention for discrete head-wise
 // block_idx", Motivation and PR2-only delta table.
@@ -365,6 +366,107 @@ __global__ void __launch_bounds__(256) gather_kernel(WriteParams P) {
   else gather_rows<MODE, D, STEGO, false, CHUNK>(P, w, pad, off, t0, h, lane, tsign);
 }
 
+// 16-bit rows, both ways: D / 8 lanes per (token, kv head), eight elements
+// each (a 16-byte piece of the bf16 row), K and V sharing the lookup.  A copy:
+// bound by memory and, for one token per sequence, by the launch and the
+// lookup's chain (sequence, table entry).
+template <int D, bool F32>
+__global__ void __launch_bounds__(256) write16_kernel(WriteParams P) {
+  constexpr int LPR = D / 8;
+  allow_dependent_launch();  // as in write_token_head_kernel
+  const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int piece = (int)(id % LPR);
+  const long long th = id / LPR;
+  const int h = (int)(th % P.num_kv_heads);
+  const long long t = th / P.num_kv_heads;
+  if (t >= P.num_tokens) return;
+  const size_t src = ((size_t)t * P.num_kv_heads + h) * D + 8 * piece;
+  float x[2][8];
+  load_row_elems<8>(P.k, F32 ? DT_F32 : DT_BF16, src, x[0]);
+  load_row_elems<8>(P.v, F32 ? DT_F32 : DT_BF16, src, x[1]);
+  const long long off = gather_row_offset<false>(P, (int)t, h);
+  if (off < 0) return;  // evicted or invalid: nothing is written
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(x[kv][2 * i], x[kv][2 * i + 1]);  // bf16 input: exact
+      w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    *reinterpret_cast<uint4*>((kv ? P.v_pages : P.k_pages) + off + 16 * piece) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <int D, bool BF16, bool CHUNK>
+__global__ void __launch_bounds__(256) gather16_kernel(WriteParams P) {
+  constexpr int LPR = D / 8;
+  const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int piece = (int)(id % LPR);
+  const long long th = id / LPR;
+  const int h = (int)(th % P.num_kv_heads);
+  const long long t = th / P.num_kv_heads;
+  if (t >= P.num_tokens) return;
+  const long long off = gather_row_offset<CHUNK>(P, (int)t, h);
+  float x[2][8];
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[kv][i] = 0.0f;
+    if (off >= 0) {
+      load_row_elems<8>((kv ? P.v_pages : P.k_pages), DT_BF16, (size_t)(off >> 1) + 8 * piece, x[kv]);
+    } else if (CHUNK && off <= -2) {  // a row of the full-precision chunk
+      const long long src = -2 - off;
+      if (KVQ_IN_BOUNDS(src < (long long)__ldg(P.cu_chunk + P.batch), P.dev_error))
+        load_row_elems<8>(kv ? P.chunk_v : P.chunk_k, P.chunk_dtype, ((size_t)src * P.num_kv_heads + h) * D + 8 * piece,
+                          x[kv]);
+    }
+  }
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    void* out = kv ? P.out_v : P.out_k;
+    const size_t o = ((size_t)t * P.num_kv_heads + h) * D + 8 * piece;
+    if constexpr (BF16) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x[kv][2 * i], x[kv][2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+      p[0] = make_float4(x[kv][0], x[kv][1], x[kv][2], x[kv][3]);
+      p[1] = make_float4(x[kv][4], x[kv][5], x[kv][6], x[kv][7]);
+    }
+  }
+}
+
+inline unsigned rows16_blocks(const WriteParams& P) {  // (the callers bound num_tokens * num_kv_heads)
+  return (unsigned)(((long long)P.num_tokens * P.num_kv_heads * (P.head_dim / 8) + 255) / 256);
+}
+
+template <int D>
+cudaError_t launch_write16(const WriteParams& P, cudaStream_t stream) {
+  if (P.dtype == DT_F32) write16_kernel<D, true><<<rows16_blocks(P), 256, 0, stream>>>(P);
+  else write16_kernel<D, false><<<rows16_blocks(P), 256, 0, stream>>>(P);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_gather16(const WriteParams& P, cudaStream_t stream) {
+  const unsigned blocks = rows16_blocks(P);
+  const bool bf16 = P.out_dtype == DT_BF16;
+  if (P.chunk_k) {
+    if (bf16) gather16_kernel<D, true, true><<<blocks, 256, 0, stream>>>(P);
+    else gather16_kernel<D, false, true><<<blocks, 256, 0, stream>>>(P);
+  } else {
+    if (bf16) gather16_kernel<D, true, false><<<blocks, 256, 0, stream>>>(P);
+    else gather16_kernel<D, false, false><<<blocks, 256, 0, stream>>>(P);
+  }
+  return cudaGetLastError();
+}
+
 template <int MODE, bool STEGO>
 void launch_gather_m(const WriteParams& P, int blocks, cudaStream_t stream) {
   // the full-precision chunk is a separate instantiation, so the plain
@@ -379,6 +481,8 @@ void launch_gather_m(const WriteParams& P, int blocks, cudaStream_t stream) {
 }
 
 cudaError_t launch_gather(const WriteParams& P, cudaStream_t stream) {
+  if (P.mode == MODE_DBF16)
+    return P.head_dim == 128 ? launch_gather16<128>(P, stream) : launch_gather16<64>(P, stream);
   const long long warps = (long long)((P.num_tokens + GATHER_TOKENS - 1) / GATHER_TOKENS) * P.num_kv_heads;
   const int blocks = (int)((warps + 7) / 8);
   switch (P.mode) {
@@ -556,6 +660,8 @@ cudaError_t launch_write_m(const WriteParams& P, cudaStream_t stream) {
 }
 
 cudaError_t launch_write(const WriteParams& P, cudaStream_t stream) {
+  if (P.mode == MODE_DBF16)
+    return P.head_dim == 128 ? launch_write16<128>(P, stream) : launch_write16<64>(P, stream);
   const long long warps = (long long)P.num_tokens * P.num_kv_heads * 2;
   const int blocks = (int)((warps + 7) / 8);
   if (P.mode == MODE_INT8) {
