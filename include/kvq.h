@@ -109,6 +109,10 @@ typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1 } kvq_dtype;
 #define KVQ_DEVERR_BOUNDS 16     /* debug library only (libkvq_debug.so, built with -DKVQ_BOUNDS_CHECK):
                                      an index computed on the device fell outside its buffer; the access
                                      was skipped (never expected) */
+#define KVQ_DEVERR_ROW_RANGE 32     /* kvq_fork: a parent >= the old batch: the row comes out empty */
+#define KVQ_DEVERR_NO_PAGES 64      /* kvq_fork: no free page left: the entry comes out -1 */
+#define KVQ_DEVERR_PAGE_CONFLICT 128 /* kvq_copy_pages: a destination that another pair reads, or that a lower pair
+                                     writes: the pair is skipped */
 
 /* One layer's paged cache (caller-allocated; store it as torch.uint8, cf.
  * [FD-UINT8] 修复).
@@ -340,6 +344,101 @@ kvq_status kvq_decode_attn_noalloc(const kvq_cache* cache, const kvq_paging* pag
                                    const void* q, int32_t dtype, int32_t num_q_heads,
                                    float softmax_scale, float* out, int32_t num_splits,
                                    int32_t* dev_error, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages.  The calls below work on page numbers: a table entry, for a uniform
+ * table the number of a block (every kv head's page of it), for a head-wise
+ * table that of one head's page.  The pages of a table are a "space": one for
+ * a uniform table, num_kv_heads of them for a head-wise one, page numbers 0 ..
+ * num_blocks - 1 in each ([FD-HEADWISE] Motivation: per-head pages that are
+ * freed and handed out by themselves).
+ *
+ * caches : host array of num_caches (1 .. 128) caches that share page numbers:
+ *   the layers of a model under one table.  Their num_blocks, num_kv_heads and
+ *   block_size are the same; modes and head_dim may differ.  Pages are copied
+ *   as bytes, K and V of every cache (INT8_CHANNEL scales belong to the cache
+ *   and stay valid).
+ * workspace : device scratch of at least the size the call's _workspace_size
+ *   gives, 256-byte aligned; what it holds on entry does not matter.  Calls
+ *   that may run at the same time (also as two captured graphs) need one each.
+ * Counters and page numbers depend on no order of execution. */
+
+/* kvq_copy_pages -- page src[i] into page dst[i], in every cache.
+ * src, dst : int32 [num_pairs] (device).  headwise != 0: numbers count the
+ *   (block, head) pages as they lie in the pool, block * num_kv_heads + head.
+ * A pair with a negative number is skipped, and so is src[i] == dst[i]; one
+ * past the pool is skipped and sets KVQ_DEVERR_BLOCK_RANGE.  Every source is
+ * read as it was before the call: a pair whose destination is another pair's
+ * source is skipped, and of several pairs with one destination the lowest is
+ * done; the skipped ones set KVQ_DEVERR_PAGE_CONFLICT. */
+kvq_status kvq_copy_workspace_size(const kvq_cache* caches, int32_t num_caches, int32_t num_pairs, int32_t headwise,
+                                   size_t* bytes);
+kvq_status kvq_copy_pages(const kvq_cache* caches, int32_t num_caches, const int32_t* src, const int32_t* dst,
+                          int32_t num_pairs, int32_t headwise, void* workspace, size_t workspace_bytes,
+                          int32_t* dev_error, void* stream);
+
+/* kvq_fork -- new table rows from old ones: what a step of beam search, a
+ * prompt that shares a prefix, a roll-back, the end of a request or the next
+ * tokens of every sequence need, in one call and without the host.
+ *
+ * New row i continues old row parents[i]: it keeps the first
+ * min(seq_len, keep_tokens[i]) tokens (keep_tokens NULL: all) and gets pages
+ * for new_tokens[i] more (NULL: none), to be written by the next kvq_write.
+ * parents[i] < 0 starts an empty row.  An old row that no new row continues is
+ * freed: its pages are free unless another row or a pin holds them.
+ *   - Pages that hold kept tokens are shared, not copied, except a partly
+ *     filled last page, which the row will write into: of the rows that end in
+ *     it the lowest keeps it, provided no row holds it further from its end
+ *     and nothing pins it; every other row gets a copy (all slots, every
+ *     cache).  -1 entries stay -1.
+ *   - Pages are handed out in ascending order of the free ones, to the rows in
+ *     order: first the copy of the last page, then the pages of new tokens.  A
+ *     page is free when no new row and no pin holds it, so one that only freed
+ *     rows held can be handed out by the same call.
+ *   - With no free page left an entry comes out -1 (its tokens are lost to the
+ *     row) and KVQ_DEVERR_NO_PAGES is set.
+ *
+ * paging     : the old rows (tables, seq_lens, max_blocks, batch; windows are
+ *              ignored).  NULL or batch 0: there are none.  Entries past a
+ *              row's last token are not looked at.
+ * parents    : int32 [new_paging->batch].  keep_tokens, new_tokens: the same, or NULL.
+ * pins       : int32 [spaces][num_blocks] or NULL: uses of a page outside the
+ *              tables (a prefix cache); a positive one keeps it.
+ * new_paging : the new rows, written: its table (of the old one's kind and
+ *              width) and seq_lens = kept + new tokens.  Entries past them
+ *              come out -1.  May not overlap the old rows or another input.
+ * page_refs  : int32 [spaces][num_blocks], written: pins (where positive) plus the new rows'
+ *              uses; 0 = free.
+ * A seq_len, keep_tokens or new_tokens below 0 counts as 0
+ * (KVQ_DEVERR_SEQ_LEN); tokens past the table's width are dropped
+ * (KVQ_DEVERR_TABLE_RANGE); entries past the pool come out -1
+ * (KVQ_DEVERR_BLOCK_RANGE). */
+kvq_status kvq_fork_workspace_size(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging,
+                                   const kvq_paging* new_paging, size_t* bytes);
+kvq_status kvq_fork(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging, const int32_t* parents,
+                    const int32_t* keep_tokens, const int32_t* new_tokens, const int32_t* pins,
+                    const kvq_paging* new_paging, int32_t* page_refs, void* workspace, size_t workspace_bytes,
+                    int32_t* dev_error, void* stream);
+
+/* kvq_compact -- the used pages of each space moved to its lowest numbers.
+ * With n pages used (named by a row below its seq_len, or pinned), the k-th
+ * used and unpinned page numbered n or above moves into the k-th unused page
+ * below n, in every cache, and the tables follow.  Pinned pages stay where
+ * they are.
+ * paging     : the rows (windows are ignored); entries past a row's last token are not looked at.
+ * pins       : as kvq_fork.
+ * new_tables : like the table of `paging`, written; may be that table itself.
+ *              Entries past a row's last token come out -1.
+ * page_map   : int32 [spaces][num_blocks], written: each page's new number, -1 for an unused one.
+ * page_refs  : int32 [spaces][num_blocks], written: pins plus uses by new number; 0 = free.
+ * num_used   : int32 [spaces], written: n.
+ * Outputs may not overlap inputs (but for new_tables) nor one another.  Bad
+ * lengths and entries as in kvq_fork. */
+kvq_status kvq_compact_workspace_size(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging,
+                                      size_t* bytes);
+kvq_status kvq_compact(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging, const int32_t* pins,
+                       int32_t* new_tables, int32_t* page_map, int32_t* page_refs, int32_t* num_used, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_error, void* stream);
 
 /* Human-readable name of a status. */
 const char* kvq_status_string(int32_t status);

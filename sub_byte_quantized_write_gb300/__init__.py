@@ -9,13 +9,17 @@ built, importing this package raises ImportError.
 Names mirror the C calls: ``kvq_write``, ``kvq_gather``, ``kvq_prefill_dense_attn``, ``kvq_decode_attn``,
 ``kvq_write_decode_attn``,
 ``kvq_decode_attn_noalloc``, ``kvq_prefill_attn``, ``kvq_decode_workspace_size``,
-``kvq_row_bytes``.
+``kvq_row_bytes``, ``kvq_copy_pages``, ``kvq_fork``, ``kvq_compact`` and their ``_workspace_size``.
+
+A call runs on the device of its cache, on `stream` if one is given, else on
+that device's current stream; what it allocates belongs to that stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional
+from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -38,6 +42,7 @@ KVQ_INT8_TOKEN_HEAD, KVQ_FP8_TOKEN_HEAD, KVQ_BF16_CACHE = 4, 5, 6
 KVQ_F32, KVQ_BF16 = 0, 1
 KVQ_DEVERR_BLOCK_RANGE, KVQ_DEVERR_TABLE_RANGE, KVQ_DEVERR_SEQ_LEN, KVQ_DEVERR_TIMEOUT = 1, 2, 4, 8
 KVQ_DEVERR_BOUNDS = 16  # debug library only
+KVQ_DEVERR_ROW_RANGE, KVQ_DEVERR_NO_PAGES, KVQ_DEVERR_PAGE_CONFLICT = 32, 64, 128
 
 
 class KvqCache(ctypes.Structure):
@@ -82,6 +87,19 @@ _lib.kvq_prefill_attn.restype = _I
 _lib.kvq_prefill_dense_attn.argtypes = [_P, _P, _P, _I, _I, _I, _PP, _P, _I, _I, _P, _I, _I, ctypes.c_float, _P, _P,
                                         _P]
 _lib.kvq_prefill_dense_attn.restype = _I
+_SZ = ctypes.POINTER(ctypes.c_size_t)
+_lib.kvq_copy_workspace_size.argtypes = [_CP, _I, _I, _I, _SZ]
+_lib.kvq_copy_workspace_size.restype = _I
+_lib.kvq_copy_pages.argtypes = [_CP, _I, _P, _P, _I, _I, _P, ctypes.c_size_t, _P, _P]
+_lib.kvq_copy_pages.restype = _I
+_lib.kvq_fork_workspace_size.argtypes = [_CP, _I, _PP, _PP, _SZ]
+_lib.kvq_fork_workspace_size.restype = _I
+_lib.kvq_fork.argtypes = [_CP, _I, _PP, _P, _P, _P, _P, _PP, _P, _P, ctypes.c_size_t, _P, _P]
+_lib.kvq_fork.restype = _I
+_lib.kvq_compact_workspace_size.argtypes = [_CP, _I, _PP, _SZ]
+_lib.kvq_compact_workspace_size.restype = _I
+_lib.kvq_compact.argtypes = [_CP, _I, _PP, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]
+_lib.kvq_compact.restype = _I
 
 
 class KvqError(RuntimeError):
@@ -121,6 +139,27 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _as_stream(stream, device):
+    """A torch stream object for `stream` (a torch stream or a raw cudaStream_t)."""
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """torch.empty for a call on `stream`: the memory belongs to the stream that uses it, so that the allocator
+    neither hands out what other work still holds nor takes it back too early."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_as_stream(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _run(device: torch.device, stream, fn, *args) -> None:
+    """fn(*args, stream) with `device` current."""
+    other = device.type == "cuda" and device.index is not None and device.index != torch.cuda.current_device()
+    with torch.cuda.device(device) if other else contextlib.nullcontext():
+        _check(fn(*args, _stream_ptr(stream)))
+
+
 def _qdtype(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return KVQ_F32
@@ -156,7 +195,19 @@ class PagedCache:
             self.ch_amax = None
             self.ch_amax_ready = None
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_struct", None)
+
     def struct(self) -> KvqCache:
+        """The C struct: built once, and again when an attribute was set or a pool's memory changed."""
+        s = self._struct
+        if s is None or s.k_pages != self.k_pages.data_ptr() or s.v_pages != self.v_pages.data_ptr():
+            s = self._build()
+            object.__setattr__(self, "_struct", s)
+        return s
+
+    def _build(self) -> KvqCache:
         return KvqCache(_dev_ptr(self.k_pages, torch.uint8, "k_pages"), _dev_ptr(self.v_pages, torch.uint8, "v_pages"),
                         self.num_blocks, self.num_kv_heads, self.block_size, self.head_dim, self.mode,
                         _dev_ptr(self.rht_signs, torch.int8, "rht_signs"),
@@ -195,9 +246,9 @@ def kvq_write(cache: PagedCache, paging: Paging, k: torch.Tensor, v: torch.Tenso
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and dtype")
     cs, ps = cache.struct(), paging.struct()
-    _check(_lib.kvq_write(ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
+    _run(cache.k_pages.device, stream, _lib.kvq_write, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
                           _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]),
-                          _dev_ptr(dev_error, torch.int32, "dev_error"), _stream_ptr(stream)))
+                          _dev_ptr(dev_error, torch.int32, "dev_error"))
 
 
 def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_tokens: int,
@@ -212,25 +263,25 @@ def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_t
     shape = (num_tokens, cache.num_kv_heads, cache.head_dim)
     dev = cache.k_pages.device
     if k_out is None:
-        k_out = torch.empty(shape, dtype=out_dtype, device=dev)
+        k_out = _empty(shape, out_dtype, dev, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=out_dtype, device=dev)
+        v_out = _empty(shape, out_dtype, dev, stream)
     if k_out.dtype != v_out.dtype:
         raise ValueError("k_out and v_out must have the same dtype")
     cs, ps = cache.struct(), paging.struct()
     if k_chunk is None:
-        _check(_lib.kvq_gather(ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(cu_tokens, torch.int32, "cu_tokens"),
+        _run(cache.k_pages.device, stream, _lib.kvq_gather, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(cu_tokens, torch.int32, "cu_tokens"),
                                int(num_tokens), _dev_ptr(k_out, name="k_out"), _dev_ptr(v_out, name="v_out"),
-                               _qdtype(k_out), _dev_ptr(dev_error, torch.int32, "dev_error"), _stream_ptr(stream)))
+                               _qdtype(k_out), _dev_ptr(dev_error, torch.int32, "dev_error"))
     else:
         if v_chunk is None or k_chunk.dtype != v_chunk.dtype:
             raise ValueError("k_chunk and v_chunk must be given together, with one dtype")
-        _check(_lib.kvq_gather_chunk(ctypes.byref(cs), ctypes.byref(ps),
+        _run(cache.k_pages.device, stream, _lib.kvq_gather_chunk, ctypes.byref(cs), ctypes.byref(ps),
                                      _dev_ptr(cu_tokens, torch.int32, "cu_tokens"), int(num_tokens),
                                      _dev_ptr(k_chunk, name="k_chunk"), _dev_ptr(v_chunk, name="v_chunk"),
                                      _qdtype(k_chunk), _dev_ptr(cu_chunk, torch.int32, "cu_chunk"),
                                      _dev_ptr(k_out, name="k_out"), _dev_ptr(v_out, name="v_out"), _qdtype(k_out),
-                                     _dev_ptr(dev_error, torch.int32, "dev_error"), _stream_ptr(stream)))
+                                     _dev_ptr(dev_error, torch.int32, "dev_error"))
     return k_out, v_out
 
 
@@ -249,15 +300,14 @@ def kvq_decode_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, softmax_
     """Decode attention of q [batch, num_q_heads, head_dim]; returns fp32 out."""
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _empty((B, Hq, D), torch.float32, q.device, stream)
     if workspace is None:
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _check(_lib.kvq_decode_attn(ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
-                                float(softmax_scale), _dev_ptr(out, torch.float32, "out"),
-                                _dev_ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
-                                num_splits, _dev_ptr(dev_error, torch.int32, "dev_error"), _stream_ptr(stream)))
+    _run(cache.k_pages.device, stream, _lib.kvq_decode_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"),
+         _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"), _dev_ptr(workspace, name="workspace"),
+         workspace.numel() * workspace.element_size(), num_splits, _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
 
 
@@ -272,17 +322,16 @@ def kvq_write_decode_attn(cache: PagedCache, paging: Paging, k: torch.Tensor, v:
         raise ValueError("k and v must have the same shape and dtype")
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _empty((B, Hq, D), torch.float32, q.device, stream)
     if workspace is None:
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _check(_lib.kvq_write_decode_attn(ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
+    _run(cache.k_pages.device, stream, _lib.kvq_write_decode_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
                                       _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"),
                                       int(k.shape[0]), _dev_ptr(q, name="q"), _qdtype(q), Hq, float(softmax_scale),
                                       _dev_ptr(out, torch.float32, "out"), _dev_ptr(workspace, torch.uint8, "workspace"),
-                                      workspace.numel(), int(num_splits), _dev_ptr(dev_error, torch.int32, "dev_error"),
-                                      _stream_ptr(stream)))
+                                      workspace.numel(), int(num_splits), _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
 
 
@@ -296,11 +345,11 @@ def kvq_decode_attn_noalloc(cache: PagedCache, paging: Paging, q: torch.Tensor, 
     device must come before any stream capture."""
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _empty((B, Hq, D), torch.float32, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _check(_lib.kvq_decode_attn_noalloc(ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
+    _run(cache.k_pages.device, stream, _lib.kvq_decode_attn_noalloc, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
                                         float(softmax_scale), _dev_ptr(out, torch.float32, "out"), num_splits,
-                                        _dev_ptr(dev_error, torch.int32, "dev_error"), _stream_ptr(stream)))
+                                        _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
 
 
@@ -310,12 +359,11 @@ def kvq_prefill_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, cu_q: t
     """Causal chunked-prefill attention of q [total_q, num_q_heads, head_dim]; returns fp32 out."""
     T, Hq, D = q.shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.float32, device=q.device)
+        out = _empty((T, Hq, D), torch.float32, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _check(_lib.kvq_prefill_attn(ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
+    _run(cache.k_pages.device, stream, _lib.kvq_prefill_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
                                  _dev_ptr(cu_q, torch.int32, "cu_q"), T, int(max_q_per_seq), float(softmax_scale),
-                                 _dev_ptr(out, torch.float32, "out"), _dev_ptr(dev_error, torch.int32, "dev_error"),
-                                 _stream_ptr(stream)))
+                                 _dev_ptr(out, torch.float32, "out"), _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
 
 
@@ -331,14 +379,180 @@ def kvq_prefill_dense_attn(k: torch.Tensor, v: torch.Tensor, cu_kv: torch.Tensor
         raise ValueError("k and v must be bfloat16 tensors of one shape")
     T, Hq, D = q.shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.float32, device=q.device)
+        out = _empty((T, Hq, D), torch.float32, q.device, stream)
     ps = KvqPaging(None, None, 0, int(seq_lens.shape[0]), _dev_ptr(seq_lens, torch.int32, "seq_lens"),
                    _dev_ptr(window_per_kv_head, torch.int32, "window_per_kv_head"), int(sink_size))
-    _check(_lib.kvq_prefill_dense_attn(_dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
+    _run(k.device, stream, _lib.kvq_prefill_dense_attn, _dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
                                        _dev_ptr(cu_kv, torch.int32, "cu_kv"), int(k.shape[0]), int(k.shape[1]),
                                        int(k.shape[2]),
                                        ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
                                        _dev_ptr(cu_q, torch.int32, "cu_q"), T, int(max_q_per_seq),
                                        float(softmax_scale), _dev_ptr(out, torch.float32, "out"),
-                                       _dev_ptr(dev_error, torch.int32, "dev_error"), _stream_ptr(stream)))
+                                       _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
+
+
+# ---------------------------------------------------------------------------
+# pages
+
+Caches = Union[PagedCache, Sequence[PagedCache]]
+
+
+def _cache_array(caches: Caches):
+    """(ctypes array, number, device) of the caches that share page numbers."""
+    cs = [caches] if isinstance(caches, PagedCache) else list(caches)
+    if not cs:
+        raise ValueError("no caches")
+    dev = cs[0].k_pages.device
+    for c in cs:
+        if c.k_pages.device != dev:
+            raise ValueError("the caches of one call must be on one device")
+    return (KvqCache * len(cs))(*[c.struct() for c in cs]), len(cs), dev
+
+
+def _page_tensor(t: Optional[torch.Tensor], name: str, dev: torch.device, numel: Optional[int] = None):
+    """Device pointer of an int32 tensor of the caches' device, with `numel` elements where that is given."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError("%s must be on the caches' device" % name)
+    if numel is not None and t.numel() != numel:
+        raise ValueError("%s must have %d elements, got %d" % (name, numel, t.numel()))
+    return _dev_ptr(t, torch.int32, name)
+
+
+def _page_paging(p: "Paging", name: str, dev: torch.device, num_kv_heads: int) -> Tuple[KvqPaging, bool, int]:
+    """(struct, head-wise, rows) of a paging state of the caches' device."""
+    headwise = p.block_tables_headwise is not None
+    t = p.block_tables_headwise if headwise else p.block_tables
+    rows = int(p.seq_lens.shape[0])
+    if t is None or t.device != dev or p.seq_lens.device != dev:
+        raise ValueError("%s needs a block table and lengths on the caches' device" % name)
+    if int(t.shape[0]) != rows * (num_kv_heads if headwise else 1):
+        raise ValueError("%s: the table's rows do not match seq_lens" % name)
+    return p.struct(), headwise, rows
+
+
+def _page_scratch(workspace, size, dev, stream, *args):
+    if workspace is None:
+        workspace = _empty(max(size(*args), 256), torch.uint8, dev, stream)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on the caches' device")
+    return _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(), workspace
+
+
+def kvq_copy_workspace_size(caches: Caches, num_pairs: int, headwise: bool = False) -> int:
+    """Bytes of scratch that kvq_copy_pages needs."""
+    cs, n, _ = _cache_array(caches)
+    size = ctypes.c_size_t(0)
+    _check(_lib.kvq_copy_workspace_size(cs, n, int(num_pairs), int(headwise), ctypes.byref(size)))
+    return size.value
+
+
+def kvq_copy_pages(caches: Caches, src: torch.Tensor, dst: torch.Tensor, headwise: bool = False,
+                   workspace: Optional[torch.Tensor] = None, dev_error: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Page src[i] into page dst[i] (int32 tensors), K and V of every cache.  headwise: the numbers count
+    (block, head) pages, block * num_kv_heads + head.  Sources are read as they were before the call; pairs
+    that conflict are skipped and set KVQ_DEVERR_PAGE_CONFLICT."""
+    cs, n, dev = _cache_array(caches)
+    pairs = int(src.numel())
+    ps, pd = _page_tensor(src, "src", dev), _page_tensor(dst, "dst", dev, pairs)
+    ws, nbytes, _keep = _page_scratch(workspace, kvq_copy_workspace_size, dev, stream, caches, pairs, headwise)
+    _run(dev, stream, _lib.kvq_copy_pages, cs, n, ps, pd, pairs, int(headwise), ws, nbytes,
+         _page_tensor(dev_error, "dev_error", dev))
+
+
+def _fork_out(caches: Caches, paging: Optional[Paging], rows: int, dev, stream) -> Paging:
+    if paging is None:
+        raise ValueError("without old rows, `out` gives the new table's kind and width")
+    headwise = paging.block_tables_headwise is not None
+    first = caches if isinstance(caches, PagedCache) else caches[0]
+    table = _empty((rows * (first.num_kv_heads if headwise else 1), paging.max_blocks), torch.int32, dev, stream)
+    kw = {"block_tables_headwise" if headwise else "block_tables": table}
+    return Paging(_empty(rows, torch.int32, dev, stream), window_per_kv_head=paging.window_per_kv_head,
+                  sink_size=paging.sink_size, **kw)
+
+
+def kvq_fork_workspace_size(caches: Caches, paging: Optional[Paging], rows: int, out: Optional[Paging] = None) -> int:
+    """Bytes of scratch that kvq_fork needs for `rows` new rows."""
+    cs, n, dev = _cache_array(caches)
+    like = (out or paging).struct()  # (the size goes by the new rows' number, the table's kind and its width)
+    like.batch = int(rows)
+    size = ctypes.c_size_t(0)
+    _check(_lib.kvq_fork_workspace_size(cs, n, None, ctypes.byref(like), ctypes.byref(size)))
+    return size.value
+
+
+def kvq_fork(caches: Caches, paging: Optional[Paging], parents: torch.Tensor,
+             new_tokens: Optional[torch.Tensor] = None, keep_tokens: Optional[torch.Tensor] = None,
+             pins: Optional[torch.Tensor] = None, out: Optional[Paging] = None,
+             page_refs: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+             dev_error: Optional[torch.Tensor] = None, stream=None) -> Tuple[Paging, torch.Tensor]:
+    """New table rows from old ones: row i continues old row parents[i] (int32; negative: starts empty), keeps its
+    first keep_tokens[i] tokens and gets pages for new_tokens[i] more.  Full pages are shared, a shared partly
+    filled last page is copied in every cache, rows that nobody continues are freed.  Returns the new paging state
+    (`out` if given: its table and seq_lens are written) and page_refs [spaces, num_blocks], the uses of every page
+    (0: free).  paging None: there are no old rows yet (`out` is needed)."""
+    cs, n, dev = _cache_array(caches)
+    Hkv, blocks = cs[0].num_kv_heads, cs[0].num_blocks
+    rows = int(parents.numel())
+    if out is None:
+        out = _fork_out(caches, paging, rows, dev, stream)
+    new, headwise, got = _page_paging(out, "out", dev, Hkv)
+    if got != rows:
+        raise ValueError("out must have one row per parent")
+    old = None if paging is None else _page_paging(paging, "paging", dev, Hkv)[0]
+    spaces = Hkv if headwise else 1
+    if page_refs is None:
+        page_refs = _empty((spaces, blocks), torch.int32, dev, stream)
+    ws, nbytes, _keep = _page_scratch(workspace, kvq_fork_workspace_size, dev, stream, caches, paging, rows, out)
+    _run(dev, stream, _lib.kvq_fork, cs, n, None if old is None else ctypes.byref(old),
+         _page_tensor(parents, "parents", dev), _page_tensor(keep_tokens, "keep_tokens", dev, rows),
+         _page_tensor(new_tokens, "new_tokens", dev, rows), _page_tensor(pins, "pins", dev, spaces * blocks),
+         ctypes.byref(new), _page_tensor(page_refs, "page_refs", dev, spaces * blocks), ws, nbytes,
+         _page_tensor(dev_error, "dev_error", dev))
+    return out, page_refs
+
+
+def kvq_compact_workspace_size(caches: Caches, paging: Paging) -> int:
+    """Bytes of scratch that kvq_compact needs."""
+    cs, n, dev = _cache_array(caches)
+    ps = paging.struct()
+    size = ctypes.c_size_t(0)
+    _check(_lib.kvq_compact_workspace_size(cs, n, ctypes.byref(ps), ctypes.byref(size)))
+    return size.value
+
+
+def kvq_compact(caches: Caches, paging: Paging, pins: Optional[torch.Tensor] = None, out: Optional[Paging] = None,
+                page_map: Optional[torch.Tensor] = None, page_refs: Optional[torch.Tensor] = None,
+                num_used: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                dev_error: Optional[torch.Tensor] = None, stream=None):
+    """The used pages of each space moved to its lowest numbers, in every cache.  Returns (paging state with the
+    rewritten table, page_map [spaces, num_blocks] (old number -> new, -1: unused), page_refs [spaces, num_blocks]
+    by new number, num_used [spaces]).  `out` gives the table to write; it may be `paging` itself.  Pages with a
+    positive `pins` stay where they are."""
+    cs, n, dev = _cache_array(caches)
+    Hkv, blocks = cs[0].num_kv_heads, cs[0].num_blocks
+    old, headwise, rows = _page_paging(paging, "paging", dev, Hkv)
+    kind = "block_tables_headwise" if headwise else "block_tables"
+    table = getattr(paging, kind)
+    if out is None:
+        out = Paging(paging.seq_lens, window_per_kv_head=paging.window_per_kv_head, sink_size=paging.sink_size,
+                     **{kind: _empty(tuple(table.shape), torch.int32, dev, stream)})
+    to = getattr(out, kind)
+    if to is None or to.shape != table.shape:
+        raise ValueError("out must have a table of the same kind and shape")
+    spaces = Hkv if headwise else 1
+    if page_map is None:
+        page_map = _empty((spaces, blocks), torch.int32, dev, stream)
+    if page_refs is None:
+        page_refs = _empty((spaces, blocks), torch.int32, dev, stream)
+    if num_used is None:
+        num_used = _empty(spaces, torch.int32, dev, stream)
+    ws, nbytes, _keep = _page_scratch(workspace, kvq_compact_workspace_size, dev, stream, caches, paging)
+    _run(dev, stream, _lib.kvq_compact, cs, n, ctypes.byref(old), _page_tensor(pins, "pins", dev, spaces * blocks),
+         _page_tensor(to, "out", dev), _page_tensor(page_map, "page_map", dev, spaces * blocks),
+         _page_tensor(page_refs, "page_refs", dev, spaces * blocks), _page_tensor(num_used, "num_used", dev, spaces), ws,
+         nbytes, _page_tensor(dev_error, "dev_error", dev))
+    return out, page_map, page_refs, num_used

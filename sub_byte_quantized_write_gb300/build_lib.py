@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libkvq_debug.so")
-SOURCES = ["kvq_api.cu", "kvq_write.cu", "kvq_decode.cu", "kvq_decode16.cu", "kvq_prefill_tc.cu"]
+SOURCES = ["kvq_api.cu", "kvq_write.cu", "kvq_decode.cu", "kvq_decode16.cu", "kvq_pages.cu",
+           "kvq_prefill_tc.cu"]
 HEADERS = ["kvq_common.cuh", "kvq_internal.h", "kvq_decode.cuh", "kvq_tc.cuh", "kvq_row.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <climits>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -584,6 +586,267 @@ kvq_status kvq_prefill_dense_attn(const void* k, const void* v, const int32_t* c
   cudaError_t e = kvq::launch_prefill(P, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   return KVQ_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// pages: copy, fork, compact
+
+namespace {
+
+// The caches of one call: the layers that share page numbers.
+kvq_status check_caches(const kvq_cache* c, int32_t n) {
+  if (!c) return fail(KVQ_ERR_INVALID_ARG, "caches is NULL");
+  if (n <= 0) return fail(KVQ_ERR_INVALID_ARG, "num_caches must be > 0");
+  if (n > kvq::PAGE_MAX_LAYERS) return fail(KVQ_ERR_UNSUPPORTED, "more than 128 caches in one call");
+  for (int i = 0; i < n; ++i) {
+    if (const kvq_status st = check_cache(c + i); st != KVQ_OK) return st;
+    if (c[i].num_blocks != c->num_blocks || c[i].num_kv_heads != c->num_kv_heads || c[i].block_size != c->block_size)
+      return fail(KVQ_ERR_INVALID_ARG, "the caches of one call must have the same num_blocks, num_kv_heads and block_size");
+    if ((long long)c->num_kv_heads * c->block_size * kvq_row_bytes(c[i].mode, c[i].head_dim) > INT_MAX)
+      return fail(KVQ_ERR_UNSUPPORTED, "block of 2 GB or more");
+  }
+  return KVQ_OK;
+}
+
+kvq::PageCopy page_copy(const kvq_cache* c, int32_t n, bool headwise, int32_t* dev_error) {
+  kvq::PageCopy p;
+  std::memset(&p, 0, sizeof(p));
+  for (int i = 0; i < n; ++i) {
+    p.k[i] = c[i].k_pages;
+    p.v[i] = c[i].v_pages;
+    p.unit_bytes[i] = (headwise ? 1 : c->num_kv_heads) * c->block_size * kvq_row_bytes(c[i].mode, c[i].head_dim);
+  }
+  p.num_layers = n;
+  p.units = c->num_blocks * (headwise ? c->num_kv_heads : 1);
+  p.dev_error = dev_error;
+  return p;
+}
+
+bool too_many_pages(const kvq_cache* c) { return (long long)c->num_blocks * c->num_kv_heads > INT_MAX; }
+
+// Carves a caller's workspace; with a NULL base it only counts.
+struct Carver {
+  uint8_t* base;
+  size_t used = 0;
+  int32_t* ints(long long n) {
+    int32_t* p = base ? reinterpret_cast<int32_t*>(base + used) : nullptr;
+    used = kvq::align256(used + (size_t)n * 4);
+    return p;
+  }
+};
+
+long long unit_tasks(const kvq::PagePlan& P) {
+  return (long long)P.spaces * ((P.num_blocks + kvq::PAGE_TASK_UNITS - 1) / kvq::PAGE_TASK_UNITS);
+}
+
+size_t fork_layout(kvq::PagePlan& P, void* base) {
+  Carver w{static_cast<uint8_t*>(base)};
+  const long long units = (long long)P.spaces * P.num_blocks, rows = (long long)P.new_batch * P.spaces;
+  P.owner = w.ints(units);
+  P.list = w.ints(units);
+  P.task_count = w.ints(unit_tasks(P));
+  P.row_ask = w.ints(rows);
+  P.row_at = w.ints(rows);
+  P.most_pairs = rows;
+  P.pair_src = w.ints(rows);
+  P.pair_dst = w.ints(rows);
+  return w.used;
+}
+
+size_t compact_layout(kvq::PagePlan& P, void* base) {
+  Carver w{static_cast<uint8_t*>(base)};
+  const long long units = (long long)P.spaces * P.num_blocks;
+  P.owner = w.ints(units);
+  P.list = w.ints(units);
+  P.task_count = w.ints(2 * unit_tasks(P));
+  P.movers = w.ints(P.spaces);
+  P.num_pairs = w.ints(1);
+  // at most half of a space's pages move, and no more than its rows name
+  P.most_pairs = std::min<long long>(P.num_blocks / 2, (long long)P.batch * P.max_blocks) * P.spaces;
+  P.pair_src = w.ints(P.most_pairs);
+  P.pair_dst = w.ints(P.most_pairs);
+  return w.used;
+}
+
+kvq::PagePlan page_plan(const kvq_cache* c, const kvq_paging* p, int32_t* dev_error) {
+  kvq::PagePlan P;
+  std::memset(&P, 0, sizeof(P));
+  P.headwise = p->block_tables_headwise != nullptr;
+  P.table = P.headwise ? p->block_tables_headwise : p->block_tables;
+  P.seq_lens = p->seq_lens;
+  P.max_blocks = p->max_blocks;
+  P.batch = p->batch;
+  P.spaces = P.headwise ? c->num_kv_heads : 1;
+  P.num_blocks = c->num_blocks;
+  P.num_kv_heads = c->num_kv_heads;
+  P.block_size = c->block_size;
+  P.dev_error = dev_error;
+  return P;
+}
+
+kvq_status check_scratch(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need) return fail(KVQ_ERR_WORKSPACE, "workspace missing or too small");
+  if (!aligned(ws, 256)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return KVQ_OK;
+}
+
+// Whether n ints at a and m ints at b share memory (NULL shares with nothing).
+bool overlap(const int32_t* a, long long n, const int32_t* b, long long m) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
+}
+
+// The new rows' plan: everything of the old rows and the new that the host can check.
+kvq_status fork_plan(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging, const kvq_paging* new_paging,
+                     int32_t* dev_error, kvq::PagePlan* out) {
+  kvq_status st = check_caches(caches, num_caches);
+  if (st != KVQ_OK) return st;
+  if ((st = check_paging(new_paging, caches->num_kv_heads)) != KVQ_OK) return st;
+  if (new_paging->batch == 0) return fail(KVQ_ERR_INVALID_ARG, "no new rows");
+  const bool old = paging && paging->batch > 0;
+  if (old) {
+    if ((st = check_paging(paging, caches->num_kv_heads)) != KVQ_OK) return st;
+    if ((paging->block_tables == nullptr) != (new_paging->block_tables == nullptr) ||
+        paging->max_blocks != new_paging->max_blocks)
+      return fail(KVQ_ERR_INVALID_ARG, "the old and the new tables must be of one kind and width");
+  }
+  if (too_many_pages(caches)) return fail(KVQ_ERR_UNSUPPORTED, "num_blocks * num_kv_heads too large");
+  kvq::PagePlan P = page_plan(caches, old ? paging : new_paging, dev_error);
+  if (!old) P.batch = 0;  // every row starts empty
+  P.new_batch = new_paging->batch;
+  if ((long long)P.new_batch * P.spaces > INT_MAX) return fail(KVQ_ERR_UNSUPPORTED, "new batch * num_kv_heads too large");
+  P.new_table = const_cast<int32_t*>(P.headwise ? new_paging->block_tables_headwise : new_paging->block_tables);
+  P.new_lens = const_cast<int32_t*>(new_paging->seq_lens);
+  *out = P;
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_copy_workspace_size(const kvq_cache* caches, int32_t num_caches, int32_t num_pairs, int32_t headwise,
+                                   size_t* bytes) {
+  const kvq_status st = check_caches(caches, num_caches);
+  if (st != KVQ_OK) return st;
+  if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is NULL");
+  if (num_pairs < 0) return fail(KVQ_ERR_INVALID_ARG, "num_pairs < 0");
+  if (too_many_pages(caches)) return fail(KVQ_ERR_UNSUPPORTED, "num_blocks * num_kv_heads too large");
+  Carver w{nullptr};
+  w.ints((long long)caches->num_blocks * (headwise ? caches->num_kv_heads : 1));
+  *bytes = w.used;
+  return KVQ_OK;
+}
+
+kvq_status kvq_copy_pages(const kvq_cache* caches, int32_t num_caches, const int32_t* src, const int32_t* dst,
+                          int32_t num_pairs, int32_t headwise, void* workspace, size_t workspace_bytes,
+                          int32_t* dev_error, void* stream) {
+  size_t need = 0;
+  kvq_status st = kvq_copy_workspace_size(caches, num_caches, num_pairs, headwise, &need);
+  if (st != KVQ_OK) return st;
+  if (num_pairs == 0) return KVQ_OK;
+  if (!src || !dst) return fail(KVQ_ERR_INVALID_ARG, "src / dst is NULL");
+  if ((st = check_scratch(workspace, workspace_bytes, need)) != KVQ_OK) return st;
+  kvq::PageCopy C = page_copy(caches, num_caches, headwise != 0, dev_error);
+  C.src = src;
+  C.dst = dst;
+  C.num_pairs = num_pairs;
+  C.claim = static_cast<int32_t*>(workspace);
+  const cudaError_t e = kvq::launch_copy_pages(C, sm_count(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+kvq_status kvq_fork_workspace_size(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging,
+                                   const kvq_paging* new_paging, size_t* bytes) {
+  if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is NULL");
+  kvq::PagePlan P;
+  const kvq_status st = fork_plan(caches, num_caches, paging, new_paging, nullptr, &P);
+  if (st != KVQ_OK) return st;
+  *bytes = fork_layout(P, nullptr);
+  return KVQ_OK;
+}
+
+kvq_status kvq_fork(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging, const int32_t* parents,
+                    const int32_t* keep_tokens, const int32_t* new_tokens, const int32_t* pins,
+                    const kvq_paging* new_paging, int32_t* page_refs, void* workspace, size_t workspace_bytes,
+                    int32_t* dev_error, void* stream) {
+  kvq::PagePlan P;
+  kvq_status st = fork_plan(caches, num_caches, paging, new_paging, dev_error, &P);
+  if (st != KVQ_OK) return st;
+  if (!parents || !page_refs) return fail(KVQ_ERR_INVALID_ARG, "parents / page_refs is NULL");
+  P.parents = parents;
+  P.keep_tokens = keep_tokens;
+  P.new_tokens = new_tokens;
+  P.pins = pins;
+  P.refs = page_refs;
+  // what is written shares no memory with what is read, nor with what else is written
+  const long long units = (long long)P.spaces * P.num_blocks, width = (long long)P.spaces * P.max_blocks;
+  const struct { const int32_t* p; long long n; } reads[] = {{P.batch ? P.table : nullptr, P.batch * width},
+      {P.batch ? P.seq_lens : nullptr, P.batch}, {parents, P.new_batch}, {keep_tokens, P.new_batch},
+      {new_tokens, P.new_batch}, {pins, units}},
+      writes[] = {{P.new_table, P.new_batch * width}, {P.new_lens, P.new_batch}, {page_refs, units}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& r : reads)
+      if (overlap(writes[i].p, writes[i].n, r.p, r.n))
+        return fail(KVQ_ERR_INVALID_ARG, "the new tables, lengths and page_refs may not overlap an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(writes[i].p, writes[i].n, writes[j].p, writes[j].n))
+        return fail(KVQ_ERR_INVALID_ARG, "the new tables, lengths and page_refs may not overlap one another");
+  }
+  const size_t need = fork_layout(P, nullptr);
+  if ((st = check_scratch(workspace, workspace_bytes, need)) != KVQ_OK) return st;
+  fork_layout(P, workspace);
+  const cudaError_t e = kvq::launch_fork(P, page_copy(caches, num_caches, P.headwise, dev_error), sm_count(),
+                                         static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+kvq_status kvq_compact_workspace_size(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging,
+                                      size_t* bytes) {
+  kvq_status st = check_caches(caches, num_caches);
+  if (st != KVQ_OK) return st;
+  if ((st = check_paging(paging, caches->num_kv_heads)) != KVQ_OK) return st;
+  if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is NULL");
+  if (too_many_pages(caches)) return fail(KVQ_ERR_UNSUPPORTED, "num_blocks * num_kv_heads too large");
+  kvq::PagePlan P = page_plan(caches, paging, nullptr);
+  *bytes = compact_layout(P, nullptr);
+  return KVQ_OK;
+}
+
+kvq_status kvq_compact(const kvq_cache* caches, int32_t num_caches, const kvq_paging* paging, const int32_t* pins,
+                       int32_t* new_tables, int32_t* page_map, int32_t* page_refs, int32_t* num_used, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  size_t need = 0;
+  kvq_status st = kvq_compact_workspace_size(caches, num_caches, paging, &need);
+  if (st != KVQ_OK) return st;
+  if (paging->batch == 0) return fail(KVQ_ERR_INVALID_ARG, "no rows");
+  if (!new_tables || !page_map || !page_refs || !num_used)
+    return fail(KVQ_ERR_INVALID_ARG, "new_tables / page_map / page_refs / num_used is NULL");
+  if ((st = check_scratch(workspace, workspace_bytes, need)) != KVQ_OK) return st;
+  kvq::PagePlan P = page_plan(caches, paging, dev_error);
+  P.pins = pins;
+  P.new_table = new_tables;
+  P.page_map = page_map;
+  P.refs = page_refs;
+  P.num_used = num_used;
+  const long long units = (long long)P.spaces * P.num_blocks, entries = (long long)P.batch * P.spaces * P.max_blocks;
+  const struct { const int32_t* p; long long n; } reads[] = {{P.table, entries}, {P.seq_lens, P.batch}, {pins, units}},
+      writes[] = {{new_tables, entries}, {page_map, units}, {page_refs, units}, {num_used, P.spaces}};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto& r : reads)
+      if (overlap(writes[i].p, writes[i].n, r.p, r.n) && !(i == 0 && r.p == P.table && new_tables == P.table))
+        return fail(KVQ_ERR_INVALID_ARG, "an output overlaps an input (new_tables may be the table itself)");
+    for (int j = 0; j < i; ++j)
+      if (overlap(writes[i].p, writes[i].n, writes[j].p, writes[j].n))
+        return fail(KVQ_ERR_INVALID_ARG, "two outputs overlap");
+  }
+  compact_layout(P, workspace);
+  const cudaError_t e = kvq::launch_compact(P, page_copy(caches, num_caches, P.headwise, dev_error), sm_count(),
+                                            static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }
 
 }  // extern "C"

@@ -14,7 +14,8 @@ namespace kvq {
 // no scale): the 16-bit pages and the dense prefill's rows.
 enum { MODE_INT4 = 0, MODE_INT2 = 1, MODE_INT8 = 2, MODE_I8T = 4, MODE_F8T = 5, MODE_DBF16 = 6 };
 enum { DT_F32 = 0, DT_BF16 = 1 };
-enum { DEVERR_BLOCK_RANGE = 1, DEVERR_TABLE_RANGE = 2, DEVERR_SEQ_LEN = 4, DEVERR_TIMEOUT = 8, DEVERR_BOUNDS = 16 };
+enum { DEVERR_BLOCK_RANGE = 1, DEVERR_TABLE_RANGE = 2, DEVERR_SEQ_LEN = 4, DEVERR_TIMEOUT = 8, DEVERR_BOUNDS = 16,
+       DEVERR_ROW_RANGE = 32, DEVERR_NO_PAGES = 64, DEVERR_PAGE_CONFLICT = 128 };
 
 __host__ __device__ constexpr int mode_bits(int mode) {
   return mode == MODE_INT4 ? 4 : (mode == MODE_INT2 ? 2 : (mode == MODE_DBF16 ? 16 : 8));

@@ -127,6 +127,57 @@ inline DecodeLayout decode_ws_layout(int batch, int num_kv_heads, int group, int
   return L;
 }
 
+// Page copies in every layer's pools (kvq_pages.cu).
+constexpr int PAGE_MAX_LAYERS = 128;
+struct PageCopy {
+  uint8_t* k[PAGE_MAX_LAYERS];
+  uint8_t* v[PAGE_MAX_LAYERS];
+  int unit_bytes[PAGE_MAX_LAYERS];  // one page: all heads of a block, or one head's
+  int num_layers, pieces;           // pieces: copy steps per page
+  int units;                        // pages of a pool
+  const int32_t* src;
+  const int32_t* dst;
+  int num_pairs;
+  const int32_t* num_pairs_dev;     // the pairs' number on the device instead, where not NULL
+  int32_t* claim;                   // [units] scratch of kvq_copy_pages
+  int32_t* dev_error;
+};
+
+// Fork and compact: tables, counters and scratch.  `spaces` sets of page
+// numbers (1, or one per kv head), row b of space s at table row b * spaces + s.
+struct PagePlan {
+  const int32_t* table;
+  const int32_t* seq_lens;
+  int max_blocks, batch, headwise, spaces, num_blocks, num_kv_heads, block_size;
+  const int32_t* parents;      // fork
+  const int32_t* keep_tokens;
+  const int32_t* new_tokens;
+  const int32_t* pins;
+  int new_batch;
+  int32_t* new_table;
+  int32_t* new_lens;
+  int32_t* refs;               // [spaces][num_blocks]
+  int32_t* page_map;           // compact: [spaces][num_blocks]
+  int32_t* num_used;           // compact: [spaces]
+  int32_t* dev_error;
+  // scratch
+  int32_t* owner;              // [spaces][num_blocks] lowest row ending in a page; compact: the movers
+  int32_t* list;               // [spaces][num_blocks] free pages; compact: the holes
+  int32_t* task_count;
+  int32_t* row_ask;            // fork: [new_batch * spaces] 2 * pages asked for + whether the last page is copied
+  int32_t* row_at;             // fork: [new_batch * spaces] first page of the row's share
+  int32_t* movers;             // compact: [spaces]
+  int32_t* pair_src;
+  int32_t* pair_dst;
+  int32_t* num_pairs;          // compact: one
+  long long most_pairs;        // entries of pair_src / pair_dst
+};
+constexpr int PAGE_TASK_UNITS = 4096;  // pages a CTA ranks at a time: the stride of task_count
+
+cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream);
+cudaError_t launch_fork(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream);
+cudaError_t launch_compact(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream);
+
 DecodeShape decode_shape(int mode, int head_dim, int group);
 // Key rows per page chunk that the decode's tensor copies move (16 or 8), or 0
 // when the configuration reads its pages another way (INT8 per channel, bf16).
