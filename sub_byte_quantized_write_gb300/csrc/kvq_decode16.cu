@@ -49,7 +49,8 @@ namespace {
 constexpr int D16_KEYS = 16;       // keys per chunk
 constexpr int D16_WARPS = 12;      // per CTA, one CTA per SM
 constexpr int D16_RUNS = 2048;     // entries of the prefix sums over the pairs
-constexpr int D16_MIN_CHUNKS = 4;  // per warp, at least
+constexpr int D16_MIN_CHUNKS = 1;  // per warp, at least
+constexpr int D16_WIDE_MERGE = 16;  // records per pair from which a CTA joins one head
 constexpr float D16_SLACK = 8.0f;  // log2 units a logit may pass the reference maximum by
 
 __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {  // read once: not kept in L1
@@ -60,7 +61,16 @@ __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {  // read once: no
   return v;
 }
 
-// D = A * B + D, m16n8k16, bf16 inputs, fp32 accumulate.
+// D = A * B, m16n8k16, bf16 inputs, fp32 sums.
+__device__ __forceinline__ void mma_bf16_fresh(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// D = A * B + D.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -151,7 +161,7 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
   }
   const int T = run_start[nruns];
   const int nw = stream_workers(T, gridDim.x * D16_WARPS, ws.fixed_workers, D16_MIN_CHUNKS);
-  const int gw = blockIdx.x * D16_WARPS + warp;
+  const int gw = warp * gridDim.x + blockIdx.x;  // few slices: spread over the SMs
   if (gw >= nw) return;  // whole warp; no CTA-wide barrier follows
   const int lo = slice_lo(gw, T, nw), hi = slice_lo(gw + 1, T, nw);
   if (lo >= hi) return;
@@ -364,8 +374,12 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
         for (int w = 0; w < 4; ++w) {
           const uint32_t a0 = prmt(v0[w], v1[w], 0x5410), a1 = prmt(v0[w], v1[w], 0x7632);
           const uint32_t a2 = prmt(v2[w], v3[w], 0x5410), a3 = prmt(v2[w], v3[w], 0x7632);
+          float o[4];  // of this chunk alone: see the header on the sums' rounding
+          mma_bf16_fresh(o, a0, a1, a2, a3, b0[0], b1_[0]);
+          mma_bf16(o, a0, a1, a2, a3, b0[1], b1_[1]);
+          mma_bf16(o, a0, a1, a2, a3, b0[2], b1_[2]);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) mma_bf16(acc[j][w], a0, a1, a2, a3, b0[k], b1_[k]);
+          for (int k = 0; k < 4; ++k) acc[j][w][k] += o[k];
         }
       }
     }
@@ -377,29 +391,99 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
   if (err && lane == 0) flag_error(P.dev_error, err);
 }
 
-// Joins the records of one (sequence, q head): one warp each.
-template <int D>
+// Joins the records of one (sequence, q head): W warps each take every W-th
+// group of four records (running maximum, sum and output of their own, joined
+// through shared memory); lane l holds dims l * D / 32 ...  W = 1 when a pair
+// is cut into few records (eight heads to a CTA), 8 when into many: one
+// warp's chain of loads over hundreds of records took 90 us of a call over one
+// long sequence.
+template <int D, int W>
 __global__ void __launch_bounds__(256) decode16_merge_kernel(const AttnParams P, const DecodeWs ws) {
   constexpr int EPL = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long wid = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  constexpr int RPS = 8;  // records per step
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
+  const long long wid = (long long)blockIdx.x * (8 / W) + warp / W;
   const int Hq = P.num_q_heads, G = P.group, Hkv = P.num_kv_heads;
-  if (wid >= (long long)P.batch * Hq) return;
-  const int b = (int)(wid / Hq), hq = (int)(wid % Hq);
+  if (wid >= (long long)P.batch * Hq) return;  // (whole CTAs, for W = 8)
+  const int b = (int)(wid / Hq), hq = (int)(wid % Hq), head = hq % G;
   const int bh = b * Hkv + hq / G, BH = P.batch * Hkv;
-  float* out = P.out + (size_t)wid * D;
   grid_dependency_wait();  // every record is written
-  const int T = ws.tile_start[BH];
-  const int start = ws.tile_start[bh], end = ws.tile_start[bh + 1];
-  if (start >= end || !KVQ_IN_BOUNDS(start >= 0 && end <= T, P.dev_error)) {  // no visible key
+  const int T = __ldcg(ws.tile_start + BH);
+  const int start = __ldcg(ws.tile_start + bh), end = __ldcg(ws.tile_start + bh + 1);
+  float m = -CUDART_INF_F, l = 0.0f, o[EPL];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) out[lane + 32 * e] = 0.0f;
-    return;
+  for (int e = 0; e < EPL; ++e) o[e] = 0.0f;
+  if (start < end && KVQ_IN_BOUNDS(start >= 0 && end <= T, P.dev_error)) {  // else no visible key: zeros
+    const int nw = stream_workers(T, ws.nwall, ws.fixed_workers, D16_MIN_CHUNKS);
+    const int w0 = worker_of(start, T, nw);
+    int n = worker_of(end - 1, T, nw) - w0 + 1;
+    if (!KVQ_IN_BOUNDS(w0 >= 0 && w0 + n - 1 + bh < ws.n_partials, P.dev_error)) n = 0;
+    const size_t rec0 = (size_t)(w0 + bh) * G + head;
+    for (int r0 = RPS * part; r0 < n; r0 += RPS * W) {
+      float2 ml[RPS];
+      float v[RPS][EPL];
+#pragma unroll
+      for (int u = 0; u < RPS; ++u) {  // the loads of a step in flight together
+        const size_t rec = rec0 + (size_t)min(r0 + u, n - 1) * G;
+        ml[u] = __ldcg(ws.part_ml + rec);
+        const float* po = ws.part_o + rec * D + EPL * lane;
+        if constexpr (EPL == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(po));
+          v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(po));
+          v[u][0] = x.x; v[u][1] = x.y;
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < RPS; ++u)
+        if (r0 + u < n && ml[u].y > 0.0f) mn = fmaxf(mn, ml[u].x);
+      if (mn == -CUDART_INF_F) continue;  // nothing visible in these
+      const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] *= f;
+#pragma unroll
+      for (int u = 0; u < RPS; ++u) {
+        if (r0 + u < n && ml[u].y > 0.0f) {
+          const float x = ex2(ml[u].x - m);
+          l = fmaf(x, ml[u].y, l);
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) o[e] = fmaf(x, v[u][e], o[e]);
+        }
+      }
+    }
   }
-  const int nw = stream_workers(T, ws.nwall, ws.fixed_workers, D16_MIN_CHUNKS);
-  const int w0 = worker_of(start, T, nw), w1 = worker_of(end - 1, T, nw);
-  const float no_signs[EPL] = {};
-  merge_records<D>(P, ws, bh, hq % G, w0, w1 - w0 + 1, no_signs, out, lane);
+  if constexpr (W > 1) {
+    __shared__ float sm_m[W], sm_l[W], sm_o[W][D];
+    if (lane == 0) {
+      sm_m[part] = m;
+      sm_l[part] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) sm_o[part][EPL * lane + e] = o[e];
+    __syncthreads();
+    if (part != 0) return;
+    float M = m;
+#pragma unroll
+    for (int w = 1; w < W; ++w) M = fmaxf(M, sm_m[w]);
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float x = sm_m[w] == -CUDART_INF_F ? 0.0f : ex2(sm_m[w] - M);
+      l = fmaf(x, sm_l[w], l);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = fmaf(x, sm_o[w][EPL * lane + e], o[e]);
+    }
+  }
+  float* out = P.out + (size_t)wid * D + EPL * lane;
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  if constexpr (EPL == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  else *reinterpret_cast<float2*>(out) = make_float2(o[0] * inv, o[1] * inv);
 }
 
 template <int D, bool Q32>
@@ -420,8 +504,11 @@ cudaError_t launch_decode16_t(const AttnParams& P, const DecodeWs& ws, int grid,
   }
   cudaError_t e = launch_dependent(decode16_kernel<D, Q32>, dim3(grid), dim3(D16_WARPS * 32), smem, stream, P, ws);
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)P.batch * P.num_q_heads;
-  return launch_dependent(decode16_merge_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P, ws);
+  const long long heads = (long long)P.batch * P.num_q_heads;
+  // a pair is cut into nwall / pairs records on average when the GPU is full
+  if (ws.nwall / (P.batch * P.num_kv_heads) >= D16_WIDE_MERGE)
+    return launch_dependent(decode16_merge_kernel<D, 8>, dim3((unsigned)heads), dim3(256), 0, stream, P, ws);
+  return launch_dependent(decode16_merge_kernel<D, 1>, dim3((unsigned)((heads + 7) / 8)), dim3(256), 0, stream, P, ws);
 }
 
 }  // namespace
