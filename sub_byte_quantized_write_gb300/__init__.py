@@ -16,7 +16,6 @@ that device's current stream; what it allocates belongs to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence, Tuple, Union
@@ -133,9 +132,15 @@ def _dev_ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
     return t.data_ptr()
 
 
+# The current stream of a device as a raw cudaStream_t; building a torch.cuda.Stream for it costs more than the
+# rest of a call's checks together.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -155,9 +160,14 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
 
 def _run(device: torch.device, stream, fn, *args) -> None:
     """fn(*args, stream) with `device` current."""
-    other = device.type == "cuda" and device.index is not None and device.index != torch.cuda.current_device()
-    with torch.cuda.device(device) if other else contextlib.nullcontext():
-        _check(fn(*args, _stream_ptr(stream)))
+    index = device.index
+    if index is None or index == torch.cuda.current_device():
+        status = fn(*args, _stream_ptr(stream))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream_ptr(stream))
+    if status != KVQ_OK:
+        raise KvqError(status)
 
 
 def _qdtype(t: torch.Tensor) -> int:
@@ -166,6 +176,20 @@ def _qdtype(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return KVQ_BF16
     raise ValueError("q/k/v must be float32 or bfloat16")
+
+
+def _set_and_forget(self, name, value):
+    self.__dict__[name] = value
+    self.__dict__["_struct"] = None
+
+
+def _kept_struct(handle, pointers):
+    """A handle's C struct, rebuilt (with its checks) unless its tensors' memory is where it was."""
+    kept = handle._struct
+    if kept is None or kept[0] != pointers:
+        kept = (pointers, handle._build())
+        handle.__dict__["_struct"] = kept
+    return kept[1]
 
 
 class PagedCache:
@@ -195,17 +219,12 @@ class PagedCache:
             self.ch_amax = None
             self.ch_amax_ready = None
 
-    def __setattr__(self, name, value):
-        object.__setattr__(self, name, value)
-        object.__setattr__(self, "_struct", None)
+    __setattr__ = _set_and_forget
 
     def struct(self) -> KvqCache:
-        """The C struct: built once, and again when an attribute was set or a pool's memory changed."""
-        s = self._struct
-        if s is None or s.k_pages != self.k_pages.data_ptr() or s.v_pages != self.v_pages.data_ptr():
-            s = self._build()
-            object.__setattr__(self, "_struct", s)
-        return s
+        """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
+        return _kept_struct(self, [t.data_ptr() for t in (self.k_pages, self.v_pages, self.rht_signs, self.ch_amax,
+                                                          self.ch_amax_ready) if t is not None])
 
     def _build(self) -> KvqCache:
         return KvqCache(_dev_ptr(self.k_pages, torch.uint8, "k_pages"), _dev_ptr(self.v_pages, torch.uint8, "v_pages"),
@@ -231,7 +250,14 @@ class Paging:
         t = block_tables if block_tables is not None else block_tables_headwise
         self.max_blocks = 0 if t is None else int(t.shape[1])
 
+    __setattr__ = _set_and_forget
+
     def struct(self) -> KvqPaging:
+        """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
+        return _kept_struct(self, [t.data_ptr() for t in (self.seq_lens, self.block_tables, self.block_tables_headwise,
+                                                          self.window_per_kv_head) if t is not None])
+
+    def _build(self) -> KvqPaging:
         return KvqPaging(_dev_ptr(self.block_tables, torch.int32, "block_tables"),
                          _dev_ptr(self.block_tables_headwise, torch.int32, "block_tables_headwise"),
                          self.max_blocks, int(self.seq_lens.shape[0]),
@@ -477,7 +503,7 @@ def _fork_out(caches: Caches, paging: Optional[Paging], rows: int, dev, stream) 
 def kvq_fork_workspace_size(caches: Caches, paging: Optional[Paging], rows: int, out: Optional[Paging] = None) -> int:
     """Bytes of scratch that kvq_fork needs for `rows` new rows."""
     cs, n, dev = _cache_array(caches)
-    like = (out or paging).struct()  # (the size goes by the new rows' number, the table's kind and its width)
+    like = (out or paging)._build()  # (the size goes by the new rows' number, the table's kind and its width)
     like.batch = int(rows)
     size = ctypes.c_size_t(0)
     _check(_lib.kvq_fork_workspace_size(cs, n, None, ctypes.byref(like), ctypes.byref(size)))
