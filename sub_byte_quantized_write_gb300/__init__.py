@@ -183,12 +183,17 @@ def _set_and_forget(self, name, value):
     self.__dict__["_struct"] = None
 
 
-def _kept_struct(handle, pointers):
-    """A handle's C struct, rebuilt (with its checks) unless its tensors' memory is where it was."""
+def _kept_struct(handle, tensors):
+    """A handle's C struct, rebuilt (with its checks) unless the tensors it was made of are where they were."""
     kept = handle._struct
-    if kept is None or kept[0] != pointers:
-        kept = (pointers, handle._build())
-        handle.__dict__["_struct"] = kept
+    if kept is not None:
+        for t, pointer in kept[0]:
+            if t.data_ptr() != pointer:
+                break
+        else:
+            return kept[1]
+    kept = ([(t, t.data_ptr()) for t in tensors(handle) if t is not None], handle._build())
+    handle.__dict__["_struct"] = kept
     return kept[1]
 
 
@@ -223,8 +228,7 @@ class PagedCache:
 
     def struct(self) -> KvqCache:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
-        return _kept_struct(self, [t.data_ptr() for t in (self.k_pages, self.v_pages, self.rht_signs, self.ch_amax,
-                                                          self.ch_amax_ready) if t is not None])
+        return _kept_struct(self, lambda c: (c.k_pages, c.v_pages, c.rht_signs, c.ch_amax, c.ch_amax_ready))
 
     def _build(self) -> KvqCache:
         return KvqCache(_dev_ptr(self.k_pages, torch.uint8, "k_pages"), _dev_ptr(self.v_pages, torch.uint8, "v_pages"),
@@ -254,8 +258,7 @@ class Paging:
 
     def struct(self) -> KvqPaging:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
-        return _kept_struct(self, [t.data_ptr() for t in (self.seq_lens, self.block_tables, self.block_tables_headwise,
-                                                          self.window_per_kv_head) if t is not None])
+        return _kept_struct(self, lambda p: (p.seq_lens, p.block_tables, p.block_tables_headwise, p.window_per_kv_head))
 
     def _build(self) -> KvqPaging:
         return KvqPaging(_dev_ptr(self.block_tables, torch.int32, "block_tables"),
@@ -425,26 +428,33 @@ Caches = Union[PagedCache, Sequence[PagedCache]]
 
 
 def _cache_array(caches: Caches):
-    """(ctypes array, number, device) of the caches that share page numbers."""
-    cs = [caches] if isinstance(caches, PagedCache) else list(caches)
+    """(ctypes array, number, device) of the caches that share page numbers; the array is kept with the first
+    cache as long as the caches' structs are the same."""
+    cs = (caches,) if isinstance(caches, PagedCache) else caches
     if not cs:
         raise ValueError("no caches")
-    dev = cs[0].k_pages.device
-    for c in cs:
-        if c.k_pages.device != dev:
+    structs = [c.struct() for c in cs]
+    kept = cs[0].__dict__.get("_group")
+    if kept is None or kept[0] != structs:
+        dev = cs[0].k_pages.device
+        if any(c.k_pages.device != dev for c in cs):
             raise ValueError("the caches of one call must be on one device")
-    return (KvqCache * len(cs))(*[c.struct() for c in cs]), len(cs), dev
+        kept = (structs, (KvqCache * len(cs))(*structs), len(cs), dev)
+        cs[0].__dict__["_group"] = kept
+    return kept[1:]
 
 
 def _page_tensor(t: Optional[torch.Tensor], name: str, dev: torch.device, numel: Optional[int] = None):
     """Device pointer of an int32 tensor of the caches' device, with `numel` elements where that is given."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError("%s must be on the caches' device" % name)
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.device != dev or t.device.type != "cuda":
+        if t.device != dev:
+            raise ValueError("%s must be on the caches' device" % name)
+        return _dev_ptr(t, torch.int32, name)  # says what is wrong
     if numel is not None and t.numel() != numel:
         raise ValueError("%s must have %d elements, got %d" % (name, numel, t.numel()))
-    return _dev_ptr(t, torch.int32, name)
+    return t.data_ptr()
 
 
 def _page_paging(p: "Paging", name: str, dev: torch.device, num_kv_heads: int) -> Tuple[KvqPaging, bool, int]:

@@ -398,13 +398,14 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
 // warp's chain of loads over hundreds of records took 90 us of a call over one
 // long sequence.
 template <int D, int W>
-__global__ void __launch_bounds__(256) decode16_merge_kernel(const AttnParams P, const DecodeWs ws) {
+__global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(const AttnParams P, const DecodeWs ws) {
   constexpr int EPL = D / 32;
   constexpr int RPS = 8;  // records per step
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
-  const long long wid = (long long)blockIdx.x * (8 / W) + warp / W;
+  constexpr int HEADS = W > 8 ? 1 : 8 / W;  // per CTA
+  const long long wid = (long long)blockIdx.x * HEADS + warp / W;
   const int Hq = P.num_q_heads, G = P.group, Hkv = P.num_kv_heads;
-  if (wid >= (long long)P.batch * Hq) return;  // (whole CTAs, for W = 8)
+  if (wid >= (long long)P.batch * Hq) return;  // (whole CTAs, for W > 1)
   const int b = (int)(wid / Hq), hq = (int)(wid % Hq), head = hq % G;
   const int bh = b * Hkv + hq / G, BH = P.batch * Hkv;
   grid_dependency_wait();  // every record is written
@@ -506,7 +507,10 @@ cudaError_t launch_decode16_t(const AttnParams& P, const DecodeWs& ws, int grid,
   if (e != cudaSuccess) return e;
   const long long heads = (long long)P.batch * P.num_q_heads;
   // a pair is cut into nwall / pairs records on average when the GPU is full
-  if (ws.nwall / (P.batch * P.num_kv_heads) >= D16_WIDE_MERGE)
+  const int cuts = ws.nwall / (P.batch * P.num_kv_heads);
+  if (cuts >= 8 * D16_WIDE_MERGE)
+    return launch_dependent(decode16_merge_kernel<D, 32>, dim3((unsigned)heads), dim3(1024), 0, stream, P, ws);
+  if (cuts >= D16_WIDE_MERGE)
     return launch_dependent(decode16_merge_kernel<D, 8>, dim3((unsigned)heads), dim3(256), 0, stream, P, ws);
   return launch_dependent(decode16_merge_kernel<D, 1>, dim3((unsigned)((heads + 7) / 8)), dim3(256), 0, stream, P, ws);
 }

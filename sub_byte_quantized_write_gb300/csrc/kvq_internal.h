@@ -133,7 +133,7 @@ struct PageCopy {
   uint8_t* k[PAGE_MAX_LAYERS];
   uint8_t* v[PAGE_MAX_LAYERS];
   int unit_bytes[PAGE_MAX_LAYERS];  // one page: all heads of a block, or one head's
-  int num_layers, pieces;           // pieces: copy steps per page
+  int num_layers, pieces, run;      // copy steps per page, and per CTA and turn
   int units;                        // pages of a pool
   const int32_t* src;
   const int32_t* dst;
