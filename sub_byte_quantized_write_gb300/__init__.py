@@ -448,7 +448,7 @@ def _page_tensor(t: Optional[torch.Tensor], name: str, dev: torch.device, numel:
     """Device pointer of an int32 tensor of the caches' device, with `numel` elements where that is given."""
     if t is None:
         return None
-    if t.dtype is not torch.int32 or not t.is_contiguous() or t.device != dev or t.device.type != "cuda":
+    if t.get_device() != dev.index or t.dtype is not torch.int32 or not t.is_contiguous():
         if t.device != dev:
             raise ValueError("%s must be on the caches' device" % name)
         return _dev_ptr(t, torch.int32, name)  # says what is wrong
@@ -461,12 +461,13 @@ def _page_paging(p: "Paging", name: str, dev: torch.device, num_kv_heads: int) -
     """(struct, head-wise, rows) of a paging state of the caches' device."""
     headwise = p.block_tables_headwise is not None
     t = p.block_tables_headwise if headwise else p.block_tables
-    rows = int(p.seq_lens.shape[0])
     if t is None or t.device != dev or p.seq_lens.device != dev:
         raise ValueError("%s needs a block table and lengths on the caches' device" % name)
-    if int(t.shape[0]) != rows * (num_kv_heads if headwise else 1):
+    struct = p.struct()
+    rows = struct.batch
+    if t.shape[0] != (rows * num_kv_heads if headwise else rows):
         raise ValueError("%s: the table's rows do not match seq_lens" % name)
-    return p.struct(), headwise, rows
+    return struct, headwise, rows
 
 
 def _page_scratch(workspace, size, dev, stream, *args):

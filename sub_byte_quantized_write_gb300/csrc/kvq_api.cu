@@ -624,7 +624,13 @@ kvq::PageCopy page_copy(const kvq_cache* c, int32_t n, bool headwise, int32_t* d
   return p;
 }
 
-bool too_many_pages(const kvq_cache* c) { return (long long)c->num_blocks * c->num_kv_heads > INT_MAX; }
+// Row segments are counted in 32 bits.
+bool too_many_rows(const kvq::PagePlan& P) {
+  const long long rows = (long long)std::max(P.batch, P.new_batch) * P.spaces;
+  return rows * (((long long)P.max_blocks + kvq::PAGE_SEG - 1) / kvq::PAGE_SEG) > INT_MAX / 2;
+}
+
+bool too_many_pages(const kvq_cache* c) { return (long long)c->num_blocks * c->num_kv_heads > INT_MAX / 2; }
 
 // Carves a caller's workspace; with a NULL base it only counts.
 struct Carver {
@@ -647,6 +653,7 @@ size_t fork_layout(kvq::PagePlan& P, void* base) {
   P.owner = w.ints(units);
   P.list = w.ints(units);
   P.task_count = w.ints(unit_tasks(P));
+  P.row_info = reinterpret_cast<int4*>(w.ints(4 * rows));
   P.row_ask = w.ints(rows);
   P.row_at = w.ints(rows);
   P.most_pairs = rows;
@@ -661,7 +668,8 @@ size_t compact_layout(kvq::PagePlan& P, void* base) {
   P.owner = w.ints(units);
   P.list = w.ints(units);
   P.task_count = w.ints(2 * unit_tasks(P));
-  P.movers = w.ints(P.spaces);
+  P.loose = w.ints(P.spaces);
+  P.below = w.ints(P.spaces);
   P.num_pairs = w.ints(1);
   // at most half of a space's pages move, and no more than its rows name
   P.most_pairs = std::min<long long>(P.num_blocks / 2, (long long)P.batch * P.max_blocks) * P.spaces;
@@ -717,7 +725,7 @@ kvq_status fork_plan(const kvq_cache* caches, int32_t num_caches, const kvq_pagi
   kvq::PagePlan P = page_plan(caches, old ? paging : new_paging, dev_error);
   if (!old) P.batch = 0;  // every row starts empty
   P.new_batch = new_paging->batch;
-  if ((long long)P.new_batch * P.spaces > INT_MAX) return fail(KVQ_ERR_UNSUPPORTED, "new batch * num_kv_heads too large");
+  if (too_many_rows(P)) return fail(KVQ_ERR_UNSUPPORTED, "table too large");
   P.new_table = const_cast<int32_t*>(P.headwise ? new_paging->block_tables_headwise : new_paging->block_tables);
   P.new_lens = const_cast<int32_t*>(new_paging->seq_lens);
   *out = P;
@@ -812,6 +820,7 @@ kvq_status kvq_compact_workspace_size(const kvq_cache* caches, int32_t num_cache
   if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is NULL");
   if (too_many_pages(caches)) return fail(KVQ_ERR_UNSUPPORTED, "num_blocks * num_kv_heads too large");
   kvq::PagePlan P = page_plan(caches, paging, nullptr);
+  if (too_many_rows(P)) return fail(KVQ_ERR_UNSUPPORTED, "table too large");
   *bytes = compact_layout(P, nullptr);
   return KVQ_OK;
 }

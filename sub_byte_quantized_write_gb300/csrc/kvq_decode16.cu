@@ -51,6 +51,7 @@ constexpr int D16_WARPS = 12;      // per CTA, one CTA per SM
 constexpr int D16_RUNS = 2048;     // entries of the prefix sums over the pairs
 constexpr int D16_MIN_CHUNKS = 1;  // per warp, at least
 constexpr int D16_WIDE_MERGE = 16;  // records per pair from which a CTA joins one head
+constexpr int D16_DIRECT_CHUNKS = 4;  // per warp, at most, for one CTA per pair to be enough
 constexpr float D16_SLACK = 8.0f;  // log2 units a logit may pass the reference maximum by
 
 __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {  // read once: not kept in L1
@@ -113,58 +114,71 @@ struct Chunk {
   uint32_t mask;  // bit k: key k is visible
 };
 
-template <int D, bool Q32>
+// DIRECT: one CTA per pair instead, its warps' shares joined in shared memory
+// and written out: no records, no prefix sums and no second launch, for calls
+// of few and short sequences.
+template <int D, bool Q32, bool DIRECT>
 __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnParams P, const DecodeWs ws) {
   constexpr int NT = D16_WARPS * 32;
   constexpr int JK = D / 32;  // 16-byte pieces of a key row per lane
   constexpr int JV = D / 64;  // 16-byte pieces of a value row per lane
   constexpr int ROW = 2 * D;  // bytes
-  extern __shared__ __align__(16) uint8_t qsm[];  // Q32: the q terms, [warp][3][JK][32 lanes][16 bytes]
-  __shared__ int run_start[D16_RUNS + 1];
+  // Q32: the q terms, [warp][3][JK][32 lanes][16 bytes]; DIRECT: then the
+  // warps' outputs [warp][G][D], maxima and sums [warp][8]
+  extern __shared__ __align__(16) uint8_t qsm[];
+  __shared__ int run_start[DIRECT ? 1 : D16_RUNS + 1];
   __shared__ int wtot[D16_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = P.group, Hkv = P.num_kv_heads, bs = P.block_size, BH = P.batch * Hkv;
   const int bs_log2 = __ffs(bs) - 1;
-  allow_dependent_launch();  // the merge kernel may launch; it waits for this grid to finish
+  int lo, hi, gw = 0, items = 1, nruns = 1;
+  if constexpr (DIRECT) {
+    const TileList t = tile_list(P, blockIdx.x / Hkv, blockIdx.x % Hkv, threadIdx.x == 0 && blockIdx.x % Hkv == 0, D16_KEYS);
+    lo = slice_lo(warp, t.n_virt, D16_WARPS);
+    hi = slice_lo(warp + 1, t.n_virt, D16_WARPS);
+  } else {
+    allow_dependent_launch();  // the merge kernel may launch; it waits for this grid to finish
 
-  // Prefix sums of the pairs' chunk counts, over runs of `items` pairs; CTA 0
-  // also publishes every pair's first chunk for the merge and reports bad lengths.
-  const int items = (BH + D16_RUNS - 1) / D16_RUNS;
-  const int nruns = (BH + items - 1) / items;
-  const int rpt = (nruns + NT - 1) / NT;  // runs per thread
-  {
-    const int first = min(BH, (int)threadIdx.x * rpt * items), last = min(BH, first + rpt * items);
-    int sum = 0;
-    for (int bh = first; bh < last; ++bh) sum += tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS).n_virt;
-    int incl = sum;
+    // Prefix sums of the pairs' chunk counts, over runs of `items` pairs; CTA 0
+    // also publishes every pair's first chunk for the merge and reports bad lengths.
+    items = (BH + D16_RUNS - 1) / D16_RUNS;
+    nruns = (BH + items - 1) / items;
+    const int rpt = (nruns + NT - 1) / NT;  // runs per thread
+    {
+      const int first = min(BH, (int)threadIdx.x * rpt * items), last = min(BH, first + rpt * items);
+      int sum = 0;
+      for (int bh = first; bh < last; ++bh) sum += tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS).n_virt;
+      int incl = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) wtot[warp] = incl;
+      __syncthreads();
+      int x = incl - sum;
+      for (int w = 0; w < warp; ++w) x += wtot[w];
+      for (int bh = first; bh < last; ++bh) {
+        if (bh % items == 0) run_start[bh / items] = x;
+        const int n = tile_list(P, bh / Hkv, bh % Hkv, blockIdx.x == 0 && bh % Hkv == 0, D16_KEYS).n_virt;
+        if (blockIdx.x == 0) ws.tile_start[bh] = x;
+        x += n;
+      }
+      if (threadIdx.x == NT - 1) {
+        run_start[nruns] = x;
+        if (blockIdx.x == 0) ws.tile_start[BH] = x;
+      }
+      __syncthreads();
     }
-    if (lane == 31) wtot[warp] = incl;
-    __syncthreads();
-    int x = incl - sum;
-    for (int w = 0; w < warp; ++w) x += wtot[w];
-    for (int bh = first; bh < last; ++bh) {
-      if (bh % items == 0) run_start[bh / items] = x;
-      const int n = tile_list(P, bh / Hkv, bh % Hkv, blockIdx.x == 0 && bh % Hkv == 0, D16_KEYS).n_virt;
-      if (blockIdx.x == 0) ws.tile_start[bh] = x;
-      x += n;
-    }
-    if (threadIdx.x == NT - 1) {
-      run_start[nruns] = x;
-      if (blockIdx.x == 0) ws.tile_start[BH] = x;
-    }
-    __syncthreads();
+    const int T = run_start[nruns];
+    const int nw = stream_workers(T, gridDim.x * D16_WARPS, ws.fixed_workers, D16_MIN_CHUNKS);
+    gw = warp * gridDim.x + blockIdx.x;  // few slices: spread over the SMs
+    if (gw >= nw) return;  // whole warp; no CTA-wide barrier follows
+    lo = slice_lo(gw, T, nw);
+    hi = slice_lo(gw + 1, T, nw);
+    if (lo >= hi) return;
   }
-  const int T = run_start[nruns];
-  const int nw = stream_workers(T, gridDim.x * D16_WARPS, ws.fixed_workers, D16_MIN_CHUNKS);
-  const int gw = warp * gridDim.x + blockIdx.x;  // few slices: spread over the SMs
-  if (gw >= nw) return;  // whole warp; no CTA-wide barrier follows
-  const int lo = slice_lo(gw, T, nw), hi = slice_lo(gw + 1, T, nw);
-  if (lo >= hi) return;
 
   int err = 0;
   auto look_up = [&](int x) -> Chunk {  // of global chunk x; lanes at or past hi get nothing
@@ -173,18 +187,24 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
     r.row = -1;
     r.mask = 0;
     if (x >= hi) return r;
-    int a = 0, z = nruns;
-    while (z - a > 1) {
-      const int mid = (a + z) >> 1;
-      if (run_start[mid] <= x) a = mid;
-      else z = mid;
+    int bh = blockIdx.x, start = 0;
+    if constexpr (!DIRECT) {
+      int a = 0, z = nruns;
+      while (z - a > 1) {
+        const int mid = (a + z) >> 1;
+        if (run_start[mid] <= x) a = mid;
+        else z = mid;
+      }
+      bh = a * items;
+      start = run_start[a];
     }
-    int bh = a * items, start = run_start[a];
     TileList t = tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
-    while (start + t.n_virt <= x) {  // (items > 1 only)
-      start += t.n_virt;
-      ++bh;
-      t = tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
+    if constexpr (!DIRECT) {
+      while (start + t.n_virt <= x) {  // (items > 1 only)
+        start += t.n_virt;
+        ++bh;
+        t = tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
+      }
     }
     r.bh = bh;
     const int key = D16_KEYS * tile_of(t, x - start);
@@ -255,17 +275,20 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
     m[0] = m[1] = -CUDART_INF_F;
     l[0] = l[1] = 0.0f;
   };
-  auto end_pair = [&](int bh) {  // the record of (worker gw, pair bh)
-    const int rec = gw + bh;
-    if (!KVQ_IN_BOUNDS(rec < ws.n_partials, P.dev_error)) return;
+  float* osm = reinterpret_cast<float*>(qsm + (Q32 ? (size_t)D16_WARPS * 3 * JK * 512 : 0));
+  float2* mlsm = reinterpret_cast<float2*>(osm + (size_t)D16_WARPS * G * D);
+  // The record of (worker gw, pair bh), or the warp's share in shared memory.
+  auto end_pair = [&](int bh) {
+    const int rec = DIRECT ? warp : gw + bh;
+    if (!DIRECT && !KVQ_IN_BOUNDS(rec < ws.n_partials, P.dev_error)) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
       const int head = 2 * c + i;
       if (head < G) {
-        if (g == 0) ws.part_ml[(size_t)rec * G + head] = make_float2(m[i], l[i]);
-        float* po = ws.part_o + ((size_t)rec * G + head) * D + 8 * g;
+        if (g == 0) (DIRECT ? mlsm : ws.part_ml)[(size_t)rec * G + head] = make_float2(m[i], l[i]);
+        float* po = (DIRECT ? osm : ws.part_o) + ((size_t)rec * G + head) * D + 8 * g;
 #pragma unroll
         for (int j = 0; j < JV; ++j) {
           *reinterpret_cast<float4*>(po + 64 * j) = make_float4(acc[j][0][i], acc[j][0][2 + i], acc[j][1][i], acc[j][1][2 + i]);
@@ -282,7 +305,7 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
   int row = __shfl_sync(0xffffffffu, cur.row, 0);
   load_k(row);
   load_v(row);
-  int bh = __shfl_sync(0xffffffffu, cur.bh, 0);
+  int bh = DIRECT ? (int)blockIdx.x : __shfl_sync(0xffffffffu, cur.bh, 0);
   begin_pair(bh);
 #pragma unroll 1
   for (int x = lo; x < hi; ++x) {
@@ -389,6 +412,31 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
   end_pair(bh);
   err = __reduce_or_sync(0xffffffffu, err);
   if (err && lane == 0) flag_error(P.dev_error, err);
+  if constexpr (DIRECT) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * D / 4; i += NT) {
+      const int head = i / (D / 4), d = 4 * (i % (D / 4));
+      float M = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < D16_WARPS; ++w) M = fmaxf(M, mlsm[w * G + head].x);
+      float sum = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < D16_WARPS; ++w) {
+        const float2 ml = mlsm[w * G + head];
+        const float f = ml.x == -CUDART_INF_F ? 0.0f : ex2(ml.x - M);
+        const float4 x = *reinterpret_cast<const float4*>(osm + (size_t)(w * G + head) * D + d);
+        sum = fmaf(f, ml.y, sum);
+        o.x = fmaf(f, x.x, o.x);
+        o.y = fmaf(f, x.y, o.y);
+        o.z = fmaf(f, x.z, o.z);
+        o.w = fmaf(f, x.w, o.w);
+      }
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // no visible key: zeros
+      *reinterpret_cast<float4*>(P.out + ((size_t)(blockIdx.x / Hkv) * P.num_q_heads + (blockIdx.x % Hkv) * G + head) * D + d) =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    }
+  }
 }
 
 // Joins the records of one (sequence, q head): W warps each take every W-th
@@ -487,10 +535,14 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
   else *reinterpret_cast<float2*>(out) = make_float2(o[0] * inv, o[1] * inv);
 }
 
-template <int D, bool Q32>
+size_t decode16_smem(int D, bool q32, bool direct, int group) {
+  return (q32 ? (size_t)D16_WARPS * 3 * (D / 32) * 512 : 0) + (direct ? (size_t)D16_WARPS * group * (D * 4 + 8) : 0);
+}
+
+template <int D, bool Q32, bool DIRECT>
 cudaError_t launch_decode16_t(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
-  const size_t smem = Q32 ? (size_t)D16_WARPS * 3 * (D / 32) * 512 : 0;
-  if (smem > 0) {
+  const int most = (int)decode16_smem(D, Q32, DIRECT, 8);
+  if (most > 0) {
     // the opt-in shared-memory size is set once per device (not inside later
     // calls, which may be captured into a CUDA graph)
     static bool attr_set[64] = {false};
@@ -498,16 +550,32 @@ cudaError_t launch_decode16_t(const AttnParams& P, const DecodeWs& ws, int grid,
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-      e = cudaFuncSetAttribute(decode16_kernel<D, Q32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = cudaFuncSetAttribute(decode16_kernel<D, Q32, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
   }
-  cudaError_t e = launch_dependent(decode16_kernel<D, Q32>, dim3(grid), dim3(D16_WARPS * 32), smem, stream, P, ws);
+  return launch_dependent(decode16_kernel<D, Q32, DIRECT>, dim3(grid), dim3(D16_WARPS * 32),
+                          decode16_smem(D, Q32, DIRECT, P.group), stream, P, ws);
+}
+
+template <int D>
+cudaError_t launch_decode16_d(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
+  const bool f32 = P.dtype == DT_F32;
+  const int pairs = P.batch * P.num_kv_heads;
+  // What the host knows of the lengths is the table's width.  One CTA per
+  // pair while each has an SM to itself and no warp more than a few chunks;
+  // beyond, equal slices of the whole list.
+  const long long chunks = (long long)P.max_blocks * (P.block_size / D16_KEYS);  // of a pair, at most
+  if (ws.fixed_workers == 0 && pairs <= grid && chunks <= D16_DIRECT_CHUNKS * D16_WARPS)
+    return f32 ? launch_decode16_t<D, true, true>(P, ws, pairs, stream)
+               : launch_decode16_t<D, false, true>(P, ws, pairs, stream);
+  cudaError_t e = f32 ? launch_decode16_t<D, true, false>(P, ws, grid, stream)
+                      : launch_decode16_t<D, false, false>(P, ws, grid, stream);
   if (e != cudaSuccess) return e;
   const long long heads = (long long)P.batch * P.num_q_heads;
   // a pair is cut into nwall / pairs records on average when the GPU is full
-  const int cuts = ws.nwall / (P.batch * P.num_kv_heads);
+  const long long cuts = chunks < ws.nwall / pairs ? chunks : ws.nwall / pairs;
   if (cuts >= 8 * D16_WIDE_MERGE)
     return launch_dependent(decode16_merge_kernel<D, 32>, dim3((unsigned)heads), dim3(1024), 0, stream, P, ws);
   if (cuts >= D16_WIDE_MERGE)
@@ -520,10 +588,7 @@ cudaError_t launch_decode16_t(const AttnParams& P, const DecodeWs& ws, int grid,
 DecodeShape decode16_shape() { return {1, D16_WARPS}; }
 
 cudaError_t launch_decode16(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
-  const bool f32 = P.dtype == DT_F32;
-  if (P.head_dim == 128)
-    return f32 ? launch_decode16_t<128, true>(P, ws, grid, stream) : launch_decode16_t<128, false>(P, ws, grid, stream);
-  return f32 ? launch_decode16_t<64, true>(P, ws, grid, stream) : launch_decode16_t<64, false>(P, ws, grid, stream);
+  return P.head_dim == 128 ? launch_decode16_d<128>(P, ws, grid, stream) : launch_decode16_d<64>(P, ws, grid, stream);
 }
 
 }  // namespace kvq

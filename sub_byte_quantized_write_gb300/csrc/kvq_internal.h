@@ -161,18 +161,21 @@ struct PagePlan {
   int32_t* num_used;           // compact: [spaces]
   int32_t* dev_error;
   // scratch
-  int32_t* owner;              // [spaces][num_blocks] lowest row ending in a page; compact: the movers
+  int32_t* owner;              // [spaces][num_blocks] lowest row ending in a page; compact: the pages that may move
   int32_t* list;               // [spaces][num_blocks] free pages; compact: the holes
   int32_t* task_count;
+  int4* row_info;              // fork: [new_batch * spaces] kept tokens, with the new ones, partly filled last page or -1
   int32_t* row_ask;            // fork: [new_batch * spaces] 2 * pages asked for + whether the last page is copied
   int32_t* row_at;             // fork: [new_batch * spaces] first page of the row's share
-  int32_t* movers;             // compact: [spaces]
+  int32_t* loose;              // compact: [spaces] used pages that may move, and those of them that stay
+  int32_t* below;
   int32_t* pair_src;
   int32_t* pair_dst;
   int32_t* num_pairs;          // compact: one
   long long most_pairs;        // entries of pair_src / pair_dst
 };
 constexpr int PAGE_TASK_UNITS = 4096;  // pages a CTA ranks at a time: the stride of task_count
+constexpr int PAGE_SEG = 256;          // entries of a table row a warp takes at a time
 
 cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream);
 cudaError_t launch_fork(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream);

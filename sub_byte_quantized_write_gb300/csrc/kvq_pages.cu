@@ -38,39 +38,51 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // Exclusive prefix sum over the CTA's PLAN_THREADS threads, and the total.
-// Every thread calls it; `sm` holds 33 ints.
-__device__ __forceinline__ int block_scan(int v, int* sm, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  __syncthreads();  // sm is free again
-  if (lane == 31) sm[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    const int t = sm[lane];
-    int s = t;
+// Every thread calls it.  `sm` holds two sets of 33 ints, used in turn, so
+// that a call needs no barrier before it writes.
+struct BlockScan {
+  int (*sm)[33];
+  int turn = 0;
+  __device__ __forceinline__ int operator()(int v, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int* a = sm[turn];
+    turn ^= 1;
+    int incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
-    sm[lane] = s - t;
-    if (lane == 31) sm[32] = s;
+    if (lane == 31) a[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+      const int t = a[lane];
+      int s = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+      }
+      a[lane] = s - t;
+      if (lane == 31) a[32] = s;
+    }
+    __syncthreads();
+    total = a[32];
+    return a[warp] + incl - v;
   }
-  __syncthreads();
-  total = sm[32];
-  return sm[warp] + incl - v;
+};
+
+// Sum of a[0 .. n - 1], by every warp for itself.
+__device__ __forceinline__ int warp_total(const int* a, int n) {
+  int v = 0;
+  for (int i = threadIdx.x & 31; i < n; i += 32) v += __ldcg(a + i);
+  return __reduce_add_sync(0xffffffffu, v);
 }
 
-__device__ __forceinline__ int block_sum(const int* a, int n, int* sm) {  // of a[0 .. n - 1]
-  int v = 0, total;
-  for (int i = threadIdx.x; i < n; i += PLAN_THREADS) v += __ldcg(a + i);
-  block_scan(v, sm, total);
-  return total;
+// Four consecutive counters from `first` on; those at or past n read as `past`.
+__device__ __forceinline__ void load4(const int32_t* a, int first, int n, int past, int (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = first + i < n ? __ldcg(a + first + i) : past;
 }
 
 // Page `id` of space `s` as a number of the pools: blocks for a uniform
@@ -130,33 +142,36 @@ __device__ void fork_init(const PagePlan& P) {
 }
 
 // Phase 1: the kept entries of every new row; their uses counted.  A partly
-// filled last page is not counted but claimed, by the lowest row that ends in it.
+// filled last page is not counted but claimed, by the lowest row that ends in
+// it.  row_info: what the later phases need of a row.
 __device__ void fork_mark(const PagePlan& P) {
-  constexpr int SEG = 128;  // entries of a row per warp and step
+  constexpr int SEG = PAGE_SEG;  // entries of a row per warp and step
   const int lane = threadIdx.x & 31;
   const int segs = (P.max_blocks + SEG - 1) / SEG;
-  const long long tasks = (long long)P.new_batch * P.spaces * segs;
+  const int tasks = P.new_batch * P.spaces * segs, step = gridDim.x * (PLAN_THREADS / 32);
   int err = 0;
-  for (long long t = (long long)blockIdx.x * (PLAN_THREADS / 32) + (threadIdx.x >> 5); t < tasks;
-       t += (long long)gridDim.x * (PLAN_THREADS / 32)) {
-    const long long r = t / segs;
-    const int b = (int)(r / P.spaces), s = (int)(r % P.spaces), e0 = (int)(t % segs) * SEG;
+  for (int t = blockIdx.x * (PLAN_THREADS / 32) + (threadIdx.x >> 5); t < tasks; t += step) {
+    const int r = t / segs, e0 = (t - r * segs) * SEG;
+    const int b = r / P.spaces, s = r - b * P.spaces;
     const ForkRow row = fork_row(P, b, err);
     if (s == 0 && e0 == 0 && lane == 0) P.new_lens[b] = row.total;
-    const int have = pages_of(P, row.kept), tail = row.kept % P.block_size ? row.kept / P.block_size : -1;
+    const int have = pages_of(P, row.kept), tail = row.kept % P.block_size ? have - 1 : -1;
     const int32_t* from = P.table + ((long long)row.parent * P.spaces + s) * P.max_blocks;
+    int32_t* to = P.new_table + (long long)r * P.max_blocks;
     int v[SEG / 32];
 #pragma unroll
     for (int k = 0; k < SEG / 32; ++k) {
       const int e = e0 + lane + 32 * k;
       v[k] = e < have ? __ldg(from + e) : -1;
     }
+    if (e0 == 0 && lane == 0 && tail < 0) P.row_info[r] = make_int4(row.kept, row.total, -1, 0);
 #pragma unroll
     for (int k = 0; k < SEG / 32; ++k) {
       const int e = e0 + lane + 32 * k;
       if (v[k] >= P.num_blocks) err |= DEVERR_BLOCK_RANGE;
       if (v[k] < 0 || v[k] >= P.num_blocks) v[k] = -1;
-      if (e < P.max_blocks) P.new_table[r * P.max_blocks + e] = v[k];
+      if (e < P.max_blocks) to[e] = v[k];
+      if (e == tail) P.row_info[r] = make_int4(row.kept, row.total, v[k], 0);
       if (v[k] >= 0) {
         const long long u = (long long)s * P.num_blocks + v[k];
         if (e == tail) atomicMin(P.owner + u, b);
@@ -168,70 +183,65 @@ __device__ void fork_mark(const PagePlan& P) {
   if (err && lane == 0) flag_error(P.dev_error, err);
 }
 
-__device__ __forceinline__ bool fork_is_free(const PagePlan& P, long long u) {
-  return __ldcg(P.refs + u) == 0 && __ldcg(P.owner + u) == INT_MAX;
+// Bit i: page first + i of space s is free.
+__device__ __forceinline__ int fork_free4(const PagePlan& P, int s, int first) {
+  int refs[4], owner[4], f = 0;
+  load4(P.refs + (long long)s * P.num_blocks, first, P.num_blocks, 1, refs);
+  load4(P.owner + (long long)s * P.num_blocks, first, P.num_blocks, 0, owner);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f |= (refs[i] == 0 && owner[i] == INT_MAX) << i;
+  return f;
 }
 
 // Phase 2: free pages per task, and the pages each row asks for: a private
 // copy of its last page unless it is the lowest row that ends in it and
 // nobody else uses it, and pages for its new tokens.
-__device__ void fork_count(const PagePlan& P, int* sm) {
+__device__ void fork_count(const PagePlan& P, BlockScan& scan) {
+  const int rows = P.new_batch * P.spaces;
+  for (int r = blockIdx.x * PLAN_THREADS + threadIdx.x; r < rows; r += gridDim.x * PLAN_THREADS) {
+    const int b = r / P.spaces, s = r - b * P.spaces;
+    const int4 row = __ldcg(P.row_info + r);  // kept, total, last page
+    int split = 0;
+    if (row.z >= 0) {
+      const long long u = (long long)s * P.num_blocks + row.z;
+      const int refs = __ldcg(P.refs + u), owner = __ldcg(P.owner + u);
+      split = refs > 0 || owner != b;
+    }
+    P.row_ask[r] = 2 * (pages_of(P, row.y) - pages_of(P, row.x) + split) + split;
+  }
   const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
   for (int t = blockIdx.x; t < P.spaces * per_space; t += gridDim.x) {
-    const int s = t / per_space, first = (t % per_space) * UNITS_PER_TASK + 4 * threadIdx.x;
-    int n = 0, total;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (first + i < P.num_blocks && fork_is_free(P, (long long)s * P.num_blocks + first + i)) ++n;
-    block_scan(n, sm, total);
+    const int s = t / per_space, first = (t - s * per_space) * UNITS_PER_TASK + 4 * threadIdx.x;
+    int total;
+    scan(__popc(fork_free4(P, s, first)), total);
     if (threadIdx.x == 0) P.task_count[t] = total;
-  }
-  int err = 0;
-  const long long rows = (long long)P.new_batch * P.spaces;
-  for (long long r = (long long)blockIdx.x * PLAN_THREADS + threadIdx.x; r < rows; r += (long long)gridDim.x * PLAN_THREADS) {
-    const int b = (int)(r / P.spaces), s = (int)(r % P.spaces);
-    const ForkRow row = fork_row(P, b, err);
-    int split = 0;
-    if (row.kept % P.block_size) {
-      const int v = __ldcg(P.new_table + r * P.max_blocks + row.kept / P.block_size);
-      if (v >= 0) {
-        const long long u = (long long)s * P.num_blocks + v;
-        split = __ldcg(P.refs + u) > 0 || __ldcg(P.owner + u) != b;
-      }
-    }
-    P.row_ask[r] = 2 * (pages_of(P, row.total) - pages_of(P, row.kept) + split) + split;
   }
 }
 
 // Phase 3: the free pages of each space in ascending order, and where each
 // row's share of them begins (rows in order).
-__device__ void fork_rank(const PagePlan& P, int* sm) {
+__device__ void fork_rank(const PagePlan& P, BlockScan& scan) {
   const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
   for (int t = blockIdx.x; t < P.spaces * (per_space + 1); t += gridDim.x) {
     if (t < P.spaces * per_space) {
-      const int s = t / per_space, k = t % per_space, first = k * UNITS_PER_TASK + 4 * threadIdx.x;
-      const int before = block_sum(P.task_count + s * per_space, k, sm);
-      bool free[4];
-      int n = 0, total;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        free[i] = first + i < P.num_blocks && fork_is_free(P, (long long)s * P.num_blocks + first + i);
-        n += free[i];
-      }
-      int at = before + block_scan(n, sm, total);
+      const int s = t / per_space, k = t - s * per_space, first = k * UNITS_PER_TASK + 4 * threadIdx.x;
+      const int f = fork_free4(P, s, first);
+      const int before = warp_total(P.task_count + s * per_space, k);
+      int total;
+      int at = before + scan(__popc(f), total);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (free[i] && KVQ_IN_BOUNDS(at < P.num_blocks, P.dev_error)) P.list[(long long)s * P.num_blocks + at++] = first + i;
+        if (((f >> i) & 1) && KVQ_IN_BOUNDS(at < P.num_blocks, P.dev_error))
+          P.list[(long long)s * P.num_blocks + at++] = first + i;
     } else {
       const int s = t - P.spaces * per_space;
       int before = 0;
       for (int b0 = 0; b0 < P.new_batch; b0 += PLAN_THREADS) {
         const int b = b0 + threadIdx.x;
-        const long long r = (long long)b * P.spaces + s;
-        const int n = b < P.new_batch ? __ldcg(P.row_ask + r) >> 1 : 0;
+        const int n = b < P.new_batch ? __ldcg(P.row_ask + (long long)b * P.spaces + s) >> 1 : 0;
         int total;
-        const int at = before + block_scan(n, sm, total);
-        if (b < P.new_batch) P.row_at[r] = at;
+        const int at = before + scan(n, total);
+        if (b < P.new_batch) P.row_at[(long long)b * P.spaces + s] = at;
         before += total;
       }
     }
@@ -239,49 +249,35 @@ __device__ void fork_rank(const PagePlan& P, int* sm) {
 }
 
 // Phase 4: the pages handed out, a warp per row; the pairs to copy.
-__device__ void fork_assign(const PagePlan& P, int* sm) {
+__device__ void fork_assign(const PagePlan& P) {
   const int lane = threadIdx.x & 31;
   const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
-  const long long rows = (long long)P.new_batch * P.spaces;
+  const int rows = P.new_batch * P.spaces;
   int err = 0;
-  // the number of free pages of each space, in turn (a warp's rows may be of any space)
-  for (int s = 0; s < P.spaces; ++s) {
-    const int n_free = block_sum(P.task_count + s * per_space, per_space, sm);
-    for (long long w = (long long)blockIdx.x * (PLAN_THREADS / 32) + (threadIdx.x >> 5); w * P.spaces + s < rows;
-         w += (long long)gridDim.x * (PLAN_THREADS / 32)) {
-      const int b = (int)w;
-      const long long r = w * P.spaces + s;
-      const ForkRow row = fork_row(P, b, err);
-      const int ask = __ldcg(P.row_ask + r), split = ask & 1, n = ask >> 1, at = __ldcg(P.row_at + r);
-      int32_t* to = P.new_table + r * P.max_blocks;
-      const int have = pages_of(P, row.kept);
-      const int32_t* list = P.list + (long long)s * P.num_blocks;
-      if (lane == 0) {
-        int src = -1, dst = -1;
-        if (row.kept % P.block_size) {
-          const int v = __ldcg(to + have - 1);
-          if (split) {
-            const int id = at < n_free ? __ldcg(list + at) : -1;
-            if (id < 0) err |= DEVERR_NO_PAGES;
-            to[have - 1] = id;
-            if (id >= 0) {
-              P.refs[(long long)s * P.num_blocks + id] = 1;
-              src = pool_unit(P, s, v);
-              dst = pool_unit(P, s, id);
-            }
-          } else if (v >= 0) {
-            P.refs[(long long)s * P.num_blocks + v] = 1;  // its only use (nothing pins it either, or it were split)
-          }
-        }
-        P.pair_src[r] = src;
-        P.pair_dst[r] = dst;
+  for (int r = blockIdx.x * (PLAN_THREADS / 32) + (threadIdx.x >> 5); r < rows; r += gridDim.x * (PLAN_THREADS / 32)) {
+    const int s = r % P.spaces;
+    const int4 row = __ldcg(P.row_info + r);
+    const int ask = __ldcg(P.row_ask + r), split = ask & 1, n = ask >> 1, at = __ldcg(P.row_at + r);
+    const int n_free = warp_total(P.task_count + s * per_space, per_space);
+    int32_t* to = P.new_table + (long long)r * P.max_blocks;
+    int32_t* refs = P.refs + (long long)s * P.num_blocks;
+    const int32_t* list = P.list + (long long)s * P.num_blocks;
+    const int have = pages_of(P, row.x);
+    int src = -1, dst = -1;
+    for (int j = lane; j < n; j += 32) {
+      const int id = at + j < n_free ? __ldcg(list + at + j) : -1;
+      if (id < 0) err |= DEVERR_NO_PAGES;
+      else refs[id] = 1;
+      to[have + j - split] = id;  // the copy of the last page first, then the new ones
+      if (split && j == 0 && id >= 0) {
+        src = pool_unit(P, s, row.z);
+        dst = pool_unit(P, s, id);
       }
-      for (int j = split + lane; j < n; j += 32) {
-        const int id = at + j < n_free ? __ldcg(list + at + j) : -1;
-        if (id < 0) err |= DEVERR_NO_PAGES;
-        else P.refs[(long long)s * P.num_blocks + id] = 1;
-        to[have + j - split] = id;
-      }
+    }
+    if (lane == 0) {
+      if (!split && row.z >= 0) refs[row.z] = 1;  // its only use (nothing pins it either, or it were split)
+      P.pair_src[r] = src;
+      P.pair_dst[r] = dst;
     }
   }
   err = __reduce_or_sync(0xffffffffu, err);
@@ -291,14 +287,15 @@ __device__ void fork_assign(const PagePlan& P, int* sm) {
 constexpr int FORK_PHASES = 5;
 
 __global__ void __launch_bounds__(PLAN_THREADS, 1) fork_plan_kernel(const PagePlan P, int first, int last) {
-  __shared__ int sm[33];
+  __shared__ int sm[2][33];
+  BlockScan scan{sm};
   allow_dependent_launch();  // the copies may launch; they wait for this grid to finish
   for (int phase = first; phase <= last; ++phase) {
     if (phase == 0) fork_init(P);
     else if (phase == 1) fork_mark(P);
-    else if (phase == 2) fork_count(P, sm);
-    else if (phase == 3) fork_rank(P, sm);
-    else fork_assign(P, sm);
+    else if (phase == 2) fork_count(P, scan);
+    else if (phase == 3) fork_rank(P, scan);
+    else fork_assign(P);
     if (phase < last) {
       __syncthreads();
       cluster_barrier();
@@ -317,35 +314,36 @@ __device__ void compact_init(const PagePlan& P) {
     P.refs[u] = P.pins ? max(0, __ldg(P.pins + u)) : 0;
 }
 
-// The entries of one row segment that count: below the sequence's last token.
-// Calls f(index in the table, entry or -1).
+// The entries of the table that count, those below a sequence's last token:
+// f(index in the table, space, entry or -1) for every entry.
 template <typename F>
 __device__ __forceinline__ void compact_entries(const PagePlan& P, bool report, F f) {
-  constexpr int SEG = 128;
+  constexpr int SEG = PAGE_SEG;
   const int lane = threadIdx.x & 31;
   const int segs = (P.max_blocks + SEG - 1) / SEG;
-  const long long tasks = (long long)P.batch * P.spaces * segs;
+  const int tasks = P.batch * P.spaces * segs, step = gridDim.x * (PLAN_THREADS / 32);
   const long long cap = (long long)P.max_blocks * P.block_size;
   int err = 0;
-  for (long long t = (long long)blockIdx.x * (PLAN_THREADS / 32) + (threadIdx.x >> 5); t < tasks;
-       t += (long long)gridDim.x * (PLAN_THREADS / 32)) {
-    const long long r = t / segs;
-    const int b = (int)(r / P.spaces), s = (int)(r % P.spaces), e0 = (int)(t % segs) * SEG;
-    long long L = __ldg(P.seq_lens + b);
+  for (int t = blockIdx.x * (PLAN_THREADS / 32) + (threadIdx.x >> 5); t < tasks; t += step) {
+    const int r = t / segs, e0 = (t - r * segs) * SEG;
+    const int b = r / P.spaces, s = r - b * P.spaces;
+    const long long L = __ldg(P.seq_lens + b);
     if (L < 0) err |= DEVERR_SEQ_LEN;
     if (L > cap) err |= DEVERR_TABLE_RANGE;
     const int have = pages_of(P, (int)max(0LL, min(L, cap)));
+    const long long i0 = (long long)r * P.max_blocks;
     int v[SEG / 32];
 #pragma unroll
     for (int k = 0; k < SEG / 32; ++k) {
       const int e = e0 + lane + 32 * k;
-      v[k] = e < have ? __ldcg(P.table + r * P.max_blocks + e) : -1;
+      v[k] = e < P.max_blocks ? __ldcg(P.table + i0 + e) : -1;
+      if (e >= have) v[k] = -1;
     }
 #pragma unroll
     for (int k = 0; k < SEG / 32; ++k) {
       const int e = e0 + lane + 32 * k;
       if (v[k] >= P.num_blocks) err |= DEVERR_BLOCK_RANGE;
-      if (e < P.max_blocks) f(r * P.max_blocks + e, s, v[k] < 0 || v[k] >= P.num_blocks ? -1 : v[k]);
+      if (e < P.max_blocks) f(i0 + e, s, v[k] < 0 || v[k] >= P.num_blocks ? -1 : v[k]);
     }
   }
   err = __reduce_or_sync(0xffffffffu, err);
@@ -358,76 +356,70 @@ __device__ void compact_mark(const PagePlan& P) {
   });
 }
 
-__device__ __forceinline__ bool pinned(const PagePlan& P, long long u) { return P.pins && __ldg(P.pins + u) > 0; }
+// Pages first .. first + 3 of space s: bit i, page first + i is used; bit 4 + i, and not pinned.
+__device__ __forceinline__ int compact_used4(const PagePlan& P, int s, int first) {
+  int refs[4], pins[4] = {0, 0, 0, 0}, f = 0;
+  load4(P.refs + (long long)s * P.num_blocks, first, P.num_blocks, 0, refs);
+  if (P.pins) load4(P.pins + (long long)s * P.num_blocks, first, P.num_blocks, 0, pins);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f |= (refs[i] > 0) << i;
+    f |= (refs[i] > 0 && pins[i] <= 0) << (4 + i);
+  }
+  return f;
+}
 
-// Phase 2: used pages per task, and the used ones that may move.
-__device__ void compact_count(const PagePlan& P, int* sm) {
+// Phase 2: used pages per task, and the used ones that may move.  (Both in
+// one scan: a task has at most 4096 of each.)
+__device__ void compact_count(const PagePlan& P, BlockScan& scan) {
   const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
   const int tasks = P.spaces * per_space;
   for (int t = blockIdx.x; t < tasks; t += gridDim.x) {
-    const int s = t / per_space, first = (t % per_space) * UNITS_PER_TASK + 4 * threadIdx.x;
-    int used = 0, loose = 0, total;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long u = (long long)s * P.num_blocks + first + i;
-      if (first + i < P.num_blocks && __ldcg(P.refs + u) > 0) {
-        ++used;
-        loose += !pinned(P, u);
-      }
+    const int s = t / per_space, first = (t - s * per_space) * UNITS_PER_TASK + 4 * threadIdx.x;
+    const int f = compact_used4(P, s, first);
+    int total;
+    scan(__popc(f & 15) + (__popc(f >> 4) << 16), total);
+    if (threadIdx.x == 0) {
+      P.task_count[t] = total & 0xFFFF;
+      P.task_count[tasks + t] = total >> 16;
     }
-    block_scan(used, sm, total);
-    if (threadIdx.x == 0) P.task_count[t] = total;
-    block_scan(loose, sm, total);
-    if (threadIdx.x == 0) P.task_count[tasks + t] = total;
   }
 }
 
-// Phase 3: every page's rank: the holes and the movers listed in order, the
-// map of all that stay.  row_ask / row_at hold the movers' count of each space.
-__device__ void compact_rank(const PagePlan& P, int* sm) {
+// Phase 3: every page's rank: the holes listed in order, and the used pages
+// that may move (those numbered n_used or above are the movers; `below` is how
+// many of the list come before them), the map of all that stay.
+__device__ void compact_rank(const PagePlan& P, BlockScan& scan) {
   const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
   const int tasks = P.spaces * per_space;
   for (int t = blockIdx.x; t < tasks; t += gridDim.x) {
-    const int s = t / per_space, k = t % per_space, first = k * UNITS_PER_TASK + 4 * threadIdx.x;
+    const int s = t / per_space, k = t - s * per_space, first = k * UNITS_PER_TASK + 4 * threadIdx.x;
     const long long u0 = (long long)s * P.num_blocks;
-    const int n_used = block_sum(P.task_count + s * per_space, per_space, sm);
-    const int used_before = block_sum(P.task_count + s * per_space, k, sm);
-    const int loose_before = block_sum(P.task_count + tasks + s * per_space, k, sm);
-    // used pages below n_used that may move: whole tasks, then the rest one by one
-    const int kb = n_used / UNITS_PER_TASK;
-    int n = 0, below;
-    for (int i = kb * UNITS_PER_TASK + threadIdx.x; i < n_used; i += PLAN_THREADS)
-      n += __ldcg(P.refs + u0 + i) > 0 && !pinned(P, u0 + i);
-    block_scan(n, sm, below);
-    below += block_sum(P.task_count + tasks + s * per_space, kb, sm);
-    bool used[4], loose[4];
-    int nu = 0, nl = 0, total;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      used[i] = first + i < P.num_blocks && __ldcg(P.refs + u0 + first + i) > 0;
-      loose[i] = used[i] && !pinned(P, u0 + first + i);
-      nu += used[i];
-      nl += loose[i];
-    }
-    int ru = used_before + block_scan(nu, sm, total);
-    int rl = loose_before + block_scan(nl, sm, total) - below;
+    const int f = compact_used4(P, s, first);
+    const int n_used = warp_total(P.task_count + s * per_space, per_space);
+    int ru = warp_total(P.task_count + s * per_space, k);
+    int rl = warp_total(P.task_count + tasks + s * per_space, k);
+    int total;
+    const int in = scan(__popc(f & 15) + (__popc(f >> 4) << 16), total);
     if (k == per_space - 1 && threadIdx.x == 0) {
       P.num_used[s] = n_used;
-      P.movers[s] = loose_before + total - below;
+      P.loose[s] = rl + (total >> 16);
+      if (n_used == P.num_blocks) P.below[s] = rl + (total >> 16);
     }
+    ru += in & 0xFFFF;
+    rl += in >> 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int id = first + i;
       if (id >= P.num_blocks) break;
-      if (!used[i] && id < n_used && KVQ_IN_BOUNDS(ru <= id, P.dev_error))
+      const bool used = (f >> i) & 1, may = (f >> (4 + i)) & 1;
+      if (id == n_used) P.below[s] = rl;
+      if (!used && id < n_used && KVQ_IN_BOUNDS(ru <= id, P.dev_error))
         P.list[u0 + id - ru] = id;  // hole: as many holes before it as unused pages
-      if (loose[i] && id >= n_used) {
-        if (KVQ_IN_BOUNDS(rl >= 0 && rl < P.num_blocks, P.dev_error)) P.owner[u0 + rl] = id;  // mover
-      } else {
-        P.page_map[u0 + id] = used[i] ? id : -1;
-      }
-      ru += used[i];
-      rl += loose[i];
+      if (may && KVQ_IN_BOUNDS(rl < P.num_blocks, P.dev_error)) P.owner[u0 + rl] = id;
+      if (!may || id < n_used) P.page_map[u0 + id] = used ? id : -1;
+      ru += used;
+      rl += may;
     }
   }
 }
@@ -437,10 +429,10 @@ __device__ void compact_rank(const PagePlan& P, int* sm) {
 __device__ void compact_pair(const PagePlan& P) {
   int before = 0;
   for (int s = 0; s < P.spaces; ++s) {
-    const int n = __ldcg(P.movers + s);
+    const int below = __ldcg(P.below + s), n = __ldcg(P.loose + s) - below;
     const long long u0 = (long long)s * P.num_blocks;
-    for (long long k = (long long)blockIdx.x * PLAN_THREADS + threadIdx.x; k < n; k += (long long)gridDim.x * PLAN_THREADS) {
-      const int src = __ldcg(P.owner + u0 + k), dst = __ldcg(P.list + u0 + k);
+    for (int k = blockIdx.x * PLAN_THREADS + threadIdx.x; k < n; k += gridDim.x * PLAN_THREADS) {
+      const int src = __ldcg(P.owner + u0 + below + k), dst = __ldcg(P.list + u0 + k);
       if (!KVQ_IN_BOUNDS(dst >= 0 && dst < src && src < P.num_blocks && before + k < P.most_pairs, P.dev_error)) continue;
       P.page_map[u0 + src] = dst;
       P.refs[u0 + dst] = __ldcg(P.refs + u0 + src);
@@ -462,13 +454,14 @@ __device__ void compact_remap(const PagePlan& P) {
 constexpr int COMPACT_PHASES = 6;
 
 __global__ void __launch_bounds__(PLAN_THREADS, 1) compact_plan_kernel(const PagePlan P, int first, int last) {
-  __shared__ int sm[33];
+  __shared__ int sm[2][33];
+  BlockScan scan{sm};
   allow_dependent_launch();  // the copies may launch; they wait for this grid to finish
   for (int phase = first; phase <= last; ++phase) {
     if (phase == 0) compact_init(P);
     else if (phase == 1) compact_mark(P);
-    else if (phase == 2) compact_count(P, sm);
-    else if (phase == 3) compact_rank(P, sm);
+    else if (phase == 2) compact_count(P, scan);
+    else if (phase == 3) compact_rank(P, scan);
     else if (phase == 4) compact_pair(P);
     else compact_remap(P);
     if (phase < last) {
