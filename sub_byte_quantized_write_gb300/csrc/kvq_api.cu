@@ -671,6 +671,7 @@ size_t compact_layout(kvq::PagePlan& P, void* base) {
   P.loose = w.ints(P.spaces);
   P.below = w.ints(P.spaces);
   P.num_pairs = w.ints(1);
+  P.turn = reinterpret_cast<unsigned long long*>(w.ints(2));
   // at most half of a space's pages move, and no more than its rows name
   P.most_pairs = std::min<long long>(P.num_blocks / 2, (long long)P.batch * P.max_blocks) * P.spaces;
   P.pair_src = w.ints(P.most_pairs);

@@ -139,6 +139,7 @@ struct PageCopy {
   const int32_t* dst;
   int num_pairs;
   const int32_t* num_pairs_dev;     // the pairs' number on the device instead, where not NULL
+  unsigned long long* turn;         // runs handed out beyond the first of each CTA, where not NULL
   int32_t* claim;                   // [units] scratch of kvq_copy_pages
   int32_t* dev_error;
 };
@@ -172,6 +173,7 @@ struct PagePlan {
   int32_t* pair_src;
   int32_t* pair_dst;
   int32_t* num_pairs;          // compact: one
+  unsigned long long* turn;    // compact: one, 0 for the copies
   long long most_pairs;        // entries of pair_src / pair_dst
 };
 constexpr int PAGE_TASK_UNITS = 4096;  // pages a CTA ranks at a time: the stride of task_count

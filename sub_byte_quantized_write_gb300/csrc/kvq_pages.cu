@@ -442,7 +442,10 @@ __device__ void compact_pair(const PagePlan& P) {
     }
     before += n;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *P.num_pairs = before;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *P.num_pairs = before;
+    *P.turn = 0;
+  }
 }
 
 __device__ void compact_remap(const PagePlan& P) {
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) copy_claim_kernel(const PageC
 // pair with the whole list (LISTED): that saves a launch, 6 of 221 us for 1200
 // pages of 32 layers and 2 us of the host's time for a few pages.
 constexpr int COPY_PIECE = 4096;
-constexpr int COPY_RUN = 32;         // pieces per CTA and turn
+constexpr int COPY_RUN = 16;         // pieces per CTA and turn
 constexpr int COPY_LISTED = 2048;    // pairs a CTA compares with
 enum { COPY_SAFE, COPY_CLAIMED, COPY_CHECKS_LIST };
 
@@ -514,7 +517,16 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const PageCopy P) {
   if (CHECK != COPY_CHECKS_LIST) grid_dependency_wait();  // the pairs come from the kernel before
   const long long pairs = P.num_pairs_dev ? __ldcg(P.num_pairs_dev) : P.num_pairs;
   const int per_pair = 2 * P.num_layers * P.pieces, runs = (per_pair + P.run - 1) / P.run;
-  for (long long w = blockIdx.x; w < pairs * runs; w += gridDim.x) {
+  __shared__ unsigned long long turn[2];
+  int phase = 0;
+  auto next = [&](long long w) -> long long {  // the CTA's next run
+    if (!P.turn) return w + gridDim.x;
+    if (threadIdx.x == 0) turn[phase] = gridDim.x + atomicAdd(P.turn, 1ull);
+    __syncthreads();
+    phase ^= 1;
+    return (long long)turn[phase ^ 1];
+  };
+  for (long long w = blockIdx.x; w < pairs * runs; w = next(w)) {
     const long long i = w / runs;
     const int first = (int)(w % runs) * P.run;
     const int s = __ldcg(P.src + i), d = __ldcg(P.dst + i);
@@ -591,11 +603,13 @@ cudaError_t launch_copies(PageCopy C, long long most_pairs, int sms, cudaStream_
   for (int i = 0; i < C.num_layers; ++i) most = C.unit_bytes[i] > most ? C.unit_bytes[i] : most;
   C.pieces = (most + COPY_PIECE - 1) / COPY_PIECE;
   // long runs when there are pairs enough to fill the GPU with them, else one piece per warp
-  const long long per_pair = 2LL * C.num_layers * C.pieces, resident = (long long)sms * 8;
+  const long long per_pair = 2LL * C.num_layers * C.pieces, resident = (long long)sms * 4;
   C.run = most_pairs * (per_pair / COPY_RUN) >= resident ? COPY_RUN : 8;
   const long long ctas = most_pairs * ((per_pair + C.run - 1) / C.run);
   if (ctas == 0) return cudaSuccess;
-  const dim3 grid((unsigned)(ctas < resident ? ctas : resident));
+  // one CTA per run where the host knows their number, else as many as fit,
+  // which take their runs in turn
+  const dim3 grid((unsigned)(ctas < resident || (!C.turn && ctas <= INT_MAX) ? ctas : resident));
   if (CHECK == COPY_CHECKS_LIST) {  // nothing before it to overlap with
     copy_pages_kernel<CHECK><<<grid, 256, 0, stream>>>(C);
     return cudaGetLastError();
@@ -627,6 +641,7 @@ cudaError_t launch_compact(const PagePlan& P, PageCopy C, int sms, cudaStream_t 
   C.src = P.pair_src;
   C.dst = P.pair_dst;
   C.num_pairs_dev = P.num_pairs;
+  C.turn = P.turn;
   return launch_copies<COPY_SAFE>(C, P.most_pairs, sms, stream);
 }
 
