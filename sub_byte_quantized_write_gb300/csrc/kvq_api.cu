@@ -691,6 +691,7 @@ kvq::PagePlan page_plan(const kvq_cache* c, const kvq_paging* p, int32_t* dev_er
   P.num_blocks = c->num_blocks;
   P.num_kv_heads = c->num_kv_heads;
   P.block_size = c->block_size;
+  P.bs_log2 = c->block_size == 16 ? 4 : c->block_size == 32 ? 5 : 6;
   P.dev_error = dev_error;
   return P;
 }

@@ -149,7 +149,7 @@ struct PageCopy {
 struct PagePlan {
   const int32_t* table;
   const int32_t* seq_lens;
-  int max_blocks, batch, headwise, spaces, num_blocks, num_kv_heads, block_size;
+  int max_blocks, batch, headwise, spaces, num_blocks, num_kv_heads, block_size, bs_log2;
   const int32_t* parents;      // fork
   const int32_t* keep_tokens;
   const int32_t* new_tokens;
@@ -176,7 +176,7 @@ struct PagePlan {
   unsigned long long* turn;    // compact: one, 0 for the copies
   long long most_pairs;        // entries of pair_src / pair_dst
 };
-constexpr int PAGE_TASK_UNITS = 4096;  // pages a CTA ranks at a time: the stride of task_count
+constexpr int PAGE_TASK_UNITS = 1024;  // fewest pages a CTA ranks at a time: sizes task_count
 constexpr int PAGE_SEG = 256;          // entries of a table row a warp takes at a time
 
 cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream);

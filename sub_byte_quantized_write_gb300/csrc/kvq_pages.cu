@@ -7,7 +7,7 @@
 // kv head for a head-wise table.  Everything but the copying is whole-number
 // work on tables and per-page counters, cheap in bytes and made of dependent
 // phases (count the uses, rank the free pages, hand them out), so it is bound
-// by latency: the phases run in one kernel, a cluster of eight CTAs with the
+// by latency: the phases run in one kernel, a cluster of 16 CTAs with the
 // hardware's cluster barrier between phases, as long as a phase is short;
 // past PLAN_FUSED_WORK elements each phase is a launch of its own over the
 // whole GPU.  The page copies are a second launch over a list of (source,
@@ -30,8 +30,11 @@ namespace {
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_CLUSTER = 8;
 constexpr long long PLAN_FUSED_WORK = 1 << 20;
-constexpr int UNITS_PER_TASK = PAGE_TASK_UNITS;  // four per thread
-static_assert(UNITS_PER_TASK == 4 * PLAN_THREADS, "four pages per thread");
+// A task, the pages that a CTA ranks at a time, has ITEMS consecutive pages per
+// thread: one (coalesced; every CTA of the cluster busy) up to PLAN_SMALL
+// tasks, four beyond.
+constexpr int PLAN_SMALL = 128;
+static_assert(PAGE_TASK_UNITS == PLAN_THREADS, "task_count has one entry per task of one page per thread");
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -79,10 +82,11 @@ __device__ __forceinline__ int warp_total(const int* a, int n) {
   return __reduce_add_sync(0xffffffffu, v);
 }
 
-// Four consecutive counters from `first` on; those at or past n read as `past`.
-__device__ __forceinline__ void load4(const int32_t* a, int first, int n, int past, int (&x)[4]) {
+// Consecutive counters from `first` on; those at or past n read as `past`.
+template <int ITEMS>
+__device__ __forceinline__ void load_items(const int32_t* a, int first, int n, int past, int (&x)[ITEMS]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = first + i < n ? __ldcg(a + first + i) : past;
+  for (int i = 0; i < ITEMS; ++i) x[i] = first + i < n ? __ldcg(a + first + i) : past;
 }
 
 // Page `id` of space `s` as a number of the pools: blocks for a uniform
@@ -129,7 +133,7 @@ __device__ __forceinline__ ForkRow fork_row(const PagePlan& P, int b, int& err) 
 }
 
 __device__ __forceinline__ int pages_of(const PagePlan& P, int tokens) {
-  return tokens / P.block_size + (tokens % P.block_size != 0);
+  return (tokens >> P.bs_log2) + ((tokens & (P.block_size - 1)) != 0);
 }
 
 // Phase 0: the counters.
@@ -155,7 +159,7 @@ __device__ void fork_mark(const PagePlan& P) {
     const int b = r / P.spaces, s = r - b * P.spaces;
     const ForkRow row = fork_row(P, b, err);
     if (s == 0 && e0 == 0 && lane == 0) P.new_lens[b] = row.total;
-    const int have = pages_of(P, row.kept), tail = row.kept % P.block_size ? have - 1 : -1;
+    const int have = pages_of(P, row.kept), tail = row.kept & (P.block_size - 1) ? have - 1 : -1;
     const int32_t* from = P.table + ((long long)row.parent * P.spaces + s) * P.max_blocks;
     int32_t* to = P.new_table + (long long)r * P.max_blocks;
     int v[SEG / 32];
@@ -184,18 +188,20 @@ __device__ void fork_mark(const PagePlan& P) {
 }
 
 // Bit i: page first + i of space s is free.
-__device__ __forceinline__ int fork_free4(const PagePlan& P, int s, int first) {
-  int refs[4], owner[4], f = 0;
-  load4(P.refs + (long long)s * P.num_blocks, first, P.num_blocks, 1, refs);
-  load4(P.owner + (long long)s * P.num_blocks, first, P.num_blocks, 0, owner);
+template <int ITEMS>
+__device__ __forceinline__ int fork_free(const PagePlan& P, int s, int first) {
+  int refs[ITEMS], owner[ITEMS], f = 0;
+  load_items(P.refs + (long long)s * P.num_blocks, first, P.num_blocks, 1, refs);
+  load_items(P.owner + (long long)s * P.num_blocks, first, P.num_blocks, 0, owner);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f |= (refs[i] == 0 && owner[i] == INT_MAX) << i;
+  for (int i = 0; i < ITEMS; ++i) f |= (refs[i] == 0 && owner[i] == INT_MAX) << i;
   return f;
 }
 
 // Phase 2: free pages per task, and the pages each row asks for: a private
 // copy of its last page unless it is the lowest row that ends in it and
 // nobody else uses it, and pages for its new tokens.
+template <int ITEMS>
 __device__ void fork_count(const PagePlan& P, BlockScan& scan) {
   const int rows = P.new_batch * P.spaces;
   for (int r = blockIdx.x * PLAN_THREADS + threadIdx.x; r < rows; r += gridDim.x * PLAN_THREADS) {
@@ -209,28 +215,31 @@ __device__ void fork_count(const PagePlan& P, BlockScan& scan) {
     }
     P.row_ask[r] = 2 * (pages_of(P, row.y) - pages_of(P, row.x) + split) + split;
   }
-  const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
+  constexpr int UNITS = ITEMS * PLAN_THREADS;
+  const int per_space = (P.num_blocks + UNITS - 1) / UNITS;
   for (int t = blockIdx.x; t < P.spaces * per_space; t += gridDim.x) {
-    const int s = t / per_space, first = (t - s * per_space) * UNITS_PER_TASK + 4 * threadIdx.x;
+    const int s = t / per_space, first = (t - s * per_space) * UNITS + ITEMS * threadIdx.x;
     int total;
-    scan(__popc(fork_free4(P, s, first)), total);
+    scan(__popc(fork_free<ITEMS>(P, s, first)), total);
     if (threadIdx.x == 0) P.task_count[t] = total;
   }
 }
 
 // Phase 3: the free pages of each space in ascending order, and where each
 // row's share of them begins (rows in order).
+template <int ITEMS>
 __device__ void fork_rank(const PagePlan& P, BlockScan& scan) {
-  const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
+  constexpr int UNITS = ITEMS * PLAN_THREADS;
+  const int per_space = (P.num_blocks + UNITS - 1) / UNITS;
   for (int t = blockIdx.x; t < P.spaces * (per_space + 1); t += gridDim.x) {
     if (t < P.spaces * per_space) {
-      const int s = t / per_space, k = t - s * per_space, first = k * UNITS_PER_TASK + 4 * threadIdx.x;
-      const int f = fork_free4(P, s, first);
+      const int s = t / per_space, k = t - s * per_space, first = k * UNITS + ITEMS * threadIdx.x;
+      const int f = fork_free<ITEMS>(P, s, first);
       const int before = warp_total(P.task_count + s * per_space, k);
       int total;
       int at = before + scan(__popc(f), total);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < ITEMS; ++i)
         if (((f >> i) & 1) && KVQ_IN_BOUNDS(at < P.num_blocks, P.dev_error))
           P.list[(long long)s * P.num_blocks + at++] = first + i;
     } else {
@@ -249,9 +258,11 @@ __device__ void fork_rank(const PagePlan& P, BlockScan& scan) {
 }
 
 // Phase 4: the pages handed out, a warp per row; the pairs to copy.
+template <int ITEMS>
 __device__ void fork_assign(const PagePlan& P) {
   const int lane = threadIdx.x & 31;
-  const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
+  constexpr int UNITS = ITEMS * PLAN_THREADS;
+  const int per_space = (P.num_blocks + UNITS - 1) / UNITS;
   const int rows = P.new_batch * P.spaces;
   int err = 0;
   for (int r = blockIdx.x * (PLAN_THREADS / 32) + (threadIdx.x >> 5); r < rows; r += gridDim.x * (PLAN_THREADS / 32)) {
@@ -286,6 +297,7 @@ __device__ void fork_assign(const PagePlan& P) {
 
 constexpr int FORK_PHASES = 5;
 
+template <int ITEMS>
 __global__ void __launch_bounds__(PLAN_THREADS, 1) fork_plan_kernel(const PagePlan P, int first, int last) {
   __shared__ int sm[2][33];
   BlockScan scan{sm};
@@ -293,9 +305,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) fork_plan_kernel(const PagePl
   for (int phase = first; phase <= last; ++phase) {
     if (phase == 0) fork_init(P);
     else if (phase == 1) fork_mark(P);
-    else if (phase == 2) fork_count(P, scan);
-    else if (phase == 3) fork_rank(P, scan);
-    else fork_assign(P);
+    else if (phase == 2) fork_count<ITEMS>(P, scan);
+    else if (phase == 3) fork_rank<ITEMS>(P, scan);
+    else fork_assign<ITEMS>(P);
     if (phase < last) {
       __syncthreads();
       cluster_barrier();
@@ -356,13 +368,14 @@ __device__ void compact_mark(const PagePlan& P) {
   });
 }
 
-// Pages first .. first + 3 of space s: bit i, page first + i is used; bit 4 + i, and not pinned.
-__device__ __forceinline__ int compact_used4(const PagePlan& P, int s, int first) {
-  int refs[4], pins[4] = {0, 0, 0, 0}, f = 0;
-  load4(P.refs + (long long)s * P.num_blocks, first, P.num_blocks, 0, refs);
-  if (P.pins) load4(P.pins + (long long)s * P.num_blocks, first, P.num_blocks, 0, pins);
+// Pages first .. first + ITEMS - 1 of space s: bit i, page first + i is used; bit 4 + i, and not pinned.
+template <int ITEMS>
+__device__ __forceinline__ int compact_used(const PagePlan& P, int s, int first) {
+  int refs[ITEMS], pins[ITEMS] = {}, f = 0;
+  load_items(P.refs + (long long)s * P.num_blocks, first, P.num_blocks, 0, refs);
+  if (P.pins) load_items(P.pins + (long long)s * P.num_blocks, first, P.num_blocks, 0, pins);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     f |= (refs[i] > 0) << i;
     f |= (refs[i] > 0 && pins[i] <= 0) << (4 + i);
   }
@@ -371,12 +384,14 @@ __device__ __forceinline__ int compact_used4(const PagePlan& P, int s, int first
 
 // Phase 2: used pages per task, and the used ones that may move.  (Both in
 // one scan: a task has at most 4096 of each.)
+template <int ITEMS>
 __device__ void compact_count(const PagePlan& P, BlockScan& scan) {
-  const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
+  constexpr int UNITS = ITEMS * PLAN_THREADS;
+  const int per_space = (P.num_blocks + UNITS - 1) / UNITS;
   const int tasks = P.spaces * per_space;
   for (int t = blockIdx.x; t < tasks; t += gridDim.x) {
-    const int s = t / per_space, first = (t - s * per_space) * UNITS_PER_TASK + 4 * threadIdx.x;
-    const int f = compact_used4(P, s, first);
+    const int s = t / per_space, first = (t - s * per_space) * UNITS + ITEMS * threadIdx.x;
+    const int f = compact_used<ITEMS>(P, s, first);
     int total;
     scan(__popc(f & 15) + (__popc(f >> 4) << 16), total);
     if (threadIdx.x == 0) {
@@ -389,13 +404,15 @@ __device__ void compact_count(const PagePlan& P, BlockScan& scan) {
 // Phase 3: every page's rank: the holes listed in order, and the used pages
 // that may move (those numbered n_used or above are the movers; `below` is how
 // many of the list come before them), the map of all that stay.
+template <int ITEMS>
 __device__ void compact_rank(const PagePlan& P, BlockScan& scan) {
-  const int per_space = (P.num_blocks + UNITS_PER_TASK - 1) / UNITS_PER_TASK;
+  constexpr int UNITS = ITEMS * PLAN_THREADS;
+  const int per_space = (P.num_blocks + UNITS - 1) / UNITS;
   const int tasks = P.spaces * per_space;
   for (int t = blockIdx.x; t < tasks; t += gridDim.x) {
-    const int s = t / per_space, k = t - s * per_space, first = k * UNITS_PER_TASK + 4 * threadIdx.x;
+    const int s = t / per_space, k = t - s * per_space, first = k * UNITS + ITEMS * threadIdx.x;
     const long long u0 = (long long)s * P.num_blocks;
-    const int f = compact_used4(P, s, first);
+    const int f = compact_used<ITEMS>(P, s, first);
     const int n_used = warp_total(P.task_count + s * per_space, per_space);
     int ru = warp_total(P.task_count + s * per_space, k);
     int rl = warp_total(P.task_count + tasks + s * per_space, k);
@@ -409,7 +426,7 @@ __device__ void compact_rank(const PagePlan& P, BlockScan& scan) {
     ru += in & 0xFFFF;
     rl += in >> 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
       const int id = first + i;
       if (id >= P.num_blocks) break;
       const bool used = (f >> i) & 1, may = (f >> (4 + i)) & 1;
@@ -456,6 +473,7 @@ __device__ void compact_remap(const PagePlan& P) {
 
 constexpr int COMPACT_PHASES = 6;
 
+template <int ITEMS>
 __global__ void __launch_bounds__(PLAN_THREADS, 1) compact_plan_kernel(const PagePlan P, int first, int last) {
   __shared__ int sm[2][33];
   BlockScan scan{sm};
@@ -463,8 +481,8 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) compact_plan_kernel(const Pag
   for (int phase = first; phase <= last; ++phase) {
     if (phase == 0) compact_init(P);
     else if (phase == 1) compact_mark(P);
-    else if (phase == 2) compact_count(P, scan);
-    else if (phase == 3) compact_rank(P, scan);
+    else if (phase == 2) compact_count<ITEMS>(P, scan);
+    else if (phase == 3) compact_rank<ITEMS>(P, scan);
     else if (phase == 4) compact_pair(P);
     else compact_remap(P);
     if (phase < last) {
@@ -569,32 +587,54 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const PageCopy P) {
 // ---------------------------------------------------------------------------
 // launch
 
+// A cluster of sixteen CTAs where the device can hold one (more than eight is
+// for a kernel to opt in to), else of eight.  Asked once per kernel and device,
+// not inside later calls, which may be captured into a graph.
 template <typename Kern, typename... Args>
-cudaError_t launch_cluster(Kern kernel, cudaStream_t stream, Args... args) {
+cudaError_t launch_cluster(Kern kernel, int (&sizes)[64], cudaStream_t stream, Args... args) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(PLAN_CLUSTER);
   cfg.blockDim = dim3(PLAN_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = PLAN_CLUSTER;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  int size = dev < 64 ? sizes[dev] : PLAN_CLUSTER;
+  if (size == 0) {
+    size = PLAN_CLUSTER;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+      attr[0].val.clusterDim.x = 2 * PLAN_CLUSTER;
+      cfg.gridDim = dim3(2 * PLAN_CLUSTER);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) size = 2 * PLAN_CLUSTER;
+    }
+    (void)cudaGetLastError();  // (a refusal of the larger size is no error of this call)
+    sizes[dev] = size;
+  }
+  attr[0].val.clusterDim.x = size;
+  cfg.gridDim = dim3(size);
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename Kern>
-cudaError_t launch_plan(Kern kernel, const PagePlan& P, int phases, int sms, cudaStream_t stream) {
+cudaError_t launch_plan(Kern kernel, int (&sizes)[64], const PagePlan& P, int phases, int sms, cudaStream_t stream) {
   const long long rows = (long long)(P.new_batch > P.batch ? P.new_batch : P.batch) * P.spaces;
   const long long work = (long long)P.spaces * P.num_blocks + rows * P.max_blocks;
-  if (work <= PLAN_FUSED_WORK) return launch_cluster(kernel, stream, P, 0, phases - 1);
+  if (work <= PLAN_FUSED_WORK) return launch_cluster(kernel, sizes, stream, P, 0, phases - 1);
   for (int i = 0; i < phases; ++i) {
     kernel<<<sms, PLAN_THREADS, 0, stream>>>(P, i, i);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+bool small_plan(const PagePlan& P) {
+  return (long long)P.spaces * ((P.num_blocks + PLAN_THREADS - 1) / PLAN_THREADS) <= PLAN_SMALL;
 }
 
 template <int CHECK>
@@ -621,13 +661,16 @@ cudaError_t launch_copies(PageCopy C, long long most_pairs, int sms, cudaStream_
 
 cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream) {
   if (C.num_pairs <= COPY_LISTED) return launch_copies<COPY_CHECKS_LIST>(C, C.num_pairs, sms, stream);
-  const cudaError_t e = launch_cluster(copy_claim_kernel, stream, C);
+  static int sizes[64] = {0};
+  const cudaError_t e = launch_cluster(copy_claim_kernel, sizes, stream, C);
   if (e != cudaSuccess) return e;
   return launch_copies<COPY_CLAIMED>(C, C.num_pairs, sms, stream);
 }
 
 cudaError_t launch_fork(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream) {
-  const cudaError_t e = launch_plan(fork_plan_kernel, P, FORK_PHASES, sms, stream);
+  static int sizes[2][64] = {{0}, {0}};
+  const cudaError_t e = small_plan(P) ? launch_plan(fork_plan_kernel<1>, sizes[0], P, FORK_PHASES, sms, stream)
+                                      : launch_plan(fork_plan_kernel<4>, sizes[1], P, FORK_PHASES, sms, stream);
   if (e != cudaSuccess) return e;
   C.src = P.pair_src;
   C.dst = P.pair_dst;
@@ -636,7 +679,9 @@ cudaError_t launch_fork(const PagePlan& P, PageCopy C, int sms, cudaStream_t str
 }
 
 cudaError_t launch_compact(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream) {
-  const cudaError_t e = launch_plan(compact_plan_kernel, P, COMPACT_PHASES, sms, stream);
+  static int sizes[2][64] = {{0}, {0}};
+  const cudaError_t e = small_plan(P) ? launch_plan(compact_plan_kernel<1>, sizes[0], P, COMPACT_PHASES, sms, stream)
+                                      : launch_plan(compact_plan_kernel<4>, sizes[1], P, COMPACT_PHASES, sms, stream);
   if (e != cudaSuccess) return e;
   C.src = P.pair_src;
   C.dst = P.pair_dst;
