@@ -184,7 +184,8 @@ def _set_and_forget(self, name, value):
 
 
 def _kept_struct(handle, tensors):
-    """A handle's C struct, rebuilt (with its checks) unless the tensors it was made of are where they were."""
+    """A handle's C struct, rebuilt (with its checks) unless the tensors it was made of are where they were.  (Give a
+    handle other tensors by setting its attributes, not by resizing the ones it has.)"""
     kept = handle._struct
     if kept is not None:
         for t, pointer in kept[0]:
@@ -195,6 +196,14 @@ def _kept_struct(handle, tensors):
     kept = ([(t, t.data_ptr()) for t in tensors(handle) if t is not None], handle._build())
     handle.__dict__["_struct"] = kept
     return kept[1]
+
+
+def _cache_tensors(c):
+    return c.k_pages, c.v_pages, c.rht_signs, c.ch_amax, c.ch_amax_ready
+
+
+def _paging_tensors(p):
+    return p.seq_lens, p.block_tables, p.block_tables_headwise, p.window_per_kv_head
 
 
 class PagedCache:
@@ -228,7 +237,7 @@ class PagedCache:
 
     def struct(self) -> KvqCache:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
-        return _kept_struct(self, lambda c: (c.k_pages, c.v_pages, c.rht_signs, c.ch_amax, c.ch_amax_ready))
+        return _kept_struct(self, _cache_tensors)
 
     def _build(self) -> KvqCache:
         return KvqCache(_dev_ptr(self.k_pages, torch.uint8, "k_pages"), _dev_ptr(self.v_pages, torch.uint8, "v_pages"),
@@ -258,7 +267,7 @@ class Paging:
 
     def struct(self) -> KvqPaging:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
-        return _kept_struct(self, lambda p: (p.seq_lens, p.block_tables, p.block_tables_headwise, p.window_per_kv_head))
+        return _kept_struct(self, _paging_tensors)
 
     def _build(self) -> KvqPaging:
         return KvqPaging(_dev_ptr(self.block_tables, torch.int32, "block_tables"),
@@ -428,20 +437,21 @@ Caches = Union[PagedCache, Sequence[PagedCache]]
 
 
 def _cache_array(caches: Caches):
-    """(ctypes array, number, device) of the caches that share page numbers; the array is kept with the first
-    cache as long as the caches' structs are the same."""
+    """(ctypes array, number, device, num_kv_heads, num_blocks) of the caches that share page numbers; kept with the
+    first cache as long as the caches' structs are the same."""
     cs = (caches,) if isinstance(caches, PagedCache) else caches
     if not cs:
         raise ValueError("no caches")
     structs = [c.struct() for c in cs]
-    kept = cs[0].__dict__.get("_group")
+    first = cs[0].__dict__
+    kept = first.get("_group")
     if kept is None or kept[0] != structs:
         dev = cs[0].k_pages.device
         if any(c.k_pages.device != dev for c in cs):
             raise ValueError("the caches of one call must be on one device")
-        kept = (structs, (KvqCache * len(cs))(*structs), len(cs), dev)
-        cs[0].__dict__["_group"] = kept
-    return kept[1:]
+        array = (KvqCache * len(cs))(*structs)
+        kept = first["_group"] = (structs, (array, len(cs), dev, array[0].num_kv_heads, array[0].num_blocks))
+    return kept[1]
 
 
 def _page_tensor(t: Optional[torch.Tensor], name: str, dev: torch.device, numel: Optional[int] = None):
@@ -461,11 +471,11 @@ def _page_paging(p: "Paging", name: str, dev: torch.device, num_kv_heads: int) -
     """(struct, head-wise, rows) of a paging state of the caches' device."""
     headwise = p.block_tables_headwise is not None
     t = p.block_tables_headwise if headwise else p.block_tables
-    if t is None or t.device != dev or p.seq_lens.device != dev:
+    if t is None or t.device != dev or p.seq_lens.get_device() != t.get_device():
         raise ValueError("%s needs a block table and lengths on the caches' device" % name)
     struct = p.struct()
     rows = struct.batch
-    if t.shape[0] != (rows * num_kv_heads if headwise else rows):
+    if len(t) != (rows * num_kv_heads if headwise else rows):
         raise ValueError("%s: the table's rows do not match seq_lens" % name)
     return struct, headwise, rows
 
@@ -473,14 +483,14 @@ def _page_paging(p: "Paging", name: str, dev: torch.device, num_kv_heads: int) -
 def _page_scratch(workspace, size, dev, stream, *args):
     if workspace is None:
         workspace = _empty(max(size(*args), 256), torch.uint8, dev, stream)
-    elif workspace.device != dev:
+    elif workspace.get_device() != dev.index:
         raise ValueError("workspace must be on the caches' device")
     return _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(), workspace
 
 
 def kvq_copy_workspace_size(caches: Caches, num_pairs: int, headwise: bool = False) -> int:
     """Bytes of scratch that kvq_copy_pages needs."""
-    cs, n, _ = _cache_array(caches)
+    cs, n, _, _, _ = _cache_array(caches)
     size = ctypes.c_size_t(0)
     _check(_lib.kvq_copy_workspace_size(cs, n, int(num_pairs), int(headwise), ctypes.byref(size)))
     return size.value
@@ -492,7 +502,7 @@ def kvq_copy_pages(caches: Caches, src: torch.Tensor, dst: torch.Tensor, headwis
     """Page src[i] into page dst[i] (int32 tensors), K and V of every cache.  headwise: the numbers count
     (block, head) pages, block * num_kv_heads + head.  Sources are read as they were before the call; pairs
     that conflict are skipped and set KVQ_DEVERR_PAGE_CONFLICT."""
-    cs, n, dev = _cache_array(caches)
+    cs, n, dev, _, _ = _cache_array(caches)
     pairs = int(src.numel())
     ps, pd = _page_tensor(src, "src", dev), _page_tensor(dst, "dst", dev, pairs)
     ws, nbytes, _keep = _page_scratch(workspace, kvq_copy_workspace_size, dev, stream, caches, pairs, headwise)
@@ -513,7 +523,7 @@ def _fork_out(caches: Caches, paging: Optional[Paging], rows: int, dev, stream) 
 
 def kvq_fork_workspace_size(caches: Caches, paging: Optional[Paging], rows: int, out: Optional[Paging] = None) -> int:
     """Bytes of scratch that kvq_fork needs for `rows` new rows."""
-    cs, n, dev = _cache_array(caches)
+    cs, n, _, _, _ = _cache_array(caches)
     like = (out or paging)._build()  # (the size goes by the new rows' number, the table's kind and its width)
     like.batch = int(rows)
     size = ctypes.c_size_t(0)
@@ -531,8 +541,7 @@ def kvq_fork(caches: Caches, paging: Optional[Paging], parents: torch.Tensor,
     filled last page is copied in every cache, rows that nobody continues are freed.  Returns the new paging state
     (`out` if given: its table and seq_lens are written) and page_refs [spaces, num_blocks], the uses of every page
     (0: free).  paging None: there are no old rows yet (`out` is needed)."""
-    cs, n, dev = _cache_array(caches)
-    Hkv, blocks = cs[0].num_kv_heads, cs[0].num_blocks
+    cs, n, dev, Hkv, blocks = _cache_array(caches)
     rows = int(parents.numel())
     if out is None:
         out = _fork_out(caches, paging, rows, dev, stream)
@@ -554,7 +563,7 @@ def kvq_fork(caches: Caches, paging: Optional[Paging], parents: torch.Tensor,
 
 def kvq_compact_workspace_size(caches: Caches, paging: Paging) -> int:
     """Bytes of scratch that kvq_compact needs."""
-    cs, n, dev = _cache_array(caches)
+    cs, n, _, _, _ = _cache_array(caches)
     ps = paging.struct()
     size = ctypes.c_size_t(0)
     _check(_lib.kvq_compact_workspace_size(cs, n, ctypes.byref(ps), ctypes.byref(size)))
@@ -569,8 +578,7 @@ def kvq_compact(caches: Caches, paging: Paging, pins: Optional[torch.Tensor] = N
     rewritten table, page_map [spaces, num_blocks] (old number -> new, -1: unused), page_refs [spaces, num_blocks]
     by new number, num_used [spaces]).  `out` gives the table to write; it may be `paging` itself.  Pages with a
     positive `pins` stay where they are."""
-    cs, n, dev = _cache_array(caches)
-    Hkv, blocks = cs[0].num_kv_heads, cs[0].num_blocks
+    cs, n, dev, Hkv, blocks = _cache_array(caches)
     old, headwise, rows = _page_paging(paging, "paging", dev, Hkv)
     kind = "block_tables_headwise" if headwise else "block_tables"
     table = getattr(paging, kind)

@@ -614,11 +614,13 @@ kvq::PageCopy page_copy(const kvq_cache* c, int32_t n, bool headwise, int32_t* d
   kvq::PageCopy p;
   std::memset(&p, 0, sizeof(p));
   for (int i = 0; i < n; ++i) {
-    p.k[i] = c[i].k_pages;
-    p.v[i] = c[i].v_pages;
+    p.pool[2 * i] = c[i].k_pages;
+    p.pool[2 * i + 1] = c[i].v_pages;
     p.unit_bytes[i] = (headwise ? 1 : c->num_kv_heads) * c->block_size * kvq_row_bytes(c[i].mode, c[i].head_dim);
+    p.most_bytes = std::max(p.most_bytes, p.unit_bytes[i]);
   }
   p.num_layers = n;
+  p.pieces = (p.most_bytes + kvq::PAGE_COPY_PIECE - 1) / kvq::PAGE_COPY_PIECE;
   p.units = c->num_blocks * (headwise ? c->num_kv_heads : 1);
   p.dev_error = dev_error;
   return p;

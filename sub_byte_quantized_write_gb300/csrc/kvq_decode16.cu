@@ -51,7 +51,7 @@ constexpr int D16_WARPS = 12;      // per CTA, one CTA per SM
 constexpr int D16_RUNS = 2048;     // entries of the prefix sums over the pairs
 constexpr int D16_MIN_CHUNKS = 1;  // per warp, at least
 constexpr int D16_WIDE_MERGE = 16;  // records per pair from which a CTA joins one head
-constexpr int D16_DIRECT_CHUNKS = 4;  // per warp, at most, for one CTA per pair to be enough
+constexpr int D16_DIRECT_COST = 6;  // see launch_decode16_d
 constexpr float D16_SLACK = 8.0f;  // log2 units a logit may pass the reference maximum by
 
 __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {  // read once: not kept in L1
@@ -563,11 +563,13 @@ template <int D>
 cudaError_t launch_decode16_d(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
   const bool f32 = P.dtype == DT_F32;
   const int pairs = P.batch * P.num_kv_heads;
-  // What the host knows of the lengths is the table's width.  One CTA per
-  // pair while each has an SM to itself and no warp more than a few chunks;
-  // beyond, equal slices of the whole list.
+  // One CTA per pair while that is short: a wave of CTAs costs about two chunks
+  // of a warp's time and each chunk of its longest warp one, and the split form
+  // with its second launch six (66 sequences of 2 keys, 264 pairs: 8.4 us).
+  // What the host knows of the lengths is the table's width.
   const long long chunks = (long long)P.max_blocks * (P.block_size / D16_KEYS);  // of a pair, at most
-  if (ws.fixed_workers == 0 && pairs <= grid && chunks <= D16_DIRECT_CHUNKS * D16_WARPS)
+  const long long waves = (pairs + grid - 1) / grid, per_warp = (chunks + D16_WARPS - 1) / D16_WARPS;
+  if (ws.fixed_workers == 0 && waves * (2 + per_warp) <= D16_DIRECT_COST)
     return f32 ? launch_decode16_t<D, true, true>(P, ws, pairs, stream)
                : launch_decode16_t<D, false, true>(P, ws, pairs, stream);
   cudaError_t e = f32 ? launch_decode16_t<D, true, false>(P, ws, grid, stream)

@@ -130,10 +130,10 @@ inline DecodeLayout decode_ws_layout(int batch, int num_kv_heads, int group, int
 // Page copies in every layer's pools (kvq_pages.cu).
 constexpr int PAGE_MAX_LAYERS = 128;
 struct PageCopy {
-  uint8_t* k[PAGE_MAX_LAYERS];
-  uint8_t* v[PAGE_MAX_LAYERS];
-  int unit_bytes[PAGE_MAX_LAYERS];  // one page: all heads of a block, or one head's
-  int num_layers, pieces, run;      // copy steps per page, and per CTA and turn
+  uint8_t* pool[2 * PAGE_MAX_LAYERS];  // K and V of each cache in turn
+  int unit_bytes[PAGE_MAX_LAYERS];     // one page: all heads of a block, or one head's
+  int num_layers, most_bytes;          // the largest unit_bytes
+  int pieces, run;                     // copy steps per page, and per CTA and turn
   int units;                        // pages of a pool
   const int32_t* src;
   const int32_t* dst;
@@ -178,6 +178,8 @@ struct PagePlan {
 };
 constexpr int PAGE_TASK_UNITS = 1024;  // fewest pages a CTA ranks at a time: sizes task_count
 constexpr int PAGE_SEG = 256;          // entries of a table row a warp takes at a time
+
+constexpr int PAGE_COPY_PIECE = 4096;  // bytes of a page that a warp copies in one step, at most
 
 cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream);
 cudaError_t launch_fork(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream);

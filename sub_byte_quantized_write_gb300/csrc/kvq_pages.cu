@@ -11,7 +11,8 @@
 // hardware's cluster barrier between phases, as long as a phase is short;
 // past PLAN_FUSED_WORK elements each phase is a launch of its own over the
 // whole GPU.  The page copies are a second launch over a list of (source,
-// destination) pairs: bound by memory.
+// destination) pairs: bound by memory.  Where they can be no more than
+// PLAN_COPIES bytes they are the cluster's last phase instead.
 //
 // Nothing depends on the order in which atomics land: counters only add, the
 // owner of a shared last page is a minimum, and page numbers are handed out
@@ -29,7 +30,8 @@ namespace {
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_CLUSTER = 8;
-constexpr long long PLAN_FUSED_WORK = 1 << 20;
+constexpr long long PLAN_FUSED_WORK = 1 << 20;  // pages and table entries
+constexpr long long PLAN_COPIES = 2 << 20;      // bytes of page copies that the plan's CTAs do themselves
 // A task, the pages that a CTA ranks at a time, has ITEMS consecutive pages per
 // thread: one (coalesced; every CTA of the cluster busy) up to PLAN_SMALL
 // tasks, four beyond.
@@ -93,6 +95,40 @@ __device__ __forceinline__ void load_items(const int32_t* a, int first, int n, i
 // table, (block, head) pages for a head-wise one.
 __device__ __forceinline__ int pool_unit(const PagePlan& P, int s, int id) {
   return P.spaces == 1 && !P.headwise ? id : id * P.num_kv_heads + s;
+}
+
+// Copies.  One warp copies one piece (up to COPY_PIECE bytes) of page s of one
+// pool into page d at a time: eight 16-byte loads per lane in flight, then the
+// stores.  Step `item` of a pair: pool item / pieces, piece item % pieces.
+constexpr int COPY_PIECE = PAGE_COPY_PIECE;
+
+template <int LOADS>  // in flight per lane
+__device__ __forceinline__ void copy_piece(const PageCopy& P, int s, int d, int item) {
+  const int lane = threadIdx.x & 31;
+  const int lk = item / P.pieces, piece = item - lk * P.pieces, bytes = P.unit_bytes[lk >> 1];
+  const int size = ((bytes + P.pieces - 1) / P.pieces + 15) & ~15, lo = piece * size, n = min(size, bytes - lo);
+  const uint8_t* from = P.pool[lk] + (size_t)s * bytes + lo;
+  uint8_t* to = P.pool[lk] + (size_t)d * bytes + lo;
+#pragma unroll 1
+  for (int at = 16 * lane; at < n; at += 512 * LOADS) {
+    uint4 x[LOADS];
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k)
+      if (at + 512 * k < n) x[k] = *reinterpret_cast<const uint4*>(from + at + 512 * k);
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k)
+      if (at + 512 * k < n) *reinterpret_cast<uint4*>(to + at + 512 * k) = x[k];
+  }
+}
+
+// The pairs of a plan, by the plan's own CTAs.
+__device__ void copy_planned(const PagePlan& P, const PageCopy& C) {
+  const int pairs = P.num_pairs ? __ldcg(P.num_pairs) : P.new_batch * P.spaces;
+  const int per_pair = 2 * C.num_layers * C.pieces, items = pairs * per_pair;  // (few: see PLAN_COPIES)
+  for (int w = blockIdx.x * (PLAN_THREADS / 32) + (threadIdx.x >> 5); w < items; w += gridDim.x * (PLAN_THREADS / 32)) {
+    const int i = w / per_pair, s = __ldcg(P.pair_src + i), d = __ldcg(P.pair_dst + i);
+    if (s >= 0 && d >= 0) copy_piece<4>(C, s, d, w - i * per_pair);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -298,7 +334,7 @@ __device__ void fork_assign(const PagePlan& P) {
 constexpr int FORK_PHASES = 5;
 
 template <int ITEMS>
-__global__ void __launch_bounds__(PLAN_THREADS, 1) fork_plan_kernel(const PagePlan P, int first, int last) {
+__global__ void __launch_bounds__(PLAN_THREADS, 1) fork_plan_kernel(const PagePlan P, const PageCopy C, int first, int last) {
   __shared__ int sm[2][33];
   BlockScan scan{sm};
   allow_dependent_launch();  // the copies may launch; they wait for this grid to finish
@@ -307,7 +343,8 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) fork_plan_kernel(const PagePl
     else if (phase == 1) fork_mark(P);
     else if (phase == 2) fork_count<ITEMS>(P, scan);
     else if (phase == 3) fork_rank<ITEMS>(P, scan);
-    else fork_assign<ITEMS>(P);
+    else if (phase == 4) fork_assign<ITEMS>(P);
+    else copy_planned(P, C);
     if (phase < last) {
       __syncthreads();
       cluster_barrier();
@@ -474,7 +511,7 @@ __device__ void compact_remap(const PagePlan& P) {
 constexpr int COMPACT_PHASES = 6;
 
 template <int ITEMS>
-__global__ void __launch_bounds__(PLAN_THREADS, 1) compact_plan_kernel(const PagePlan P, int first, int last) {
+__global__ void __launch_bounds__(PLAN_THREADS, 1) compact_plan_kernel(const PagePlan P, const PageCopy C, int first, int last) {
   __shared__ int sm[2][33];
   BlockScan scan{sm};
   allow_dependent_launch();  // the copies may launch; they wait for this grid to finish
@@ -484,7 +521,8 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) compact_plan_kernel(const Pag
     else if (phase == 2) compact_count<ITEMS>(P, scan);
     else if (phase == 3) compact_rank<ITEMS>(P, scan);
     else if (phase == 4) compact_pair(P);
-    else compact_remap(P);
+    else if (phase == 5) compact_remap(P);
+    else copy_planned(P, C);
     if (phase < last) {
       __syncthreads();
       cluster_barrier();
@@ -517,21 +555,22 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) copy_claim_kernel(const PageC
   }
 }
 
-// One warp copies one piece (up to COPY_PIECE bytes) of one page of one pool
-// at a time: eight 16-byte loads per lane in flight, then the stores.  A CTA
-// takes a run of consecutive pieces of one pair.  How a pair is known to be
+// A CTA takes a run of consecutive pieces of one pair.  How a pair is known to be
 // free of conflicts: by construction (fork, compact), by the claims of the
 // kernel before, or, for short lists, by the CTA itself, which compares the
-// pair with the whole list (LISTED): that saves a launch, 6 of 221 us for 1200
-// pages of 32 layers and 2 us of the host's time for a few pages.
-constexpr int COPY_PIECE = 4096;
+// pair with the whole list: that saves a launch, 6 of 221 us for 1200 pages of 32
+// layers and 2 us of the host's time for a few pages.
+// (Measured and not kept for pages of 2 KB or less, one head's of a low-bit
+// cache, which leave most of a warp's loads empty: a step over several pools,
+// with the page's bytes laid end to end or pool by pool: 91 and 97 us instead
+// of 78 for 126,000 pages of 1152 bytes.)
 constexpr int COPY_RUN = 16;         // pieces per CTA and turn
 constexpr int COPY_LISTED = 2048;    // pairs a CTA compares with
 enum { COPY_SAFE, COPY_CLAIMED, COPY_CHECKS_LIST };
 
 template <int CHECK>
 __global__ void __launch_bounds__(256) copy_pages_kernel(const PageCopy P) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5;
   if (CHECK != COPY_CHECKS_LIST) grid_dependency_wait();  // the pairs come from the kernel before
   const long long pairs = P.num_pairs_dev ? __ldcg(P.num_pairs_dev) : P.num_pairs;
   const int per_pair = 2 * P.num_layers * P.pieces, runs = (per_pair + P.run - 1) / P.run;
@@ -567,20 +606,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const PageCopy P) {
       if (first == 0 && threadIdx.x == 0) flag_error(P.dev_error, DEVERR_PAGE_CONFLICT);
       continue;
     }
-    for (int item = first + warp; item < min(first + P.run, per_pair); item += 8) {
-      const int lk = item / P.pieces, piece = item % P.pieces, layer = lk >> 1, bytes = P.unit_bytes[layer];
-      const int size = ((bytes + P.pieces - 1) / P.pieces + 15) & ~15, lo = piece * size, n = min(size, bytes - lo);
-      uint8_t* pool = (lk & 1) ? P.v[layer] : P.k[layer];
-      const uint8_t* from = pool + (size_t)s * bytes + lo + 16 * lane;
-      uint8_t* to = pool + (size_t)d * bytes + lo + 16 * lane;
-      uint4 x[COPY_PIECE / 512];
-#pragma unroll
-      for (int k = 0; k < COPY_PIECE / 512; ++k)
-        if (512 * k + 16 * lane < n) x[k] = *reinterpret_cast<const uint4*>(from + 512 * k);
-#pragma unroll
-      for (int k = 0; k < COPY_PIECE / 512; ++k)
-        if (512 * k + 16 * lane < n) *reinterpret_cast<uint4*>(to + 512 * k) = x[k];
-    }
+    for (int item = first + warp; item < min(first + P.run, per_pair); item += 8) copy_piece<COPY_PIECE / 512>(P, s, d, item);
   }
 }
 
@@ -605,32 +631,18 @@ cudaError_t launch_cluster(Kern kernel, int (&sizes)[64], cudaStream_t stream, A
   cfg.numAttrs = 1;
   int size = dev < 64 ? sizes[dev] : PLAN_CLUSTER;
   if (size == 0) {
-    size = PLAN_CLUSTER;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
-      attr[0].val.clusterDim.x = 2 * PLAN_CLUSTER;
-      cfg.gridDim = dim3(2 * PLAN_CLUSTER);
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) size = 2 * PLAN_CLUSTER;
-    }
-    (void)cudaGetLastError();  // (a refusal of the larger size is no error of this call)
+    attr[0].val.clusterDim.x = 2 * PLAN_CLUSTER;
+    cfg.gridDim = dim3(2 * PLAN_CLUSTER);
+    int n = 0;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) (void)cudaGetLastError();  // (a refusal of the larger size is no error of this call)
+    size = e == cudaSuccess && n > 0 ? 2 * PLAN_CLUSTER : PLAN_CLUSTER;
     sizes[dev] = size;
   }
   attr[0].val.clusterDim.x = size;
   cfg.gridDim = dim3(size);
   return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <typename Kern>
-cudaError_t launch_plan(Kern kernel, int (&sizes)[64], const PagePlan& P, int phases, int sms, cudaStream_t stream) {
-  const long long rows = (long long)(P.new_batch > P.batch ? P.new_batch : P.batch) * P.spaces;
-  const long long work = (long long)P.spaces * P.num_blocks + rows * P.max_blocks;
-  if (work <= PLAN_FUSED_WORK) return launch_cluster(kernel, sizes, stream, P, 0, phases - 1);
-  for (int i = 0; i < phases; ++i) {
-    kernel<<<sms, PLAN_THREADS, 0, stream>>>(P, i, i);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
 }
 
 bool small_plan(const PagePlan& P) {
@@ -639,11 +651,9 @@ bool small_plan(const PagePlan& P) {
 
 template <int CHECK>
 cudaError_t launch_copies(PageCopy C, long long most_pairs, int sms, cudaStream_t stream) {
-  int most = 0;
-  for (int i = 0; i < C.num_layers; ++i) most = C.unit_bytes[i] > most ? C.unit_bytes[i] : most;
-  C.pieces = (most + COPY_PIECE - 1) / COPY_PIECE;
+  const long long per_pair = 2LL * C.num_layers * C.pieces;
+  const long long resident = (long long)sms * 4;
   // long runs when there are pairs enough to fill the GPU with them, else one piece per warp
-  const long long per_pair = 2LL * C.num_layers * C.pieces, resident = (long long)sms * 4;
   C.run = most_pairs * (per_pair / COPY_RUN) >= resident ? COPY_RUN : 8;
   const long long ctas = most_pairs * ((per_pair + C.run - 1) / C.run);
   if (ctas == 0) return cudaSuccess;
@@ -655,6 +665,27 @@ cudaError_t launch_copies(PageCopy C, long long most_pairs, int sms, cudaStream_
     return cudaGetLastError();
   }
   return launch_dependent(copy_pages_kernel<CHECK>, grid, dim3(256), 0, stream, C);
+}
+
+// The phases of a plan and the copies: in one launch, in two, or, for large
+// plans, in one per phase and the copies'.
+template <typename Kern>
+cudaError_t launch_plan(Kern kernel, int (&sizes)[64], const PagePlan& P, const PageCopy& C, int phases, int sms,
+                        cudaStream_t stream) {
+  const long long rows = (long long)(P.new_batch > P.batch ? P.new_batch : P.batch) * P.spaces;
+  const long long work = (long long)P.spaces * P.num_blocks + rows * P.max_blocks;
+  if (work <= PLAN_FUSED_WORK) {
+    const bool copies = P.most_pairs * 2 * C.num_layers * C.most_bytes <= PLAN_COPIES;
+    const cudaError_t e = launch_cluster(kernel, sizes, stream, P, C, 0, copies ? phases : phases - 1);
+    if (e != cudaSuccess || copies) return e;
+  } else {
+    for (int i = 0; i < phases; ++i) {
+      kernel<<<sms, PLAN_THREADS, 0, stream>>>(P, C, i, i);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return launch_copies<COPY_SAFE>(C, P.most_pairs, sms, stream);
 }
 
 }  // namespace
@@ -669,25 +700,21 @@ cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream) {
 
 cudaError_t launch_fork(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream) {
   static int sizes[2][64] = {{0}, {0}};
-  const cudaError_t e = small_plan(P) ? launch_plan(fork_plan_kernel<1>, sizes[0], P, FORK_PHASES, sms, stream)
-                                      : launch_plan(fork_plan_kernel<4>, sizes[1], P, FORK_PHASES, sms, stream);
-  if (e != cudaSuccess) return e;
   C.src = P.pair_src;
   C.dst = P.pair_dst;
   C.num_pairs = P.new_batch * P.spaces;
-  return launch_copies<COPY_SAFE>(C, C.num_pairs, sms, stream);
+  return small_plan(P) ? launch_plan(fork_plan_kernel<1>, sizes[0], P, C, FORK_PHASES, sms, stream)
+                       : launch_plan(fork_plan_kernel<4>, sizes[1], P, C, FORK_PHASES, sms, stream);
 }
 
 cudaError_t launch_compact(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream) {
   static int sizes[2][64] = {{0}, {0}};
-  const cudaError_t e = small_plan(P) ? launch_plan(compact_plan_kernel<1>, sizes[0], P, COMPACT_PHASES, sms, stream)
-                                      : launch_plan(compact_plan_kernel<4>, sizes[1], P, COMPACT_PHASES, sms, stream);
-  if (e != cudaSuccess) return e;
   C.src = P.pair_src;
   C.dst = P.pair_dst;
   C.num_pairs_dev = P.num_pairs;
   C.turn = P.turn;
-  return launch_copies<COPY_SAFE>(C, P.most_pairs, sms, stream);
+  return small_plan(P) ? launch_plan(compact_plan_kernel<1>, sizes[0], P, C, COMPACT_PHASES, sms, stream)
+                       : launch_plan(compact_plan_kernel<4>, sizes[1], P, C, COMPACT_PHASES, sms, stream);
 }
 
 }  // namespace kvq

@@ -198,10 +198,13 @@ constexpr int GATHER_TOKENS = 8;
 // Byte offset of (token t, kv head h)'s row in a pool, -1 (evicted or
 // invalid; invalid rows set their error bit), or -2 - r for row r of the
 // full-precision chunk.
-template <bool CHUNK>
+// GUESS: token t is first looked for in sequence t, where a decode step's one
+// token per sequence is, which saves the search's chain of loads.
+template <bool CHUNK, bool GUESS = false>
 __device__ __forceinline__ long long gather_row_offset(const WriteParams& P, int t, int h) {
   if (t >= P.num_tokens) return -1;
   int lo = 0, hi = P.batch - 1;  // the last sequence whose first token is <= t
+  if (GUESS && t < P.batch && __ldg(P.cu_new + t) <= t && t < __ldg(P.cu_new + t + 1)) lo = hi = t;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (__ldg(P.cu_new + mid) <= t) lo = mid;
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(256) write16_kernel(WriteParams P) {
   float x[2][8];
   load_row_elems<8>(P.k, F32 ? DT_F32 : DT_BF16, src, x[0]);
   load_row_elems<8>(P.v, F32 ? DT_F32 : DT_BF16, src, x[1]);
-  const long long off = gather_row_offset<false>(P, (int)t, h);
+  const long long off = gather_row_offset<false, true>(P, (int)t, h);
   if (off < 0) return;  // evicted or invalid: nothing is written
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {

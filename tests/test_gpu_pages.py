@@ -319,3 +319,36 @@ def test_a_search_over_both_kinds_of_layers(headwise):
         assert int((p.block_tables_headwise if headwise else p.block_tables).max()) < int(used.max())
         check()
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("n", [2048, 2049, 5000])
+def test_copy_pages_conflicts_of_long_lists(n):
+    """The same answers on both sides of the list length from which pages are claimed in scratch."""
+    K = kvq()
+    r = np.random.default_rng(n)
+    blocks = 6000
+    src, dst = r.integers(-1, blocks + 1, n), r.integers(-1, blocks + 1, n)
+    src[::3] = r.permutation(blocks)[:len(src[::3])]
+    cs = caches(blocks, 1, 16, ("INT2_TOKEN_HEAD", "INT4_TOKEN_HEAD"), (64, 64))
+    before, err = pools(cs), torch.zeros(1, dtype=torch.int32, device="cuda")
+    K.kvq_copy_pages(cs, i32(src), i32(dst), dev_error=err)
+    done, bits = ref.copy_pairs(src, dst, blocks)
+    assert len(done) > 100 and bits & ref.CONFLICT
+    same(pools(cs), apply(before, [(0, a, b) for a, b in done], False))
+    assert int(err.item()) == bits
+
+
+def test_copy_pages_of_small_and_large_pages_together():
+    """Caches whose pages differ in size, small (laid end to end) and large (in pieces), and 128 caches at once."""
+    K = kvq()
+    r = np.random.default_rng(0)
+    for Hkv, bs, modes, dims in [(1, 16, ("INT2_TOKEN_HEAD", "INT8_TOKEN_HEAD", "INT4_TOKEN_HEAD"), (64, 64, 128)),
+                                 (3, 64, ("INT2_TOKEN_HEAD", "BF16_CACHE", "INT8_TOKEN_HEAD"), (64, 128, 64)),
+                                 (1, 16, ("INT4_TOKEN_HEAD",) * 128, (64,) * 128)]:
+        for headwise in (False, True):
+            cs = caches(50, Hkv, bs, modes, dims)
+            order = r.permutation(50 * (Hkv if headwise else 1))
+            src, dst = order[:20], order[20:40]
+            before = pools(cs)
+            K.kvq_copy_pages(cs, i32(src), i32(dst), headwise=headwise)
+            same(pools(cs), _flat(before, list(zip(src, dst))) if headwise else apply(before, [(0, a, b) for a, b in zip(src, dst)], False))
