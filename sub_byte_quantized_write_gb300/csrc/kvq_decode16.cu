@@ -439,19 +439,35 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
   }
 }
 
+template <int N>
+__device__ __forceinline__ void load_dims(const float* p, float (&v)[N]) {  // through L2: other SMs wrote them
+  if constexpr (N == 4) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else if constexpr (N == 2) {
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+    v[0] = x.x; v[1] = x.y;
+  } else {
+    v[0] = __ldcg(p);
+  }
+}
+
 // Joins the records of one (sequence, q head): W warps each take every W-th
-// group of four records (running maximum, sum and output of their own, joined
-// through shared memory); lane l holds dims l * D / 32 ...  W = 1 when a pair
-// is cut into few records (eight heads to a CTA), 8 when into many: one
-// warp's chain of loads over hundreds of records took 90 us of a call over one
-// long sequence.
+// group of RPS records (running maximum, sum and output of their own, joined
+// through shared memory); lane l holds EPL dims.  W = 1 when a pair is cut into
+// few records (eight heads to a CTA), 8 or 32 when into many; with 32 each CTA
+// takes 32 dims only, so that a call over one long sequence has CTAs enough to
+// read its records at speed (one warp per head took 90 us over one sequence
+// of 131071 keys, one CTA of 32 warps per head 11).
 template <int D, int W>
 __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(const AttnParams P, const DecodeWs ws) {
-  constexpr int EPL = D / 32;
-  constexpr int RPS = 8;  // records per step
+  constexpr int EPL = W > 8 ? 1 : D / 32;
+  constexpr int CUTS = D / 32 / EPL;          // CTAs per head
+  constexpr int HEADS = W > 8 ? 1 : 8 / W;    // heads per CTA
+  constexpr int RPS = 8;                      // records per step
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
-  constexpr int HEADS = W > 8 ? 1 : 8 / W;  // per CTA
-  const long long wid = (long long)blockIdx.x * HEADS + warp / W;
+  const long long wid = (long long)(blockIdx.x / CUTS) * HEADS + warp / W;
+  const int d0 = (blockIdx.x % CUTS) * 32 * EPL + EPL * lane;  // the lane's first dim
   const int Hq = P.num_q_heads, G = P.group, Hkv = P.num_kv_heads;
   if (wid >= (long long)P.batch * Hq) return;  // (whole CTAs, for W > 1)
   const int b = (int)(wid / Hq), hq = (int)(wid % Hq), head = hq % G;
@@ -475,14 +491,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
       for (int u = 0; u < RPS; ++u) {  // the loads of a step in flight together
         const size_t rec = rec0 + (size_t)min(r0 + u, n - 1) * G;
         ml[u] = __ldcg(ws.part_ml + rec);
-        const float* po = ws.part_o + rec * D + EPL * lane;
-        if constexpr (EPL == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(po));
-          v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(po));
-          v[u][0] = x.x; v[u][1] = x.y;
-        }
+        load_dims<EPL>(ws.part_o + rec * D + d0, v[u]);
       }
       float mn = m;
 #pragma unroll
@@ -506,7 +515,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
     }
   }
   if constexpr (W > 1) {
-    __shared__ float sm_m[W], sm_l[W], sm_o[W][D];
+    __shared__ float sm_m[W], sm_l[W], sm_o[W][32 * EPL];
     if (lane == 0) {
       sm_m[part] = m;
       sm_l[part] = l;
@@ -529,10 +538,11 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
       for (int e = 0; e < EPL; ++e) o[e] = fmaf(x, sm_o[w][EPL * lane + e], o[e]);
     }
   }
-  float* out = P.out + (size_t)wid * D + EPL * lane;
+  float* out = P.out + (size_t)wid * D + d0;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   if constexpr (EPL == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-  else *reinterpret_cast<float2*>(out) = make_float2(o[0] * inv, o[1] * inv);
+  else if constexpr (EPL == 2) *reinterpret_cast<float2*>(out) = make_float2(o[0] * inv, o[1] * inv);
+  else *out = o[0] * inv;
 }
 
 size_t decode16_smem(int D, bool q32, bool direct, int group) {
@@ -579,7 +589,7 @@ cudaError_t launch_decode16_d(const AttnParams& P, const DecodeWs& ws, int grid,
   // a pair is cut into nwall / pairs records on average when the GPU is full
   const long long cuts = chunks < ws.nwall / pairs ? chunks : ws.nwall / pairs;
   if (cuts >= 8 * D16_WIDE_MERGE)
-    return launch_dependent(decode16_merge_kernel<D, 32>, dim3((unsigned)heads), dim3(1024), 0, stream, P, ws);
+    return launch_dependent(decode16_merge_kernel<D, 32>, dim3((unsigned)(heads * (D / 32))), dim3(1024), 0, stream, P, ws);
   if (cuts >= D16_WIDE_MERGE)
     return launch_dependent(decode16_merge_kernel<D, 8>, dim3((unsigned)heads), dim3(256), 0, stream, P, ws);
   return launch_dependent(decode16_merge_kernel<D, 1>, dim3((unsigned)((heads + 7) / 8)), dim3(256), 0, stream, P, ws);
