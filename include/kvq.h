@@ -370,7 +370,8 @@ kvq_status kvq_decode_attn_noalloc(const kvq_cache* cache, const kvq_paging* pag
  * past the pool is skipped and sets KVQ_DEVERR_BLOCK_RANGE.  Every source is
  * read as it was before the call: a pair whose destination is another pair's
  * source is skipped, and of several pairs with one destination the lowest is
- * done; the skipped ones set KVQ_DEVERR_PAGE_CONFLICT. */
+ * done; the skipped ones set KVQ_DEVERR_PAGE_CONFLICT.  Up to 2048 pairs need
+ * no workspace (size 0, NULL). */
 kvq_status kvq_copy_workspace_size(const kvq_cache* caches, int32_t num_caches, int32_t num_pairs, int32_t headwise,
                                    size_t* bytes);
 kvq_status kvq_copy_pages(const kvq_cache* caches, int32_t num_caches, const int32_t* src, const int32_t* dst,

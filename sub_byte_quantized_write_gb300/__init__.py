@@ -489,7 +489,7 @@ def _page_scratch(workspace, size, dev, stream, *args):
 
 
 def kvq_copy_workspace_size(caches: Caches, num_pairs: int, headwise: bool = False) -> int:
-    """Bytes of scratch that kvq_copy_pages needs."""
+    """Bytes of scratch that kvq_copy_pages needs (0 for short lists)."""
     cs, n, _, _, _ = _cache_array(caches)
     size = ctypes.c_size_t(0)
     _check(_lib.kvq_copy_workspace_size(cs, n, int(num_pairs), int(headwise), ctypes.byref(size)))
@@ -505,7 +505,9 @@ def kvq_copy_pages(caches: Caches, src: torch.Tensor, dst: torch.Tensor, headwis
     cs, n, dev, _, _ = _cache_array(caches)
     pairs = int(src.numel())
     ps, pd = _page_tensor(src, "src", dev), _page_tensor(dst, "dst", dev, pairs)
-    ws, nbytes, _keep = _page_scratch(workspace, kvq_copy_workspace_size, dev, stream, caches, pairs, headwise)
+    ws, nbytes = None, 0
+    if workspace is not None or kvq_copy_workspace_size(caches, pairs, headwise) > 0:  # short lists need none
+        ws, nbytes, _keep = _page_scratch(workspace, kvq_copy_workspace_size, dev, stream, caches, pairs, headwise)
     _run(dev, stream, _lib.kvq_copy_pages, cs, n, ps, pd, pairs, int(headwise), ws, nbytes,
          _page_tensor(dev_error, "dev_error", dev))
 

@@ -366,6 +366,8 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
   if (cache->mode == KVQ_BF16_CACHE) {
     if ((long long)cache->num_blocks * cache->num_kv_heads * (cache->block_size / 16) > 0x7FFFFFFFLL)
       return fail(KVQ_ERR_UNSUPPORTED, "pool too large for 32-bit chunk numbers");
+    if ((long long)paging->max_blocks * cache->block_size > 0x7FFFFFFFLL)
+      return fail(KVQ_ERR_UNSUPPORTED, "table too wide for 32-bit positions");
     if (fw.k) {  // 16-bit pages: the step's write is a launch of its own, which the decode's start overlaps
       const cudaError_t e = kvq::launch_write(
           write_params(cache, paging, fw.k, fw.v, fw.dtype, fw.cu_new, fw.num_tokens, dev_error),
@@ -748,7 +750,7 @@ kvq_status kvq_copy_workspace_size(const kvq_cache* caches, int32_t num_caches, 
   if (num_pairs < 0) return fail(KVQ_ERR_INVALID_ARG, "num_pairs < 0");
   if (too_many_pages(caches)) return fail(KVQ_ERR_UNSUPPORTED, "num_blocks * num_kv_heads too large");
   Carver w{nullptr};
-  w.ints((long long)caches->num_blocks * (headwise ? caches->num_kv_heads : 1));
+  if (num_pairs > kvq::PAGE_COPY_LISTED) w.ints((long long)caches->num_blocks * (headwise ? caches->num_kv_heads : 1));
   *bytes = w.used;
   return KVQ_OK;
 }
@@ -761,7 +763,7 @@ kvq_status kvq_copy_pages(const kvq_cache* caches, int32_t num_caches, const int
   if (st != KVQ_OK) return st;
   if (num_pairs == 0) return KVQ_OK;
   if (!src || !dst) return fail(KVQ_ERR_INVALID_ARG, "src / dst is NULL");
-  if ((st = check_scratch(workspace, workspace_bytes, need)) != KVQ_OK) return st;
+  if (need > 0 && (st = check_scratch(workspace, workspace_bytes, need)) != KVQ_OK) return st;
   kvq::PageCopy C = page_copy(caches, num_caches, headwise != 0, dev_error);
   C.src = src;
   C.dst = dst;

@@ -56,7 +56,7 @@ constexpr float D16_SLACK = 8.0f;  // log2 units a logit may pass the reference 
 
 __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {  // read once: not kept in L1
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;

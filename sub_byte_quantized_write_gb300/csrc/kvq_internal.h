@@ -140,7 +140,7 @@ struct PageCopy {
   int num_pairs;
   const int32_t* num_pairs_dev;     // the pairs' number on the device instead, where not NULL
   unsigned long long* turn;         // runs handed out beyond the first of each CTA, where not NULL
-  int32_t* claim;                   // [units] scratch of kvq_copy_pages
+  int32_t* claim;                   // [units] scratch of kvq_copy_pages for long lists
   int32_t* dev_error;
 };
 
@@ -179,7 +179,8 @@ struct PagePlan {
 constexpr int PAGE_TASK_UNITS = 1024;  // fewest pages a CTA ranks at a time: sizes task_count
 constexpr int PAGE_SEG = 256;          // entries of a table row a warp takes at a time
 
-constexpr int PAGE_COPY_PIECE = 4096;  // bytes of a page that a warp copies in one step, at most
+constexpr int PAGE_COPY_PIECE = 4096;   // bytes of a page that a warp copies in one step, at most
+constexpr int PAGE_COPY_LISTED = 2048;  // pairs up to which kvq_copy_pages needs no scratch
 
 cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream);
 cudaError_t launch_fork(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream);

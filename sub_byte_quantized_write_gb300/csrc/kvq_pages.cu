@@ -334,10 +334,13 @@ __device__ void fork_assign(const PagePlan& P) {
 constexpr int FORK_PHASES = 5;
 
 template <int ITEMS>
-__global__ void __launch_bounds__(PLAN_THREADS, 1) fork_plan_kernel(const PagePlan P, const PageCopy C, int first, int last) {
+__global__ void __launch_bounds__(PLAN_THREADS, 1) fork_plan_kernel(const PagePlan P, const PageCopy C, int first, int last, bool copies_follow) {
   __shared__ int sm[2][33];
   BlockScan scan{sm};
-  allow_dependent_launch();  // the copies may launch; they wait for this grid to finish
+  // The copies may launch; they wait for this grid to finish.  No other kernel
+  // may: the next one in the stream can be a decode, which reads the tables and
+  // lengths written here before it waits.
+  if (copies_follow) allow_dependent_launch();
   for (int phase = first; phase <= last; ++phase) {
     if (phase == 0) fork_init(P);
     else if (phase == 1) fork_mark(P);
@@ -511,10 +514,13 @@ __device__ void compact_remap(const PagePlan& P) {
 constexpr int COMPACT_PHASES = 6;
 
 template <int ITEMS>
-__global__ void __launch_bounds__(PLAN_THREADS, 1) compact_plan_kernel(const PagePlan P, const PageCopy C, int first, int last) {
+__global__ void __launch_bounds__(PLAN_THREADS, 1) compact_plan_kernel(const PagePlan P, const PageCopy C, int first, int last, bool copies_follow) {
   __shared__ int sm[2][33];
   BlockScan scan{sm};
-  allow_dependent_launch();  // the copies may launch; they wait for this grid to finish
+  // The copies may launch; they wait for this grid to finish.  No other kernel
+  // may: the next one in the stream can be a decode, which reads the tables and
+  // lengths written here before it waits.
+  if (copies_follow) allow_dependent_launch();
   for (int phase = first; phase <= last; ++phase) {
     if (phase == 0) compact_init(P);
     else if (phase == 1) compact_mark(P);
@@ -565,7 +571,6 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) copy_claim_kernel(const PageC
 // with the page's bytes laid end to end or pool by pool: 91 and 97 us instead
 // of 78 for 126,000 pages of 1152 bytes.)
 constexpr int COPY_RUN = 16;         // pieces per CTA and turn
-constexpr int COPY_LISTED = 2048;    // pairs a CTA compares with
 enum { COPY_SAFE, COPY_CLAIMED, COPY_CHECKS_LIST };
 
 template <int CHECK>
@@ -676,11 +681,11 @@ cudaError_t launch_plan(Kern kernel, int (&sizes)[64], const PagePlan& P, const 
   const long long work = (long long)P.spaces * P.num_blocks + rows * P.max_blocks;
   if (work <= PLAN_FUSED_WORK) {
     const bool copies = P.most_pairs * 2 * C.num_layers * C.most_bytes <= PLAN_COPIES;
-    const cudaError_t e = launch_cluster(kernel, sizes, stream, P, C, 0, copies ? phases : phases - 1);
+    const cudaError_t e = launch_cluster(kernel, sizes, stream, P, C, 0, copies ? phases : phases - 1, !copies);
     if (e != cudaSuccess || copies) return e;
   } else {
     for (int i = 0; i < phases; ++i) {
-      kernel<<<sms, PLAN_THREADS, 0, stream>>>(P, C, i, i);
+      kernel<<<sms, PLAN_THREADS, 0, stream>>>(P, C, i, i, i == phases - 1 && P.most_pairs > 0);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }
@@ -691,7 +696,7 @@ cudaError_t launch_plan(Kern kernel, int (&sizes)[64], const PagePlan& P, const 
 }  // namespace
 
 cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream) {
-  if (C.num_pairs <= COPY_LISTED) return launch_copies<COPY_CHECKS_LIST>(C, C.num_pairs, sms, stream);
+  if (C.num_pairs <= PAGE_COPY_LISTED) return launch_copies<COPY_CHECKS_LIST>(C, C.num_pairs, sms, stream);
   static int sizes[64] = {0};
   const cudaError_t e = launch_cluster(copy_claim_kernel, sizes, stream, C);
   if (e != cudaSuccess) return e;

@@ -29,6 +29,9 @@ def test_refusals(K):  # noqa: F811
     assert L.kvq_decode_attn(ref(c), ref(_paging(K)), 256, 1, 18, 0.1, 256, 256, 1 << 30, 0, None, None) == K.KVQ_ERR_UNSUPPORTED
     big = _cache(K, mode=K.KVQ_BF16_CACHE, num_blocks=0x7FFFFFFF, num_kv_heads=2)
     assert L.kvq_decode_attn(ref(big), ref(_paging(K)), 256, 1, 8, 0.1, 256, 256, 1 << 30, 0, None, None) == K.KVQ_ERR_UNSUPPORTED
+    wide = _paging(K, max_blocks=0x7FFFFFF)
+    c64 = _cache(K, mode=K.KVQ_BF16_CACHE, block_size=64)
+    assert L.kvq_decode_attn(ref(c64), ref(wide), 256, 1, 8, 0.1, 256, 256, 1 << 30, 0, None, None) == K.KVQ_ERR_UNSUPPORTED
     assert L.kvq_write_decode_attn(ref(c), ref(_paging(K)), None, 4096, 1, 4096, 2, 256, 1, 8, 0.1, 256, 256, 1 << 30, 0,
                                    None, None) == K.KVQ_ERR_INVALID_ARG
 

@@ -352,3 +352,56 @@ def test_copy_pages_of_small_and_large_pages_together():
             before = pools(cs)
             K.kvq_copy_pages(cs, i32(src), i32(dst), headwise=headwise)
             same(pools(cs), _flat(before, list(zip(src, dst))) if headwise else apply(before, [(0, a, b) for a, b in zip(src, dst)], False))
+
+
+def test_pages_past_four_gigabytes():
+    K = kvq()
+    blocks, Hkv, bs, D = 150000, 8, 16, 128     # 4.9 GB a pool
+    shape = (blocks, Hkv, bs, 2 * D)
+    c = K.PagedCache(K.KVQ_BF16_CACHE, blocks, Hkv, bs, D, k_pages=torch.empty(shape, dtype=torch.uint8, device="cuda"),
+                     v_pages=torch.empty(shape, dtype=torch.uint8, device="cuda"))
+    for n, p in enumerate((c.k_pages, c.v_pages)):
+        for i in (3, 149998):
+            p[i] = torch.randint(0, 256, p[i].shape, dtype=torch.uint8, device="cuda")
+    k, v = c.k_pages[149998].clone(), c.v_pages[3].clone()
+    K.kvq_copy_pages(c, i32([149998, 3]), i32([7, 149999]))
+    assert torch.equal(c.k_pages[7], k) and torch.equal(c.v_pages[149999], v)
+    # two rows that end in page 149998, and their compaction to pages 0 and 1
+    p = paging([[[149998]], [[149998]]], [9, 9], False)
+    out, _ = K.kvq_fork(c, p, i32([1, 0]))
+    assert out.block_tables.cpu().tolist() == [[149998], [0]]
+    assert torch.equal(c.k_pages[0], k)
+    out, _, _, used = K.kvq_compact(c, out)
+    assert out.block_tables.cpu().tolist() == [[1], [0]] and used.item() == 2
+    assert torch.equal(c.k_pages[1], k)
+
+
+@pytest.mark.parametrize("big", [False, True])
+def test_decode_right_behind_a_fork_and_a_compaction(big):
+    """No wait, no other kernel between: the decode starts from the tables and lengths that the call before writes."""
+    K = kvq()
+    Hkv, G, D, bs, width = 2, 4, 128, 16, 9
+    n = 40 if big else 4
+    cs = caches(2000 if big else 60, Hkv, bs, ("BF16_CACHE",) * 3, (D,) * 3)
+    full = cs[0]
+    lens = np.array([100 + 3 * (i % 9) for i in range(n)])
+    k = torch.randn((2, int(lens.sum()), Hkv, D), device="cuda").bfloat16()
+    p = paging(np.full((n, 1, width), -1), np.zeros(n), False)
+    p, _ = K.kvq_fork(cs, p, i32([-1] * n), new_tokens=i32(lens))
+    K.kvq_write(full, p, k[0], k[1], i32(np.concatenate([[0], np.cumsum(lens)])))
+    parents = np.arange(n)[::-1] // 2
+    start = np.concatenate([[0], np.cumsum(lens)])
+    hist = [k[:, start[b]:start[b + 1]] for b in parents]
+    q = torch.randn((n, Hkv * G, D), device="cuda").bfloat16()
+    par = i32(parents)
+    new = paging(np.full((n, 1, width), 7), np.full(n, 5), False)     # wrong until the fork has run
+    torch.cuda.synchronize()
+    K.kvq_fork(cs, p, par, out=new)
+    outs = [K.kvq_decode_attn(full, new, q, D ** -0.5)]
+    K.kvq_compact(cs, new, out=new)
+    outs.append(K.kvq_decode_attn(full, new, q, D ** -0.5))
+    c = dict(k=torch.cat([h[0] for h in hist]), v=torch.cat([h[1] for h in hist]), q=q, lens=lens[parents], D=D, G=G, bs=bs,
+             Hkv=Hkv, window=None, sink=0, scale=D ** -0.5, table=new.block_tables.cpu().numpy().reshape(n, 1, width))
+    want = decode16_ref.attention64(c)
+    for o in outs:
+        decode16_ref.check(o, want)

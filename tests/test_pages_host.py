@@ -14,8 +14,9 @@ def arr(K, *cs):  # noqa: F811
 def test_workspace_sizes(K):  # noqa: F811
     L, ref, n = K.lib(), ctypes.byref, ctypes.c_size_t(0)
     cs = arr(K, _cache(K), _cache(K, mode=K.KVQ_BF16_CACHE, head_dim=64))
-    assert L.kvq_copy_workspace_size(cs, 2, 5, 0, ref(n)) == K.KVQ_OK and n.value >= 40
-    assert L.kvq_copy_workspace_size(cs, 2, 5, 1, ref(n)) == K.KVQ_OK and n.value >= 80
+    assert L.kvq_copy_workspace_size(cs, 2, 2048, 0, ref(n)) == K.KVQ_OK and n.value == 0
+    assert L.kvq_copy_workspace_size(cs, 2, 2049, 0, ref(n)) == K.KVQ_OK and n.value >= 40
+    assert L.kvq_copy_workspace_size(cs, 2, 2049, 1, ref(n)) == K.KVQ_OK and n.value >= 80
     assert L.kvq_fork_workspace_size(cs, 2, ref(_paging(K)), ref(_paging(K, batch=7)), ref(n)) == K.KVQ_OK and n.value > 0
     assert L.kvq_fork_workspace_size(cs, 2, None, ref(_paging(K, batch=7)), ref(n)) == K.KVQ_OK
     assert L.kvq_compact_workspace_size(cs, 2, ref(_paging(K)), ref(n)) == K.KVQ_OK and n.value > 0
@@ -37,9 +38,9 @@ def test_copy_refusals(K):  # noqa: F811
     L, cs = K.lib(), arr(K, _cache(K))
     assert L.kvq_copy_pages(cs, 1, 4096, None, 3, 0, 4096, 1 << 20, None, None) == K.KVQ_ERR_INVALID_ARG
     assert L.kvq_copy_pages(cs, 1, 4096, 8192, -1, 0, 4096, 1 << 20, None, None) == K.KVQ_ERR_INVALID_ARG
-    assert L.kvq_copy_pages(cs, 1, 4096, 8192, 3, 0, 4096, 16, None, None) == K.KVQ_ERR_WORKSPACE
-    assert L.kvq_copy_pages(cs, 1, 4096, 8192, 3, 0, None, 0, None, None) == K.KVQ_ERR_WORKSPACE
-    assert L.kvq_copy_pages(cs, 1, 4096, 8192, 3, 0, 4100, 1 << 20, None, None) == K.KVQ_ERR_INVALID_ARG
+    assert L.kvq_copy_pages(cs, 1, 4096, 8192, 3000, 0, 4096, 16, None, None) == K.KVQ_ERR_WORKSPACE
+    assert L.kvq_copy_pages(cs, 1, 4096, 8192, 3000, 0, None, 0, None, None) == K.KVQ_ERR_WORKSPACE
+    assert L.kvq_copy_pages(cs, 1, 4096, 8192, 3000, 0, 4100, 1 << 20, None, None) == K.KVQ_ERR_INVALID_ARG
     assert L.kvq_copy_pages(cs, 1, None, None, 0, 0, None, 0, None, None) == K.KVQ_OK   # nothing to do
 
 
