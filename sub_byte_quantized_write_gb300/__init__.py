@@ -278,15 +278,41 @@ class Paging:
                          self.sink_size)
 
 
+def _check_rows(cache: PagedCache, t: torch.Tensor, name: str) -> None:
+    """t is [tokens, num_kv_heads, head_dim] of the cache's device."""
+    if t.dim() != 3 or t.shape[1] != cache.num_kv_heads or t.shape[2] != cache.head_dim:
+        raise ValueError("%s must be [tokens, %d, %d], got %s" % (name, cache.num_kv_heads, cache.head_dim,
+                                                                  tuple(t.shape)))
+    if t.get_device() != cache.k_pages.get_device():
+        raise ValueError("%s must be on the cache's device" % name)
+
+
+def _check_cu(cu: torch.Tensor, batch: int, name: str) -> None:
+    if cu.numel() != batch + 1:
+        raise ValueError("%s must have batch + 1 = %d elements, got %d" % (name, batch + 1, cu.numel()))
+
+
+def _check_q(cache: PagedCache, batch: int, q: torch.Tensor, out: Optional[torch.Tensor]) -> None:
+    """q is [batch, num_q_heads, head_dim] of the cache's device, and out, if given, as large."""
+    if q.dim() != 3 or q.shape[0] != batch or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [%d, num_q_heads, %d], got %s" % (batch, cache.head_dim, tuple(q.shape)))
+    if q.get_device() != cache.k_pages.get_device():
+        raise ValueError("q must be on the cache's device")
+    if out is not None and out.numel() != q.numel():
+        raise ValueError("out must be as large as q")
+
+
 def kvq_write(cache: PagedCache, paging: Paging, k: torch.Tensor, v: torch.Tensor,
               cu_new_tokens: torch.Tensor, dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
-    """Quantise k, v [num_tokens, num_kv_heads, head_dim] and scatter them into the pages."""
+    """Quantise k, v [num_tokens, num_kv_heads, head_dim] and scatter them into the pages (16-bit caches: as bf16)."""
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and dtype")
     cs, ps = cache.struct(), paging.struct()
-    _run(cache.k_pages.device, stream, _lib.kvq_write, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
-                          _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]),
-                          _dev_ptr(dev_error, torch.int32, "dev_error"))
+    _check_rows(cache, k, "k")
+    _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
+    _run(cache.k_pages.device, stream, _lib.kvq_write, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"),
+         _dev_ptr(v, name="v"), _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]),
+         _dev_ptr(dev_error, torch.int32, "dev_error"))
 
 
 def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_tokens: int,
@@ -307,19 +333,25 @@ def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_t
     if k_out.dtype != v_out.dtype:
         raise ValueError("k_out and v_out must have the same dtype")
     cs, ps = cache.struct(), paging.struct()
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _check_rows(cache, t, name)
+        if t.shape[0] < num_tokens:
+            raise ValueError("%s has fewer than num_tokens rows" % name)
+    _check_cu(cu_tokens, ps.batch, "cu_tokens")
     if k_chunk is None:
-        _run(cache.k_pages.device, stream, _lib.kvq_gather, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(cu_tokens, torch.int32, "cu_tokens"),
-                               int(num_tokens), _dev_ptr(k_out, name="k_out"), _dev_ptr(v_out, name="v_out"),
-                               _qdtype(k_out), _dev_ptr(dev_error, torch.int32, "dev_error"))
+        _run(dev, stream, _lib.kvq_gather, ctypes.byref(cs), ctypes.byref(ps),
+             _dev_ptr(cu_tokens, torch.int32, "cu_tokens"), int(num_tokens), _dev_ptr(k_out, name="k_out"),
+             _dev_ptr(v_out, name="v_out"), _qdtype(k_out), _dev_ptr(dev_error, torch.int32, "dev_error"))
     else:
-        if v_chunk is None or k_chunk.dtype != v_chunk.dtype:
-            raise ValueError("k_chunk and v_chunk must be given together, with one dtype")
-        _run(cache.k_pages.device, stream, _lib.kvq_gather_chunk, ctypes.byref(cs), ctypes.byref(ps),
-                                     _dev_ptr(cu_tokens, torch.int32, "cu_tokens"), int(num_tokens),
-                                     _dev_ptr(k_chunk, name="k_chunk"), _dev_ptr(v_chunk, name="v_chunk"),
-                                     _qdtype(k_chunk), _dev_ptr(cu_chunk, torch.int32, "cu_chunk"),
-                                     _dev_ptr(k_out, name="k_out"), _dev_ptr(v_out, name="v_out"), _qdtype(k_out),
-                                     _dev_ptr(dev_error, torch.int32, "dev_error"))
+        if v_chunk is None or k_chunk.dtype != v_chunk.dtype or k_chunk.shape != v_chunk.shape:
+            raise ValueError("k_chunk and v_chunk must be given together, with one dtype and shape")
+        _check_rows(cache, k_chunk, "k_chunk")
+        _check_cu(cu_chunk, ps.batch, "cu_chunk")
+        _run(dev, stream, _lib.kvq_gather_chunk, ctypes.byref(cs), ctypes.byref(ps),
+             _dev_ptr(cu_tokens, torch.int32, "cu_tokens"), int(num_tokens), _dev_ptr(k_chunk, name="k_chunk"),
+             _dev_ptr(v_chunk, name="v_chunk"), _qdtype(k_chunk), _dev_ptr(cu_chunk, torch.int32, "cu_chunk"),
+             _dev_ptr(k_out, name="k_out"), _dev_ptr(v_out, name="v_out"), _qdtype(k_out),
+             _dev_ptr(dev_error, torch.int32, "dev_error"))
     return k_out, v_out
 
 
@@ -343,9 +375,11 @@ def kvq_decode_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, softmax_
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
         workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
+    _check_q(cache, ps.batch, q, out)
     _run(cache.k_pages.device, stream, _lib.kvq_decode_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"),
-         _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"), _dev_ptr(workspace, name="workspace"),
-         workspace.numel() * workspace.element_size(), num_splits, _dev_ptr(dev_error, torch.int32, "dev_error"))
+         _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"),
+         _dev_ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(), num_splits,
+         _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
 
 
@@ -365,11 +399,14 @@ def kvq_write_decode_attn(cache: PagedCache, paging: Paging, k: torch.Tensor, v:
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
         workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _run(cache.k_pages.device, stream, _lib.kvq_write_decode_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
-                                      _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"),
-                                      int(k.shape[0]), _dev_ptr(q, name="q"), _qdtype(q), Hq, float(softmax_scale),
-                                      _dev_ptr(out, torch.float32, "out"), _dev_ptr(workspace, torch.uint8, "workspace"),
-                                      workspace.numel(), int(num_splits), _dev_ptr(dev_error, torch.int32, "dev_error"))
+    _check_rows(cache, k, "k")
+    _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
+    _check_q(cache, ps.batch, q, out)
+    _run(cache.k_pages.device, stream, _lib.kvq_write_decode_attn, ctypes.byref(cs), ctypes.byref(ps),
+         _dev_ptr(k, name="k"), _dev_ptr(v, name="v"), _qdtype(k),
+         _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]), _dev_ptr(q, name="q"), _qdtype(q), Hq,
+         float(softmax_scale), _dev_ptr(out, torch.float32, "out"), _dev_ptr(workspace, torch.uint8, "workspace"),
+         workspace.numel(), int(num_splits), _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
 
 
@@ -385,9 +422,10 @@ def kvq_decode_attn_noalloc(cache: PagedCache, paging: Paging, q: torch.Tensor, 
     if out is None:
         out = _empty((B, Hq, D), torch.float32, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _run(cache.k_pages.device, stream, _lib.kvq_decode_attn_noalloc, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
-                                        float(softmax_scale), _dev_ptr(out, torch.float32, "out"), num_splits,
-                                        _dev_ptr(dev_error, torch.int32, "dev_error"))
+    _check_q(cache, ps.batch, q, out)
+    _run(cache.k_pages.device, stream, _lib.kvq_decode_attn_noalloc, ctypes.byref(cs), ctypes.byref(ps),
+         _dev_ptr(q, name="q"), _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"), num_splits,
+         _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
 
 
@@ -399,9 +437,9 @@ def kvq_prefill_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, cu_q: t
     if out is None:
         out = _empty((T, Hq, D), torch.float32, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _run(cache.k_pages.device, stream, _lib.kvq_prefill_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
-                                 _dev_ptr(cu_q, torch.int32, "cu_q"), T, int(max_q_per_seq), float(softmax_scale),
-                                 _dev_ptr(out, torch.float32, "out"), _dev_ptr(dev_error, torch.int32, "dev_error"))
+    _run(cache.k_pages.device, stream, _lib.kvq_prefill_attn, ctypes.byref(cs), ctypes.byref(ps),
+         _dev_ptr(q, name="q"), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q"), T, int(max_q_per_seq),
+         float(softmax_scale), _dev_ptr(out, torch.float32, "out"), _dev_ptr(dev_error, torch.int32, "dev_error"))
     return out
 
 
@@ -600,6 +638,6 @@ def kvq_compact(caches: Caches, paging: Paging, pins: Optional[torch.Tensor] = N
     ws, nbytes, _keep = _page_scratch(workspace, kvq_compact_workspace_size, dev, stream, caches, paging)
     _run(dev, stream, _lib.kvq_compact, cs, n, ctypes.byref(old), _page_tensor(pins, "pins", dev, spaces * blocks),
          _page_tensor(to, "out", dev), _page_tensor(page_map, "page_map", dev, spaces * blocks),
-         _page_tensor(page_refs, "page_refs", dev, spaces * blocks), _page_tensor(num_used, "num_used", dev, spaces), ws,
-         nbytes, _page_tensor(dev_error, "dev_error", dev))
+         _page_tensor(page_refs, "page_refs", dev, spaces * blocks), _page_tensor(num_used, "num_used", dev, spaces),
+         ws, nbytes, _page_tensor(dev_error, "dev_error", dev))
     return out, page_map, page_refs, num_used

@@ -368,6 +368,8 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
       return fail(KVQ_ERR_UNSUPPORTED, "pool too large for 32-bit chunk numbers");
     if ((long long)paging->max_blocks * cache->block_size > 0x7FFFFFFFLL)
       return fail(KVQ_ERR_UNSUPPORTED, "table too wide for 32-bit positions");
+    if ((long long)paging->batch * cache->num_kv_heads * paging->max_blocks > 0x7FFFFFFFLL / (cache->block_size / 16))
+      return fail(KVQ_ERR_UNSUPPORTED, "batch * num_kv_heads * table width too large");
     if (fw.k) {  // 16-bit pages: the step's write is a launch of its own, which the decode's start overlaps
       const cudaError_t e = kvq::launch_write(
           write_params(cache, paging, fw.k, fw.v, fw.dtype, fw.cu_new, fw.num_tokens, dev_error),
@@ -628,10 +630,9 @@ kvq::PageCopy page_copy(const kvq_cache* c, int32_t n, bool headwise, int32_t* d
   return p;
 }
 
-// Row segments are counted in 32 bits.
+// Table entries, and with them the pages that all rows ask for, are counted in 32 bits.
 bool too_many_rows(const kvq::PagePlan& P) {
-  const long long rows = (long long)std::max(P.batch, P.new_batch) * P.spaces;
-  return rows * (((long long)P.max_blocks + kvq::PAGE_SEG - 1) / kvq::PAGE_SEG) > INT_MAX / 2;
+  return (long long)std::max(P.batch, P.new_batch) * P.spaces * P.max_blocks > INT_MAX - kvq::PAGE_SEG;
 }
 
 bool too_many_pages(const kvq_cache* c) { return (long long)c->num_blocks * c->num_kv_heads > INT_MAX / 2; }

@@ -34,8 +34,17 @@
 //    outputs are rescaled) only when a logit passes it by 2^8, so most chunks
 //    take one vote and no reduction.  Weights up to 2^8 lose nothing in fp32
 //    or bf16, whose exponents have the range.
+//    Sums of one chunk are joined to the running ones in fp32: carried in the
+//    instructions' accumulators, which truncate, they were off by 3e-6 to 6e-6
+//    of the output over slices of 64 to 160 chunks, now 4e-7.
 //  * Masked keys: the logit is replaced by -inf and the value row by zeros,
 //    since a stale slot may hold a NaN, which a zero weight would not cancel.
+// Measured (one GB300, 6792 GB/s a plain copy's): 64 sequences of 1024 .. 8192
+// keys, 8 kv heads, 1.21 GB: 184 us a call, 6.6 TB/s (the stream kernel 177 to
+// 181 us; 21% of the issue slots, 18% of the tensor pipe busy); 32 sequences of
+// 32768 with windows, 2.42 GB: 350 us, 6.9 TB/s; one sequence of 131071 keys,
+// 4 kv heads: 50 us, 5.3 TB/s (its start and the merge of 1824 records are 10 us
+// of it).  12 warps of 168 registers keep 96 KB per SM in flight.
 
 #include <math_constants.h>
 

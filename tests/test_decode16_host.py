@@ -32,6 +32,8 @@ def test_refusals(K):  # noqa: F811
     wide = _paging(K, max_blocks=0x7FFFFFF)
     c64 = _cache(K, mode=K.KVQ_BF16_CACHE, block_size=64)
     assert L.kvq_decode_attn(ref(c64), ref(wide), 256, 1, 8, 0.1, 256, 256, 1 << 30, 0, None, None) == K.KVQ_ERR_UNSUPPORTED
+    many = _paging(K, batch=60000, max_blocks=20000)
+    assert L.kvq_decode_attn(ref(c), ref(many), 256, 1, 8, 0.1, 256, 256, 1 << 40, 0, None, None) == K.KVQ_ERR_UNSUPPORTED
     assert L.kvq_write_decode_attn(ref(c), ref(_paging(K)), None, 4096, 1, 4096, 2, 256, 1, 8, 0.1, 256, 256, 1 << 30, 0,
                                    None, None) == K.KVQ_ERR_INVALID_ARG
 

@@ -213,3 +213,22 @@ def test_low_bit_decode_with_more_splits_than_tiles(mode):
     write_step(c)
     q = q_host(wl)
     assert max_err(decode_gpu(c, q, num_splits=100000), decode_oracle(c, q)) <= ATOL
+
+
+def test_binding_refuses_tensors_of_other_shapes():
+    K = kvq()
+    c = ref.make(2, 2, 4, 128, 16, [20, 3], seed=1)
+    bad = [c["q"][:1], c["q"][:, :, :64].contiguous(), c["q"][0], c["q"].cpu()]
+    for q in bad:
+        with pytest.raises(ValueError):
+            K.kvq_decode_attn(c["cache"], c["pag"], q, 0.1)
+    with pytest.raises(ValueError):
+        K.kvq_decode_attn(c["cache"], c["pag"], c["q"], 0.1, out=torch.empty(2, 7, 128, device="cuda"))
+    for k in (c["k"][:, :1].contiguous(), c["k"][:, :, :64].contiguous()):
+        with pytest.raises(ValueError):
+            K.kvq_write(c["cache"], c["pag"], k, k, c["cu"])
+    with pytest.raises(ValueError):
+        K.kvq_write(c["cache"], c["pag"], c["k"], c["v"], c["cu"][:2].contiguous())
+    with pytest.raises(ValueError):
+        K.kvq_gather(c["cache"], c["pag"], c["cu"], 23, k_out=torch.empty(22, 2, 128, device="cuda"))
+    K.kvq_decode_attn(c["cache"], c["pag"], c["q"], c["scale"])

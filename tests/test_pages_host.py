@@ -67,6 +67,7 @@ def test_fork_refusals(K):  # noqa: F811
                dict(seq_lens=1 << 20), dict(seq_lens=(2 << 20) + 4)):
         assert _fork(K, cs, old, new(**kw)) == bad, kw
         assert b"overlap" in K.lib().kvq_last_error()
+    assert _fork(K, cs, None, new(batch=65535, max_blocks=40000)) == K.KVQ_ERR_UNSUPPORTED
     assert _fork(K, cs, old, new(), pins=2 << 20) == bad
     assert _fork(K, cs, old, new(), more=2 << 20) == bad
 
