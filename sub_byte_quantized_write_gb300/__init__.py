@@ -161,8 +161,8 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
 def _run(device: torch.device, stream, fn, *args) -> None:
     """fn(*args, stream) with `device` current."""
     index = device.index
-    if index is None or index == torch.cuda.current_device():
-        status = fn(*args, _stream_ptr(stream))
+    if index == torch.cuda.current_device():
+        status = fn(*args, _current_raw_stream(index) if stream is None else _stream_ptr(stream))
     else:
         with torch.cuda.device(device):
             status = fn(*args, _stream_ptr(stream))
@@ -193,7 +193,8 @@ def _kept_struct(handle, tensors):
                 break
         else:
             return kept[1]
-    kept = ([(t, t.data_ptr()) for t in tensors(handle) if t is not None], handle._build())
+    given = [t for t in tensors(handle) if t is not None]
+    kept = ([(t, t.data_ptr()) for t in given], handle._build(), {t.device for t in given})
     handle.__dict__["_struct"] = kept
     return kept[1]
 
@@ -292,10 +293,11 @@ def _check_cu(cu: torch.Tensor, batch: int, name: str) -> None:
         raise ValueError("%s must have batch + 1 = %d elements, got %d" % (name, batch + 1, cu.numel()))
 
 
-def _check_q(cache: PagedCache, batch: int, q: torch.Tensor, out: Optional[torch.Tensor]) -> None:
+def _check_q(cache: PagedCache, ps: KvqPaging, q: torch.Tensor, out: Optional[torch.Tensor]) -> None:
     """q is [batch, num_q_heads, head_dim] of the cache's device, and out, if given, as large."""
-    if q.dim() != 3 or q.shape[0] != batch or q.shape[2] != cache.head_dim:
-        raise ValueError("q must be [%d, num_q_heads, %d], got %s" % (batch, cache.head_dim, tuple(q.shape)))
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != ps.batch or shape[2] != cache.head_dim:
+        raise ValueError("q must be [%d, num_q_heads, %d], got %s" % (ps.batch, cache.head_dim, tuple(shape)))
     if q.get_device() != cache.k_pages.get_device():
         raise ValueError("q must be on the cache's device")
     if out is not None and out.numel() != q.numel():
@@ -369,13 +371,14 @@ def kvq_decode_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, softmax_
                     num_splits: int = 0, dev_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Decode attention of q [batch, num_q_heads, head_dim]; returns fp32 out."""
     B, Hq, D = q.shape
+    given = out
     if out is None:
         out = _empty((B, Hq, D), torch.float32, q.device, stream)
     if workspace is None:
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
         workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _check_q(cache, ps.batch, q, out)
+    _check_q(cache, ps, q, given)
     _run(cache.k_pages.device, stream, _lib.kvq_decode_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"),
          _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"),
          _dev_ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(), num_splits,
@@ -393,6 +396,7 @@ def kvq_write_decode_attn(cache: PagedCache, paging: Paging, k: torch.Tensor, v:
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and dtype")
     B, Hq, D = q.shape
+    given = out
     if out is None:
         out = _empty((B, Hq, D), torch.float32, q.device, stream)
     if workspace is None:
@@ -401,7 +405,7 @@ def kvq_write_decode_attn(cache: PagedCache, paging: Paging, k: torch.Tensor, v:
     cs, ps = cache.struct(), paging.struct()
     _check_rows(cache, k, "k")
     _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
-    _check_q(cache, ps.batch, q, out)
+    _check_q(cache, ps, q, given)
     _run(cache.k_pages.device, stream, _lib.kvq_write_decode_attn, ctypes.byref(cs), ctypes.byref(ps),
          _dev_ptr(k, name="k"), _dev_ptr(v, name="v"), _qdtype(k),
          _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]), _dev_ptr(q, name="q"), _qdtype(q), Hq,
@@ -419,10 +423,11 @@ def kvq_decode_attn_noalloc(cache: PagedCache, paging: Paging, q: torch.Tensor, 
     overlap on the GPU race on it, so serialise them.  The first call on a
     device must come before any stream capture."""
     B, Hq, D = q.shape
+    given = out
     if out is None:
         out = _empty((B, Hq, D), torch.float32, q.device, stream)
     cs, ps = cache.struct(), paging.struct()
-    _check_q(cache, ps.batch, q, out)
+    _check_q(cache, ps, q, given)
     _run(cache.k_pages.device, stream, _lib.kvq_decode_attn_noalloc, ctypes.byref(cs), ctypes.byref(ps),
          _dev_ptr(q, name="q"), _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"), num_splits,
          _dev_ptr(dev_error, torch.int32, "dev_error"))
@@ -509,9 +514,11 @@ def _page_paging(p: "Paging", name: str, dev: torch.device, num_kv_heads: int) -
     """(struct, head-wise, rows) of a paging state of the caches' device."""
     headwise = p.block_tables_headwise is not None
     t = p.block_tables_headwise if headwise else p.block_tables
-    if t is None or t.device != dev or p.seq_lens.get_device() != t.get_device():
-        raise ValueError("%s needs a block table and lengths on the caches' device" % name)
+    if t is None:
+        raise ValueError("%s needs a block table" % name)
     struct = p.struct()
+    if p._struct[2] != {dev}:
+        raise ValueError("%s must be on the caches' device" % name)
     rows = struct.batch
     if len(t) != (rows * num_kv_heads if headwise else rows):
         raise ValueError("%s: the table's rows do not match seq_lens" % name)
