@@ -183,20 +183,23 @@ def _set_and_forget(self, name, value):
     self.__dict__["_struct"] = None
 
 
+class _Kept:
+    """What a handle's C struct was made of, and the struct.  (Compared by identity.)"""
+    __slots__ = ("tensors", "pointers", "struct", "devices")
+
+    def __init__(self, tensors, struct):
+        self.tensors, self.struct = tensors, struct
+        self.pointers = [t.data_ptr() for t in tensors]
+        self.devices = {t.device for t in tensors}
+
+
 def _kept_struct(handle, tensors):
     """A handle's C struct, rebuilt (with its checks) unless the tensors it was made of are where they were.  (Give a
     handle other tensors by setting its attributes, not by resizing the ones it has.)"""
     kept = handle._struct
-    if kept is not None:
-        for t, pointer in kept[0]:
-            if t.data_ptr() != pointer:
-                break
-        else:
-            return kept[1]
-    given = [t for t in tensors(handle) if t is not None]
-    kept = ([(t, t.data_ptr()) for t in given], handle._build(), {t.device for t in given})
-    handle.__dict__["_struct"] = kept
-    return kept[1]
+    if kept is None or [t.data_ptr() for t in kept.tensors] != kept.pointers:
+        kept = handle.__dict__["_struct"] = _Kept([t for t in tensors(handle) if t is not None], handle._build())
+    return kept.struct
 
 
 def _cache_tensors(c):
@@ -216,23 +219,24 @@ class PagedCache:
     def __init__(self, mode: int, num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int,
                  rht_signs: Optional[torch.Tensor] = None, device="cuda", k_pages=None, v_pages=None,
                  ch_amax=None, ch_amax_ready=None):
-        self.mode, self.num_blocks, self.num_kv_heads = mode, num_blocks, num_kv_heads
-        self.block_size, self.head_dim = block_size, head_dim
-        self.row_bytes = kvq_row_bytes(mode, head_dim)
-        if self.row_bytes == 0:
+        row_bytes = kvq_row_bytes(mode, head_dim)
+        if row_bytes == 0:
             raise ValueError("unsupported mode/head_dim")
-        shape = (num_blocks, num_kv_heads, block_size, self.row_bytes)
-        self.k_pages = k_pages if k_pages is not None else torch.zeros(shape, dtype=torch.uint8, device=device)
-        self.v_pages = v_pages if v_pages is not None else torch.zeros(shape, dtype=torch.uint8, device=device)
-        self.rht_signs = rht_signs
-        if mode == KVQ_INT8_CHANNEL:
-            self.ch_amax = ch_amax if ch_amax is not None else torch.zeros(
-                (2, num_kv_heads, head_dim), dtype=torch.float32, device=device)
-            self.ch_amax_ready = ch_amax_ready if ch_amax_ready is not None else torch.zeros(
-                1, dtype=torch.int32, device=device)
+        shape = (num_blocks, num_kv_heads, block_size, row_bytes)
+        if k_pages is None:
+            k_pages = torch.zeros(shape, dtype=torch.uint8, device=device)
+        if v_pages is None:
+            v_pages = torch.zeros(shape, dtype=torch.uint8, device=device)
+        if mode != KVQ_INT8_CHANNEL:
+            ch_amax = ch_amax_ready = None
         else:
-            self.ch_amax = None
-            self.ch_amax_ready = None
+            if ch_amax is None:
+                ch_amax = torch.zeros((2, num_kv_heads, head_dim), dtype=torch.float32, device=device)
+            if ch_amax_ready is None:
+                ch_amax_ready = torch.zeros(1, dtype=torch.int32, device=device)
+        self.__dict__.update(mode=mode, num_blocks=num_blocks, num_kv_heads=num_kv_heads, block_size=block_size,
+                             head_dim=head_dim, row_bytes=row_bytes, k_pages=k_pages, v_pages=v_pages,
+                             rht_signs=rht_signs, ch_amax=ch_amax, ch_amax_ready=ch_amax_ready, _struct=None)
 
     __setattr__ = _set_and_forget
 
@@ -241,6 +245,9 @@ class PagedCache:
         return _kept_struct(self, _cache_tensors)
 
     def _build(self) -> KvqCache:
+        need = self.num_blocks * self.num_kv_heads * self.block_size * self.row_bytes
+        if self.k_pages.numel() < need or self.v_pages.numel() < need:
+            raise ValueError("k_pages / v_pages hold fewer than num_blocks blocks")
         return KvqCache(_dev_ptr(self.k_pages, torch.uint8, "k_pages"), _dev_ptr(self.v_pages, torch.uint8, "v_pages"),
                         self.num_blocks, self.num_kv_heads, self.block_size, self.head_dim, self.mode,
                         _dev_ptr(self.rht_signs, torch.int8, "rht_signs"),
@@ -256,13 +263,10 @@ class Paging:
     def __init__(self, seq_lens: torch.Tensor, block_tables: Optional[torch.Tensor] = None,
                  block_tables_headwise: Optional[torch.Tensor] = None,
                  window_per_kv_head: Optional[torch.Tensor] = None, sink_size: int = 0):
-        self.seq_lens = seq_lens
-        self.block_tables = block_tables
-        self.block_tables_headwise = block_tables_headwise
-        self.window_per_kv_head = window_per_kv_head
-        self.sink_size = int(sink_size)
         t = block_tables if block_tables is not None else block_tables_headwise
-        self.max_blocks = 0 if t is None else int(t.shape[1])
+        self.__dict__.update(seq_lens=seq_lens, block_tables=block_tables,
+                             block_tables_headwise=block_tables_headwise, window_per_kv_head=window_per_kv_head,
+                             sink_size=int(sink_size), max_blocks=0 if t is None else int(t.shape[1]), _struct=None)
 
     __setattr__ = _set_and_forget
 
@@ -271,6 +275,9 @@ class Paging:
         return _kept_struct(self, _paging_tensors)
 
     def _build(self) -> KvqPaging:
+        for t in (self.block_tables, self.block_tables_headwise):
+            if t is not None and t.shape[0] < self.seq_lens.shape[0]:
+                raise ValueError("the block table has fewer rows than seq_lens")
         return KvqPaging(_dev_ptr(self.block_tables, torch.int32, "block_tables"),
                          _dev_ptr(self.block_tables_headwise, torch.int32, "block_tables_headwise"),
                          self.max_blocks, int(self.seq_lens.shape[0]),
@@ -485,16 +492,19 @@ def _cache_array(caches: Caches):
     cs = (caches,) if isinstance(caches, PagedCache) else caches
     if not cs:
         raise ValueError("no caches")
-    structs = [c.struct() for c in cs]
     first = cs[0].__dict__
     kept = first.get("_group")
-    if kept is None or kept[0] != structs:
-        dev = cs[0].k_pages.device
-        if any(c.k_pages.device != dev for c in cs):
-            raise ValueError("the caches of one call must be on one device")
-        array = (KvqCache * len(cs))(*structs)
-        kept = first["_group"] = (structs, (array, len(cs), dev, array[0].num_kv_heads, array[0].num_blocks))
-    return kept[1]
+    if kept is not None and [c._struct for c in cs] == kept[0] and [t.data_ptr() for t in kept[1]] == kept[2]:
+        return kept[3]
+    structs = [c.struct() for c in cs]
+    dev = cs[0].k_pages.device
+    if any(c._struct.devices != {dev} for c in cs):
+        raise ValueError("the caches of one call must be on one device")
+    tensors = [t for c in cs for t in c._struct.tensors]
+    array = (KvqCache * len(cs))(*structs)
+    first["_group"] = ([c._struct for c in cs], tensors, [t.data_ptr() for t in tensors],
+                       (array, len(cs), dev, array[0].num_kv_heads, array[0].num_blocks))
+    return first["_group"][3]
 
 
 def _page_tensor(t: Optional[torch.Tensor], name: str, dev: torch.device, numel: Optional[int] = None):
@@ -517,7 +527,7 @@ def _page_paging(p: "Paging", name: str, dev: torch.device, num_kv_heads: int) -
     if t is None:
         raise ValueError("%s needs a block table" % name)
     struct = p.struct()
-    if p._struct[2] != {dev}:
+    if p._struct.devices != {dev}:
         raise ValueError("%s must be on the caches' device" % name)
     rows = struct.batch
     if len(t) != (rows * num_kv_heads if headwise else rows):
