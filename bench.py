@@ -550,7 +550,8 @@ def run_gpu(args, rank, world, local_rank):
         cfg["decode_workers"] = st["splits"]
         achieved = units["decode"] / (att / 1e3) / 1e9
         traffic = recorded_units("decode_stream_%s.md" % args.workload, "dram_bytes_per_decode_call",
-                                 kernel_source_hash(("kvq_decode.cu", "kvq_common.cuh", "kvq_internal.h", "kvq_api.cu")))
+                                 kernel_source_hash(("kvq_decode.cu", "kvq_decode.cuh", "kvq_common.cuh", "kvq_internal.h",
+                                                     "kvq_api.cu")))
         roof = {"bound": "hbm", "kernel": "decode attention (query prep + stream-K split-KV + merge, "
                                           "one kvq_decode_attn call)",
                 "achieved": round(achieved, 1), "peak": hbm, "peak_kind": peak_kind + " (copy bandwidth)",
