@@ -84,7 +84,8 @@ typedef enum {
  *   rounded to nearest even, saturating at 448); s = 0 gives zero codes;
  *   value code * s.
  * BF16_CACHE: nothing is quantised: the row's values as bf16 (fp32 input
- *   rounds to nearest even), no RHT.  For layers kept in full precision next
+ *   rounds to nearest even; what rounds past the largest bf16 becomes
+ *   infinite), no RHT.  For layers kept in full precision next
  *   to quantised ones.  kvq_write, kvq_gather(_chunk), the decode calls and
  *   the page calls take it; kvq_prefill_attn does not (gather the pages and
  *   call kvq_prefill_dense_attn). */
