@@ -17,6 +17,7 @@ that device's current stream; what it allocates belongs to that stream.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 from typing import Optional, Sequence, Tuple, Union
 
@@ -178,17 +179,30 @@ def _qdtype(t: torch.Tensor) -> int:
     raise ValueError("q/k/v must be float32 or bfloat16")
 
 
-def _set_and_forget(self, name, value):
-    self.__dict__[name] = value
-    self.__dict__["_struct"] = None
+class _Handle:
+    """Holds tensors and, in `_struct`, the C struct made of them; setting an attribute drops the struct, and copies
+    and pickles leave it out."""
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__["_struct"] = None
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("_struct", "_group")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state, _struct=None)
+
+
+_serial = itertools.count()
 
 
 class _Kept:
-    """What a handle's C struct was made of, and the struct.  (Compared by identity.)"""
-    __slots__ = ("tensors", "pointers", "struct", "devices")
+    """What a handle's C struct was made of, the struct, and a number of its own."""
+    __slots__ = ("tensors", "pointers", "struct", "devices", "serial")
 
     def __init__(self, tensors, struct):
-        self.tensors, self.struct = tensors, struct
+        self.tensors, self.struct, self.serial = tensors, struct, next(_serial)
         self.pointers = [t.data_ptr() for t in tensors]
         self.devices = {t.device for t in tensors}
 
@@ -210,7 +224,7 @@ def _paging_tensors(p):
     return p.seq_lens, p.block_tables, p.block_tables_headwise, p.window_per_kv_head
 
 
-class PagedCache:
+class PagedCache(_Handle):
     """One layer's paged cache: uint8 K and V pools of shape
     [num_blocks, num_kv_heads, block_size, row_bytes] (allocated here, as
     torch.uint8, unless given), the RHT sign vector and, for INT8, the
@@ -238,8 +252,6 @@ class PagedCache:
                              head_dim=head_dim, row_bytes=row_bytes, k_pages=k_pages, v_pages=v_pages,
                              rht_signs=rht_signs, ch_amax=ch_amax, ch_amax_ready=ch_amax_ready, _struct=None)
 
-    __setattr__ = _set_and_forget
-
     def struct(self) -> KvqCache:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
         return _kept_struct(self, _cache_tensors)
@@ -255,7 +267,7 @@ class PagedCache:
                         _dev_ptr(self.ch_amax_ready, torch.int32, "ch_amax_ready"))
 
 
-class Paging:
+class Paging(_Handle):
     """Block table (uniform [batch, max_blocks] or head-wise
     [batch * num_kv_heads, max_blocks], int32, -1 = evicted), seq_lens [batch]
     and the optional per-kv-head sliding window plus sink size."""
@@ -267,8 +279,6 @@ class Paging:
         self.__dict__.update(seq_lens=seq_lens, block_tables=block_tables,
                              block_tables_headwise=block_tables_headwise, window_per_kv_head=window_per_kv_head,
                              sink_size=int(sink_size), max_blocks=0 if t is None else int(t.shape[1]), _struct=None)
-
-    __setattr__ = _set_and_forget
 
     def struct(self) -> KvqPaging:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
@@ -488,23 +498,25 @@ Caches = Union[PagedCache, Sequence[PagedCache]]
 
 def _cache_array(caches: Caches):
     """(ctypes array, number, device, num_kv_heads, num_blocks) of the caches that share page numbers; kept with the
-    first cache as long as the caches' structs are the same."""
+    first cache as long as the caches' structs are the same (by their numbers and pointers: nothing here keeps another
+    cache's memory alive)."""
     cs = (caches,) if isinstance(caches, PagedCache) else caches
     if not cs:
         raise ValueError("no caches")
     first = cs[0].__dict__
-    kept = first.get("_group")
-    if kept is not None and [c._struct for c in cs] == kept[0] and [t.data_ptr() for t in kept[1]] == kept[2]:
-        return kept[3]
-    structs = [c.struct() for c in cs]
+    group = first.get("_group")
+    structs = [c._struct for c in cs]
+    if (group is not None and None not in structs and [k.serial for k in structs] == group[0]
+            and [t.data_ptr() for k in structs for t in k.tensors] == group[1]):
+        return group[2]
     dev = cs[0].k_pages.device
-    if any(c._struct.devices != {dev} for c in cs):
+    array = (KvqCache * len(cs))(*[c.struct() for c in cs])
+    structs = [c._struct for c in cs]
+    if any(k.devices != {dev} for k in structs):
         raise ValueError("the caches of one call must be on one device")
-    tensors = [t for c in cs for t in c._struct.tensors]
-    array = (KvqCache * len(cs))(*structs)
-    first["_group"] = ([c._struct for c in cs], tensors, [t.data_ptr() for t in tensors],
-                       (array, len(cs), dev, array[0].num_kv_heads, array[0].num_blocks))
-    return first["_group"][3]
+    first["_group"] = group = ([k.serial for k in structs], [p for k in structs for p in k.pointers],
+                               (array, len(cs), dev, array[0].num_kv_heads, array[0].num_blocks))
+    return group[2]
 
 
 def _page_tensor(t: Optional[torch.Tensor], name: str, dev: torch.device, numel: Optional[int] = None):

@@ -405,3 +405,19 @@ def test_decode_right_behind_a_fork_and_a_compaction(big):
     want = decode16_ref.attention64(c)
     for o in outs:
         decode16_ref.check(o, want)
+
+
+def test_a_call_keeps_no_other_cache_alive():
+    import weakref
+    K = kvq()
+    cs = caches(8, 1, 16)
+    K.kvq_copy_pages(cs, i32([1]), i32([2]))
+    gone = weakref.ref(cs[1].k_pages)
+    del cs[1:]
+    assert gone() is None
+    # and a changed handle is seen
+    new = torch.zeros_like(cs[0].k_pages)
+    new[1] = 7
+    cs[0].k_pages = new
+    K.kvq_copy_pages(cs, i32([1]), i32([2]))
+    assert bool((new[2] == 7).all())

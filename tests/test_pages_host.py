@@ -1,5 +1,7 @@
 """Host-side checks of the page calls: sizes and refusals, before anything is launched."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -109,3 +111,15 @@ def test_python_refusals(K):  # noqa: F811
     assert old.struct() is first
     old.k_pages = torch.zeros_like(old.k_pages)
     assert old.struct().k_pages == old.k_pages.data_ptr()
+
+
+def test_handles_copy_and_pickle(K):  # noqa: F811
+    c = K.PagedCache(K.KVQ_BF16_CACHE, 3, 2, 16, 64, device="cpu")
+    c._build = lambda: K.KvqCache(c.k_pages.data_ptr())
+    c.struct()
+    del c.__dict__["_build"]
+    c.k_pages[1] = 5
+    for d in (copy.copy(c), copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
+        assert d.num_blocks == 3 and torch.equal(d.k_pages, c.k_pages) and d._struct is None
+    p = copy.deepcopy(K.Paging(torch.zeros(2, dtype=torch.int32), block_tables=torch.zeros((2, 3), dtype=torch.int32)))
+    assert p.max_blocks == 3 and p.block_tables.shape == (2, 3)
