@@ -1572,7 +1572,7 @@ DecodeShape decode_shape_dnt(int mode) {
 }
 
 DecodeShape decode_shape(int mode, int head_dim, int group) {
-  if (mode == MODE_DBF16) return decode16_shape();
+  if (mode == MODE_DBF16) return decode16_shape(head_dim);
   if (head_dim == 64) return group > 4 ? decode_shape_dnt<64, 2>(mode) : decode_shape_dnt<64, 1>(mode);
   return group > 4 ? decode_shape_dnt<128, 2>(mode) : decode_shape_dnt<128, 1>(mode);
 }

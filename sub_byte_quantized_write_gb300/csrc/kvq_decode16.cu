@@ -44,7 +44,11 @@
 // 181 us; 21% of the issue slots, 18% of the tensor pipe busy); 32 sequences of
 // 32768 with windows, 2.42 GB: 350 us, 6.9 TB/s; one sequence of 131071 keys,
 // 4 kv heads: 50 us, 5.3 TB/s (its start and the merge of 1824 records are 10 us
-// of it).  12 warps of 168 registers keep 96 KB per SM in flight.
+// of it).  12 warps of 168 registers keep 96 KB per SM in flight; 13 and 14,
+// which spill, take 229 and 235 us.  At D = 64 a warp has half as much in
+// flight: 16 warps of 125 registers read 0.60 GB (the first case's lengths) in
+// 99 us against 103 with 12 and 141 with 24, 8 sequences of 65536 in 164 against
+// 174 us (6.5 TB/s).
 
 #include <math_constants.h>
 
@@ -56,7 +60,8 @@ namespace kvq {
 namespace {
 
 constexpr int D16_KEYS = 16;       // keys per chunk
-constexpr int D16_WARPS = 12;      // per CTA, one CTA per SM
+// Warps per CTA, one CTA per SM: as many as 64 K registers hold without spills.
+__host__ __device__ constexpr int d16_warps(int head_dim) { return head_dim == 128 ? 12 : 16; }
 constexpr int D16_RUNS = 2048;     // entries of the prefix sums over the pairs
 constexpr int D16_MIN_CHUNKS = 1;  // per warp, at least
 constexpr int D16_WIDE_MERGE = 16;  // records per pair from which a CTA joins one head
@@ -127,8 +132,8 @@ struct Chunk {
 // and written out: no records, no prefix sums and no second launch, for calls
 // of few and short sequences.
 template <int D, bool Q32, bool DIRECT>
-__global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnParams P, const DecodeWs ws) {
-  constexpr int NT = D16_WARPS * 32;
+__global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const AttnParams P, const DecodeWs ws) {
+  constexpr int WARPS = d16_warps(D), NT = WARPS * 32;
   constexpr int JK = D / 32;  // 16-byte pieces of a key row per lane
   constexpr int JV = D / 64;  // 16-byte pieces of a value row per lane
   constexpr int ROW = 2 * D;  // bytes
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
   // warps' outputs [warp][G][D], maxima and sums [warp][8]
   extern __shared__ __align__(16) uint8_t qsm[];
   __shared__ int run_start[DIRECT ? 1 : D16_RUNS + 1];
-  __shared__ int wtot[D16_WARPS];
+  __shared__ int wtot[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = P.group, Hkv = P.num_kv_heads, bs = P.block_size, BH = P.batch * Hkv;
@@ -144,8 +149,8 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
   int lo, hi, gw = 0, items = 1, nruns = 1;
   if constexpr (DIRECT) {
     const TileList t = tile_list(P, blockIdx.x / Hkv, blockIdx.x % Hkv, threadIdx.x == 0 && blockIdx.x % Hkv == 0, D16_KEYS);
-    lo = slice_lo(warp, t.n_virt, D16_WARPS);
-    hi = slice_lo(warp + 1, t.n_virt, D16_WARPS);
+    lo = slice_lo(warp, t.n_virt, WARPS);
+    hi = slice_lo(warp + 1, t.n_virt, WARPS);
   } else {
     allow_dependent_launch();  // the merge kernel may launch; it waits for this grid to finish
 
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
       __syncthreads();
     }
     const int T = run_start[nruns];
-    const int nw = stream_workers(T, gridDim.x * D16_WARPS, ws.fixed_workers, D16_MIN_CHUNKS);
+    const int nw = stream_workers(T, gridDim.x * WARPS, ws.fixed_workers, D16_MIN_CHUNKS);
     gw = warp * gridDim.x + blockIdx.x;  // few slices: spread over the SMs
     if (gw >= nw) return;  // whole warp; no CTA-wide barrier follows
     lo = slice_lo(gw, T, nw);
@@ -284,8 +289,8 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
     m[0] = m[1] = -CUDART_INF_F;
     l[0] = l[1] = 0.0f;
   };
-  float* osm = reinterpret_cast<float*>(qsm + (Q32 ? (size_t)D16_WARPS * 3 * JK * 512 : 0));
-  float2* mlsm = reinterpret_cast<float2*>(osm + (size_t)D16_WARPS * G * D);
+  float* osm = reinterpret_cast<float*>(qsm + (Q32 ? (size_t)WARPS * 3 * JK * 512 : 0));
+  float2* mlsm = reinterpret_cast<float2*>(osm + (size_t)WARPS * G * D);
   // The record of (worker gw, pair bh), or the warp's share in shared memory.
   auto end_pair = [&](int bh) {
     const int rec = DIRECT ? warp : gw + bh;
@@ -427,11 +432,11 @@ __global__ void __launch_bounds__(D16_WARPS * 32, 1) decode16_kernel(const AttnP
       const int head = i / (D / 4), d = 4 * (i % (D / 4));
       float M = -CUDART_INF_F;
 #pragma unroll
-      for (int w = 0; w < D16_WARPS; ++w) M = fmaxf(M, mlsm[w * G + head].x);
+      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mlsm[w * G + head].x);
       float sum = 0.0f;
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < D16_WARPS; ++w) {
+      for (int w = 0; w < WARPS; ++w) {
         const float2 ml = mlsm[w * G + head];
         const float f = ml.x == -CUDART_INF_F ? 0.0f : ex2(ml.x - M);
         const float4 x = *reinterpret_cast<const float4*>(osm + (size_t)(w * G + head) * D + d);
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
 }
 
 size_t decode16_smem(int D, bool q32, bool direct, int group) {
-  return (q32 ? (size_t)D16_WARPS * 3 * (D / 32) * 512 : 0) + (direct ? (size_t)D16_WARPS * group * (D * 4 + 8) : 0);
+  return (q32 ? (size_t)d16_warps(D) * 3 * (D / 32) * 512 : 0) + (direct ? (size_t)d16_warps(D) * group * (D * 4 + 8) : 0);
 }
 
 template <int D, bool Q32, bool DIRECT>
@@ -574,7 +579,7 @@ cudaError_t launch_decode16_t(const AttnParams& P, const DecodeWs& ws, int grid,
       if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
   }
-  return launch_dependent(decode16_kernel<D, Q32, DIRECT>, dim3(grid), dim3(D16_WARPS * 32),
+  return launch_dependent(decode16_kernel<D, Q32, DIRECT>, dim3(grid), dim3(d16_warps(D) * 32),
                           decode16_smem(D, Q32, DIRECT, P.group), stream, P, ws);
 }
 
@@ -587,7 +592,7 @@ cudaError_t launch_decode16_d(const AttnParams& P, const DecodeWs& ws, int grid,
   // with its second launch six (66 sequences of 2 keys, 264 pairs: 8.4 us).
   // What the host knows of the lengths is the table's width.
   const long long chunks = (long long)P.max_blocks * (P.block_size / D16_KEYS);  // of a pair, at most
-  const long long waves = (pairs + grid - 1) / grid, per_warp = (chunks + D16_WARPS - 1) / D16_WARPS;
+  const long long waves = (pairs + grid - 1) / grid, per_warp = (chunks + d16_warps(D) - 1) / d16_warps(D);
   if (ws.fixed_workers == 0 && waves * (2 + per_warp) <= D16_DIRECT_COST)
     return f32 ? launch_decode16_t<D, true, true>(P, ws, pairs, stream)
                : launch_decode16_t<D, false, true>(P, ws, pairs, stream);
@@ -606,7 +611,7 @@ cudaError_t launch_decode16_d(const AttnParams& P, const DecodeWs& ws, int grid,
 
 }  // namespace
 
-DecodeShape decode16_shape() { return {1, D16_WARPS}; }
+DecodeShape decode16_shape(int head_dim) { return {1, d16_warps(head_dim)}; }
 
 cudaError_t launch_decode16(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
   return P.head_dim == 128 ? launch_decode16_d<128>(P, ws, grid, stream) : launch_decode16_d<64>(P, ws, grid, stream);

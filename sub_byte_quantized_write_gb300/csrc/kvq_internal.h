@@ -198,7 +198,7 @@ cudaError_t launch_gather(const WriteParams& P, cudaStream_t stream);
 cudaError_t launch_decode(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream);
 // the decode over 16-bit pages (kvq_decode16.cu), which launch_decode and
 // decode_shape hand to
-DecodeShape decode16_shape();
+DecodeShape decode16_shape(int head_dim);
 cudaError_t launch_decode16(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream);
 cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream);
 

@@ -14,7 +14,9 @@
 // destination) pairs: bound by memory.  Where they can be no more than
 // PLAN_COPIES bytes they are the cluster's last phase instead: 3 us less of the
 // host's time per call against 1 us more on the GPU (four beams: 20.3 and 11.3
-// against 23.5 and 10.7 us).
+// against 23.5 and 10.7 us).  The border between the two forms of the plan: a
+// fork over 93 thousand pages and entries takes 18.9 us in a cluster and 20.5
+// in launches, over 233 thousand 29 and 20.
 //
 // What bounds the plan is its chain of loads: per phase one or two trips to L2
 // and the barrier's flush (1.2 thousand cycles of 2 to 5 thousand, by clock
@@ -37,7 +39,7 @@ namespace {
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_CLUSTER = 8;
-constexpr long long PLAN_FUSED_WORK = 1 << 20;  // pages and table entries
+constexpr long long PLAN_FUSED_WORK = 1 << 17;  // pages and table entries
 constexpr long long PLAN_COPIES = 2 << 20;      // bytes of page copies that the plan's CTAs do themselves
 // A task, the pages that a CTA ranks at a time, has ITEMS consecutive pages per
 // thread: one (coalesced; every CTA of the cluster busy) up to PLAN_SMALL
@@ -583,15 +585,22 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) copy_claim_kernel(const PageC
 // cache, which leave most of a warp's loads empty: a step over several pools,
 // with the page's bytes laid end to end or pool by pool: 91 and 97 us instead
 // of 78 for 126,000 pages of 1152 bytes.)
-constexpr int COPY_RUN = 16;         // pieces per CTA and turn
+// Where a pair has fewer steps than a run (few layers, small pages) a run spans
+// several pairs, each warp looking up its own (ONE_PAIR false): 660 thousand
+// pages of 320 bytes in one layer, 630 us instead of 2030.  Not so for short
+// lists: checked by warps, 468 pages of one layer took 7.5 us instead of 4.8.
+constexpr int COPY_RUN = 16;  // copy steps per CTA and turn; twice that over several pairs
 enum { COPY_SAFE, COPY_CLAIMED, COPY_CHECKS_LIST };
 
-template <int CHECK>
+template <int CHECK, bool ONE_PAIR>
 __global__ void __launch_bounds__(256) copy_pages_kernel(const PageCopy P) {
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (CHECK != COPY_CHECKS_LIST) grid_dependency_wait();  // the pairs come from the kernel before
   const long long pairs = P.num_pairs_dev ? __ldcg(P.num_pairs_dev) : P.num_pairs;
-  const int per_pair = 2 * P.num_layers * P.pieces, runs = (per_pair + P.run - 1) / P.run;
+  const int per_pair = 2 * P.num_layers * P.pieces;
+  // runs: of each pair, or of all pairs' steps end to end
+  const int runs_pp = (per_pair + P.run - 1) / P.run;
+  const long long steps = pairs * per_pair, runs = ONE_PAIR ? pairs * runs_pp : (steps + P.run - 1) / P.run;
   __shared__ unsigned long long turn[2];
   int phase = 0;
   auto next = [&](long long w) -> long long {  // the CTA's next run
@@ -601,31 +610,45 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const PageCopy P) {
     phase ^= 1;
     return (long long)turn[phase ^ 1];
   };
-  for (long long w = blockIdx.x; w < pairs * runs; w = next(w)) {
-    const long long i = w / runs;
-    const int first = (int)(w % runs) * P.run;
-    const int s = __ldcg(P.src + i), d = __ldcg(P.dst + i);
-    if (s < 0 || d < 0 || s == d) continue;
-    if (s >= P.units || d >= P.units) {
-      if (first == 0 && threadIdx.x == 0) flag_error(P.dev_error, DEVERR_BLOCK_RANGE);
-      continue;
-    }
-    bool conflict = false;  // read by another pair, or written by a lower one
-    if (CHECK == COPY_CLAIMED) conflict = __ldcg(P.claim + d) != (int)i;
-    if (CHECK == COPY_CHECKS_LIST) {
-      int hit = 0;
-      for (int j = threadIdx.x; j < P.num_pairs; j += 256) {
-        const int a = __ldg(P.src + j), b = __ldg(P.dst + j);
-        hit |= a >= 0 && b >= 0 && a < P.units && b < P.units && (a == d || (b == d && a != b && j < i));
+  for (long long w = blockIdx.x; w < runs; w = next(w)) {
+    const long long first = ONE_PAIR ? w / runs_pp * per_pair + w % runs_pp * P.run : w * P.run;
+    const long long last = ONE_PAIR ? min(first + P.run, (w / runs_pp + 1) * per_pair) : min(first + P.run, steps);
+    long long i = -1;
+    int s = -1, d = -1;
+    bool go = false;
+    auto look_up = [&](long long pair) {  // by the CTA (ONE_PAIR) or the warp
+      i = pair;
+      s = __ldcg(P.src + i);
+      d = __ldcg(P.dst + i);
+      go = s >= 0 && d >= 0 && s != d;
+      if (!go) return;
+      const bool reports = lane == 0 && (ONE_PAIR ? first == i * per_pair && warp == 0 : true);
+      if (s >= P.units || d >= P.units) {
+        if (reports) flag_error(P.dev_error, DEVERR_BLOCK_RANGE);
+        go = false;
+        return;
       }
-      conflict = __syncthreads_or(hit);
+      bool conflict = false;
+      if (CHECK == COPY_CLAIMED) conflict = __ldcg(P.claim + d) != (int)i;
+      if (CHECK == COPY_CHECKS_LIST) {
+        static_assert(CHECK != COPY_CHECKS_LIST || ONE_PAIR, "the CTA compares its one pair with the list");
+        int hit = 0;  // read by another pair, or written by a lower one
+        for (int j = threadIdx.x; j < P.num_pairs; j += 256) {
+          const int a = __ldg(P.src + j), b = __ldg(P.dst + j);
+          hit |= a >= 0 && b >= 0 && a < P.units && b < P.units && (a == d || (b == d && a != b && j < i));
+        }
+        conflict = __syncthreads_or(hit);
+      }
+      if (conflict) {
+        if (reports) flag_error(P.dev_error, DEVERR_PAGE_CONFLICT);
+        go = false;
+      }
+    };
+    if (ONE_PAIR) look_up(w / runs_pp);
+    for (long long item = first + warp; item < last; item += 8) {
+      if (!ONE_PAIR && item / per_pair != i) look_up(item / per_pair);
+      if (go) copy_piece<COPY_PIECE / 512>(P, s, d, (int)(item - i * per_pair));
     }
-    if (conflict) {
-      if (first == 0 && threadIdx.x == 0) flag_error(P.dev_error, DEVERR_PAGE_CONFLICT);
-      continue;
-    }
-    for (int item = first + warp; item < min(first + P.run, per_pair); item += 8)
-      copy_piece<COPY_PIECE / 512>(P, s, d, item);
   }
 }
 
@@ -672,18 +695,22 @@ template <int CHECK>
 cudaError_t launch_copies(PageCopy C, long long most_pairs, int sms, cudaStream_t stream) {
   const long long per_pair = 2LL * C.num_layers * C.pieces;
   const long long resident = (long long)sms * 4;
-  // long runs when there are pairs enough to fill the GPU with them, else one piece per warp
-  C.run = most_pairs * (per_pair / COPY_RUN) >= resident ? COPY_RUN : 8;
-  const long long ctas = most_pairs * ((per_pair + C.run - 1) / C.run);
+  // long runs when there are steps enough to fill the GPU with them, else one step per warp
+  C.run = most_pairs * per_pair < resident * COPY_RUN ? 8 : per_pair < COPY_RUN ? 2 * COPY_RUN : COPY_RUN;
+  const bool one_pair = CHECK == COPY_CHECKS_LIST || per_pair >= C.run;
+  const long long ctas =
+      one_pair ? most_pairs * ((per_pair + C.run - 1) / C.run) : (most_pairs * per_pair + C.run - 1) / C.run;
   if (ctas == 0) return cudaSuccess;
   // one CTA per run where the host knows their number, else as many as fit,
   // which take their runs in turn
   const dim3 grid((unsigned)(ctas < resident || (!C.turn && ctas <= INT_MAX) ? ctas : resident));
-  if (CHECK == COPY_CHECKS_LIST) {  // nothing before it to overlap with
-    copy_pages_kernel<CHECK><<<grid, 256, 0, stream>>>(C);
+  if constexpr (CHECK == COPY_CHECKS_LIST) {  // nothing before it to overlap with
+    copy_pages_kernel<CHECK, true><<<grid, 256, 0, stream>>>(C);
     return cudaGetLastError();
+  } else {
+    return one_pair ? launch_dependent(copy_pages_kernel<CHECK, true>, grid, dim3(256), 0, stream, C)
+                    : launch_dependent(copy_pages_kernel<CHECK, false>, grid, dim3(256), 0, stream, C);
   }
-  return launch_dependent(copy_pages_kernel<CHECK>, grid, dim3(256), 0, stream, C);
 }
 
 // The phases of a plan and the copies: in one launch, in two, or, for large

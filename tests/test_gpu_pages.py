@@ -105,7 +105,8 @@ def test_copy_pages_conflicts(seed):
     blocks = 40
     n = int(r.integers(1, 60))
     src, dst = r.integers(-2, blocks + 3, n), r.integers(-2, blocks + 3, n)
-    cs = caches(blocks, 2, 16, seed=seed)
+    layers = 1 if seed % 2 else 3   # runs of copy steps that span pairs, or stay within one
+    cs = caches(blocks, 2, 16, ("INT4_TOKEN_HEAD", "BF16_CACHE", "INT2_TOKEN_HEAD") * layers, (64, 128, 64) * layers, seed=seed)
     before, err = pools(cs), torch.zeros(1, dtype=torch.int32, device="cuda")
     ws = torch.full((K.kvq_copy_workspace_size(cs, n),), 0x5A, dtype=torch.uint8, device="cuda")
     K.kvq_copy_pages(cs, i32(src), i32(dst), workspace=ws, dev_error=err)
@@ -200,7 +201,7 @@ def test_compact(shape, seed, inplace):
 
 
 def test_fork_and_compact_of_a_large_pool():
-    """1.2 million pages: past what one cluster plans, every phase a launch of its own."""
+    """1.2 million pages: past what one cluster plans, every phase is a launch of its own."""
     K = kvq()
     nb, bs, width = 1200000, 16, 500
     cs = [K.PagedCache(K.KVQ_INT2_TOKEN_HEAD, nb, 1, bs, 64)]
@@ -329,7 +330,8 @@ def test_copy_pages_conflicts_of_long_lists(n):
     blocks = 6000
     src, dst = r.integers(-1, blocks + 1, n), r.integers(-1, blocks + 1, n)
     src[::3] = r.permutation(blocks)[:len(src[::3])]
-    cs = caches(blocks, 1, 16, ("INT2_TOKEN_HEAD", "INT4_TOKEN_HEAD"), (64, 64))
+    layers = 10 if n == 5000 else 2
+    cs = caches(blocks, 1, 16, ("INT2_TOKEN_HEAD", "INT4_TOKEN_HEAD") * (layers // 2), (64, 64) * (layers // 2))
     before, err = pools(cs), torch.zeros(1, dtype=torch.int32, device="cuda")
     K.kvq_copy_pages(cs, i32(src), i32(dst), dev_error=err)
     done, bits = ref.copy_pairs(src, dst, blocks)
