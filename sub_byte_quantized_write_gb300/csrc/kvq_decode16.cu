@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
   constexpr int JV = D / 64;  // 16-byte pieces of a value row per lane
   constexpr int ROW = 2 * D;  // bytes
   // Q32: the q terms, [warp][3][JK][32 lanes][16 bytes]; DIRECT: then the
-  // warps' outputs [warp][G][D], maxima and sums [warp][8]
+  // warps' outputs [warp][G][D], maxima and sums [warp][G]
   extern __shared__ __align__(16) uint8_t qsm[];
   __shared__ int run_start[DIRECT ? 1 : D16_RUNS + 1];
   __shared__ int wtot[WARPS];
@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
   const int bs_log2 = __ffs(bs) - 1;
   int lo, hi, gw = 0, items = 1, nruns = 1;
   if constexpr (DIRECT) {
-    const TileList t = tile_list(P, blockIdx.x / Hkv, blockIdx.x % Hkv, threadIdx.x == 0 && blockIdx.x % Hkv == 0, D16_KEYS);
+    const bool reports = threadIdx.x == 0 && blockIdx.x % Hkv == 0;
+    const TileList t = tile_list(P, blockIdx.x / Hkv, blockIdx.x % Hkv, reports, D16_KEYS);
     lo = slice_lo(warp, t.n_virt, WARPS);
     hi = slice_lo(warp + 1, t.n_virt, WARPS);
   } else {
@@ -195,12 +196,13 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
   }
 
   int err = 0;
-  auto look_up = [&](int x) -> Chunk {  // of global chunk x; lanes at or past hi get nothing
+  auto look_up = [&](int at) -> Chunk {  // of chunk `at` of the slice; lanes past its end get nothing
     Chunk r;
     r.bh = -1;
     r.row = -1;
     r.mask = 0;
-    if (x >= hi) return r;
+    if (at >= hi - lo) return r;
+    const int x = lo + at;
     int bh = blockIdx.x, start = 0;
     if constexpr (!DIRECT) {
       int a = 0, z = nruns;
@@ -252,7 +254,8 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
 #pragma unroll
     for (int j = 0; j < JV; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) vr[k][j] = ld_stream(p + (8 * (k >> 1) + (k & 1)) * ROW + 128 * j);  // keys 2c, 2c+1, 2c+8, 2c+9
+      for (int k = 0; k < 4; ++k)  // keys 2c, 2c+1, 2c+8, 2c+9
+        vr[k][j] = ld_stream(p + (8 * (k >> 1) + (k & 1)) * ROW + 128 * j);
   };
 
   uint4 qf[Q32 ? 1 : JK];  // head g's dims 32 j + 8 c .. + 7
@@ -305,14 +308,15 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
         float* po = (DIRECT ? osm : ws.part_o) + ((size_t)rec * G + head) * D + 8 * g;
 #pragma unroll
         for (int j = 0; j < JV; ++j) {
-          *reinterpret_cast<float4*>(po + 64 * j) = make_float4(acc[j][0][i], acc[j][0][2 + i], acc[j][1][i], acc[j][1][2 + i]);
-          *reinterpret_cast<float4*>(po + 64 * j + 4) = make_float4(acc[j][2][i], acc[j][2][2 + i], acc[j][3][i], acc[j][3][2 + i]);
+          float4* to = reinterpret_cast<float4*>(po + 64 * j);
+          to[0] = make_float4(acc[j][0][i], acc[j][0][2 + i], acc[j][1][i], acc[j][1][2 + i]);
+          to[1] = make_float4(acc[j][2][i], acc[j][2][2 + i], acc[j][3][i], acc[j][3][2 + i]);
         }
       }
     }
   };
 
-  Chunk cur = look_up(lo + lane), nxt = look_up(lo + 32 + lane);
+  Chunk cur = look_up(lane), nxt = look_up(32 + lane);
   // The pages: the write of this step's tokens may still run (this grid
   // starts alongside it).
   grid_dependency_wait();
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
     const int b1 = __shfl_sync(0xffffffffu, cur.bh, i);
     if (i == 31) {  // the next block of 32 chunks, looked up one block ago
       cur = nxt;
-      nxt = look_up(x + 33 + lane);
+      nxt = look_up(x - lo + 33 + lane);
     }
     const int row1 = __shfl_sync(0xffffffffu, cur.row, (i + 1) & 31);  // of chunk x + 1
     if (b1 != bh) {
@@ -393,13 +397,13 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
       const float p0 = ex2(y[0] - m0), p1 = ex2(y[1] - m1), p2 = ex2(y[2] - m0), p3 = ex2(y[3] - m1);
       l[0] += p0 + p2;
       l[1] += p1 + p3;
-      uint32_t b0[3], b1_[3];
-      split3(p0, p1, b0);
-      split3(p2, p3, b1_);
+      uint32_t wlo[3], whi[3];  // the weights of keys 0-7 and 8-15, three terms
+      split3(p0, p1, wlo);
+      split3(p2, p3, whi);
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        b0[k] = transpose8x8(b0[k]);
-        b1_[k] = transpose8x8(b1_[k]);
+        wlo[k] = transpose8x8(wlo[k]);
+        whi[k] = transpose8x8(whi[k]);
       }
 #pragma unroll
       for (int j = 0; j < JV; ++j) {
@@ -412,9 +416,9 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
           const uint32_t a0 = prmt(v0[w], v1[w], 0x5410), a1 = prmt(v0[w], v1[w], 0x7632);
           const uint32_t a2 = prmt(v2[w], v3[w], 0x5410), a3 = prmt(v2[w], v3[w], 0x7632);
           float o[4];  // of this chunk alone: see the header on the sums' rounding
-          mma_bf16_fresh(o, a0, a1, a2, a3, b0[0], b1_[0]);
-          mma_bf16(o, a0, a1, a2, a3, b0[1], b1_[1]);
-          mma_bf16(o, a0, a1, a2, a3, b0[2], b1_[2]);
+          mma_bf16_fresh(o, a0, a1, a2, a3, wlo[0], whi[0]);
+          mma_bf16(o, a0, a1, a2, a3, wlo[1], whi[1]);
+          mma_bf16(o, a0, a1, a2, a3, wlo[2], whi[2]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[j][w][k] += o[k];
         }
@@ -447,8 +451,8 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
         o.w = fmaf(f, x.w, o.w);
       }
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // no visible key: zeros
-      *reinterpret_cast<float4*>(P.out + ((size_t)(blockIdx.x / Hkv) * P.num_q_heads + (blockIdx.x % Hkv) * G + head) * D + d) =
-          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      const size_t row = (size_t)(blockIdx.x / Hkv) * P.num_q_heads + (blockIdx.x % Hkv) * G + head;
+      *reinterpret_cast<float4*>(P.out + row * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
   }
 }

@@ -610,44 +610,45 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const PageCopy P) {
     phase ^= 1;
     return (long long)turn[phase ^ 1];
   };
+  long long i = -1;  // the pair looked up last, by the CTA (ONE_PAIR) or the warp: page s into page d
+  int s = -1, d = -1;
+  auto look_up = [&](long long pair, bool reports) -> bool {  // whether to copy it
+    i = pair;
+    s = __ldcg(P.src + i);
+    d = __ldcg(P.dst + i);
+    if (s < 0 || d < 0 || s == d) return false;
+    if (s >= P.units || d >= P.units) {
+      if (reports) flag_error(P.dev_error, DEVERR_BLOCK_RANGE);
+      return false;
+    }
+    bool conflict = false;  // read by another pair, or written by a lower one
+    if (CHECK == COPY_CLAIMED) conflict = __ldcg(P.claim + d) != (int)i;
+    if constexpr (CHECK == COPY_CHECKS_LIST) {
+      static_assert(ONE_PAIR, "the CTA compares its one pair with the list");
+      int hit = 0;
+      for (int j = threadIdx.x; j < P.num_pairs; j += 256) {
+        const int a = __ldg(P.src + j), b = __ldg(P.dst + j);
+        hit |= a >= 0 && b >= 0 && a < P.units && b < P.units && (a == d || (b == d && a != b && j < i));
+      }
+      conflict = __syncthreads_or(hit);
+    }
+    if (conflict && reports) flag_error(P.dev_error, DEVERR_PAGE_CONFLICT);
+    return !conflict;
+  };
   for (long long w = blockIdx.x; w < runs; w = next(w)) {
-    const long long first = ONE_PAIR ? w / runs_pp * per_pair + w % runs_pp * P.run : w * P.run;
-    const long long last = ONE_PAIR ? min(first + P.run, (w / runs_pp + 1) * per_pair) : min(first + P.run, steps);
-    long long i = -1;
-    int s = -1, d = -1;
-    bool go = false;
-    auto look_up = [&](long long pair) {  // by the CTA (ONE_PAIR) or the warp
-      i = pair;
-      s = __ldcg(P.src + i);
-      d = __ldcg(P.dst + i);
-      go = s >= 0 && d >= 0 && s != d;
-      if (!go) return;
-      const bool reports = lane == 0 && (ONE_PAIR ? first == i * per_pair && warp == 0 : true);
-      if (s >= P.units || d >= P.units) {
-        if (reports) flag_error(P.dev_error, DEVERR_BLOCK_RANGE);
-        go = false;
-        return;
+    if constexpr (ONE_PAIR) {
+      const int first = (int)(w % runs_pp) * P.run, last = min(first + P.run, per_pair);
+      if (!look_up(w / runs_pp, first == 0 && threadIdx.x == 0)) continue;
+      for (int item = first + warp; item < last; item += 8) copy_piece<COPY_PIECE / 512>(P, s, d, item);
+    } else {
+      const long long last = min((w + 1) * P.run, steps);
+      bool go = false;
+      for (long long item = w * P.run + warp; item < last; item += 8) {
+        const long long pair = item / per_pair;
+        if (pair != i) go = look_up(pair, lane == 0);
+        if (go) copy_piece<COPY_PIECE / 512>(P, s, d, (int)(item - pair * per_pair));
       }
-      bool conflict = false;
-      if (CHECK == COPY_CLAIMED) conflict = __ldcg(P.claim + d) != (int)i;
-      if (CHECK == COPY_CHECKS_LIST) {
-        static_assert(CHECK != COPY_CHECKS_LIST || ONE_PAIR, "the CTA compares its one pair with the list");
-        int hit = 0;  // read by another pair, or written by a lower one
-        for (int j = threadIdx.x; j < P.num_pairs; j += 256) {
-          const int a = __ldg(P.src + j), b = __ldg(P.dst + j);
-          hit |= a >= 0 && b >= 0 && a < P.units && b < P.units && (a == d || (b == d && a != b && j < i));
-        }
-        conflict = __syncthreads_or(hit);
-      }
-      if (conflict) {
-        if (reports) flag_error(P.dev_error, DEVERR_PAGE_CONFLICT);
-        go = false;
-      }
-    };
-    if (ONE_PAIR) look_up(w / runs_pp);
-    for (long long item = first + warp; item < last; item += 8) {
-      if (!ONE_PAIR && item / per_pair != i) look_up(item / per_pair);
-      if (go) copy_piece<COPY_PIECE / 512>(P, s, d, (int)(item - i * per_pair));
+      i = -1;
     }
   }
 }
