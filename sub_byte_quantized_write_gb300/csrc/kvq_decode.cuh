@@ -41,7 +41,7 @@ __device__ __forceinline__ TileList tile_list(const AttnParams& P, int b, int h,
     const int kw = (L - 1) - t.W + 1;  // first key inside the window of the query at L - 1
     if (kw > 0) {
       t.ns = (min(P.sink, t.Leff) + KT - 1) / KT;
-      t.tw = kw / KT;
+      t.tw = min(kw / KT, t.n_total);  // (a length past the table: no tile of the window is left)
       t.gap = t.tw > t.ns;
     }
   }

@@ -102,6 +102,37 @@ def test_decode16_bad_pages_and_lengths_set_their_bits():
     assert int(c["err"].item()) == K.KVQ_DEVERR_BLOCK_RANGE | K.KVQ_DEVERR_TABLE_RANGE
 
 
+@pytest.mark.parametrize("sink", [0, 20])
+def test_decode16_windows_of_lengths_past_the_table(sink):
+    """The window of a length that passes its table row by more than the window holds no key; the sinks stay."""
+    K = kvq()
+    c = ref.make(3, 2, 4, 128, 16, [90, 208, 40], headwise=True, window=[16, 0], sink=sink, seed=12, max_blocks=13)
+    c["pag"].seq_lens.copy_(torch.tensor([90, 5000, 40]))
+    out = decode(c)
+    ref.check(out, ref.attention64(c, lens=np.array([90, 5000, 40])))
+    assert out[1, :4].any() == (sink > 0) and int(c["err"].item()) == K.KVQ_DEVERR_TABLE_RANGE
+
+
+@pytest.mark.parametrize("mode", ["INT4_TOKEN_HEAD", "INT8_CHANNEL"])
+def test_low_bit_windows_of_lengths_past_the_table(mode):
+    import kvq_inputs as gen
+    from harness import ATOL, build_case, decode_gpu, q_host, write_step
+    K = kvq()
+    wl = gen.custom({"INT4_TOKEN_HEAD": gen.MODE_INT4, "INT8_CHANNEL": gen.MODE_INT8}[mode], 8, 2, 128, 16, "bf16",
+                    seq_lens=[300, 64, 130], n_new=[1, 1, 1], seed=6)
+    c = build_case(wl)
+    write_step(c)
+    q = q_host(wl)
+    want = decode_gpu(c, q)
+    pag = K.Paging(torch.tensor([300, 100000, 130], dtype=torch.int32, device="cuda"), block_tables=c.gpag.block_tables,
+                   window_per_kv_head=torch.tensor([16, 0], dtype=torch.int32, device="cuda"))
+    out = decode_gpu(c, q, paging=pag)
+    assert not out[1, :4].any()         # no key of the window is in the table, and there is no sink
+    # the head without a window sees the same keys, in other slices (entries past the 64 tokens are -1)
+    assert np.abs(out[:, 4:] - want[:, 4:]).max() <= ATOL
+    assert int(c.dev_err.item()) == K.KVQ_DEVERR_TABLE_RANGE
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("D", [64, 128])
 def test_write16_gather16_round_trip(D, dtype):
