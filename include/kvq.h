@@ -88,7 +88,9 @@ typedef enum {
  *   infinite), no RHT.  For layers kept in full precision next
  *   to quantised ones.  kvq_write, kvq_gather(_chunk), the decode calls and
  *   the page calls take it; kvq_prefill_attn does not (gather the pages and
- *   call kvq_prefill_dense_attn). */
+ *   call kvq_prefill_dense_attn).  Slots that a decode does not see may hold
+ *   anything; a NaN that it sees makes the outputs it enters NaN, and what an
+ *   infinity that it sees enters is not defined. */
 typedef enum {
   KVQ_INT4_TOKEN_HEAD = 0,
   KVQ_INT2_TOKEN_HEAD = 1,

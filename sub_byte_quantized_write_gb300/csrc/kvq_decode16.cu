@@ -514,8 +514,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
       float mn = m;
 #pragma unroll
       for (int u = 0; u < RPS; ++u)
-        if (r0 + u < n && ml[u].y > 0.0f) mn = fmaxf(mn, ml[u].x);
-      if (mn == -CUDART_INF_F) continue;  // nothing visible in these
+        if (r0 + u < n) mn = fmaxf(mn, ml[u].x);
       const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - mn);
       m = mn;
       l *= f;
@@ -523,8 +522,8 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
       for (int e = 0; e < EPL; ++e) o[e] *= f;
 #pragma unroll
       for (int u = 0; u < RPS; ++u) {
-        if (r0 + u < n && ml[u].y > 0.0f) {
-          const float x = ex2(ml[u].x - m);
+        if (r0 + u < n) {  // (a record of no visible key adds zeros, one that met a NaN its NaN)
+          const float x = ml[u].x == -CUDART_INF_F ? 0.0f : ex2(ml[u].x - m);
           l = fmaf(x, ml[u].y, l);
 #pragma unroll
           for (int e = 0; e < EPL; ++e) o[e] = fmaf(x, v[u][e], o[e]);

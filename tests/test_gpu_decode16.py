@@ -133,6 +133,31 @@ def test_low_bit_windows_of_lengths_past_the_table(mode):
     assert int(c.dev_err.item()) == K.KVQ_DEVERR_TABLE_RANGE
 
 
+@pytest.mark.parametrize("splits", [0, 3, 200])
+@pytest.mark.parametrize("lens", [[60, 33], [9000, 700]])
+def test_decode16_visible_nans_reach_their_outputs_alone(lens, splits):
+    """A NaN in a visible key: the outputs of its kv head's q heads; in a visible value: its dim of them."""
+    c = ref.make(2, 2, 4, 128, 16, lens, seed=13)
+    want = decode(c, num_splits=splits)
+    kp, vp = c["cache"].k_pages.view(torch.bfloat16), c["cache"].v_pages.view(torch.bfloat16)
+    for key in (0, 32, lens[0] - 1):
+        page = int(c["table"][0, 0, key // 16])
+        held = kp[page, 1, key % 16, 5].clone()
+        kp[page, 1, key % 16, 5] = float("nan")
+        out = decode(c, num_splits=splits)
+        assert torch.isnan(out[0, 4:]).all()
+        out[0, 4:] = want[0, 4:]
+        assert torch.equal(out, want)
+        kp[page, 1, key % 16, 5] = held
+        held = vp[page, 1, key % 16, 77].clone()
+        vp[page, 1, key % 16, 77] = float("nan")
+        out = decode(c, num_splits=splits)
+        assert torch.isnan(out[0, 4:, 77]).all()
+        out[0, 4:, 77] = want[0, 4:, 77]
+        assert torch.equal(out, want)
+        vp[page, 1, key % 16, 77] = held
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("D", [64, 128])
 def test_write16_gather16_round_trip(D, dtype):
