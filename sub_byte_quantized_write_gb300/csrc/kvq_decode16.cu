@@ -304,7 +304,9 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
       for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
       const int head = 2 * c + i;
       if (head < G) {
-        if (g == 0) (DIRECT ? mlsm : ws.part_ml)[(size_t)rec * G + head] = make_float2(m[i], l[i]);
+        // (a NaN among the logits may have left no maximum: the join wants a finite one to add the NaN by)
+        if (g == 0)
+          (DIRECT ? mlsm : ws.part_ml)[(size_t)rec * G + head] = make_float2(isnan(l[i]) ? fmaxf(m[i], 0.0f) : m[i], l[i]);
         float* po = (DIRECT ? osm : ws.part_o) + ((size_t)rec * G + head) * D + 8 * g;
 #pragma unroll
         for (int j = 0; j < JV; ++j) {
@@ -514,7 +516,8 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
       float mn = m;
 #pragma unroll
       for (int u = 0; u < RPS; ++u)
-        if (r0 + u < n) mn = fmaxf(mn, ml[u].x);
+        if (r0 + u < n && ml[u].y != 0.0f) mn = fmaxf(mn, ml[u].x);
+      if (mn == -CUDART_INF_F) continue;  // nothing visible in these
       const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - mn);
       m = mn;
       l *= f;
@@ -522,8 +525,8 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
       for (int e = 0; e < EPL; ++e) o[e] *= f;
 #pragma unroll
       for (int u = 0; u < RPS; ++u) {
-        if (r0 + u < n) {  // (a record of no visible key adds zeros, one that met a NaN its NaN)
-          const float x = ml[u].x == -CUDART_INF_F ? 0.0f : ex2(ml[u].x - m);
+        if (r0 + u < n && ml[u].y != 0.0f) {
+          const float x = ex2(ml[u].x - m);
           l = fmaf(x, ml[u].y, l);
 #pragma unroll
           for (int e = 0; e < EPL; ++e) o[e] = fmaf(x, v[u][e], o[e]);
