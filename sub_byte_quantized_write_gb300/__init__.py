@@ -198,13 +198,15 @@ _serial = itertools.count()
 
 
 class _Kept:
-    """What a handle's C struct was made of, the struct, and a number of its own."""
-    __slots__ = ("tensors", "pointers", "struct", "devices", "serial")
+    """What a handle's C struct was made of, the struct, a number of its own, and that of the paging state that a
+    cache was last checked against."""
+    __slots__ = ("tensors", "pointers", "struct", "devices", "serial", "paired")
 
     def __init__(self, tensors, struct):
         self.tensors, self.struct, self.serial = tensors, struct, next(_serial)
         self.pointers = [t.data_ptr() for t in tensors]
         self.devices = {t.device for t in tensors}
+        self.paired = None
 
 
 def _kept_struct(handle, tensors):
@@ -296,13 +298,34 @@ class Paging(_Handle):
                          self.sink_size)
 
 
+def _structs(cache: PagedCache, paging: Paging) -> Tuple[KvqCache, KvqPaging]:
+    """The C structs of a cache and of a paging state that fits it."""
+    cs, ps = cache.struct(), paging.struct()
+    kept, other = cache._struct, paging._struct
+    if kept.paired != other.serial:
+        Hkv, t, w = cache.num_kv_heads, paging.block_tables_headwise, paging.window_per_kv_head
+        if len(kept.devices) != 1 or other.devices != kept.devices:
+            raise ValueError("the cache and the paging state must be on one device")
+        if t is not None and t.shape[0] < ps.batch * Hkv:
+            raise ValueError("a head-wise block table needs batch * num_kv_heads = %d rows" % (ps.batch * Hkv))
+        if w is not None and w.numel() < Hkv:
+            raise ValueError("window_per_kv_head must have %d elements, got %d" % (Hkv, w.numel()))
+        kept.paired = other.serial
+    return cs, ps
+
+
+def _on_device(cache: PagedCache, **tensors: Optional[torch.Tensor]) -> None:
+    dev = cache.k_pages.get_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError("%s must be on the cache's device" % name)
+
+
 def _check_rows(cache: PagedCache, t: torch.Tensor, name: str) -> None:
-    """t is [tokens, num_kv_heads, head_dim] of the cache's device."""
+    """t is [tokens, num_kv_heads, head_dim]."""
     if t.dim() != 3 or t.shape[1] != cache.num_kv_heads or t.shape[2] != cache.head_dim:
         raise ValueError("%s must be [tokens, %d, %d], got %s" % (name, cache.num_kv_heads, cache.head_dim,
                                                                   tuple(t.shape)))
-    if t.get_device() != cache.k_pages.get_device():
-        raise ValueError("%s must be on the cache's device" % name)
 
 
 def _check_cu(cu: torch.Tensor, batch: int, name: str) -> None:
@@ -311,12 +334,10 @@ def _check_cu(cu: torch.Tensor, batch: int, name: str) -> None:
 
 
 def _check_q(cache: PagedCache, ps: KvqPaging, q: torch.Tensor, out: Optional[torch.Tensor]) -> None:
-    """q is [batch, num_q_heads, head_dim] of the cache's device, and out, if given, as large."""
+    """q is [batch, num_q_heads, head_dim] and out, if given, as large."""
     shape = q.shape
     if len(shape) != 3 or shape[0] != ps.batch or shape[2] != cache.head_dim:
         raise ValueError("q must be [%d, num_q_heads, %d], got %s" % (ps.batch, cache.head_dim, tuple(shape)))
-    if q.get_device() != cache.k_pages.get_device():
-        raise ValueError("q must be on the cache's device")
     if out is not None and out.numel() != q.numel():
         raise ValueError("out must be as large as q")
 
@@ -326,9 +347,10 @@ def kvq_write(cache: PagedCache, paging: Paging, k: torch.Tensor, v: torch.Tenso
     """Quantise k, v [num_tokens, num_kv_heads, head_dim] and scatter them into the pages (16-bit caches: as bf16)."""
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and dtype")
-    cs, ps = cache.struct(), paging.struct()
+    cs, ps = _structs(cache, paging)
     _check_rows(cache, k, "k")
     _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
+    _on_device(cache, k=k, v=v, cu_new_tokens=cu_new_tokens, dev_error=dev_error)
     _run(cache.k_pages.device, stream, _lib.kvq_write, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"),
          _dev_ptr(v, name="v"), _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]),
          _dev_ptr(dev_error, torch.int32, "dev_error"))
@@ -351,12 +373,14 @@ def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_t
         v_out = _empty(shape, out_dtype, dev, stream)
     if k_out.dtype != v_out.dtype:
         raise ValueError("k_out and v_out must have the same dtype")
-    cs, ps = cache.struct(), paging.struct()
+    cs, ps = _structs(cache, paging)
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         _check_rows(cache, t, name)
         if t.shape[0] < num_tokens:
             raise ValueError("%s has fewer than num_tokens rows" % name)
     _check_cu(cu_tokens, ps.batch, "cu_tokens")
+    _on_device(cache, k_out=k_out, v_out=v_out, cu_tokens=cu_tokens, k_chunk=k_chunk, v_chunk=v_chunk,
+               cu_chunk=cu_chunk, dev_error=dev_error)
     if k_chunk is None:
         _run(dev, stream, _lib.kvq_gather, ctypes.byref(cs), ctypes.byref(ps),
              _dev_ptr(cu_tokens, torch.int32, "cu_tokens"), int(num_tokens), _dev_ptr(k_out, name="k_out"),
@@ -376,7 +400,7 @@ def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_t
 
 def kvq_decode_workspace_size(cache: PagedCache, paging: Paging, num_q_heads: int, num_splits: int = 0):
     """(bytes, splits) the decode call needs for its split-KV partials."""
-    cs, ps = cache.struct(), paging.struct()
+    cs, ps = _structs(cache, paging)
     nbytes, splits = ctypes.c_size_t(0), ctypes.c_int32(0)
     _check(_lib.kvq_decode_workspace_size(ctypes.byref(cs), ctypes.byref(ps), num_q_heads, num_splits,
                                           ctypes.byref(nbytes), ctypes.byref(splits)))
@@ -394,8 +418,9 @@ def kvq_decode_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, softmax_
     if workspace is None:
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
         workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
-    cs, ps = cache.struct(), paging.struct()
+    cs, ps = _structs(cache, paging)
     _check_q(cache, ps, q, given)
+    _on_device(cache, q=q, out=out, workspace=workspace, dev_error=dev_error)
     _run(cache.k_pages.device, stream, _lib.kvq_decode_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"),
          _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"),
          _dev_ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(), num_splits,
@@ -419,10 +444,11 @@ def kvq_write_decode_attn(cache: PagedCache, paging: Paging, k: torch.Tensor, v:
     if workspace is None:
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
         workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
-    cs, ps = cache.struct(), paging.struct()
+    cs, ps = _structs(cache, paging)
     _check_rows(cache, k, "k")
     _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
     _check_q(cache, ps, q, given)
+    _on_device(cache, k=k, v=v, cu_new_tokens=cu_new_tokens, q=q, out=out, workspace=workspace, dev_error=dev_error)
     _run(cache.k_pages.device, stream, _lib.kvq_write_decode_attn, ctypes.byref(cs), ctypes.byref(ps),
          _dev_ptr(k, name="k"), _dev_ptr(v, name="v"), _qdtype(k),
          _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]), _dev_ptr(q, name="q"), _qdtype(q), Hq,
@@ -443,8 +469,9 @@ def kvq_decode_attn_noalloc(cache: PagedCache, paging: Paging, q: torch.Tensor, 
     given = out
     if out is None:
         out = _empty((B, Hq, D), torch.float32, q.device, stream)
-    cs, ps = cache.struct(), paging.struct()
+    cs, ps = _structs(cache, paging)
     _check_q(cache, ps, q, given)
+    _on_device(cache, q=q, out=out, dev_error=dev_error)
     _run(cache.k_pages.device, stream, _lib.kvq_decode_attn_noalloc, ctypes.byref(cs), ctypes.byref(ps),
          _dev_ptr(q, name="q"), _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"), num_splits,
          _dev_ptr(dev_error, torch.int32, "dev_error"))
@@ -458,7 +485,8 @@ def kvq_prefill_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, cu_q: t
     T, Hq, D = q.shape
     if out is None:
         out = _empty((T, Hq, D), torch.float32, q.device, stream)
-    cs, ps = cache.struct(), paging.struct()
+    cs, ps = _structs(cache, paging)
+    _on_device(cache, q=q, cu_q=cu_q, out=out, dev_error=dev_error)
     _run(cache.k_pages.device, stream, _lib.kvq_prefill_attn, ctypes.byref(cs), ctypes.byref(ps),
          _dev_ptr(q, name="q"), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q"), T, int(max_q_per_seq),
          float(softmax_scale), _dev_ptr(out, torch.float32, "out"), _dev_ptr(dev_error, torch.int32, "dev_error"))

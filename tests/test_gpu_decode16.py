@@ -288,3 +288,31 @@ def test_binding_refuses_tensors_of_other_shapes():
     with pytest.raises(ValueError):
         K.kvq_gather(c["cache"], c["pag"], c["cu"], 23, k_out=torch.empty(22, 2, 128, device="cuda"))
     K.kvq_decode_attn(c["cache"], c["pag"], c["q"], c["scale"])
+
+
+def test_binding_refuses_pagings_that_do_not_fit_the_cache():
+    K = kvq()
+    c = ref.make(2, 2, 4, 128, 16, [20, 3], headwise=True, window=[8, 0], seed=1)
+    pag, ws = c["pag"], torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    new = c["k"][:2].contiguous()
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+
+    def calls(p, **kw):
+        yield lambda: K.kvq_decode_attn(c["cache"], p, c["q"], 0.1, workspace=ws, **kw)
+        yield lambda: K.kvq_decode_attn_noalloc(c["cache"], p, c["q"], 0.1, **kw)
+        yield lambda: K.kvq_write_decode_attn(c["cache"], p, new, new, cu, c["q"], 0.1, workspace=ws, **kw)
+        yield lambda: K.kvq_write(c["cache"], p, c["k"], c["v"], c["cu"], **kw)
+        yield lambda: K.kvq_gather(c["cache"], p, c["cu"], 23, **kw)
+
+    short = K.Paging(pag.seq_lens, block_tables_headwise=pag.block_tables_headwise[:2].contiguous())
+    narrow = K.Paging(pag.seq_lens, block_tables_headwise=pag.block_tables_headwise,
+                      window_per_kv_head=pag.window_per_kv_head[:1].contiguous())
+    for p, kw in ((short, {}), (narrow, {}), (pag, dict(dev_error=torch.zeros(1, dtype=torch.int32)))):
+        for call in calls(p, **kw):
+            with pytest.raises(ValueError):
+                call()
+    pag.window_per_kv_head = narrow.window_per_kv_head     # a paging state that fitted, changed
+    with pytest.raises(ValueError):
+        decode(c)
+    pag.window_per_kv_head = torch.tensor([8, 0], dtype=torch.int32, device="cuda")
+    ref.check(decode(c), ref.attention64(c))
