@@ -41,11 +41,12 @@ __device__ __forceinline__ TileList tile_list(const AttnParams& P, int b, int h,
     const int kw = (L - 1) - t.W + 1;  // first key inside the window of the query at L - 1
     if (kw > 0) {
       t.ns = (min(P.sink, t.Leff) + KT - 1) / KT;
-      t.tw = min(kw / KT, t.n_total);  // (a length past the table: no tile of the window is left)
+      t.tw = kw / KT;
       t.gap = t.tw > t.ns;
     }
   }
-  t.n_virt = t.gap ? t.ns + (t.n_total - t.tw) : t.n_total;
+  // (max: of a length past the table, the window may start behind the last tile)
+  t.n_virt = t.gap ? t.ns + max(t.n_total - t.tw, 0) : t.n_total;
   return t;
 }
 
