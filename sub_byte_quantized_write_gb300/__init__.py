@@ -121,10 +121,14 @@ def kvq_row_bytes(mode: int, head_dim: int) -> int:
     return _lib.kvq_row_bytes(mode, head_dim)
 
 
-def _dev_ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
+def _dev_ptr(t: Optional[torch.Tensor], dtype=None, name="tensor", dev: Optional[int] = None):
+    """Device pointer of a contiguous tensor, on device `dev` where that is given."""
     if t is None:
         return None
-    if not t.is_cuda:
+    if dev is not None:
+        if t.get_device() != dev:
+            raise ValueError("%s must be on the cache's device" % name)
+    elif not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -314,13 +318,6 @@ def _structs(cache: PagedCache, paging: Paging) -> Tuple[KvqCache, KvqPaging]:
     return cs, ps
 
 
-def _on_device(cache: PagedCache, **tensors: Optional[torch.Tensor]) -> None:
-    dev = cache.k_pages.get_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError("%s must be on the cache's device" % name)
-
-
 def _check_rows(cache: PagedCache, t: torch.Tensor, name: str) -> None:
     """t is [tokens, num_kv_heads, head_dim]."""
     if t.dim() != 3 or t.shape[1] != cache.num_kv_heads or t.shape[2] != cache.head_dim:
@@ -348,12 +345,13 @@ def kvq_write(cache: PagedCache, paging: Paging, k: torch.Tensor, v: torch.Tenso
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and dtype")
     cs, ps = _structs(cache, paging)
+    dev = cache.k_pages.get_device()
     _check_rows(cache, k, "k")
     _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
-    _on_device(cache, k=k, v=v, cu_new_tokens=cu_new_tokens, dev_error=dev_error)
-    _run(cache.k_pages.device, stream, _lib.kvq_write, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(k, name="k"),
-         _dev_ptr(v, name="v"), _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]),
-         _dev_ptr(dev_error, torch.int32, "dev_error"))
+    _run(cache.k_pages.device, stream, _lib.kvq_write, ctypes.byref(cs), ctypes.byref(ps),
+         _dev_ptr(k, None, "k", dev), _dev_ptr(v, None, "v", dev), _qdtype(k),
+         _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens", dev), int(k.shape[0]),
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
 
 
 def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_tokens: int,
@@ -366,35 +364,35 @@ def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_t
     With k_chunk / v_chunk / cu_chunk (kvq_gather_chunk) the last positions
     of each sequence come from those full-precision rows instead."""
     shape = (num_tokens, cache.num_kv_heads, cache.head_dim)
-    dev = cache.k_pages.device
+    device = cache.k_pages.device
     if k_out is None:
-        k_out = _empty(shape, out_dtype, dev, stream)
+        k_out = _empty(shape, out_dtype, device, stream)
     if v_out is None:
-        v_out = _empty(shape, out_dtype, dev, stream)
+        v_out = _empty(shape, out_dtype, device, stream)
     if k_out.dtype != v_out.dtype:
         raise ValueError("k_out and v_out must have the same dtype")
     cs, ps = _structs(cache, paging)
+    dev = cache.k_pages.get_device()
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         _check_rows(cache, t, name)
         if t.shape[0] < num_tokens:
             raise ValueError("%s has fewer than num_tokens rows" % name)
     _check_cu(cu_tokens, ps.batch, "cu_tokens")
-    _on_device(cache, k_out=k_out, v_out=v_out, cu_tokens=cu_tokens, k_chunk=k_chunk, v_chunk=v_chunk,
-               cu_chunk=cu_chunk, dev_error=dev_error)
     if k_chunk is None:
-        _run(dev, stream, _lib.kvq_gather, ctypes.byref(cs), ctypes.byref(ps),
-             _dev_ptr(cu_tokens, torch.int32, "cu_tokens"), int(num_tokens), _dev_ptr(k_out, name="k_out"),
-             _dev_ptr(v_out, name="v_out"), _qdtype(k_out), _dev_ptr(dev_error, torch.int32, "dev_error"))
+        _run(device, stream, _lib.kvq_gather, ctypes.byref(cs), ctypes.byref(ps),
+             _dev_ptr(cu_tokens, torch.int32, "cu_tokens", dev), int(num_tokens), _dev_ptr(k_out, None, "k_out", dev),
+             _dev_ptr(v_out, None, "v_out", dev), _qdtype(k_out), _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     else:
         if v_chunk is None or k_chunk.dtype != v_chunk.dtype or k_chunk.shape != v_chunk.shape:
             raise ValueError("k_chunk and v_chunk must be given together, with one dtype and shape")
         _check_rows(cache, k_chunk, "k_chunk")
         _check_cu(cu_chunk, ps.batch, "cu_chunk")
-        _run(dev, stream, _lib.kvq_gather_chunk, ctypes.byref(cs), ctypes.byref(ps),
-             _dev_ptr(cu_tokens, torch.int32, "cu_tokens"), int(num_tokens), _dev_ptr(k_chunk, name="k_chunk"),
-             _dev_ptr(v_chunk, name="v_chunk"), _qdtype(k_chunk), _dev_ptr(cu_chunk, torch.int32, "cu_chunk"),
-             _dev_ptr(k_out, name="k_out"), _dev_ptr(v_out, name="v_out"), _qdtype(k_out),
-             _dev_ptr(dev_error, torch.int32, "dev_error"))
+        _run(device, stream, _lib.kvq_gather_chunk, ctypes.byref(cs), ctypes.byref(ps),
+             _dev_ptr(cu_tokens, torch.int32, "cu_tokens", dev), int(num_tokens),
+             _dev_ptr(k_chunk, None, "k_chunk", dev), _dev_ptr(v_chunk, None, "v_chunk", dev), _qdtype(k_chunk),
+             _dev_ptr(cu_chunk, torch.int32, "cu_chunk", dev),
+             _dev_ptr(k_out, None, "k_out", dev), _dev_ptr(v_out, None, "v_out", dev), _qdtype(k_out),
+             _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     return k_out, v_out
 
 
@@ -419,12 +417,12 @@ def kvq_decode_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, softmax_
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
         workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cs, ps = _structs(cache, paging)
+    dev = cache.k_pages.get_device()
     _check_q(cache, ps, q, given)
-    _on_device(cache, q=q, out=out, workspace=workspace, dev_error=dev_error)
-    _run(cache.k_pages.device, stream, _lib.kvq_decode_attn, ctypes.byref(cs), ctypes.byref(ps), _dev_ptr(q, name="q"),
-         _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"),
-         _dev_ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(), num_splits,
-         _dev_ptr(dev_error, torch.int32, "dev_error"))
+    _run(cache.k_pages.device, stream, _lib.kvq_decode_attn, ctypes.byref(cs), ctypes.byref(ps),
+         _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev),
+         _dev_ptr(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(), num_splits,
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     return out
 
 
@@ -445,15 +443,16 @@ def kvq_write_decode_attn(cache: PagedCache, paging: Paging, k: torch.Tensor, v:
         nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
         workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cs, ps = _structs(cache, paging)
+    dev = cache.k_pages.get_device()
     _check_rows(cache, k, "k")
     _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
     _check_q(cache, ps, q, given)
-    _on_device(cache, k=k, v=v, cu_new_tokens=cu_new_tokens, q=q, out=out, workspace=workspace, dev_error=dev_error)
     _run(cache.k_pages.device, stream, _lib.kvq_write_decode_attn, ctypes.byref(cs), ctypes.byref(ps),
-         _dev_ptr(k, name="k"), _dev_ptr(v, name="v"), _qdtype(k),
-         _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens"), int(k.shape[0]), _dev_ptr(q, name="q"), _qdtype(q), Hq,
-         float(softmax_scale), _dev_ptr(out, torch.float32, "out"), _dev_ptr(workspace, torch.uint8, "workspace"),
-         workspace.numel(), int(num_splits), _dev_ptr(dev_error, torch.int32, "dev_error"))
+         _dev_ptr(k, None, "k", dev), _dev_ptr(v, None, "v", dev), _qdtype(k),
+         _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens", dev), int(k.shape[0]), _dev_ptr(q, None, "q", dev),
+         _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev),
+         _dev_ptr(workspace, torch.uint8, "workspace", dev), workspace.numel(), int(num_splits),
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     return out
 
 
@@ -470,11 +469,11 @@ def kvq_decode_attn_noalloc(cache: PagedCache, paging: Paging, q: torch.Tensor, 
     if out is None:
         out = _empty((B, Hq, D), torch.float32, q.device, stream)
     cs, ps = _structs(cache, paging)
+    dev = cache.k_pages.get_device()
     _check_q(cache, ps, q, given)
-    _on_device(cache, q=q, out=out, dev_error=dev_error)
     _run(cache.k_pages.device, stream, _lib.kvq_decode_attn_noalloc, ctypes.byref(cs), ctypes.byref(ps),
-         _dev_ptr(q, name="q"), _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out"), num_splits,
-         _dev_ptr(dev_error, torch.int32, "dev_error"))
+         _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev),
+         num_splits, _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     return out
 
 
@@ -486,10 +485,11 @@ def kvq_prefill_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, cu_q: t
     if out is None:
         out = _empty((T, Hq, D), torch.float32, q.device, stream)
     cs, ps = _structs(cache, paging)
-    _on_device(cache, q=q, cu_q=cu_q, out=out, dev_error=dev_error)
+    dev = cache.k_pages.get_device()
     _run(cache.k_pages.device, stream, _lib.kvq_prefill_attn, ctypes.byref(cs), ctypes.byref(ps),
-         _dev_ptr(q, name="q"), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q"), T, int(max_q_per_seq),
-         float(softmax_scale), _dev_ptr(out, torch.float32, "out"), _dev_ptr(dev_error, torch.int32, "dev_error"))
+         _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q", dev), T, int(max_q_per_seq),
+         float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev),
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     return out
 
 
