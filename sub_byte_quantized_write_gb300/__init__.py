@@ -276,15 +276,20 @@ class PagedCache(_Handle):
 class Paging(_Handle):
     """Block table (uniform [batch, max_blocks] or head-wise
     [batch * num_kv_heads, max_blocks], int32, -1 = evicted), seq_lens [batch]
-    and the optional per-kv-head sliding window plus sink size."""
+    and the optional per-kv-head sliding window plus sink size.  max_blocks is
+    the width of the table that is set."""
 
     def __init__(self, seq_lens: torch.Tensor, block_tables: Optional[torch.Tensor] = None,
                  block_tables_headwise: Optional[torch.Tensor] = None,
                  window_per_kv_head: Optional[torch.Tensor] = None, sink_size: int = 0):
-        t = block_tables if block_tables is not None else block_tables_headwise
         self.__dict__.update(seq_lens=seq_lens, block_tables=block_tables,
                              block_tables_headwise=block_tables_headwise, window_per_kv_head=window_per_kv_head,
-                             sink_size=int(sink_size), max_blocks=0 if t is None else int(t.shape[1]), _struct=None)
+                             sink_size=int(sink_size), _struct=None)
+
+    @property
+    def max_blocks(self) -> int:
+        t = self.block_tables if self.block_tables is not None else self.block_tables_headwise
+        return 0 if t is None else int(t.shape[-1])
 
     def struct(self) -> KvqPaging:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
@@ -292,7 +297,11 @@ class Paging(_Handle):
 
     def _build(self) -> KvqPaging:
         for t in (self.block_tables, self.block_tables_headwise):
-            if t is not None and t.shape[0] < self.seq_lens.shape[0]:
+            if t is None:
+                continue
+            if t.dim() != 2:
+                raise ValueError("a block table has two dimensions, got %d" % t.dim())
+            if t.shape[0] < self.seq_lens.shape[0]:
                 raise ValueError("the block table has fewer rows than seq_lens")
         return KvqPaging(_dev_ptr(self.block_tables, torch.int32, "block_tables"),
                          _dev_ptr(self.block_tables_headwise, torch.int32, "block_tables_headwise"),
