@@ -255,8 +255,12 @@ class PagedCache(_Handle):
             if ch_amax_ready is None:
                 ch_amax_ready = torch.zeros(1, dtype=torch.int32, device=device)
         self.__dict__.update(mode=mode, num_blocks=num_blocks, num_kv_heads=num_kv_heads, block_size=block_size,
-                             head_dim=head_dim, row_bytes=row_bytes, k_pages=k_pages, v_pages=v_pages,
+                             head_dim=head_dim, k_pages=k_pages, v_pages=v_pages,
                              rht_signs=rht_signs, ch_amax=ch_amax, ch_amax_ready=ch_amax_ready, _struct=None)
+
+    @property
+    def row_bytes(self) -> int:
+        return kvq_row_bytes(self.mode, self.head_dim)
 
     def struct(self) -> KvqCache:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
@@ -266,6 +270,11 @@ class PagedCache(_Handle):
         need = self.num_blocks * self.num_kv_heads * self.block_size * self.row_bytes
         if self.k_pages.numel() < need or self.v_pages.numel() < need:
             raise ValueError("k_pages / v_pages hold fewer than num_blocks blocks")
+        for t, name, least in ((self.rht_signs, "rht_signs", self.head_dim),
+                               (self.ch_amax, "ch_amax", 2 * self.num_kv_heads * self.head_dim),
+                               (self.ch_amax_ready, "ch_amax_ready", 1)):
+            if t is not None and 0 < t.numel() < least:  # (none at all is NULL, which the library judges)
+                raise ValueError("%s must have %d elements, got %d" % (name, least, t.numel()))
         return KvqCache(_dev_ptr(self.k_pages, torch.uint8, "k_pages"), _dev_ptr(self.v_pages, torch.uint8, "v_pages"),
                         self.num_blocks, self.num_kv_heads, self.block_size, self.head_dim, self.mode,
                         _dev_ptr(self.rht_signs, torch.int8, "rht_signs"),

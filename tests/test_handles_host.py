@@ -33,3 +33,34 @@ def test_the_width_follows_the_table(host, kind):
         setattr(late, kind, t)
         with pytest.raises(ValueError):
             late.struct()
+
+
+def test_the_pools_are_checked_for_the_row_the_mode_has_now(host):
+    c = host.PagedCache(host.KVQ_INT4_TOKEN_HEAD, 3, 2, 16, 64, device="cpu")
+    c.struct()
+    for name, value in (("mode", host.KVQ_BF16_CACHE), ("head_dim", 128), ("num_blocks", 4)):
+        old = getattr(c, name)
+        setattr(c, name, value)
+        with pytest.raises(ValueError):
+            c.struct()
+        setattr(c, name, old)
+        assert c.struct().num_blocks == 3
+    c.mode = host.KVQ_INT2_TOKEN_HEAD
+    assert c.struct().mode == host.KVQ_INT2_TOKEN_HEAD and c.row_bytes == 20
+
+
+def test_signs_and_channel_maxima_are_as_long_as_the_head_now_is(host):
+    c = host.PagedCache(host.KVQ_INT4_TOKEN_HEAD, 3, 2, 16, 64, rht_signs=torch.ones(64, dtype=torch.int8), device="cpu")
+    c.struct()
+    row = host.kvq_row_bytes(host.KVQ_INT4_TOKEN_HEAD, 128)
+    c.k_pages = c.v_pages = torch.zeros((3, 2, 16, row), dtype=torch.uint8)
+    c.head_dim = 128
+    with pytest.raises(ValueError, match="rht_signs"):
+        c.struct()
+    c.rht_signs = torch.ones(128, dtype=torch.int8)
+    assert c.struct().head_dim == 128
+    c = host.PagedCache(host.KVQ_INT8_CHANNEL, 3, 2, 16, 64, device="cpu")
+    c.struct()
+    c.ch_amax = torch.zeros((2, 1, 64))
+    with pytest.raises(ValueError, match="ch_amax"):
+        c.struct()
