@@ -204,21 +204,23 @@ _serial = itertools.count()
 class _Kept:
     """What a handle's C struct was made of, the struct, a number of its own, and that of the paging state that a
     cache was last checked against."""
-    __slots__ = ("tensors", "pointers", "struct", "devices", "serial", "paired")
+    __slots__ = ("tensors", "pointers", "shapes", "struct", "devices", "serial", "paired")
 
-    def __init__(self, tensors, struct):
+    def __init__(self, tensors, struct, by_shape):
         self.tensors, self.struct, self.serial = tensors, struct, next(_serial)
         self.pointers = [t.data_ptr() for t in tensors]
+        self.shapes = [t.shape for t in tensors] if by_shape else None
         self.devices = {t.device for t in tensors}
         self.paired = None
 
 
-def _kept_struct(handle, tensors):
-    """A handle's C struct, rebuilt (with its checks) unless the tensors it was made of are where they were.  (Give a
-    handle other tensors by setting its attributes, not by resizing the ones it has.)"""
+def _kept_struct(handle, tensors, by_shape):
+    """A handle's C struct, rebuilt (with its checks) unless the tensors it was made of are where they were and, where
+    the struct takes numbers from their shapes (by_shape), as large."""
     kept = handle._struct
-    if kept is None or [t.data_ptr() for t in kept.tensors] != kept.pointers:
-        kept = handle.__dict__["_struct"] = _Kept([t for t in tensors(handle) if t is not None], handle._build())
+    if (kept is None or [t.data_ptr() for t in kept.tensors] != kept.pointers
+            or by_shape and [t.shape for t in kept.tensors] != kept.shapes):
+        kept = handle.__dict__["_struct"] = _Kept([t for t in tensors(handle) if t is not None], handle._build(), by_shape)
     return kept.struct
 
 
@@ -264,7 +266,7 @@ class PagedCache(_Handle):
 
     def struct(self) -> KvqCache:
         """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
-        return _kept_struct(self, _cache_tensors)
+        return _kept_struct(self, _cache_tensors, False)
 
     def _build(self) -> KvqCache:
         need = self.num_blocks * self.num_kv_heads * self.block_size * self.row_bytes
@@ -301,8 +303,8 @@ class Paging(_Handle):
         return 0 if t is None else int(t.shape[-1])
 
     def struct(self) -> KvqPaging:
-        """The C struct: built once, and again when an attribute was set or a tensor's memory changed."""
-        return _kept_struct(self, _paging_tensors)
+        """The C struct: built once, and again when an attribute was set or a tensor's memory or shape changed."""
+        return _kept_struct(self, _paging_tensors, True)
 
     def _build(self) -> KvqPaging:
         for t in (self.block_tables, self.block_tables_headwise):

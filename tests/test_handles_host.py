@@ -64,3 +64,25 @@ def test_signs_and_channel_maxima_are_as_long_as_the_head_now_is(host):
     c.ch_amax = torch.zeros((2, 1, 64))
     with pytest.raises(ValueError, match="ch_amax"):
         c.struct()
+
+
+def test_a_paging_state_resized_in_place_is_seen(host):
+    """The number of sequences and the table's width come from the tensors as they are at the call."""
+    lens, table = torch.zeros(4, dtype=torch.int32), i32(4, 6)
+    p = host.Paging(lens, block_tables=table)
+    assert (p.struct().batch, p.struct().max_blocks) == (4, 6)
+    first = p.struct()
+    assert p.struct() is first
+    at = lens.data_ptr()
+    lens.resize_(2)
+    assert lens.data_ptr() == at and p.struct().batch == 2
+    buf = torch.zeros(9, dtype=torch.int32)
+    p.seq_lens = buf[:3]
+    assert p.struct().batch == 3
+    p.seq_lens.data = buf[:4]           # the same address, another length
+    assert p.struct().batch == 4
+    table.resize_(4, 3)
+    assert p.struct().max_blocks == 3
+    p.seq_lens.data = buf[:9]
+    with pytest.raises(ValueError):     # more sequences than the table has rows
+        p.struct()
