@@ -338,25 +338,28 @@ def _structs(cache: PagedCache, paging: Paging) -> Tuple[KvqCache, KvqPaging]:
     return cs, ps
 
 
+# Sizes.  Buffers may be larger than the call needs (those of a captured step are sized for its largest batch), and a
+# token's rows may come flat: what is refused is what would be read or written past its end, or at another stride.
+
 def _check_rows(cache: PagedCache, t: torch.Tensor, name: str) -> None:
-    """t is [tokens, num_kv_heads, head_dim]."""
-    if t.dim() != 3 or t.shape[1] != cache.num_kv_heads or t.shape[2] != cache.head_dim:
+    """t is [tokens, num_kv_heads, head_dim], or [tokens, num_kv_heads * head_dim]."""
+    if t.dim() == 0 or t.numel() != t.shape[0] * cache.num_kv_heads * cache.head_dim:
         raise ValueError("%s must be [tokens, %d, %d], got %s" % (name, cache.num_kv_heads, cache.head_dim,
                                                                   tuple(t.shape)))
 
 
-def _check_cu(cu: torch.Tensor, batch: int, name: str) -> None:
-    if cu.numel() != batch + 1:
+def _check_cu(cu: Optional[torch.Tensor], batch: int, name: str) -> None:
+    if cu is not None and cu.numel() <= batch:
         raise ValueError("%s must have batch + 1 = %d elements, got %d" % (name, batch + 1, cu.numel()))
 
 
 def _check_q(cache: PagedCache, ps: KvqPaging, q: torch.Tensor, out: Optional[torch.Tensor]) -> None:
-    """q is [batch, num_q_heads, head_dim] and out, if given, as large."""
+    """q is [batch or more, num_q_heads, head_dim]; out, if given, holds the batch's rows."""
     shape = q.shape
-    if len(shape) != 3 or shape[0] != ps.batch or shape[2] != cache.head_dim:
+    if len(shape) != 3 or shape[0] < ps.batch or shape[2] != cache.head_dim:
         raise ValueError("q must be [%d, num_q_heads, %d], got %s" % (ps.batch, cache.head_dim, tuple(shape)))
-    if out is not None and out.numel() != q.numel():
-        raise ValueError("out must be as large as q")
+    if out is not None and out.numel() < ps.batch * shape[1] * shape[2]:
+        raise ValueError("out must hold [%d, %d, %d]" % (ps.batch, shape[1], shape[2]))
 
 
 def kvq_write(cache: PagedCache, paging: Paging, k: torch.Tensor, v: torch.Tensor,
@@ -394,17 +397,16 @@ def kvq_gather(cache: PagedCache, paging: Paging, cu_tokens: torch.Tensor, num_t
     cs, ps = _structs(cache, paging)
     dev = cache.k_pages.get_device()
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        _check_rows(cache, t, name)
-        if t.shape[0] < num_tokens:
-            raise ValueError("%s has fewer than num_tokens rows" % name)
+        if t.numel() < num_tokens * cache.num_kv_heads * cache.head_dim:
+            raise ValueError("%s must hold [%d, %d, %d], got %s" % (name, *shape, tuple(t.shape)))
     _check_cu(cu_tokens, ps.batch, "cu_tokens")
     if k_chunk is None:
         _run(device, stream, _lib.kvq_gather, ctypes.byref(cs), ctypes.byref(ps),
              _dev_ptr(cu_tokens, torch.int32, "cu_tokens", dev), int(num_tokens), _dev_ptr(k_out, None, "k_out", dev),
              _dev_ptr(v_out, None, "v_out", dev), _qdtype(k_out), _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     else:
-        if v_chunk is None or k_chunk.dtype != v_chunk.dtype or k_chunk.shape != v_chunk.shape:
-            raise ValueError("k_chunk and v_chunk must be given together, with one dtype and shape")
+        if v_chunk is None or k_chunk.dtype != v_chunk.dtype or k_chunk.numel() != v_chunk.numel():
+            raise ValueError("k_chunk and v_chunk must be given together, with one dtype and size")
         _check_rows(cache, k_chunk, "k_chunk")
         _check_cu(cu_chunk, ps.batch, "cu_chunk")
         _run(device, stream, _lib.kvq_gather_chunk, ctypes.byref(cs), ctypes.byref(ps),
