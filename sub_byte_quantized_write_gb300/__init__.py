@@ -362,6 +362,16 @@ def _check_q(cache: PagedCache, ps: KvqPaging, q: torch.Tensor, out: Optional[to
         raise ValueError("out must hold [%d, %d, %d]" % (ps.batch, shape[1], shape[2]))
 
 
+def _check_prefill(q: torch.Tensor, head_dim: int, cu_q: Optional[torch.Tensor], batch: int,
+                   out: Optional[torch.Tensor]) -> None:
+    """q is [total_q, num_q_heads, head_dim] and out, if given, as large at least."""
+    if q.shape[2] != head_dim:
+        raise ValueError("q must be [total_q, num_q_heads, %d], got %s" % (head_dim, tuple(q.shape)))
+    if out is not None and out.numel() < q.numel():
+        raise ValueError("out must hold %s" % (list(q.shape),))
+    _check_cu(cu_q, batch, "cu_q")
+
+
 def kvq_write(cache: PagedCache, paging: Paging, k: torch.Tensor, v: torch.Tensor,
               cu_new_tokens: torch.Tensor, dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise k, v [num_tokens, num_kv_heads, head_dim] and scatter them into the pages (16-bit caches: as bf16)."""
@@ -504,10 +514,11 @@ def kvq_prefill_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, cu_q: t
                      dev_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal chunked-prefill attention of q [total_q, num_q_heads, head_dim]; returns fp32 out."""
     T, Hq, D = q.shape
-    if out is None:
-        out = _empty((T, Hq, D), torch.float32, q.device, stream)
     cs, ps = _structs(cache, paging)
     dev = cache.k_pages.get_device()
+    _check_prefill(q, cache.head_dim, cu_q, ps.batch, out)
+    if out is None:
+        out = _empty((T, Hq, D), torch.float32, q.device, stream)
     _run(cache.k_pages.device, stream, _lib.kvq_prefill_attn, ctypes.byref(cs), ctypes.byref(ps),
          _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q", dev), T, int(max_q_per_seq),
          float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev),
@@ -526,17 +537,22 @@ def kvq_prefill_dense_attn(k: torch.Tensor, v: torch.Tensor, cu_kv: torch.Tensor
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.shape != v.shape:
         raise ValueError("k and v must be bfloat16 tensors of one shape")
     T, Hq, D = q.shape
+    if k.dim() != 3:
+        raise ValueError("k and v must be [rows, num_kv_heads, head_dim], got %s" % (tuple(k.shape),))
+    dev, batch = k.get_device(), int(seq_lens.shape[0])
+    _check_prefill(q, k.shape[2], cu_q, batch, out)
+    _check_cu(cu_kv, batch, "cu_kv")
+    if window_per_kv_head is not None and window_per_kv_head.numel() < k.shape[1]:
+        raise ValueError("window_per_kv_head must have %d elements, got %d" % (k.shape[1], window_per_kv_head.numel()))
     if out is None:
         out = _empty((T, Hq, D), torch.float32, q.device, stream)
-    ps = KvqPaging(None, None, 0, int(seq_lens.shape[0]), _dev_ptr(seq_lens, torch.int32, "seq_lens"),
-                   _dev_ptr(window_per_kv_head, torch.int32, "window_per_kv_head"), int(sink_size))
-    _run(k.device, stream, _lib.kvq_prefill_dense_attn, _dev_ptr(k, name="k"), _dev_ptr(v, name="v"),
-                                       _dev_ptr(cu_kv, torch.int32, "cu_kv"), int(k.shape[0]), int(k.shape[1]),
-                                       int(k.shape[2]),
-                                       ctypes.byref(ps), _dev_ptr(q, name="q"), _qdtype(q), Hq,
-                                       _dev_ptr(cu_q, torch.int32, "cu_q"), T, int(max_q_per_seq),
-                                       float(softmax_scale), _dev_ptr(out, torch.float32, "out"),
-                                       _dev_ptr(dev_error, torch.int32, "dev_error"))
+    ps = KvqPaging(None, None, 0, batch, _dev_ptr(seq_lens, torch.int32, "seq_lens", dev),
+                   _dev_ptr(window_per_kv_head, torch.int32, "window_per_kv_head", dev), int(sink_size))
+    _run(k.device, stream, _lib.kvq_prefill_dense_attn, _dev_ptr(k, None, "k", dev), _dev_ptr(v, None, "v", dev),
+         _dev_ptr(cu_kv, torch.int32, "cu_kv", dev), int(k.shape[0]), int(k.shape[1]), int(k.shape[2]),
+         ctypes.byref(ps), _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q", dev), T,
+         int(max_q_per_seq), float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev),
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     return out
 
 
