@@ -107,7 +107,7 @@ typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1 } kvq_dtype;
 /* Bits OR-ed into *dev_error by the kernels. */
 #define KVQ_DEVERR_BLOCK_RANGE 1 /* table entry >= num_blocks: row skipped */
 #define KVQ_DEVERR_TABLE_RANGE 2 /* position / block_size >= max_blocks: row skipped */
-#define KVQ_DEVERR_SEQ_LEN 4     /* negative seq_len, or more new tokens than seq_len */
+#define KVQ_DEVERR_SEQ_LEN 4     /* negative seq_len, more new tokens than seq_len, or queries past total_q */
 #define KVQ_DEVERR_TIMEOUT 8     /* a bounded wait for an asynchronous copy gave up (never expected) */
 #define KVQ_DEVERR_BOUNDS 16     /* debug library only (libkvq_debug.so, built with -DKVQ_BOUNDS_CHECK):
                                      an index computed on the device fell outside its buffer; the access
@@ -315,7 +315,8 @@ kvq_status kvq_write_decode_attn(const kvq_cache* cache, const kvq_paging* pagin
  *
  * q    : [total_q][num_q_heads][head_dim] of `dtype`.
  * cu_q : int32 [batch + 1]; sequence b's queries are rows cu_q[b] .. cu_q[b+1]-1
- *        at positions seq_lens[b] - n_b + i.
+ *        at positions seq_lens[b] - n_b + i.  Rows outside 0 .. total_q - 1 are
+ *        skipped and set KVQ_DEVERR_SEQ_LEN.
  * max_q_per_seq : host upper bound on n_b (sizes the grid).
  * out  : fp32 [total_q][num_q_heads][head_dim]. */
 kvq_status kvq_prefill_attn(const kvq_cache* cache, const kvq_paging* paging,

@@ -281,7 +281,10 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
       return;
     }
   }
-  const int nq = min(QB, n - q0);
+  // rows past the q that was given are neither read nor written
+  const int nq = cq0 < 0 ? 0 : min(min(QB, n - q0), P.total_q - cq0 - q0);
+  if (nq < min(QB, n - q0) && tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
+  if (nq <= 0) return;
   const int p_min = L - n + q0, p_max = L - n + q0 + nq - 1;
 
   float* sc = reinterpret_cast<float*>(sm + C::OFF_SC);
