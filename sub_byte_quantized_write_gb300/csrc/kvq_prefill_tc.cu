@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
       gap = tw > ns;
     }
   }
-  const int n_virt = gap ? ns + (n_total - tw) : n_total;
+  // (max: of a length past the table, the windows may start behind the last tile)
+  const int n_virt = gap ? ns + max(n_total - tw, 0) : n_total;
   auto tile_of = [&](int v) { return (gap && v >= ns) ? tw + (v - ns) : v; };
 
   // ---- set-up: barriers, TMEM, query rows
