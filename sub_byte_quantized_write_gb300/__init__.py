@@ -163,6 +163,15 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _copy(to: torch.Tensor, t: torch.Tensor, stream) -> None:
+    """to = t, on `stream`."""
+    if stream is None:
+        to.copy_(t)
+    else:
+        with torch.cuda.stream(_as_stream(stream, t.device)):
+            to.copy_(t)
+
+
 def _run(device: torch.device, stream, fn, *args) -> None:
     """fn(*args, stream) with `device` current."""
     index = device.index
@@ -711,8 +720,8 @@ def kvq_compact(caches: Caches, paging: Paging, pins: Optional[torch.Tensor] = N
                 dev_error: Optional[torch.Tensor] = None, stream=None):
     """The used pages of each space moved to its lowest numbers, in every cache.  Returns (paging state with the
     rewritten table, page_map [spaces, num_blocks] (old number -> new, -1: unused), page_refs [spaces, num_blocks]
-    by new number, num_used [spaces]).  `out` gives the table to write; it may be `paging` itself.  Pages with a
-    positive `pins` stay where they are."""
+    by new number, num_used [spaces]).  `out` gives the table to write; it may be `paging` itself, and gets its
+    lengths where it has a tensor of its own for them.  Pages with a positive `pins` stay where they are."""
     cs, n, dev, Hkv, blocks = _cache_array(caches)
     old, headwise, rows = _page_paging(paging, "paging", dev, Hkv)
     kind = "block_tables_headwise" if headwise else "block_tables"
@@ -723,6 +732,7 @@ def kvq_compact(caches: Caches, paging: Paging, pins: Optional[torch.Tensor] = N
     to = getattr(out, kind)
     if to is None or to.shape != table.shape:
         raise ValueError("out must have a table of the same kind and shape")
+    own_lens = _page_tensor(out.seq_lens, "out.seq_lens", dev, rows) != paging.seq_lens.data_ptr()
     spaces = Hkv if headwise else 1
     if page_map is None:
         page_map = _empty((spaces, blocks), torch.int32, dev, stream)
@@ -735,4 +745,6 @@ def kvq_compact(caches: Caches, paging: Paging, pins: Optional[torch.Tensor] = N
          _page_tensor(to, "out", dev), _page_tensor(page_map, "page_map", dev, spaces * blocks),
          _page_tensor(page_refs, "page_refs", dev, spaces * blocks), _page_tensor(num_used, "num_used", dev, spaces),
          ws, nbytes, _page_tensor(dev_error, "dev_error", dev))
+    if own_lens:
+        _copy(out.seq_lens, paging.seq_lens, stream)
     return out, page_map, page_refs, num_used

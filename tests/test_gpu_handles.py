@@ -40,3 +40,31 @@ def test_tables_of_other_widths_on_a_used_handle(headwise):
     assert bool((buf[:100] == 77).all()) and bool((buf[-100:] == 77).all())
     used = (torch.tensor([64, 33, 60]) + bs - 1) // bs
     assert ((narrow >= 0).sum(1).view(B, spaces).cpu() == used[:, None]).all()
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_compaction_into_a_state_with_lengths_of_its_own(side):
+    K = kvq()
+    c = ref.make(3, 2, 4, 128, 16, [100, 33, 60], seed=8)
+    want = ref.attention64(c)
+    pag = c["pag"]
+    out = K.Paging(torch.full((3,), 10 ** 6, dtype=torch.int32, device="cuda"), block_tables=torch.empty_like(pag.block_tables))
+    stream = torch.cuda.Stream() if side else None
+    if side:
+        stream.wait_stream(torch.cuda.current_stream())
+    got, _, _, used = K.kvq_compact(c["cache"], pag, out=out, stream=stream)
+    o = K.kvq_decode_attn(c["cache"], got, c["q"], c["scale"], dev_error=c["err"], stream=stream)
+    torch.cuda.synchronize()
+    assert got is out and out.seq_lens.tolist() == [100, 33, 60] and int(c["err"].item()) == 0
+    assert int(out.block_tables.max()) == int(used) - 1
+    ref.check(o, want)
+    with pytest.raises(ValueError):     # lengths of another number of rows
+        K.kvq_compact(c["cache"], pag, out=K.Paging(out.seq_lens[:2], block_tables=out.block_tables))
+    # captured: the lengths follow at each replay
+    graph, ws = torch.cuda.CUDAGraph(), torch.empty(K.kvq_compact_workspace_size(c["cache"], pag), dtype=torch.uint8, device="cuda")
+    with torch.cuda.graph(graph):
+        K.kvq_compact(c["cache"], got, out=pag, workspace=ws)
+    pag.seq_lens.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert pag.seq_lens.tolist() == [100, 33, 60]
