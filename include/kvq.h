@@ -31,7 +31,10 @@
  *     for kvq_decode_attn_noalloc, one static scratch array per device.
  *   - Calls enqueue work on `stream` (a cudaStream_t passed as void*; NULL is
  *     the legacy default stream) and never synchronise.  Outputs are valid
- *     once the stream reaches the work.
+ *     once the stream reaches the work.  A decode call may be launched while
+ *     the kernel in front of it still runs (programmatic dependent launch, if
+ *     that kernel allows it); it reads and writes nothing that this kernel
+ *     could touch before it has ended.
  *   - Host-detectable errors (NULL pointers, unsupported shapes, misaligned
  *     pointers, a too-small workspace, Hq % Hkv != 0) return a status before
  *     any launch and leave all device memory untouched.  A failed launch

@@ -60,20 +60,31 @@ __device__ __forceinline__ bool in_bounds(bool ok, int32_t* dev_error) {
 #define KVQ_IN_BOUNDS(ok, err) true
 #endif
 
+// A load of an input.  READ_ONLY: by the read-only path, for memory that
+// nothing writes while the grid runs.  A grid that may start before the kernel
+// in front of it ends reads that kernel's outputs by ordinary loads after
+// grid_dependency_wait(): read-only ones can be moved above the wait (they
+// were: lengths of a kernel that still ran set a 16-bit decode's tile count).
+template <bool READ_ONLY, typename T>
+__device__ __forceinline__ T load_input(const T* p) {
+  if constexpr (READ_ONLY) return __ldg(p);
+  else return *p;
+}
+
 // Load EPL consecutive input elements (fp32 or bf16) as fp32 (EPL = 2, 4, 8
 // or 16; elem_off a multiple of EPL, so the vector loads are aligned).
-template <int EPL>
+template <int EPL, bool READ_ONLY = true>
 __device__ __forceinline__ void load_row_elems(const void* base, int dtype, size_t elem_off, float (&x)[EPL]) {
   if (dtype == DT_F32) {
     const float* p = reinterpret_cast<const float*>(base) + elem_off;
     if constexpr (EPL >= 4) {
 #pragma unroll
       for (int c = 0; c < EPL / 4; ++c) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p) + c);
+        const float4 v = load_input<READ_ONLY>(reinterpret_cast<const float4*>(p) + c);
         x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
       }
     } else {
-      float2 v = __ldg(reinterpret_cast<const float2*>(p));
+      float2 v = load_input<READ_ONLY>(reinterpret_cast<const float2*>(p));
       x[0] = v.x; x[1] = v.y;
     }
   } else {
@@ -81,7 +92,7 @@ __device__ __forceinline__ void load_row_elems(const void* base, int dtype, size
     if constexpr (EPL >= 8) {
 #pragma unroll
       for (int c = 0; c < EPL / 8; ++c) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + c);
+        const uint4 v = load_input<READ_ONLY>(reinterpret_cast<const uint4*>(p) + c);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -90,11 +101,11 @@ __device__ __forceinline__ void load_row_elems(const void* base, int dtype, size
         }
       }
     } else if constexpr (EPL == 4) {
-      uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      uint2 v = load_input<READ_ONLY>(reinterpret_cast<const uint2*>(p));
       x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
       x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
     } else {
-      uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p));
+      uint32_t v = load_input<READ_ONLY>(reinterpret_cast<const uint32_t*>(p));
       x[0] = __uint_as_float(v << 16); x[1] = __uint_as_float(v & 0xFFFF0000u);
     }
   }

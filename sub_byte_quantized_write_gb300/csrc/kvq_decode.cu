@@ -320,16 +320,16 @@ __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int
   constexpr int EPL = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = P.num_kv_heads, bs = P.block_size;
-  const int t0 = __ldg(P.cu_new + b), n = __ldg(P.cu_new + b + 1) - t0;
+  const int t0 = load_input<false>(P.cu_new + b), n = load_input<false>(P.cu_new + b + 1) - t0;
   if (n <= 0) return;
-  const int L = __ldg(P.seq_lens + b);
+  const int L = load_input<false>(P.seq_lens + b);
   if (L < 0 || n > L) {
     if (threadIdx.x == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
     return;
   }
   const int R = row_bytes_of(MODE, D);
   const int32_t* tbl = P.table + (size_t)(P.headwise ? b * Hkv + h : b) * P.max_blocks;
-  const RowSigns<EPL> sg = load_row_signs<EPL>(P.signs, lane);
+  const RowSigns<EPL> sg = load_row_signs<EPL, false>(P.signs, lane);
   for (int r = warp; r < 2 * n; r += 4) {
     const int i = r >> 1, kv = r & 1;
     if (t0 + i < 0 || t0 + i >= P.num_new) continue;  // as the write: rows 0 .. num_tokens - 1 only
@@ -339,7 +339,7 @@ __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int
       if (lane == 0) flag_error(P.dev_error, DEVERR_TABLE_RANGE);
       continue;
     }
-    const int blk = __ldg(tbl + lb);
+    const int blk = load_input<false>(tbl + lb);
     if (blk < 0) continue;  // evicted slot: nothing is written
     if (blk >= P.num_blocks) {
       if (lane == 0) flag_error(P.dev_error, DEVERR_BLOCK_RANGE);
@@ -347,7 +347,7 @@ __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int
     }
     if (!KVQ_IN_BOUNDS(((size_t)blk * Hkv + h) * bs + p % bs < (size_t)P.num_blocks * Hkv * bs, P.dev_error)) continue;
     float x[EPL];
-    load_row_elems<EPL>(kv ? P.new_v : P.new_k, P.new_dtype, ((size_t)(t0 + i) * Hkv + h) * D + lane * EPL, x);
+    load_row_elems<EPL, false>(kv ? P.new_v : P.new_k, P.new_dtype, ((size_t)(t0 + i) * Hkv + h) * D + lane * EPL, x);
     uint8_t* pages = const_cast<uint8_t*>(kv ? P.v_pages : P.k_pages);
     quantise_store_row<MODE, D, STEGO, 32>(sg, x, pages + (((size_t)blk * Hkv + h) * bs + p % bs) * R, lane,
                                            true);
@@ -362,13 +362,17 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = P.num_kv_heads, G = P.group, Hq = P.num_q_heads;
   __shared__ __half qh[2][NH][D];
-  allow_dependent_launch();  // the stream kernel may launch; it waits for this grid to finish
-  // This kernel may start while the write kernel before it still runs
-  // (programmatic launch): nothing here reads what the write produces except
-  // the INT8 channel scales, so INT8 waits for the write first and the other
-  // modes only before exiting -- the stream kernel, which waits for this
-  // grid, then also sees the new tokens.
-  if (MODE == MODE_INT8) grid_dependency_wait();
+  // This kernel may start while the kernel before it still runs (programmatic
+  // launch: the library's own write lets it, and so may a caller's kernel).
+  // That one may still write the queries, tables and lengths, or read memory
+  // that has since become the workspace, so nothing is touched before the
+  // wait; and the stream kernel, which looks at tables and lengths before its
+  // own wait, may launch only after it.  A write call and a decode call of its
+  // own behind it take 2 us longer so (INT4, 64 sequences: 76.1 against 74.4)
+  // than with the preparation under way while the write ran; the fused call
+  // (74.2) has its write here.
+  grid_dependency_wait();
+  allow_dependent_launch();
   // query fragments of one (sequence, kv head)
   const int bh = blockIdx.x;
   const int b = bh / Hkv, h = bh % Hkv;
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
     float x[EPL];
     if (i < G) {
       const int hq = h * G + i;
-      load_row_elems<EPL>(P.q, P.dtype, ((size_t)b * Hq + hq) * D + lane * EPL, x);
+      load_row_elems<EPL, false>(P.q, P.dtype, ((size_t)b * Hq + hq) * D + lane * EPL, x);
       if constexpr (MODE == MODE_INT8) {
         const float* am = P.ch_amax + (size_t)h * D + lane * EPL;  // K channel scales
 #pragma unroll
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
         if (P.signs) {
 #pragma unroll
           for (int e = 0; e < EPL; ++e)
-            if (__ldg(P.signs + lane * EPL + e) < 0) x[e] = -x[e];
+            if (load_input<false>(P.signs + lane * EPL + e) < 0) x[e] = -x[e];
           wht_warp<EPL>(x, lane);
         }
       }
@@ -450,10 +454,8 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
     }
     dst[q4] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
   }
-  if (MODE != MODE_INT8) grid_dependency_wait();
   if constexpr (MODE != MODE_INT8) {
-    // the step's write, after the kernels before it are done with the pools
-    if (P.new_k) fused_write_pair<MODE, D, STEGO>(P, b, h);
+    if (P.new_k) fused_write_pair<MODE, D, STEGO>(P, b, h);  // the step's write
   }
 }
 
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(128, (StreamCfg<MODE, D, NT>::CTAS)) decode_st
     uint32_t tmp[PER_LANE];
 #pragma unroll
     for (int i = 0; i < PER_LANE / 4; ++i) {
-      const uint4 v = __ldg(src + i);
+      const uint4 v = load_input<false>(src + i);
       tmp[4 * i] = v.x; tmp[4 * i + 1] = v.y; tmp[4 * i + 2] = v.z; tmp[4 * i + 3] = v.w;
     }
 #pragma unroll
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(128, (StreamCfg<MODE, D, NT>::CTAS)) decode_st
         bq[nt][s][0] = tmp[(nt * C::KSTEPS + s) * 2];
         bq[nt][s][1] = tmp[(nt * C::KSTEPS + s) * 2 + 1];
       }
-      const float4 bg = __ldg(ws.qbg + (size_t)qbh * NH + 4 * nt + tq);
+      const float4 bg = load_input<false>(ws.qbg + (size_t)qbh * NH + 4 * nt + tq);
       bet[nt] = bg.x;
       gam[nt] = bg.y;
       kcorr[nt] = bg.z;
@@ -730,9 +732,8 @@ __global__ void __launch_bounds__(128, (StreamCfg<MODE, D, NT>::CTAS)) decode_st
   };
 
   lookup();
-  // Copies wait for the kernels before: the write of this step's tokens may
-  // still run (the preparation kernel starts alongside it), and the query
-  // images and per-head constants must be ready.
+  // Copies wait for the preparation kernel: the query images and per-head
+  // constants, and the step's new rows where it writes them.
   grid_dependency_wait();
 #pragma unroll 1
   for (int k = 0; k < NSTAGE - 1; ++k) issue();
@@ -1176,7 +1177,7 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
     uint32_t tmp[PER_LANE];
 #pragma unroll
     for (int i = 0; i < PER_LANE / 4; ++i) {
-      const uint4 v = __ldg(src + i);
+      const uint4 v = load_input<false>(src + i);
       tmp[4 * i] = v.x; tmp[4 * i + 1] = v.y; tmp[4 * i + 2] = v.z; tmp[4 * i + 3] = v.w;
     }
 #pragma unroll
@@ -1186,7 +1187,7 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
         bq[nt][s][0] = tmp[(nt * C::KSTEPS + s) * 2];
         bq[nt][s][1] = tmp[(nt * C::KSTEPS + s) * 2 + 1];
       }
-      const float4 bg = __ldg(ws.qbg + (size_t)qbh * NH + 4 * nt + tq);
+      const float4 bg = load_input<false>(ws.qbg + (size_t)qbh * NH + 4 * nt + tq);
       bet[nt] = bg.x;
       gam[nt] = TC::BYTES ? 0.0f : bg.y;
       kap[nt] = TC::BYTES ? 0.0f : fmaf(-bg.x, bg.z, HR * bg.y);  // 2^(b-1) gamma - beta fold
@@ -1468,8 +1469,7 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
   };
 
   lookup();
-  // Copies wait for the kernel before: the write of this step's tokens may
-  // still run (this grid starts alongside it).
+  // Copies wait for the preparation kernel, which may write the step's new rows.
   grid_dependency_wait();
 #pragma unroll 1
   for (int k = 0; k < NSTAGE - 1; ++k) issue();

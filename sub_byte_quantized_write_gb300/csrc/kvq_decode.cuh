@@ -19,9 +19,10 @@ struct TileList {
   bool gap;
 };
 
+template <bool READ_ONLY = true>
 __device__ __forceinline__ TileList tile_list(const AttnParams& P, int b, int h, bool flag_errors, int KT) {
   TileList t;
-  int L = __ldg(P.seq_lens + b);
+  int L = load_input<READ_ONLY>(P.seq_lens + b);
   if (L < 0) {
     if (flag_errors) flag_error(P.dev_error, DEVERR_SEQ_LEN);
     L = 0;
@@ -32,7 +33,7 @@ __device__ __forceinline__ TileList tile_list(const AttnParams& P, int b, int h,
     if (flag_errors) flag_error(P.dev_error, DEVERR_TABLE_RANGE);
     t.Leff = P.max_blocks * P.block_size;
   }
-  t.W = P.window ? __ldg(P.window + h) : 0;
+  t.W = P.window ? load_input<READ_ONLY>(P.window + h) : 0;
   t.n_total = (t.Leff + KT - 1) / KT;
   t.ns = 0;
   t.tw = 0;

@@ -146,10 +146,15 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
   const int g = lane >> 2, c = lane & 3;
   const int G = P.group, Hkv = P.num_kv_heads, bs = P.block_size, BH = P.batch * Hkv;
   const int bs_log2 = __ffs(bs) - 1;
+  // The kernel before may still run (programmatic launch).  The write of the
+  // same call touches neither queries, tables and lengths nor the workspace,
+  // so only the pages wait for it; another may be writing the former or
+  // reading memory that has since become the latter.
+  if (P.new_k == nullptr) grid_dependency_wait();
   int lo, hi, gw = 0, items = 1, nruns = 1;
   if constexpr (DIRECT) {
     const bool reports = threadIdx.x == 0 && blockIdx.x % Hkv == 0;
-    const TileList t = tile_list(P, blockIdx.x / Hkv, blockIdx.x % Hkv, reports, D16_KEYS);
+    const TileList t = tile_list<false>(P, blockIdx.x / Hkv, blockIdx.x % Hkv, reports, D16_KEYS);
     lo = slice_lo(warp, t.n_virt, WARPS);
     hi = slice_lo(warp + 1, t.n_virt, WARPS);
   } else {
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
     {
       const int first = min(BH, (int)threadIdx.x * rpt * items), last = min(BH, first + rpt * items);
       int sum = 0;
-      for (int bh = first; bh < last; ++bh) sum += tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS).n_virt;
+      for (int bh = first; bh < last; ++bh) sum += tile_list<false>(P, bh / Hkv, bh % Hkv, false, D16_KEYS).n_virt;
       int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
       for (int w = 0; w < warp; ++w) x += wtot[w];
       for (int bh = first; bh < last; ++bh) {
         if (bh % items == 0) run_start[bh / items] = x;
-        const int n = tile_list(P, bh / Hkv, bh % Hkv, blockIdx.x == 0 && bh % Hkv == 0, D16_KEYS).n_virt;
+        const int n = tile_list<false>(P, bh / Hkv, bh % Hkv, blockIdx.x == 0 && bh % Hkv == 0, D16_KEYS).n_virt;
         if (blockIdx.x == 0) ws.tile_start[bh] = x;
         x += n;
       }
@@ -214,12 +219,12 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
       bh = a * items;
       start = run_start[a];
     }
-    TileList t = tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
+    TileList t = tile_list<false>(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
     if constexpr (!DIRECT) {
       while (start + t.n_virt <= x) {  // (items > 1 only)
         start += t.n_virt;
         ++bh;
-        t = tile_list(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
+        t = tile_list<false>(P, bh / Hkv, bh % Hkv, false, D16_KEYS);
       }
     }
     r.bh = bh;
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
     }
     if (!KVQ_IN_BOUNDS((key >> bs_log2) < P.max_blocks, P.dev_error)) r.mask = 0;
     if (r.mask) {
-      const int e = __ldg(P.table + (size_t)(P.headwise ? bh : bh / Hkv) * P.max_blocks + (key >> bs_log2));
+      const int e = load_input<false>(P.table + (size_t)(P.headwise ? bh : bh / Hkv) * P.max_blocks + (key >> bs_log2));
       if (e >= P.num_blocks) err |= DEVERR_BLOCK_RANGE;
       else if (e >= 0) r.row = (e * Hkv + bh % Hkv) * (bs / D16_KEYS) + ((key & (bs - 1)) / D16_KEYS);
     }
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-        if (g < G) load_row_elems<8>(P.q, DT_F32, q0 + 32 * j, x);
+        if (g < G) load_row_elems<8, false>(P.q, DT_F32, q0 + 32 * j, x);
         uint32_t t[4][3];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split3(x[2 * i], x[2 * i + 1], t[i]);
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
         for (int k = 0; k < 3; ++k)
           *reinterpret_cast<uint4*>(qw + (k * JK + j) * 512) = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
       } else {
-        qf[j] = g < G ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.q) + 2 * q0) + 4 * j)
+        qf[j] = g < G ? load_input<false>(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.q) + 2 * q0) + 4 * j)
                       : make_uint4(0, 0, 0, 0);
       }
     }
@@ -319,9 +324,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
   };
 
   Chunk cur = look_up(lane), nxt = look_up(32 + lane);
-  // The pages: the write of this step's tokens may still run (this grid
-  // starts alongside it).
-  grid_dependency_wait();
+  grid_dependency_wait();  // the pages: the write of this step's tokens may still run
   int row = __shfl_sync(0xffffffffu, cur.row, 0);
   load_k(row);
   load_v(row);

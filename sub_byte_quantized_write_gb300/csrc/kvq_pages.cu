@@ -347,9 +347,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1)
     fork_plan_kernel(const PagePlan P, const PageCopy C, int first, int last, bool copies_follow) {
   __shared__ int sm[2][33];
   BlockScan scan{sm};
-  // The copies may launch; they wait for this grid to finish.  No other kernel
-  // may: the next one in the stream can be a decode, which reads the tables and
-  // lengths written here before it waits.
+  // The copies may launch; they wait for this grid to finish.
   if (copies_follow) allow_dependent_launch();
   for (int phase = first; phase <= last; ++phase) {
     if (phase == 0) fork_init(P);
@@ -528,9 +526,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1)
     compact_plan_kernel(const PagePlan P, const PageCopy C, int first, int last, bool copies_follow) {
   __shared__ int sm[2][33];
   BlockScan scan{sm};
-  // The copies may launch; they wait for this grid to finish.  No other kernel
-  // may: the next one in the stream can be a decode, which reads the tables and
-  // lengths written here before it waits.
+  // The copies may launch; they wait for this grid to finish.
   if (copies_follow) allow_dependent_launch();
   for (int phase = first; phase <= last; ++phase) {
     if (phase == 0) compact_init(P);

@@ -41,7 +41,7 @@ struct RowSigns {
   uint32_t m[EPL];
   bool on;
 };
-template <int EPL>
+template <int EPL, bool READ_ONLY = true>
 __device__ __forceinline__ RowSigns<EPL> load_row_signs(const int8_t* signs, int sub) {
   RowSigns<EPL> r;
   r.on = signs != nullptr;
@@ -55,14 +55,14 @@ __device__ __forceinline__ RowSigns<EPL> load_row_signs(const int8_t* signs, int
       if constexpr (EPL >= 16) {
 #pragma unroll
         for (int v = 0; v < EPL / 16; ++v) {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + v);
+          const uint4 q = load_input<READ_ONLY>(reinterpret_cast<const uint4*>(p) + v);
           w[4 * v] = q.x; w[4 * v + 1] = q.y; w[4 * v + 2] = q.z; w[4 * v + 3] = q.w;
         }
       } else if constexpr (EPL == 8) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 q = load_input<READ_ONLY>(reinterpret_cast<const uint2*>(p));
         w[0] = q.x; w[1] = q.y;
       } else {
-        w[0] = __ldg(reinterpret_cast<const unsigned int*>(p));
+        w[0] = load_input<READ_ONLY>(reinterpret_cast<const unsigned int*>(p));
       }
 #pragma unroll
       for (int i = 0; i < EPL; ++i) r.m[i] = (w[i / 4] << (24 - 8 * (i % 4))) & 0x80000000u;
@@ -70,7 +70,7 @@ __device__ __forceinline__ RowSigns<EPL> load_row_signs(const int8_t* signs, int
     }
   }
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) r.m[i] = (uint32_t)(__ldg(p + i) & 0x80) << 24;
+  for (int i = 0; i < EPL; ++i) r.m[i] = (uint32_t)(load_input<READ_ONLY>(p + i) & 0x80) << 24;
   return r;
 }
 

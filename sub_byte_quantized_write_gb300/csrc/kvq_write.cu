@@ -102,8 +102,7 @@ template <int MODE, int D, bool STEGO>
 __global__ void __launch_bounds__(256) write_token_head_kernel(WriteParams P) {
   constexpr int EPL = D / 32;
   const int lane = threadIdx.x & 31;
-  // a decode call after this write may start its query preparation now; it
-  // waits for this grid before anything reads the pages written here
+  // a decode call after this write may launch now; it waits for this grid
   allow_dependent_launch();
   const long long wid = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int kv = (int)(wid & 1);
