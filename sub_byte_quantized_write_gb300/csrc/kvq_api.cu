@@ -155,6 +155,13 @@ kvq_status check_q(const kvq_cache* c, const void* q, int32_t dtype, int32_t hq,
   return KVQ_OK;
 }
 
+// The rows of one write or gather launch fit its grid.
+kvq_status check_tokens(const kvq_cache* c, int32_t num_tokens) {
+  if ((long long)num_tokens * c->num_kv_heads * 2 / 8 + 1 > 0x7FFFFFFFLL)
+    return fail(KVQ_ERR_UNSUPPORTED, "too many tokens for one call");
+  return KVQ_OK;
+}
+
 // The prefill launch's grid (query tiles, kv heads, sequences) must fit the
 // launch limits: x < 2^31, y and z <= 65535.
 kvq_status check_prefill_grid(const kvq::AttnParams& P) {
@@ -235,8 +242,7 @@ kvq_status kvq_write(const kvq_cache* cache, const kvq_paging* paging, const voi
   if (!k || !v || !cu_new_tokens) return fail(KVQ_ERR_INVALID_ARG, "k / v / cu_new_tokens is NULL");
   if (dtype != KVQ_F32 && dtype != KVQ_BF16) return fail(KVQ_ERR_UNSUPPORTED, "dtype must be KVQ_F32 or KVQ_BF16");
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(KVQ_ERR_INVALID_ARG, "k / v must be 16-byte aligned");
-  if ((long long)num_tokens * cache->num_kv_heads * 2 / 8 + 1 > 0x7FFFFFFFLL)
-    return fail(KVQ_ERR_UNSUPPORTED, "too many tokens for one call");
+  if ((st = check_tokens(cache, num_tokens)) != KVQ_OK) return st;
   const kvq::WriteParams P = write_params(cache, paging, k, v, dtype, cu_new_tokens, num_tokens, dev_error);
   cudaError_t e = kvq::launch_write(P, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
@@ -269,8 +275,7 @@ kvq_status kvq_gather_chunk(const kvq_cache* cache, const kvq_paging* paging, co
     return fail(KVQ_ERR_UNSUPPORTED, "chunk_dtype must be KVQ_F32 or KVQ_BF16");
   if (k_chunk && (!aligned(k_chunk, 16) || !aligned(v_chunk, 16)))
     return fail(KVQ_ERR_INVALID_ARG, "k_chunk / v_chunk must be 16-byte aligned");
-  if ((long long)num_tokens * cache->num_kv_heads * 2 / 8 + 1 > 0x7FFFFFFFLL)
-    return fail(KVQ_ERR_UNSUPPORTED, "too many tokens for one call");
+  if ((st = check_tokens(cache, num_tokens)) != KVQ_OK) return st;
   kvq::WriteParams P;
   std::memset(&P, 0, sizeof(P));
   P.k_pages = cache->k_pages;
@@ -371,6 +376,7 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
     if ((long long)paging->batch * cache->num_kv_heads * paging->max_blocks > 0x7FFFFFFFLL / (cache->block_size / 16))
       return fail(KVQ_ERR_UNSUPPORTED, "batch * num_kv_heads * table width too large");
     if (fw.k) {  // 16-bit pages: the step's write is a launch of its own, which the decode's start overlaps
+      if ((st = check_tokens(cache, fw.num_tokens)) != KVQ_OK) return st;
       const cudaError_t e = kvq::launch_write(
           write_params(cache, paging, fw.k, fw.v, fw.dtype, fw.cu_new, fw.num_tokens, dev_error),
           static_cast<cudaStream_t>(stream));

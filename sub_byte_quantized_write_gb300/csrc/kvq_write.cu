@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(256) gather16_kernel(WriteParams P) {
   }
 }
 
-inline unsigned rows16_blocks(const WriteParams& P) {  // (the callers bound num_tokens * num_kv_heads)
+inline unsigned rows16_blocks(const WriteParams& P) {  // (num_tokens * num_kv_heads <= 2^33: the API's check)
   return (unsigned)(((long long)P.num_tokens * P.num_kv_heads * (P.head_dim / 8) + 255) / 256);
 }
 

@@ -43,3 +43,14 @@ def test_python_cache_shapes(K):  # noqa: F811
     assert tuple(c.k_pages.shape) == (3, 2, 16, 128)
     with pytest.raises(ValueError):
         K.PagedCache(K.KVQ_BF16_CACHE, 3, 2, 16, 80, device="cpu")
+
+
+def test_a_step_of_more_tokens_than_one_write_takes(K):  # noqa: F811
+    """The bound of kvq_write holds for the write inside a 16-bit step."""
+    L, ref = K.lib(), ctypes.byref
+    c = _cache(K, mode=K.KVQ_BF16_CACHE, num_kv_heads=8)
+    many = 0x7FFFFFFF
+    assert L.kvq_write(ref(c), ref(_paging(K)), 4096, 4096, 1, 4096, many, None, None) == K.KVQ_ERR_UNSUPPORTED
+    assert L.kvq_write_decode_attn(ref(c), ref(_paging(K)), 4096, 4096, 1, 4096, many, 256, 1, 8, 0.1, 256, 256, 1 << 40, 0,
+                                   None, None) == K.KVQ_ERR_UNSUPPORTED
+    assert b"too many tokens" in L.kvq_last_error()
