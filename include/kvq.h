@@ -174,7 +174,8 @@ typedef struct {
  *   Token position p of a row lives in page table[row][p / block_size], slot
  *   p % block_size.  An entry < 0 (-1 sentinel) marks an evicted block: it is
  *   never dereferenced, writes to it are dropped and its keys contribute
- *   nothing ([FD-HEADWISE] PR2-only delta, Correctness gates).
+ *   nothing ([FD-HEADWISE] PR2-only delta, Correctness gates).  The attention
+ *   calls take max_blocks * block_size up to 2^31 - 1.
  * seq_lens int32 [batch]: tokens in the cache for each sequence AFTER this
  *   step's write.  Decode queries sit at position seq_lens[b] - 1.
  * window_per_kv_head int32 [num_kv_heads] or NULL (= all heads full):

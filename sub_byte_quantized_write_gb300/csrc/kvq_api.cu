@@ -155,6 +155,13 @@ kvq_status check_q(const kvq_cache* c, const void* q, int32_t dtype, int32_t hq,
   return KVQ_OK;
 }
 
+// The attention kernels count a sequence's positions in 32 bits.
+kvq_status check_positions(const kvq_cache* c, const kvq_paging* p) {
+  if ((long long)p->max_blocks * c->block_size > 0x7FFFFFFFLL)
+    return fail(KVQ_ERR_UNSUPPORTED, "table too wide for 32-bit positions");
+  return KVQ_OK;
+}
+
 // The rows of one write or gather launch fit its grid.
 kvq_status check_tokens(const kvq_cache* c, int32_t num_tokens) {
   if ((long long)num_tokens * c->num_kv_heads * 2 / 8 + 1 > 0x7FFFFFFFLL)
@@ -354,6 +361,7 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
   if ((st = check_q(cache, q, dtype, num_q_heads, out)) != KVQ_OK) return st;
   if ((long long)paging->batch * cache->num_kv_heads + 1 > 0x7FFFFFFFLL)
     return fail(KVQ_ERR_UNSUPPORTED, "batch * num_kv_heads too large");
+  if ((st = check_positions(cache, paging)) != KVQ_OK) return st;
   const kvq::DecodeLayout L = decode_layout(cache, paging, num_q_heads);
   if (!workspace || workspace_bytes < L.total) return fail(KVQ_ERR_WORKSPACE, "workspace missing or too small");
   if (!aligned(workspace, 256)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -371,8 +379,6 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
   if (cache->mode == KVQ_BF16_CACHE) {
     if ((long long)cache->num_blocks * cache->num_kv_heads * (cache->block_size / 16) > 0x7FFFFFFFLL)
       return fail(KVQ_ERR_UNSUPPORTED, "pool too large for 32-bit chunk numbers");
-    if ((long long)paging->max_blocks * cache->block_size > 0x7FFFFFFFLL)
-      return fail(KVQ_ERR_UNSUPPORTED, "table too wide for 32-bit positions");
     if ((long long)paging->batch * cache->num_kv_heads * paging->max_blocks > 0x7FFFFFFFLL / (cache->block_size / 16))
       return fail(KVQ_ERR_UNSUPPORTED, "batch * num_kv_heads * table width too large");
     if (fw.k) {  // 16-bit pages: the step's write is a launch of its own, which the decode's start overlaps
@@ -471,6 +477,7 @@ kvq_status kvq_prefill_attn(const kvq_cache* cache, const kvq_paging* paging, co
   if (paging->batch == 0 || total_q == 0 || max_q_per_seq == 0) return KVQ_OK;
   if ((st = check_q(cache, q, dtype, num_q_heads, out)) != KVQ_OK) return st;
   if (!cu_q) return fail(KVQ_ERR_INVALID_ARG, "cu_q is NULL");
+  if ((st = check_positions(cache, paging)) != KVQ_OK) return st;
   kvq::AttnParams P = attn_params(cache, paging, q, dtype, num_q_heads, softmax_scale, out, dev_error);
   P.cu_q = cu_q;
   P.total_q = total_q;
