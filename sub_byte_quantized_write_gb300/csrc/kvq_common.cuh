@@ -338,7 +338,8 @@ __device__ __forceinline__ uint64_t l2_evict_first_policy() {
 
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialisation may start while its predecessor runs; it must call
-// grid_dependency_wait() before touching anything the predecessor writes.
+// grid_dependency_wait() before touching anything the predecessor writes, and
+// read that by load_input<false>.
 // The predecessor lets it launch early with allow_dependent_launch().
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

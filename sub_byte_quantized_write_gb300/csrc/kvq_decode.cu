@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(128, (StreamCfg<MODE, D, NT>::CTAS)) decode_st
   allow_dependent_launch();  // the merge kernel may launch; it waits for this grid to finish
   // Slices come from the tile counts themselves (a prefix scan per CTA over
   // all (sequence, kv head) pairs, thread t owning a contiguous run of
-  // pairs), worked out while the kernels before still run.
+  // pairs), worked out while the preparation kernel runs.
   __shared__ int run_start[129];
   const int items = (BH + 127) / 128;
   {

@@ -69,7 +69,7 @@ struct AttnParams {
   // decode with the step's write (kvq_write_decode_attn): the preparation
   // kernel quantises and stores the new K / V rows [num_new][Hkv][D] of
   // new_dtype; sequence b's are rows cu_new[b] .. cu_new[b+1] - 1 (NULL new_k:
-  // no write)
+  // no write).  16-bit pages: the write is the launch in front of the decode.
   const void* new_k;
   const void* new_v;
   int new_dtype, num_new;
