@@ -732,7 +732,7 @@ def kvq_compact(caches: Caches, paging: Paging, pins: Optional[torch.Tensor] = N
     to = getattr(out, kind)
     if to is None or to.shape != table.shape:
         raise ValueError("out must have a table of the same kind and shape")
-    own_lens = _page_tensor(out.seq_lens, "out.seq_lens", dev, rows) != paging.seq_lens.data_ptr()
+    own_lens = _page_tensor(out.seq_lens, "out.seq_lens", dev, rows) not in (None, paging.seq_lens.data_ptr())
     spaces = Hkv if headwise else 1
     if page_map is None:
         page_map = _empty((spaces, blocks), torch.int32, dev, stream)

@@ -68,3 +68,10 @@ def test_compaction_into_a_state_with_lengths_of_its_own(side):
     graph.replay()
     torch.cuda.synchronize()
     assert pag.seq_lens.tolist() == [100, 33, 60]
+
+
+def test_compaction_into_a_table_without_lengths():
+    K = kvq()
+    c = ref.make(3, 2, 4, 128, 16, [100, 33, 60], seed=8)
+    out, _, _, used = K.kvq_compact(c["cache"], c["pag"], out=K.Paging(None, block_tables=torch.empty_like(c["pag"].block_tables)))
+    assert out.seq_lens is None and int(out.block_tables.max()) == int(used) - 1
