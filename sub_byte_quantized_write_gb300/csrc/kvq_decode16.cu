@@ -40,10 +40,10 @@
 //  * Masked keys: the logit is replaced by -inf and the value row by zeros,
 //    since a stale slot may hold a NaN, which a zero weight would not cancel.
 // Measured (one GB300, 6792 GB/s a plain copy's): 64 sequences of 1024 .. 8192
-// keys, 8 kv heads, 1.21 GB: 184 us a call, 6.6 TB/s (the stream kernel 177 to
-// 181 us; 21% of the issue slots, 18% of the tensor pipe busy); 32 sequences of
-// 32768 with windows, 2.42 GB: 350 us, 6.9 TB/s; one sequence of 131071 keys,
-// 4 kv heads: 50 us, 5.3 TB/s (its start and the merge of 1824 records are 10 us
+// keys, 8 kv heads, 1.21 GB: 182 us a call, 6.6 TB/s (with fp32 queries too; 21%
+// of the issue slots, 18% of the tensor pipe busy); 32 sequences of
+// 32768 with windows, 2.42 GB: 345 us, 7.0 TB/s; one sequence of 131071 keys,
+// 4 kv heads: 50 us, 5.4 TB/s (its start and the merge of 1824 records are 10 us
 // of it).  12 warps of 168 registers keep 96 KB per SM in flight; 13 and 14,
 // which spill, take 229 and 235 us.  At D = 64 a warp has half as much in
 // flight: 16 warps of 125 registers read 0.60 GB (the first case's lengths) in
