@@ -219,6 +219,83 @@ kvq_status kvq_write(const kvq_cache* cache, const kvq_paging* paging,
                      const int32_t* cu_new_tokens, int32_t num_tokens,
                      int32_t* dev_error, void* stream);
 
+/* Rotary positions.  Pair i of a row at position p turns by the angle p f_i:
+ * (a, b) becomes scale * (a cos - b sin, b cos + a sin).  The pairs are dims
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) where interleaved; dims from rot_dim on
+ * stay as they are.  Angles are counted in 64-bit fixed point (exact to 2^-33
+ * of a turn at any 32-bit position, beside inv_freq's own rounding), the rest
+ * in fp32; rows are rounded once, where they are stored.
+ * inv_freq : fp32 [rot_dim / 2] (device): f_i, radians per position, below 2^16 in size.
+ * rot_dim  : a multiple of 16, up to head_dim.
+ * scale    : on cosine and sine; 1 unless a scaled context asks for another.
+ *
+ * `positions`, where a call takes it: int32 [num_tokens] (device; negative ones
+ * turn backwards) in place of the places in the sequence, or NULL.  It only
+ * sets the angle, not the slot a row is stored in. */
+typedef struct {
+  const float* inv_freq;
+  int32_t rot_dim;
+  int32_t interleaved;
+  float scale;
+} kvq_rotary;
+
+/* How kvq_rope_frequencies spreads a context over `factor` times the first.
+ *   PLAIN       f_i = base^(-2i / rot_dim)
+ *   LINEAR      f_i / factor
+ *   BASE        PLAIN with base * factor^(rot_dim / (rot_dim - 2))
+ *   TURNS       pairs that make `fast` turns or more over the first context as
+ *               they are, `slow` turns or fewer f_i / factor, in between a ramp
+ *               over the pair's number; scale 0.1 ln(factor) + 1
+ *   WAVELENGTH  the same ends, in between a ramp over the turns; scale 1 */
+typedef enum {
+  KVQ_ROPE_PLAIN = 0,
+  KVQ_ROPE_LINEAR = 1,
+  KVQ_ROPE_BASE = 2,
+  KVQ_ROPE_TURNS = 3,
+  KVQ_ROPE_WAVELENGTH = 4
+} kvq_rope_kind;
+typedef struct {
+  int32_t kind;   /* kvq_rope_kind */
+  double factor;  /* 1 or more */
+  double context; /* TURNS, WAVELENGTH: tokens of the first context */
+  double fast;    /* TURNS, WAVELENGTH: turns over it, fast > slow > 0 (often 32 and 1, or 4 and 1) */
+  double slow;
+} kvq_rope_scaling;
+
+/* Fills inv_freq [rot_dim / 2] and *scale (nullable) of a kvq_rotary, both on
+ * the HOST; worked out in 64 bits.  scaling NULL: PLAIN. */
+kvq_status kvq_rope_frequencies(int32_t rot_dim, double base, const kvq_rope_scaling* scaling, float* inv_freq,
+                                float* scale);
+
+/* kvq_rope -- rows of q and k turned to their positions: what stands between a
+ * layer's projections and kvq_write, the prefill calls or kvq_decode_attn.
+ * q, k       : [num_tokens][heads][head_dim] of `dtype`, 16-byte aligned; q or k
+ *              may be NULL.  Tokens are *_stride elements apart (0: heads *
+ *              head_dim; a multiple of 16 bytes), so rows of a packed projection
+ *              can be given as they lie.
+ * q_out, k_out : the turned rows, of the same dtype; may be q / k themselves (with
+ *              the same stride), and may not overlap an input otherwise.
+ * paging     : seq_lens and batch are used (tables and windows are not looked
+ *              at): token i of sequence b, row cu_tokens[b] + i, is at position
+ *              seq_lens[b] - n_b + i (kvq_write's map).  Rows outside every
+ *              sequence are left as they were; a sequence with more tokens than
+ *              seq_lens sets KVQ_DEVERR_SEQ_LEN and is left too.
+ * positions  : given, every row turns to its own entry, and paging and cu_tokens
+ *              are not looked at (may be NULL). */
+kvq_status kvq_rope(const kvq_rotary* rope, const int32_t* positions, const kvq_paging* paging,
+                    const int32_t* cu_tokens, const void* q, void* q_out, int32_t num_q_heads, int64_t q_stride,
+                    int64_t q_out_stride, const void* k, void* k_out, int32_t num_kv_heads, int64_t k_stride,
+                    int64_t k_out_stride, int32_t head_dim, int32_t dtype, int32_t num_tokens, int32_t* dev_error,
+                    void* stream);
+
+/* kvq_rope_write -- kvq_write of K rows that are turned on the way (in fp32,
+ * with no rounding between the turn and the quantiser), V rows as given.  Not
+ * for KVQ_INT8_CHANNEL (KVQ_ERR_UNSUPPORTED: kvq_rope, then kvq_write).  The
+ * rest as kvq_write. */
+kvq_status kvq_rope_write(const kvq_cache* cache, const kvq_paging* paging, const kvq_rotary* rope,
+                          const int32_t* positions, const void* k, const void* v, int32_t dtype,
+                          const int32_t* cu_new_tokens, int32_t num_tokens, int32_t* dev_error, void* stream);
+
 /* kvq_gather -- read rows of given positions back from the pages as dense,
  * dequantised values in the input domain (inverse RHT applied): the gather
  * and dequantise step a prefill can run before dense attention ([FD-INT2]
@@ -310,6 +387,20 @@ kvq_status kvq_write_decode_attn(const kvq_cache* cache, const kvq_paging* pagin
                                  float softmax_scale, float* out,
                                  void* workspace, size_t workspace_bytes, int32_t num_splits,
                                  int32_t* dev_error, void* stream);
+
+/* kvq_rope_write_decode_attn -- kvq_write_decode_attn with rotary positions:
+ * the query of each sequence and its new K rows are turned inside the call, the
+ * rows then written and attended to as there.  A query turns to the position of
+ * its sequence's last token: seq_lens[b] - 1, or, with `positions` and new
+ * tokens of the sequence, the entry of the last of them.  16-bit pages and
+ * num_tokens == 0 as in kvq_write_decode_attn; not for KVQ_INT8_CHANNEL. */
+kvq_status kvq_rope_write_decode_attn(const kvq_cache* cache, const kvq_paging* paging, const kvq_rotary* rope,
+                                      const int32_t* positions, const void* k, const void* v, int32_t kv_dtype,
+                                      const int32_t* cu_new_tokens, int32_t num_tokens,
+                                      const void* q, int32_t q_dtype, int32_t num_q_heads,
+                                      float softmax_scale, float* out,
+                                      void* workspace, size_t workspace_bytes, int32_t num_splits,
+                                      int32_t* dev_error, void* stream);
 
 /* kvq_prefill_attn -- causal chunked-prefill attention of a chunk of queries
  * against everything in the cache, the chunk itself included (write the chunk

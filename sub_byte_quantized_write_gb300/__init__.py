@@ -9,7 +9,8 @@ built, importing this package raises ImportError.
 Names mirror the C calls: ``kvq_write``, ``kvq_gather``, ``kvq_prefill_dense_attn``, ``kvq_decode_attn``,
 ``kvq_write_decode_attn``,
 ``kvq_decode_attn_noalloc``, ``kvq_prefill_attn``, ``kvq_decode_workspace_size``,
-``kvq_row_bytes``, ``kvq_copy_pages``, ``kvq_fork``, ``kvq_compact`` and their ``_workspace_size``.
+``kvq_row_bytes``, ``kvq_copy_pages``, ``kvq_fork``, ``kvq_compact`` and their ``_workspace_size``,
+``kvq_rope``, ``kvq_rope_write``, ``kvq_rope_write_decode_attn``, ``kvq_rope_frequencies``.
 
 A call runs on the device of its cache, on `stream` if one is given, else on
 that device's current stream; what it allocates belongs to that stream.
@@ -42,6 +43,7 @@ KVQ_INT8_TOKEN_HEAD, KVQ_FP8_TOKEN_HEAD, KVQ_BF16_CACHE = 4, 5, 6
 KVQ_F32, KVQ_BF16 = 0, 1
 KVQ_DEVERR_BLOCK_RANGE, KVQ_DEVERR_TABLE_RANGE, KVQ_DEVERR_SEQ_LEN, KVQ_DEVERR_TIMEOUT = 1, 2, 4, 8
 KVQ_DEVERR_BOUNDS = 16  # debug library only
+KVQ_ROPE_PLAIN, KVQ_ROPE_LINEAR, KVQ_ROPE_BASE, KVQ_ROPE_TURNS, KVQ_ROPE_WAVELENGTH = 0, 1, 2, 3, 4
 KVQ_DEVERR_ROW_RANGE, KVQ_DEVERR_NO_PAGES, KVQ_DEVERR_PAGE_CONFLICT = 32, 64, 128
 
 
@@ -58,6 +60,16 @@ class KvqPaging(ctypes.Structure):
                 ("max_blocks", ctypes.c_int32), ("batch", ctypes.c_int32),
                 ("seq_lens", ctypes.c_void_p), ("window_per_kv_head", ctypes.c_void_p),
                 ("sink_size", ctypes.c_int32)]
+
+
+class KvqRotary(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class KvqRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("context", ctypes.c_double),
+                ("fast", ctypes.c_double), ("slow", ctypes.c_double)]
 
 
 _P, _I = ctypes.c_void_p, ctypes.c_int32
@@ -87,6 +99,17 @@ _lib.kvq_prefill_attn.restype = _I
 _lib.kvq_prefill_dense_attn.argtypes = [_P, _P, _P, _I, _I, _I, _PP, _P, _I, _I, _P, _I, _I, ctypes.c_float, _P, _P,
                                         _P]
 _lib.kvq_prefill_dense_attn.restype = _I
+_RP, _L = ctypes.POINTER(KvqRotary), ctypes.c_int64
+_lib.kvq_rope_frequencies.argtypes = [_I, ctypes.c_double, ctypes.POINTER(KvqRopeScaling),
+                                      ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]
+_lib.kvq_rope_frequencies.restype = _I
+_lib.kvq_rope.argtypes = [_RP, _P, _PP, _P, _P, _P, _I, _L, _L, _P, _P, _I, _L, _L, _I, _I, _I, _P, _P]
+_lib.kvq_rope.restype = _I
+_lib.kvq_rope_write.argtypes = [_CP, _PP, _RP, _P, _P, _P, _I, _P, _I, _P, _P]
+_lib.kvq_rope_write.restype = _I
+_lib.kvq_rope_write_decode_attn.argtypes = [_CP, _PP, _RP, _P, _P, _P, _I, _P, _I, _P, _I, _I, ctypes.c_float, _P, _P,
+                                            ctypes.c_size_t, _I, _P, _P]
+_lib.kvq_rope_write_decode_attn.restype = _I
 _SZ = ctypes.POINTER(ctypes.c_size_t)
 _lib.kvq_copy_workspace_size.argtypes = [_CP, _I, _I, _I, _SZ]
 _lib.kvq_copy_workspace_size.restype = _I
@@ -237,6 +260,10 @@ def _cache_tensors(c):
     return c.k_pages, c.v_pages, c.rht_signs, c.ch_amax, c.ch_amax_ready
 
 
+def _rope_tensors(r):
+    return (r.inv_freq,)
+
+
 def _paging_tensors(p):
     return p.seq_lens, p.block_tables, p.block_tables_headwise, p.window_per_kv_head
 
@@ -329,6 +356,39 @@ class Paging(_Handle):
                          _dev_ptr(self.seq_lens, torch.int32, "seq_lens"),
                          _dev_ptr(self.window_per_kv_head, torch.int32, "window_per_kv_head"),
                          self.sink_size)
+
+
+class Rope(_Handle):
+    """Rotary positions of a layer: inv_freq fp32 [rot_dim / 2] (radians per position; rot_dim a multiple of 16 up
+    to head_dim), the layout of the pairs (dims (i, i + rot_dim / 2), or (2i, 2i + 1) where interleaved) and the
+    factor on cosine and sine.  kvq_rope_frequencies gives inv_freq and scale."""
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False, scale: float = 1.0):
+        self.__dict__.update(inv_freq=inv_freq, interleaved=bool(interleaved), scale=float(scale), _struct=None)
+
+    @property
+    def rot_dim(self) -> int:
+        return 2 * self.inv_freq.numel()
+
+    def struct(self) -> KvqRotary:
+        """The C struct: built once, and again when an attribute was set or the tensor's memory or shape changed."""
+        return _kept_struct(self, _rope_tensors, True)
+
+    def _build(self) -> KvqRotary:
+        return KvqRotary(_dev_ptr(self.inv_freq, torch.float32, "inv_freq"), self.rot_dim, int(self.interleaved),
+                         self.scale)
+
+
+def _rope_struct(rope: Rope, dev: int) -> KvqRotary:
+    struct = rope.struct()
+    if rope.inv_freq.get_device() != dev:
+        raise ValueError("inv_freq must be on the device of the call")
+    return struct
+
+
+def _check_positions(positions: Optional[torch.Tensor], tokens: int) -> None:
+    if positions is not None and positions.numel() < tokens:
+        raise ValueError("positions must have %d elements, got %d" % (tokens, positions.numel()))
 
 
 def _structs(cache: PagedCache, paging: Paging) -> Tuple[KvqCache, KvqPaging]:
@@ -562,6 +622,131 @@ def kvq_prefill_dense_attn(k: torch.Tensor, v: torch.Tensor, cu_kv: torch.Tensor
          ctypes.byref(ps), _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q", dev), T,
          int(max_q_per_seq), float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev),
          _dev_ptr(dev_error, torch.int32, "dev_error", dev))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+
+def kvq_rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = KVQ_ROPE_PLAIN, factor: float = 1.0,
+                         context: float = 0.0, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(inv_freq fp32 [rot_dim / 2] on `device`, scale) of a Rope; `kind` and the rest as in kvq_rope_scaling."""
+    host, scale = torch.empty(max(1, rot_dim // 2), dtype=torch.float32), ctypes.c_float(1.0)
+    scaling = KvqRopeScaling(int(kind), float(factor), float(context), float(fast), float(slow))
+    _check(_lib.kvq_rope_frequencies(int(rot_dim), float(base), ctypes.byref(scaling),
+                                     ctypes.cast(host.data_ptr(), ctypes.POINTER(ctypes.c_float)), ctypes.byref(scale)))
+    return host.to(device), scale.value
+
+
+def _token_rows(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype) -> Tuple[int, int]:
+    """(pointer, elements between tokens) of t [tokens, heads, head_dim], whose tokens may lie apart."""
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the device of inv_freq" % name)
+    if t.dtype is not dtype:
+        raise ValueError("q, k and their outputs must have one dtype")
+    _, H, D = t.shape
+    step, head, dim = t.stride()
+    if t.shape[0] <= 1:
+        step = H * D
+    if (dim != 1 and D > 1) or (head != D and H > 1) or step < H * D:
+        raise ValueError("%s: the heads of a token must lie one after another" % name)
+    return t.data_ptr(), step
+
+
+def kvq_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], seq_lens: Optional[torch.Tensor] = None,
+             cu_tokens: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+             q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+             dev_error: Optional[torch.Tensor] = None, stream=None):
+    """q [tokens, num_q_heads, head_dim] and k [tokens, num_kv_heads, head_dim] (either may be None) turned to their
+    positions: by seq_lens and cu_tokens as in kvq_write, or `positions` (int32 [tokens]).  Returns (q_out, k_out),
+    which may be q and k themselves; rows outside every sequence are left as they were."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("neither q nor k is given")
+    device, tokens = first.device, int(first.shape[0])
+    dev = first.get_device()
+    rs = _rope_struct(rope, dev)
+    args, outs = [], []
+    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            if out is not None:
+                raise ValueError("%s_out without %s" % (name, name))
+            args += [None, None, 0, 0, 0]
+            outs.append(None)
+            continue
+        if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != first.shape[2]:
+            raise ValueError("q and k must be [tokens, heads, head_dim] of the same tokens and head_dim")
+        if out is None:
+            out = _empty(t.shape, t.dtype, device, stream)
+        elif out.shape != t.shape:
+            raise ValueError("%s_out must have the shape of %s" % (name, name))
+        p, step = _token_rows(t, name, dev, first.dtype)
+        po, step_out = _token_rows(out, name + "_out", dev, first.dtype)
+        args += [p, po, int(t.shape[1]), step, step_out]
+        outs.append(out)
+    ps = None
+    if positions is None:
+        if seq_lens is None or cu_tokens is None:
+            raise ValueError("seq_lens and cu_tokens, or positions, must be given")
+        _check_cu(cu_tokens, int(seq_lens.shape[0]), "cu_tokens")
+        ps = ctypes.byref(KvqPaging(None, None, 0, int(seq_lens.shape[0]), _dev_ptr(seq_lens, torch.int32, "seq_lens", dev),
+                                    None, 0))
+    else:
+        _check_positions(positions, tokens)
+        cu_tokens = None
+    _run(device, stream, _lib.kvq_rope, ctypes.byref(rs), _dev_ptr(positions, torch.int32, "positions", dev), ps,
+         _dev_ptr(cu_tokens, torch.int32, "cu_tokens", dev), *args, int(first.shape[2]), _qdtype(first), tokens,
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
+    return outs[0], outs[1]
+
+
+def kvq_rope_write(cache: PagedCache, paging: Paging, rope: Rope, k: torch.Tensor, v: torch.Tensor,
+                   cu_new_tokens: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                   dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """kvq_write of K rows that are turned to their positions on the way (not for INT8 per-channel caches)."""
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    cs, ps = _structs(cache, paging)
+    dev = cache.k_pages.get_device()
+    rs = _rope_struct(rope, dev)
+    _check_rows(cache, k, "k")
+    _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
+    _check_positions(positions, int(k.shape[0]))
+    _run(cache.k_pages.device, stream, _lib.kvq_rope_write, ctypes.byref(cs), ctypes.byref(ps), ctypes.byref(rs),
+         _dev_ptr(positions, torch.int32, "positions", dev), _dev_ptr(k, None, "k", dev), _dev_ptr(v, None, "v", dev),
+         _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens", dev), int(k.shape[0]),
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
+
+
+def kvq_rope_write_decode_attn(cache: PagedCache, paging: Paging, rope: Rope, k: torch.Tensor, v: torch.Tensor,
+                               cu_new_tokens: torch.Tensor, q: torch.Tensor, softmax_scale: float,
+                               positions: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None, num_splits: int = 0,
+                               dev_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """kvq_write_decode_attn with rotary positions: the queries and the new K rows are turned inside the call, the
+    query of a sequence to its last token's position; returns fp32 out."""
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    B, Hq, D = q.shape
+    given = out
+    if out is None:
+        out = _empty((B, Hq, D), torch.float32, q.device, stream)
+    if workspace is None:
+        nbytes, _ = kvq_decode_workspace_size(cache, paging, Hq, num_splits)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
+    cs, ps = _structs(cache, paging)
+    dev = cache.k_pages.get_device()
+    rs = _rope_struct(rope, dev)
+    _check_rows(cache, k, "k")
+    _check_cu(cu_new_tokens, ps.batch, "cu_new_tokens")
+    _check_positions(positions, int(k.shape[0]))
+    _check_q(cache, ps, q, given)
+    _run(cache.k_pages.device, stream, _lib.kvq_rope_write_decode_attn, ctypes.byref(cs), ctypes.byref(ps),
+         ctypes.byref(rs), _dev_ptr(positions, torch.int32, "positions", dev), _dev_ptr(k, None, "k", dev),
+         _dev_ptr(v, None, "v", dev), _qdtype(k), _dev_ptr(cu_new_tokens, torch.int32, "cu_new_tokens", dev),
+         int(k.shape[0]), _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, float(softmax_scale),
+         _dev_ptr(out, torch.float32, "out", dev), _dev_ptr(workspace, torch.uint8, "workspace", dev),
+         workspace.numel(), int(num_splits), _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     return out
 
 

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -179,6 +180,21 @@ kvq_status check_prefill_grid(const kvq::AttnParams& P) {
   return KVQ_OK;
 }
 
+kvq_status check_rotary(const kvq_rotary* r, int32_t head_dim) {
+  if (!r || !r->inv_freq) return fail(KVQ_ERR_INVALID_ARG, "rope / inv_freq is NULL");
+  if (!aligned(r->inv_freq, 4)) return fail(KVQ_ERR_INVALID_ARG, "inv_freq must be 4-byte aligned");
+  if (r->rot_dim <= 0 || r->rot_dim > head_dim || r->rot_dim % 16 != 0)
+    return fail(KVQ_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16 up to head_dim");
+  if (r->interleaved != 0 && r->interleaved != 1) return fail(KVQ_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (!std::isfinite(r->scale)) return fail(KVQ_ERR_INVALID_ARG, "scale must be finite");
+  return KVQ_OK;
+}
+
+kvq::RopeArgs rope_args(const kvq_rotary* r, const int32_t* positions) {
+  kvq::RopeArgs a = {r->inv_freq, positions, r->rot_dim, r->interleaved, r->scale};
+  return a;
+}
+
 kvq::DecodeLayout decode_layout(const kvq_cache* c, const kvq_paging* p, int32_t num_q_heads) {
   const int group = num_q_heads / c->num_kv_heads;
   return kvq::decode_ws_layout(p->batch, c->num_kv_heads, group, c->head_dim, sm_count(),
@@ -208,6 +224,42 @@ kvq_status noalloc_scratch(void** out) {
   *out = g_noalloc_ptr[dev];
   return KVQ_OK;
 }
+
+// kvq_write and kvq_rope_write (rope not NULL).
+kvq_status write_call(const kvq_cache* cache, const kvq_paging* paging, const kvq_rotary* rope, const int32_t* positions,
+                      const void* k, const void* v, int32_t dtype, const int32_t* cu_new_tokens, int32_t num_tokens,
+                      int32_t* dev_error, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if ((st = check_paging(paging, cache->num_kv_heads)) != KVQ_OK) return st;
+  if (num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "num_tokens < 0");
+  if (num_tokens == 0 || paging->batch == 0) return KVQ_OK;
+  if (!k || !v || !cu_new_tokens) return fail(KVQ_ERR_INVALID_ARG, "k / v / cu_new_tokens is NULL");
+  if (dtype != KVQ_F32 && dtype != KVQ_BF16) return fail(KVQ_ERR_UNSUPPORTED, "dtype must be KVQ_F32 or KVQ_BF16");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(KVQ_ERR_INVALID_ARG, "k / v must be 16-byte aligned");
+  if ((st = check_tokens(cache, num_tokens)) != KVQ_OK) return st;
+  kvq::WriteParams P = write_params(cache, paging, k, v, dtype, cu_new_tokens, num_tokens, dev_error);
+  if (rope) P.rope = rope_args(rope, positions);
+  cudaError_t e = rope && cache->mode == KVQ_BF16_CACHE
+                      ? kvq::launch_rope_write16(P, nullptr, 0, 0, nullptr, sm_count(), static_cast<cudaStream_t>(stream))
+                      : kvq::launch_write(P, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  return KVQ_OK;
+}
+
+// Whether `tokens` rows of `wa` bytes, `sa` bytes apart, share memory with
+// rows of `wb` bytes, `sb` apart: rows of one stride may lie between one
+// another (q and k in one packed buffer).
+bool rows_overlap(const void* a, long long sa, long long wa, const void* b, long long sb, long long wb, int tokens) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if (x >= y + (uintptr_t)((tokens - 1) * sb + wb) || y >= x + (uintptr_t)((tokens - 1) * sa + wa)) return false;
+  if (sa != sb) return true;
+  const long long d = y >= x ? (long long)((y - x) % sa) : (sa - (long long)((x - y) % sa)) % sa;
+  return d < wa || d + wb > sa;
+}
+
+// Heads times dims of one CTA's tokens are counted in 32 bits.
+constexpr long long kvq_rope_most_tokens = 8;
 
 }  // namespace
 
@@ -241,18 +293,130 @@ const char* kvq_last_error(void) { return g_last_error.c_str(); }
 kvq_status kvq_write(const kvq_cache* cache, const kvq_paging* paging, const void* k, const void* v,
                      int32_t dtype, const int32_t* cu_new_tokens, int32_t num_tokens, int32_t* dev_error,
                      void* stream) {
+  return write_call(cache, paging, nullptr, nullptr, k, v, dtype, cu_new_tokens, num_tokens, dev_error, stream);
+}
+
+kvq_status kvq_rope_write(const kvq_cache* cache, const kvq_paging* paging, const kvq_rotary* rope,
+                          const int32_t* positions, const void* k, const void* v, int32_t dtype,
+                          const int32_t* cu_new_tokens, int32_t num_tokens, int32_t* dev_error, void* stream) {
   kvq_status st = check_cache(cache);
   if (st != KVQ_OK) return st;
-  if ((st = check_paging(paging, cache->num_kv_heads)) != KVQ_OK) return st;
-  if (num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "num_tokens < 0");
-  if (num_tokens == 0 || paging->batch == 0) return KVQ_OK;
-  if (!k || !v || !cu_new_tokens) return fail(KVQ_ERR_INVALID_ARG, "k / v / cu_new_tokens is NULL");
+  if (cache->mode == KVQ_INT8_CHANNEL)
+    return fail(KVQ_ERR_UNSUPPORTED, "INT8 per-channel caches take rows that kvq_rope has turned (kvq_rope, then kvq_write)");
+  if ((st = check_rotary(rope, cache->head_dim)) != KVQ_OK) return st;
+  return write_call(cache, paging, rope, positions, k, v, dtype, cu_new_tokens, num_tokens, dev_error, stream);
+}
+
+kvq_status kvq_rope(const kvq_rotary* rope, const int32_t* positions, const kvq_paging* paging,
+                    const int32_t* cu_tokens, const void* q, void* q_out, int32_t num_q_heads, int64_t q_stride,
+                    int64_t q_out_stride, const void* k, void* k_out, int32_t num_kv_heads, int64_t k_stride,
+                    int64_t k_out_stride, int32_t head_dim, int32_t dtype, int32_t num_tokens, int32_t* dev_error,
+                    void* stream) {
+  if (head_dim != 64 && head_dim != 128) return fail(KVQ_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  kvq_status st = check_rotary(rope, head_dim);
+  if (st != KVQ_OK) return st;
   if (dtype != KVQ_F32 && dtype != KVQ_BF16) return fail(KVQ_ERR_UNSUPPORTED, "dtype must be KVQ_F32 or KVQ_BF16");
-  if (!aligned(k, 16) || !aligned(v, 16)) return fail(KVQ_ERR_INVALID_ARG, "k / v must be 16-byte aligned");
-  if ((st = check_tokens(cache, num_tokens)) != KVQ_OK) return st;
-  const kvq::WriteParams P = write_params(cache, paging, k, v, dtype, cu_new_tokens, num_tokens, dev_error);
-  cudaError_t e = kvq::launch_write(P, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e);
+  if (num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "num_tokens < 0");
+  kvq::RopeRows R;
+  std::memset(&R, 0, sizeof(R));
+  if (!positions) {
+    if (!paging) return fail(KVQ_ERR_INVALID_ARG, "positions or paging must be given");
+    if (paging->batch < 0) return fail(KVQ_ERR_INVALID_ARG, "batch < 0");
+    if (paging->batch == 0 || num_tokens == 0) return KVQ_OK;
+    if (!paging->seq_lens || !cu_tokens) return fail(KVQ_ERR_INVALID_ARG, "seq_lens / cu_tokens is NULL");
+    R.seq_lens = paging->seq_lens;
+    R.cu = cu_tokens;
+    R.batch = paging->batch;
+  }
+  if (num_tokens == 0) return KVQ_OK;
+  if (!q && !k) return fail(KVQ_ERR_INVALID_ARG, "neither q nor k is given");
+  R.rope = rope_args(rope, positions);
+  R.num_tokens = num_tokens;
+  R.head_dim = head_dim;
+  R.dtype = dtype;
+  R.dev_error = dev_error;
+  const long long size = dtype == KVQ_F32 ? 4 : 2;
+  const struct { const void* in; void* out; int32_t heads; int64_t is, os; } t[2] = {
+      {q, q_out, num_q_heads, q_stride, q_out_stride}, {k, k_out, num_kv_heads, k_stride, k_out_stride}};
+  for (int i = 0; i < 2; ++i) {
+    if (!t[i].in) continue;
+    if (!t[i].out) return fail(KVQ_ERR_INVALID_ARG, "q_out / k_out is NULL");
+    if (!aligned(t[i].in, 16) || !aligned(t[i].out, 16))
+      return fail(KVQ_ERR_INVALID_ARG, "q / k and their outputs must be 16-byte aligned");
+    if (t[i].heads <= 0) return fail(KVQ_ERR_INVALID_ARG, "num_q_heads / num_kv_heads must be > 0");
+    if ((long long)t[i].heads * head_dim * kvq_rope_most_tokens > INT_MAX)
+      return fail(KVQ_ERR_UNSUPPORTED, "too many heads");
+    const long long row = (long long)t[i].heads * head_dim;
+    const long long is = t[i].is ? t[i].is : row, os = t[i].os ? t[i].os : row;
+    if (is < row || os < row || is * size % 16 != 0 || os * size % 16 != 0)
+      return fail(KVQ_ERR_INVALID_ARG, "a stride must hold the token's rows and be a multiple of 16 bytes");
+    if (is > LLONG_MAX / 16 / num_tokens || os > LLONG_MAX / 16 / num_tokens)
+      return fail(KVQ_ERR_UNSUPPORTED, "stride too large");
+    R.in[i] = t[i].in;
+    R.out[i] = t[i].out;
+    R.heads[i] = t[i].heads;
+    R.in_stride[i] = is;
+    R.out_stride[i] = os;
+  }
+  // rows are written where others are still to be read only if they are the same rows
+  for (int i = 0; i < 2; ++i) {
+    for (int j = 0; j < 2; ++j) {
+      if (!R.out[i] || !R.in[j]) continue;
+      const bool same = i == j && R.out[i] == R.in[j] && R.out_stride[i] == R.in_stride[j];
+      if (!same && rows_overlap(R.out[i], R.out_stride[i] * size, R.heads[i] * head_dim * size, R.in[j],
+                                R.in_stride[j] * size, R.heads[j] * head_dim * size, num_tokens))
+        return fail(KVQ_ERR_INVALID_ARG, "an output may be its own input, but may not overlap one otherwise");
+    }
+  }
+  if (R.out[0] && R.out[1] &&
+      rows_overlap(R.out[0], R.out_stride[0] * size, R.heads[0] * head_dim * size, R.out[1], R.out_stride[1] * size,
+                   R.heads[1] * head_dim * size, num_tokens))
+    return fail(KVQ_ERR_INVALID_ARG, "q_out and k_out overlap");
+  const cudaError_t e = kvq::launch_rope(R, sm_count(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+kvq_status kvq_rope_frequencies(int32_t rot_dim, double base, const kvq_rope_scaling* scaling, float* inv_freq,
+                                float* scale) {
+  if (!inv_freq) return fail(KVQ_ERR_INVALID_ARG, "inv_freq is NULL");
+  if (rot_dim <= 0 || rot_dim % 2 != 0) return fail(KVQ_ERR_INVALID_ARG, "rot_dim must be even and > 0");
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(KVQ_ERR_INVALID_ARG, "base must be above 1");
+  const int32_t kind = scaling ? scaling->kind : KVQ_ROPE_PLAIN;
+  const double factor = scaling ? scaling->factor : 1.0;
+  if (kind < KVQ_ROPE_PLAIN || kind > KVQ_ROPE_WAVELENGTH) return fail(KVQ_ERR_UNSUPPORTED, "unknown kind of scaling");
+  if (kind != KVQ_ROPE_PLAIN && !(factor >= 1.0 && std::isfinite(factor)))
+    return fail(KVQ_ERR_INVALID_ARG, "factor must be 1 or more");
+  const double ctx = scaling ? scaling->context : 0.0, fast = scaling ? scaling->fast : 0.0,
+               slow = scaling ? scaling->slow : 0.0;
+  if ((kind == KVQ_ROPE_TURNS || kind == KVQ_ROPE_WAVELENGTH) &&
+      !(ctx > 0.0 && slow > 0.0 && fast > slow && std::isfinite(ctx) && std::isfinite(fast)))
+    return fail(KVQ_ERR_INVALID_ARG, "context, fast and slow must be positive, and fast above slow");
+  if (kind == KVQ_ROPE_BASE) {
+    if (rot_dim <= 2) return fail(KVQ_ERR_INVALID_ARG, "a raised base needs more than one pair");
+    base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  }
+  const double two_pi = 6.283185307179586;
+  double lo = 0.0, hi = 0.0;
+  if (kind == KVQ_ROPE_TURNS) {  // the pairs that make `fast` and `slow` turns over the first context
+    const double per = rot_dim / (2.0 * std::log(base));
+    lo = std::max(std::floor(per * std::log(ctx / (fast * two_pi))), 0.0);
+    hi = std::min(std::ceil(per * std::log(ctx / (slow * two_pi))), rot_dim - 1.0);
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (kind == KVQ_ROPE_LINEAR) {
+      f /= factor;
+    } else if (kind == KVQ_ROPE_TURNS) {
+      const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+      f = f * (1.0 - ramp) + f / factor * ramp;
+    } else if (kind == KVQ_ROPE_WAVELENGTH) {
+      const double turns = ctx * f / two_pi;  // over the first context
+      const double keep = std::min(std::max((turns - slow) / (fast - slow), 0.0), 1.0);
+      f = keep * f + (1.0 - keep) * f / factor;
+    }
+    inv_freq[i] = (float)f;
+  }
+  if (scale) *scale = kind == KVQ_ROPE_TURNS ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
   return KVQ_OK;
 }
 
@@ -349,6 +513,8 @@ struct FusedWrite {
   int32_t dtype = 0;
   const int32_t* cu_new = nullptr;
   int32_t num_tokens = 0;
+  const kvq_rotary* rope = nullptr;  // the query and the new K rows are turned
+  const int32_t* positions = nullptr;
 };
 
 kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const void* q, int32_t dtype,
@@ -381,14 +547,25 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
       return fail(KVQ_ERR_UNSUPPORTED, "pool too large for 32-bit chunk numbers");
     if ((long long)paging->batch * cache->num_kv_heads * paging->max_blocks > 0x7FFFFFFFLL / (cache->block_size / 16))
       return fail(KVQ_ERR_UNSUPPORTED, "batch * num_kv_heads * table width too large");
-    if (fw.k) {  // 16-bit pages: the step's write is a launch of its own, which the decode's start overlaps
+    if (fw.k || fw.rope) {  // 16-bit pages: the step's write is a launch of its own, which the decode's start overlaps
       if ((st = check_tokens(cache, fw.num_tokens)) != KVQ_OK) return st;
-      const cudaError_t e = kvq::launch_write(
-          write_params(cache, paging, fw.k, fw.v, fw.dtype, fw.cu_new, fw.num_tokens, dev_error),
-          static_cast<cudaStream_t>(stream));
+      kvq::WriteParams W = write_params(cache, paging, fw.k, fw.v, fw.dtype, fw.cu_new, fw.num_tokens, dev_error);
+      cudaError_t e;
+      if (fw.rope) {
+        // the turned queries go where the low-bit modes keep theirs: 16 D bytes
+        // per n-tile of up to 4 heads, which is those heads' rows in fp32
+        W.rope = rope_args(fw.rope, fw.positions);
+        float* turned = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.off_qfrag);
+        e = kvq::launch_rope_write16(W, q, dtype, num_q_heads, turned, sm_count(), static_cast<cudaStream_t>(stream));
+        P.q = turned;
+        P.dtype = KVQ_F32;
+      } else {
+        e = kvq::launch_write(W, static_cast<cudaStream_t>(stream));
+      }
       if (e != cudaSuccess) return cuda_fail(e);
     }
   }
+  if (fw.rope) P.rope = rope_args(fw.rope, fw.positions);
   uint8_t* w = static_cast<uint8_t*>(workspace);
   kvq::DecodeWs ws;
   ws.tile_start = reinterpret_cast<int*>(w + L.off_tile_start);
@@ -409,6 +586,35 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
   return KVQ_OK;
 }
 
+// kvq_write_decode_attn and kvq_rope_write_decode_attn (rope not NULL).
+kvq_status step_call(const kvq_cache* cache, const kvq_paging* paging, const kvq_rotary* rope, const int32_t* positions,
+                     const void* k, const void* v, int32_t kv_dtype, const int32_t* cu_new_tokens, int32_t num_tokens,
+                     const void* q, int32_t q_dtype, int32_t num_q_heads, float softmax_scale, float* out,
+                     void* workspace, size_t workspace_bytes, int32_t num_splits, int32_t* dev_error, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (cache->mode == KVQ_INT8_CHANNEL)
+    return fail(KVQ_ERR_UNSUPPORTED, "the fused write + decode does not take INT8 per-channel caches");
+  if ((st = check_paging(paging, cache->num_kv_heads)) != KVQ_OK) return st;
+  if (num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "num_tokens < 0");
+  FusedWrite fw;
+  fw.rope = rope;
+  fw.positions = positions;
+  if (num_tokens > 0 && paging->batch > 0) {
+    if (!k || !v || !cu_new_tokens) return fail(KVQ_ERR_INVALID_ARG, "k / v / cu_new_tokens is NULL");
+    if (kv_dtype != KVQ_F32 && kv_dtype != KVQ_BF16)
+      return fail(KVQ_ERR_UNSUPPORTED, "kv_dtype must be KVQ_F32 or KVQ_BF16");
+    if (!aligned(k, 16) || !aligned(v, 16)) return fail(KVQ_ERR_INVALID_ARG, "k / v must be 16-byte aligned");
+    fw.k = k;
+    fw.v = v;
+    fw.dtype = kv_dtype;
+    fw.cu_new = cu_new_tokens;
+    fw.num_tokens = num_tokens;
+  }
+  return decode_call(cache, paging, q, q_dtype, num_q_heads, softmax_scale, out, workspace, workspace_bytes,
+                     num_splits, dev_error, stream, fw);
+}
+
 }  // namespace
 
 extern "C" {
@@ -425,26 +631,20 @@ kvq_status kvq_write_decode_attn(const kvq_cache* cache, const kvq_paging* pagin
                                  int32_t q_dtype, int32_t num_q_heads, float softmax_scale, float* out,
                                  void* workspace, size_t workspace_bytes, int32_t num_splits, int32_t* dev_error,
                                  void* stream) {
-  kvq_status st = check_cache(cache);
+  return step_call(cache, paging, nullptr, nullptr, k, v, kv_dtype, cu_new_tokens, num_tokens, q, q_dtype, num_q_heads,
+                   softmax_scale, out, workspace, workspace_bytes, num_splits, dev_error, stream);
+}
+
+kvq_status kvq_rope_write_decode_attn(const kvq_cache* cache, const kvq_paging* paging, const kvq_rotary* rope,
+                                      const int32_t* positions, const void* k, const void* v, int32_t kv_dtype,
+                                      const int32_t* cu_new_tokens, int32_t num_tokens, const void* q, int32_t q_dtype,
+                                      int32_t num_q_heads, float softmax_scale, float* out, void* workspace,
+                                      size_t workspace_bytes, int32_t num_splits, int32_t* dev_error, void* stream) {
+  const kvq_status st = check_cache(cache);
   if (st != KVQ_OK) return st;
-  if (cache->mode == KVQ_INT8_CHANNEL)
-    return fail(KVQ_ERR_UNSUPPORTED, "the fused write + decode does not take INT8 per-channel caches");
-  if ((st = check_paging(paging, cache->num_kv_heads)) != KVQ_OK) return st;
-  if (num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "num_tokens < 0");
-  FusedWrite fw;
-  if (num_tokens > 0 && paging->batch > 0) {
-    if (!k || !v || !cu_new_tokens) return fail(KVQ_ERR_INVALID_ARG, "k / v / cu_new_tokens is NULL");
-    if (kv_dtype != KVQ_F32 && kv_dtype != KVQ_BF16)
-      return fail(KVQ_ERR_UNSUPPORTED, "kv_dtype must be KVQ_F32 or KVQ_BF16");
-    if (!aligned(k, 16) || !aligned(v, 16)) return fail(KVQ_ERR_INVALID_ARG, "k / v must be 16-byte aligned");
-    fw.k = k;
-    fw.v = v;
-    fw.dtype = kv_dtype;
-    fw.cu_new = cu_new_tokens;
-    fw.num_tokens = num_tokens;
-  }
-  return decode_call(cache, paging, q, q_dtype, num_q_heads, softmax_scale, out, workspace, workspace_bytes,
-                     num_splits, dev_error, stream, fw);
+  if (const kvq_status rs = check_rotary(rope, cache->head_dim); rs != KVQ_OK) return rs;
+  return step_call(cache, paging, rope, positions, k, v, kv_dtype, cu_new_tokens, num_tokens, q, q_dtype, num_q_heads,
+                   softmax_scale, out, workspace, workspace_bytes, num_splits, dev_error, stream);
 }
 
 kvq_status kvq_decode_attn_noalloc(const kvq_cache* cache, const kvq_paging* paging, const void* q,

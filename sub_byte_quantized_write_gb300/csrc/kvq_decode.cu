@@ -315,7 +315,7 @@ __host__ __device__ constexpr int decode_tile_keys() {
 // them (the same row function, so the same bytes; a -1 destination is
 // skipped, errors set the same bits): the step's write fused into the
 // decode.  One warp per row, the CTA's four warps in turn.
-template <int MODE, int D, bool STEGO>
+template <int MODE, int D, bool STEGO, bool ROPE>
 __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int h) {
   constexpr int EPL = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -348,13 +348,28 @@ __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int
     if (!KVQ_IN_BOUNDS(((size_t)blk * Hkv + h) * bs + p % bs < (size_t)P.num_blocks * Hkv * bs, P.dev_error)) continue;
     float x[EPL];
     load_row_elems<EPL, false>(kv ? P.new_v : P.new_k, P.new_dtype, ((size_t)(t0 + i) * Hkv + h) * D + lane * EPL, x);
+    if constexpr (ROPE) {
+      if (kv == 0) {  // (warp-uniform)
+        const int angle = P.rope.positions ? load_input<false>(P.rope.positions + t0 + i) : p;
+        rope_row(rope_lane<EPL, false>(P.rope, angle, lane), x);
+      }
+    }
     uint8_t* pages = const_cast<uint8_t*>(kv ? P.v_pages : P.k_pages);
     quantise_store_row<MODE, D, STEGO, 32>(sg, x, pages + (((size_t)blk * Hkv + h) * bs + p % bs) * R, lane,
                                            true);
   }
 }
 
-template <int MODE, int D, int NT, bool STEGO>
+// The position a decode query turns to: its sequence's last token's.
+__device__ __forceinline__ int query_position(const AttnParams& P, int b) {
+  if (P.rope.positions && P.num_new > 0) {
+    const int c0 = load_input<false>(P.cu_new + b), c1 = load_input<false>(P.cu_new + b + 1);
+    if (c1 > c0 && c1 >= 1 && c1 <= P.num_new) return load_input<false>(P.rope.positions + c1 - 1);
+  }
+  return load_input<false>(P.seq_lens + b) - 1;
+}
+
+template <int MODE, int D, int NT, bool STEGO, bool ROPE>
 __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs ws) {
   using C = DecCfg<MODE, D>;
   constexpr int EPL = D / 32;
@@ -378,11 +393,14 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
   const int b = bh / Hkv, h = bh % Hkv;
   const float log2e = 1.4426950408889634f;
   const float dnorm = (MODE != MODE_INT8 && P.signs) ? (float)D : 1.0f;
+  RopeLane<EPL> turn;
+  if constexpr (ROPE) turn = rope_lane<EPL, false>(P.rope, query_position(P, b), lane);
   for (int i = warp; i < NH; i += 4) {
     float x[EPL];
     if (i < G) {
       const int hq = h * G + i;
       load_row_elems<EPL, false>(P.q, P.dtype, ((size_t)b * Hq + hq) * D + lane * EPL, x);
+      if constexpr (ROPE) rope_row(turn, x);
       if constexpr (MODE == MODE_INT8) {
         const float* am = P.ch_amax + (size_t)h * D + lane * EPL;  // K channel scales
 #pragma unroll
@@ -455,7 +473,7 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
     dst[q4] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
   }
   if constexpr (MODE != MODE_INT8) {
-    if (P.new_k) fused_write_pair<MODE, D, STEGO>(P, b, h);  // the step's write
+    if (P.new_k) fused_write_pair<MODE, D, STEGO, ROPE>(P, b, h);  // the step's write
   }
 }
 
@@ -1600,7 +1618,10 @@ cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, c
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   const int BH = P.batch * P.num_kv_heads;
-  e = launch_dependent(decode_prep_kernel<MODE, D, NT, STEGO>, dim3(BH), dim3(128), 0, stream, P, ws);
+  if (MODE != MODE_INT8 && P.rope.inv_freq)  // (INT8 per channel: refused by the API)
+    e = launch_dependent(decode_prep_kernel<MODE, D, NT, STEGO, MODE != MODE_INT8>, dim3(BH), dim3(128), 0, stream, P, ws);
+  else
+    e = launch_dependent(decode_prep_kernel<MODE, D, NT, STEGO, false>, dim3(BH), dim3(128), 0, stream, P, ws);
   if (e != cudaSuccess) return e;
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

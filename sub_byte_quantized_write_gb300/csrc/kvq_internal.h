@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "kvq_common.cuh"
+#include "kvq_rope.cuh"
 
 namespace kvq {
 
@@ -36,6 +37,21 @@ struct WriteParams {
   const void* chunk_v;
   const int32_t* cu_chunk;
   int chunk_dtype;
+  RopeArgs rope;  // K rows are turned before they are stored
+};
+
+// kvq_rope: rows of q and k turned to their positions (q or k NULL: none).
+struct RopeRows {
+  RopeArgs rope;
+  const int32_t* seq_lens;
+  const int32_t* cu;
+  int batch, num_tokens, head_dim, dtype;
+  const void* in[2];   // q, k: [num_tokens] tokens of heads[] rows, stride[] elements apart
+  void* out[2];
+  int heads[2];
+  long long in_stride[2], out_stride[2];
+  int tokens_per_cta;
+  int32_t* dev_error;
 };
 
 // Shared by the decode and prefill kernels.
@@ -74,6 +90,7 @@ struct AttnParams {
   const void* new_v;
   int new_dtype, num_new;
   const int32_t* cu_new;
+  RopeArgs rope;          // the query and the new K rows are turned to their positions
   CUtensorMap kv_map[2];  // 128-byte aligned by its own declaration
 };
 
@@ -195,6 +212,13 @@ int decode_chunk_rows(int mode, int head_dim, int group);
 
 cudaError_t launch_write(const WriteParams& P, cudaStream_t stream);
 cudaError_t launch_gather(const WriteParams& P, cudaStream_t stream);
+// rotary positions (kvq_rope.cu)
+cudaError_t launch_rope(RopeRows R, int sms, cudaStream_t stream);
+// The step's write over 16-bit pages with rope: turned K and plain V rows into
+// the pages, and the turned queries [batch][num_q_heads][D] as fp32 to q_out
+// (q NULL: the write alone).
+cudaError_t launch_rope_write16(const WriteParams& P, const void* q, int q_dtype, int num_q_heads, float* q_out,
+                                int sms, cudaStream_t stream);
 cudaError_t launch_decode(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream);
 // the decode over 16-bit pages (kvq_decode16.cu), which launch_decode and
 // decode_shape hand to

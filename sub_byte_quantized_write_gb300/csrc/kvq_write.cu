@@ -37,7 +37,8 @@ namespace kvq {
 // The owning sequence is found with one round of parallel loads: lane j
 // holds cu[j + 32 i] and ballots whether it is <= t (cu is non-decreasing,
 // so the ballot's population count locates the sequence).
-__device__ __forceinline__ uint8_t* dest_row(const WriteParams& P, uint8_t* pages, int t, int h, int lane) {
+// `pos`: the token's position.
+__device__ __forceinline__ uint8_t* dest_row(const WriteParams& P, uint8_t* pages, int t, int h, int lane, int& pos) {
   int b = -1, cu_b = 0, cu_b1 = 0, L = 0;
   int prev_c = 0, prev_l = 0;  // cu and seq_lens at the previous chunk's last lane
   for (int base = 0; base <= P.batch; base += 32) {
@@ -69,6 +70,7 @@ __device__ __forceinline__ uint8_t* dest_row(const WriteParams& P, uint8_t* page
     return nullptr;
   }
   const int p = L - n + (t - cu_b);
+  pos = p;
   const int row = P.headwise ? b * P.num_kv_heads + h : b;
   const int lb = p / P.block_size;
   if (lb >= P.max_blocks) {
@@ -98,7 +100,7 @@ __device__ __forceinline__ uint32_t gather_word(uint32_t bits, int lane) {
   return v;
 }
 
-template <int MODE, int D, bool STEGO>
+template <int MODE, int D, bool STEGO, bool ROPE>
 __global__ void __launch_bounds__(256) write_token_head_kernel(WriteParams P) {
   constexpr int EPL = D / 32;
   const int lane = threadIdx.x & 31;
@@ -113,8 +115,15 @@ __global__ void __launch_bounds__(256) write_token_head_kernel(WriteParams P) {
   float x[EPL];  // issued before the (dependent) table lookups
   load_row_elems<EPL>(kv ? P.v : P.k, P.dtype, ((size_t)t * P.num_kv_heads + h) * D + lane * EPL, x);
   const RowSigns<EPL> sg = load_row_signs<EPL>(P.signs, lane);
-  uint8_t* dst = dest_row(P, kv ? P.v_pages : P.k_pages, (int)t, h, lane);
+  int pos = 0;
+  uint8_t* dst = dest_row(P, kv ? P.v_pages : P.k_pages, (int)t, h, lane, pos);
   if (dst == nullptr) return;  // warp-uniform
+  if constexpr (ROPE) {
+    if (kv == 0) {
+      if (P.rope.positions) pos = __ldg(P.rope.positions + t);
+      rope_row(rope_lane<EPL, true>(P.rope, pos, lane), x);
+    }
+  }
   quantise_store_row<MODE, D, STEGO, 32>(sg, x, dst, lane, true);
 }
 
@@ -157,7 +166,8 @@ __global__ void __launch_bounds__(256) int8_quant_kernel(WriteParams P) {
   if (t >= P.num_tokens) return;
   float x[EPL];
   load_row_elems<EPL>(kv ? P.v : P.k, P.dtype, ((size_t)t * P.num_kv_heads + h) * D + lane * EPL, x);
-  uint8_t* dst = dest_row(P, kv ? P.v_pages : P.k_pages, (int)t, h, lane);
+  int pos = 0;
+  uint8_t* dst = dest_row(P, kv ? P.v_pages : P.k_pages, (int)t, h, lane, pos);
   if (dst == nullptr) return;
   const float* am = P.ch_amax + ((size_t)kv * P.num_kv_heads + h) * D + lane * EPL;
   uint32_t bits = 0;
@@ -199,8 +209,9 @@ constexpr int GATHER_TOKENS = 8;
 // full-precision chunk.
 // GUESS: token t is first looked for in sequence t, where a decode step's one
 // token per sequence is, which saves the search's chain of loads.
+// `pos`: where not NULL, the token's position (of rows that are found).
 template <bool CHUNK, bool GUESS = false>
-__device__ __forceinline__ long long gather_row_offset(const WriteParams& P, int t, int h) {
+__device__ __forceinline__ long long gather_row_offset(const WriteParams& P, int t, int h, int* pos = nullptr) {
   if (t >= P.num_tokens) return -1;
   int lo = 0, hi = P.batch - 1;  // the last sequence whose first token is <= t
   if (GUESS && t < P.batch && __ldg(P.cu_new + t) <= t && t < __ldg(P.cu_new + t + 1)) lo = hi = t;
@@ -218,6 +229,7 @@ __device__ __forceinline__ long long gather_row_offset(const WriteParams& P, int
     return -1;
   }
   const int p = L - n + (t - cu_b);
+  if (pos) *pos = p;
   if constexpr (CHUNK) {
     const int c0 = __ldg(P.cu_chunk + b), m = __ldg(P.cu_chunk + b + 1) - c0;
     if (m < 0 || m > L) {
@@ -520,12 +532,75 @@ constexpr int WRITE_STAGES = 2;  // input stages per warp
 constexpr int WRITE_CTAS_PER_SM = 3;
 
 // Shared memory of write_batch_kernel: per warp and stage, the unit's K rows
-// then V rows as they are in the input ([4][D] of the input dtype each).
-inline size_t write_batch_smem(int head_dim, int dtype) {
-  return (size_t)WRITE_WARPS * WRITE_STAGES * 2 * WRITE_TOKENS * head_dim * (dtype == DT_F32 ? 4 : 2);
+// then V rows as they are in the input ([4][D] of the input dtype each); with
+// rope, then per warp the cosines and sines of four tokens, and the pairs'
+// turns per position.
+inline size_t write_batch_smem(int head_dim, int dtype, bool rope) {
+  return (size_t)WRITE_WARPS * WRITE_STAGES * 2 * WRITE_TOKENS * head_dim * (dtype == DT_F32 ? 4 : 2) +
+         (rope ? (size_t)WRITE_WARPS * WRITE_TOKENS * (head_dim / 2) * 8 + (head_dim / 2) * 8 : 0);
 }
 
-template <int MODE, int D, bool STEGO, bool F32>
+// Cosine and sine of pair p of one token in its table of D / 2 pairs: 16-byte
+// pieces of two pairs, XOR-swizzled in groups of eight so that lanes that read
+// pieces 8 apart hit different banks.
+__device__ __forceinline__ int rope_slot(int p) { return ((((p >> 1) & ~7) | (((p >> 1) ^ (p >> 4)) & 7)) << 1) | (p & 1); }
+
+// Eight elements at p (16-byte aligned) as fp32.
+template <bool F32>
+__device__ __forceinline__ void lds8(const uint8_t* p, float (&x)[8]) {
+#pragma unroll
+  for (int c = 0; c < (F32 ? 2 : 1); ++c) {
+    const uint4 v = lds128(p + 16 * c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (F32) {
+        x[4 * c + k] = __uint_as_float(w[k]);
+      } else {
+        x[2 * k] = __uint_as_float(w[k] << 16);
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+// Turns elements d0 .. d0 + EPL - 1 (in x) of the row at `row` in shared
+// memory by the token's table; partners are read from the row, in blocks of
+// eight (pairs are whole multiples of 8 elements apart).
+template <int EPL, bool F32>
+__device__ __forceinline__ void rope_from_smem(const RopeArgs& R, const float2* table, const uint8_t* row, int d0,
+                                               float (&x)[EPL]) {
+  const int half = R.rot / 2;
+#pragma unroll
+  for (int b = 0; b < EPL / 8; ++b) {
+    const int d = d0 + 8 * b;
+    if (d >= R.rot) continue;
+    if (R.inter) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 w = table[rope_slot((d + e) / 2)];
+        const float p = x[8 * b + e], q = x[8 * b + e + 1];
+        x[8 * b + e] = fmaf(p, w.x, q * -w.y);
+        x[8 * b + e + 1] = fmaf(q, w.x, p * w.y);
+      }
+    } else {
+      const bool first = d < half;
+      const int i = first ? d : d - half;
+      float o[8];
+      lds8<F32>(row + (first ? d + half : i) * (F32 ? 4 : 2), o);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(table + rope_slot(i + e));
+        x[8 * b + e] = fmaf(x[8 * b + e], w.x, o[e] * (first ? -w.y : w.y));
+        x[8 * b + e + 1] = fmaf(x[8 * b + e + 1], w.z, o[e + 1] * (first ? -w.w : w.w));
+      }
+    }
+  }
+}
+
+// ROPE: a warp's units are consecutive ones, the heads of a few token groups,
+// so that a group's cosines and sines are worked out once per warp.
+template <int MODE, int D, bool STEGO, bool F32, bool ROPE>
 __global__ void __launch_bounds__(WRITE_WARPS * 32, WRITE_CTAS_PER_SM) write_batch_kernel(WriteParams P) {
   constexpr int EPL = D / WRITE_LPR;
   constexpr int ESZ = F32 ? 4 : 2;
@@ -543,9 +618,29 @@ __global__ void __launch_bounds__(WRITE_WARPS * 32, WRITE_CTAS_PER_SM) write_bat
   const RowSigns<EPL> sg = load_row_signs<EPL>(P.signs, sub);  // shared by every row of this lane
   // unit u = grp * Hkv + h, taken by warps u, u + nw, u + 2 nw, ...
   const int nw = gridDim.x * WRITE_WARPS;
-  const int step_g = nw / Hkv, step_h = nw % Hkv;
+  int step_g = nw / Hkv, step_h = nw % Hkv;
   const int w0 = blockIdx.x * WRITE_WARPS + warp;
-  int grp = w0 / Hkv, h = w0 % Hkv;
+  int grp = w0 / Hkv, h = w0 % Hkv, left = 0;
+  float2* table = nullptr;           // [WRITE_TOKENS][D / 2] of this warp
+  const uint64_t* turns = nullptr;   // [rot / 2]
+  int turned = -1;                   // the group the table is of
+  if constexpr (ROPE) {
+    uint8_t* tsm = wsm + (size_t)WRITE_WARPS * WRITE_STAGES * UNIT;
+    table = reinterpret_cast<float2*>(tsm) + warp * WRITE_TOKENS * (D / 2);
+    uint64_t* tu = reinterpret_cast<uint64_t*>(tsm + (size_t)WRITE_WARPS * WRITE_TOKENS * (D / 2) * 8);
+    for (int i = threadIdx.x; i < P.rope.rot / 2; i += blockDim.x) tu[i] = rope_turns(__ldg(P.rope.inv_freq + i));
+    turns = tu;
+    __syncthreads();
+    // (units, warps and their product stay below 2^31 * 2^31)
+    const long long units = (long long)groups * Hkv;
+    const long long u0 = units * w0 / nw;
+    left = (int)(units * (w0 + 1) / nw - u0);
+    grp = (int)(u0 / Hkv);
+    h = (int)(u0 % Hkv);
+    if (left == 0) grp = groups;
+    step_g = 0;
+    step_h = 1;
+  }
 
   // input rows of unit (gg, hh) into stage st (rows past the input are not read)
   auto issue = [&](int gg, int hh, int st) {
@@ -566,13 +661,18 @@ __global__ void __launch_bounds__(WRITE_WARPS * 32, WRITE_CTAS_PER_SM) write_bat
     cp_async_commit();
   };
   // destination byte offset of token WRITE_TOKENS gg + lane (lanes 0..3), -1: none
+  int my_pos = 0, next_pos = 0;  // ROPE: the token's position
   auto lookup = [&](int gg, int hh) -> long long {
     if (gg >= groups || lane >= WRITE_TOKENS) return -1;
-    return gather_row_offset<false>(P, gg * WRITE_TOKENS + lane, hh);
+    const long long off = gather_row_offset<false>(P, gg * WRITE_TOKENS + lane, hh, ROPE ? &next_pos : nullptr);
+    if constexpr (ROPE)
+      if (off >= 0 && P.rope.positions) next_pos = __ldg(P.rope.positions + gg * WRITE_TOKENS + lane);
+    return off;
   };
 
   issue(grp, h, 0);
   long long my_off = lookup(grp, h);
+  my_pos = next_pos;
   int st = 0;
   while (grp < groups) {
     int ng = grp + step_g, nh = h + step_h;
@@ -580,6 +680,8 @@ __global__ void __launch_bounds__(WRITE_WARPS * 32, WRITE_CTAS_PER_SM) write_bat
       nh -= Hkv;
       ++ng;
     }
+    if constexpr (ROPE)
+      if (--left == 0) ng = groups;  // the warp's last unit
     issue(ng, nh, st ^ 1);
     const long long next_off = lookup(ng, nh);
     cp_async_wait<1>();  // this unit's rows have landed
@@ -604,6 +706,26 @@ __global__ void __launch_bounds__(WRITE_WARPS * 32, WRITE_CTAS_PER_SM) write_bat
         }
       }
     }
+    if constexpr (ROPE) {
+      // (a token that is evicted for one head may be stored for the next: each
+      // head's lookup gives the position anew, and a table is of the group
+      // only if every token of it had one)
+      const unsigned found = __ballot_sync(0xffffffffu, my_off >= 0) & ((1u << WRITE_TOKENS) - 1u);
+      if (turned != grp) {
+#pragma unroll
+        for (int k = 0; k < WRITE_TOKENS; ++k) {
+          const int pos = __shfl_sync(0xffffffffu, my_pos, k);
+          if ((found >> k) & 1)
+            for (int i = lane; i < P.rope.rot / 2; i += 32) {
+              const float2 w = rope_cos_sin(turns[i], pos);
+              table[k * (D / 2) + rope_slot(i)] = make_float2(w.x * P.rope.scale, w.y * P.rope.scale);
+            }
+        }
+        turned = found == (1u << WRITE_TOKENS) - 1u ? grp : -1;
+        __syncwarp();
+      }
+      if ((found >> g) & 1) rope_from_smem<EPL, F32>(P.rope, table + g * (D / 2), buf + st * UNIT + g * IN_ROW, sub * EPL, x[0]);
+    }
     __syncwarp();  // every lane has read this stage before it is filled again
     const long long off = __shfl_sync(0xffffffffu, my_off, g);  // -1: an evicted, invalid or absent row
 #pragma unroll
@@ -611,6 +733,7 @@ __global__ void __launch_bounds__(WRITE_WARPS * 32, WRITE_CTAS_PER_SM) write_bat
       quantise_store_row<MODE, D, STEGO, WRITE_LPR>(sg, x[kv], (kv ? P.v_pages : P.k_pages) + (off >= 0 ? off : 0),
                                                     lane, off >= 0);
     my_off = next_off;
+    my_pos = next_pos;
     grp = ng;
     h = nh;
     st ^= 1;
@@ -618,7 +741,7 @@ __global__ void __launch_bounds__(WRITE_WARPS * 32, WRITE_CTAS_PER_SM) write_bat
   cp_async_wait<0>();
 }
 
-template <int MODE, bool STEGO>
+template <int MODE, bool STEGO, bool ROPE>
 cudaError_t launch_write_m(const WriteParams& P, cudaStream_t stream) {
   if (P.num_tokens >= WRITE_BATCH_MIN_TOKENS) {
     // one CTA of eight persistent warps per unit group, at most
@@ -629,40 +752,50 @@ cudaError_t launch_write_m(const WriteParams& P, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const size_t smem = write_batch_smem(P.head_dim, P.dtype);
+    const size_t smem = write_batch_smem(P.head_dim, P.dtype, ROPE);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-      const int mx = (int)write_batch_smem(128, DT_F32);
-      const void* fns[4] = {(const void*)write_batch_kernel<MODE, 128, STEGO, false>,
-                            (const void*)write_batch_kernel<MODE, 128, STEGO, true>,
-                            (const void*)write_batch_kernel<MODE, 64, STEGO, false>,
-                            (const void*)write_batch_kernel<MODE, 64, STEGO, true>};
+      const int mx = (int)write_batch_smem(128, DT_F32, ROPE);
+      const void* fns[4] = {(const void*)write_batch_kernel<MODE, 128, STEGO, false, ROPE>,
+                            (const void*)write_batch_kernel<MODE, 128, STEGO, true, ROPE>,
+                            (const void*)write_batch_kernel<MODE, 64, STEGO, false, ROPE>,
+                            (const void*)write_batch_kernel<MODE, 64, STEGO, true, ROPE>};
       for (const void* f : fns)
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, mx)) != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     // units of four tokens of one kv head; the kernel counts them in 32 bits
     const long long units = (long long)((P.num_tokens + WRITE_TOKENS - 1) / WRITE_TOKENS) * P.num_kv_heads;
-    const int blocks = (int)std::min<long long>((units + WRITE_WARPS - 1) / WRITE_WARPS, (long long)sms * WRITE_CTAS_PER_SM);
+    const int ctas = smem * WRITE_CTAS_PER_SM > 220 * 1024 ? 2 : WRITE_CTAS_PER_SM;  // (rope over fp32 rows of 128 dims)
+    const int blocks = (int)std::min<long long>((units + WRITE_WARPS - 1) / WRITE_WARPS, (long long)sms * ctas);
     const dim3 grid(blocks), block(WRITE_WARPS * 32);
     const bool f32 = P.dtype == DT_F32;
     if (P.head_dim == 128) {
-      if (f32) write_batch_kernel<MODE, 128, STEGO, true><<<grid, block, smem, stream>>>(P);
-      else write_batch_kernel<MODE, 128, STEGO, false><<<grid, block, smem, stream>>>(P);
+      if (f32) write_batch_kernel<MODE, 128, STEGO, true, ROPE><<<grid, block, smem, stream>>>(P);
+      else write_batch_kernel<MODE, 128, STEGO, false, ROPE><<<grid, block, smem, stream>>>(P);
     } else {
-      if (f32) write_batch_kernel<MODE, 64, STEGO, true><<<grid, block, smem, stream>>>(P);
-      else write_batch_kernel<MODE, 64, STEGO, false><<<grid, block, smem, stream>>>(P);
+      if (f32) write_batch_kernel<MODE, 64, STEGO, true, ROPE><<<grid, block, smem, stream>>>(P);
+      else write_batch_kernel<MODE, 64, STEGO, false, ROPE><<<grid, block, smem, stream>>>(P);
     }
   } else {
     const long long warps = (long long)P.num_tokens * P.num_kv_heads * 2;
     const int blocks = (int)((warps + 7) / 8);
-    if (P.head_dim == 128) write_token_head_kernel<MODE, 128, STEGO><<<blocks, 256, 0, stream>>>(P);
-    else write_token_head_kernel<MODE, 64, STEGO><<<blocks, 256, 0, stream>>>(P);
+    if (P.head_dim == 128) write_token_head_kernel<MODE, 128, STEGO, ROPE><<<blocks, 256, 0, stream>>>(P);
+    else write_token_head_kernel<MODE, 64, STEGO, ROPE><<<blocks, 256, 0, stream>>>(P);
   }
   return cudaGetLastError();
 }
 
+template <bool ROPE>
+cudaError_t launch_write_modes(const WriteParams& P, cudaStream_t stream) {
+  if (P.mode == MODE_I8T) return launch_write_m<MODE_I8T, false, ROPE>(P, stream);
+  if (P.mode == MODE_F8T) return launch_write_m<MODE_F8T, false, ROPE>(P, stream);
+  if (P.mode == MODE_INT4 && P.stego) return launch_write_m<MODE_INT4, true, ROPE>(P, stream);
+  if (P.mode == MODE_INT4) return launch_write_m<MODE_INT4, false, ROPE>(P, stream);
+  return launch_write_m<MODE_INT2, false, ROPE>(P, stream);
+}
+
 cudaError_t launch_write(const WriteParams& P, cudaStream_t stream) {
-  if (P.mode == MODE_DBF16)
+  if (P.mode == MODE_DBF16)  // (with rope: launch_rope_write16)
     return P.head_dim == 128 ? launch_write16<128>(P, stream) : launch_write16<64>(P, stream);
   const long long warps = (long long)P.num_tokens * P.num_kv_heads * 2;
   const int blocks = (int)((warps + 7) / 8);
@@ -674,11 +807,7 @@ cudaError_t launch_write(const WriteParams& P, cudaStream_t stream) {
     else int8_quant_kernel<64><<<blocks, 256, 0, stream>>>(P);
     return cudaGetLastError();
   }
-  if (P.mode == MODE_I8T) return launch_write_m<MODE_I8T, false>(P, stream);
-  if (P.mode == MODE_F8T) return launch_write_m<MODE_F8T, false>(P, stream);
-  if (P.mode == MODE_INT4 && P.stego) return launch_write_m<MODE_INT4, true>(P, stream);
-  if (P.mode == MODE_INT4) return launch_write_m<MODE_INT4, false>(P, stream);
-  return launch_write_m<MODE_INT2, false>(P, stream);
+  return P.rope.inv_freq ? launch_write_modes<true>(P, stream) : launch_write_modes<false>(P, stream);
 }
 
 }  // namespace kvq
