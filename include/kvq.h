@@ -420,6 +420,49 @@ kvq_status kvq_prefill_attn(const kvq_cache* cache, const kvq_paging* paging,
                             float softmax_scale, float* out,
                             int32_t* dev_error, void* stream);
 
+/* kvq_cross_attn -- attention of some queries per sequence to every cached row
+ * of another sequence of tokens, of its own length: a decoder's cross attention
+ * to an encoder's states, which were written once (kvq_write).  Not causal.
+ *
+ * paging : the encoder's tables; seq_lens[b] rows are seen by every query of
+ *        sequence b.  -1 entries contribute nothing.  No windows
+ *        (window_per_kv_head NULL, else KVQ_ERR_UNSUPPORTED).
+ * q    : [total_q][num_q_heads][head_dim] of `dtype`; GQA group size 1..8.
+ * cu_q : int32 [batch + 1]; sequence b's queries are rows cu_q[b] ..
+ *        cu_q[b+1]-1, from none to max_q_per_seq, whatever seq_lens[b] is.
+ *        Queries past max_q_per_seq, or rows outside 0 .. total_q - 1, are
+ *        skipped and set KVQ_DEVERR_SEQ_LEN.
+ * out  : fp32 [total_q][num_q_heads][head_dim].  A query that sees no row gets
+ *        zeros; rows of no sequence are left as they were.  A negative
+ *        seq_lens[b] counts as 0 and sets KVQ_DEVERR_SEQ_LEN, one past the table
+ *        as the table's end (KVQ_DEVERR_TABLE_RANGE).
+ * workspace : as kvq_decode_attn, of kvq_cross_workspace_size() bytes (may be 0,
+ *        then NULL is taken).
+ * Every mode is taken, 16-bit pages too. */
+kvq_status kvq_cross_workspace_size(const kvq_cache* cache, const kvq_paging* paging, int32_t num_q_heads,
+                                    int32_t max_q_per_seq, size_t* bytes);
+kvq_status kvq_cross_attn(const kvq_cache* cache, const kvq_paging* paging, const void* q, int32_t dtype,
+                          int32_t num_q_heads, const int32_t* cu_q, int32_t total_q, int32_t max_q_per_seq,
+                          float softmax_scale, float* out, void* workspace, size_t workspace_bytes,
+                          int32_t* dev_error, void* stream);
+
+/* kvq_cross_dense_attn -- kvq_cross_attn over dense bf16 rows, as an encoder
+ * leaves them.
+ * k, v        : bf16 [num_kv_rows][num_kv_heads][head_dim], 16-byte aligned;
+ *               sequence b's row j is row cu_kv[b] + j.
+ * cu_kv       : int32 [batch + 1] (device); a sequence with cu_kv[b + 1] - cu_kv[b]
+ *               < seq_lens[b], or with rows outside k and v, is skipped (its
+ *               outputs are left as they were) and sets KVQ_DEVERR_SEQ_LEN.
+ * paging      : seq_lens and batch; both tables and window_per_kv_head NULL.
+ * workspace   : of kvq_cross_dense_workspace_size() bytes (may be 0). */
+kvq_status kvq_cross_dense_workspace_size(int32_t num_kv_rows, int32_t num_kv_heads, int32_t head_dim, int32_t batch,
+                                          int32_t num_q_heads, int32_t max_q_per_seq, size_t* bytes);
+kvq_status kvq_cross_dense_attn(const void* k, const void* v, const int32_t* cu_kv, int32_t num_kv_rows,
+                                int32_t num_kv_heads, int32_t head_dim, const kvq_paging* paging, const void* q,
+                                int32_t dtype, int32_t num_q_heads, const int32_t* cu_q, int32_t total_q,
+                                int32_t max_q_per_seq, float softmax_scale, float* out, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_error, void* stream);
+
 /* kvq_decode_attn_noalloc -- kvq_decode_attn for callers that cannot
  * allocate device memory (no counterpart on the pages; an addition of this
  * library).  Some callers must not or cannot call cudaMalloc at call time:

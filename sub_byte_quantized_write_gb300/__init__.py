@@ -10,7 +10,7 @@ Names mirror the C calls: ``kvq_write``, ``kvq_gather``, ``kvq_prefill_dense_att
 ``kvq_write_decode_attn``,
 ``kvq_decode_attn_noalloc``, ``kvq_prefill_attn``, ``kvq_decode_workspace_size``,
 ``kvq_row_bytes``, ``kvq_copy_pages``, ``kvq_fork``, ``kvq_compact`` and their ``_workspace_size``,
-``kvq_rope``, ``kvq_rope_write``, ``kvq_rope_write_decode_attn``, ``kvq_rope_frequencies``.
+``kvq_cross_attn``, ``kvq_cross_dense_attn`` and theirs, ``kvq_rope``, ``kvq_rope_write``, ``kvq_rope_write_decode_attn``, ``kvq_rope_frequencies``.
 
 A call runs on the device of its cache, on `stream` if one is given, else on
 that device's current stream; what it allocates belongs to that stream.
@@ -111,6 +111,15 @@ _lib.kvq_rope_write_decode_attn.argtypes = [_CP, _PP, _RP, _P, _P, _P, _I, _P, _
                                             ctypes.c_size_t, _I, _P, _P]
 _lib.kvq_rope_write_decode_attn.restype = _I
 _SZ = ctypes.POINTER(ctypes.c_size_t)
+_lib.kvq_cross_workspace_size.argtypes = [_CP, _PP, _I, _I, _SZ]
+_lib.kvq_cross_workspace_size.restype = _I
+_lib.kvq_cross_attn.argtypes = [_CP, _PP, _P, _I, _I, _P, _I, _I, ctypes.c_float, _P, _P, ctypes.c_size_t, _P, _P]
+_lib.kvq_cross_attn.restype = _I
+_lib.kvq_cross_dense_workspace_size.argtypes = [_I, _I, _I, _I, _I, _I, _SZ]
+_lib.kvq_cross_dense_workspace_size.restype = _I
+_lib.kvq_cross_dense_attn.argtypes = [_P, _P, _P, _I, _I, _I, _PP, _P, _I, _I, _P, _I, _I, ctypes.c_float, _P, _P,
+                                      ctypes.c_size_t, _P, _P]
+_lib.kvq_cross_dense_attn.restype = _I
 _lib.kvq_copy_workspace_size.argtypes = [_CP, _I, _I, _I, _SZ]
 _lib.kvq_copy_workspace_size.restype = _I
 _lib.kvq_copy_pages.argtypes = [_CP, _I, _P, _P, _I, _I, _P, ctypes.c_size_t, _P, _P]
@@ -621,6 +630,92 @@ def kvq_prefill_dense_attn(k: torch.Tensor, v: torch.Tensor, cu_kv: torch.Tensor
          _dev_ptr(cu_kv, torch.int32, "cu_kv", dev), int(k.shape[0]), int(k.shape[1]), int(k.shape[2]),
          ctypes.byref(ps), _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q", dev), T,
          int(max_q_per_seq), float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev),
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# cross attention
+
+def kvq_cross_workspace_size(cache: PagedCache, paging: Paging, num_q_heads: int, max_q_per_seq: int) -> int:
+    """Bytes of scratch that kvq_cross_attn needs (may be 0)."""
+    cs, ps = _structs(cache, paging)
+    size = ctypes.c_size_t(0)
+    _check(_lib.kvq_cross_workspace_size(ctypes.byref(cs), ctypes.byref(ps), int(num_q_heads), int(max_q_per_seq),
+                                         ctypes.byref(size)))
+    return size.value
+
+
+def _check_cross(q: torch.Tensor, head_dim: int, cu_q: torch.Tensor, batch: int, out: Optional[torch.Tensor]) -> None:
+    if q.dim() != 3:
+        raise ValueError("q must be [total_q, num_q_heads, %d], got %s" % (head_dim, tuple(q.shape)))
+    _check_prefill(q, head_dim, cu_q, batch, out)
+
+
+def _scratch(workspace, nbytes: int, dev: int, q: torch.Tensor, stream):
+    """(pointer, bytes, the tensor) of a call's scratch: the one given, or one of nbytes bytes."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = _empty(nbytes, torch.uint8, q.device, stream)
+    return _dev_ptr(workspace, torch.uint8, "workspace", dev), workspace.numel(), workspace
+
+
+def kvq_cross_attn(cache: PagedCache, paging: Paging, q: torch.Tensor, cu_q: torch.Tensor, max_q_per_seq: int,
+                   softmax_scale: float, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   dev_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of q [total_q, num_q_heads, head_dim] (sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1, at
+    most max_q_per_seq) to every cached row of their sequence, seq_lens[b] of them; not causal.  Returns fp32 out."""
+    cs, ps = _structs(cache, paging)
+    dev = cache.k_pages.get_device()
+    _check_cross(q, cache.head_dim, cu_q, ps.batch, out)
+    T, Hq, _ = q.shape
+    nbytes = 0 if workspace is not None else kvq_cross_workspace_size(cache, paging, Hq, max_q_per_seq)
+    if out is None:
+        out = _empty(q.shape, torch.float32, q.device, stream)
+    wp, wn, _keep = _scratch(workspace, nbytes, dev, q, stream)
+    _run(cache.k_pages.device, stream, _lib.kvq_cross_attn, ctypes.byref(cs), ctypes.byref(ps),
+         _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q", dev), T, int(max_q_per_seq),
+         float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev), wp, wn,
+         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
+    return out
+
+
+def _check_dense(k: torch.Tensor) -> None:
+    if k.dim() != 3:
+        raise ValueError("k and v must be [rows, num_kv_heads, head_dim], got %s" % (tuple(k.shape),))
+
+
+def kvq_cross_dense_workspace_size(k: torch.Tensor, seq_lens: torch.Tensor, num_q_heads: int, max_q_per_seq: int) -> int:
+    """Bytes of scratch that kvq_cross_dense_attn over k [rows, num_kv_heads, head_dim] needs (may be 0)."""
+    _check_dense(k)
+    size = ctypes.c_size_t(0)
+    _check(_lib.kvq_cross_dense_workspace_size(int(k.shape[0]), int(k.shape[1]), int(k.shape[2]), int(seq_lens.shape[0]),
+                                               int(num_q_heads), int(max_q_per_seq), ctypes.byref(size)))
+    return size.value
+
+
+def kvq_cross_dense_attn(k: torch.Tensor, v: torch.Tensor, cu_kv: torch.Tensor, seq_lens: torch.Tensor,
+                         q: torch.Tensor, cu_q: torch.Tensor, max_q_per_seq: int, softmax_scale: float,
+                         out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         dev_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """kvq_cross_attn over dense bf16 k, v [rows, num_kv_heads, head_dim] (sequence b's row j at row cu_kv[b] + j)."""
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.shape != v.shape:
+        raise ValueError("k and v must be bfloat16 tensors of one shape")
+    _check_dense(k)
+    dev, batch = k.get_device(), int(seq_lens.shape[0])
+    _check_cross(q, k.shape[2], cu_q, batch, out)
+    _check_cu(cu_kv, batch, "cu_kv")
+    T, Hq, _ = q.shape
+    nbytes = 0 if workspace is not None else kvq_cross_dense_workspace_size(k, seq_lens, Hq, max_q_per_seq)
+    if out is None:
+        out = _empty(q.shape, torch.float32, q.device, stream)
+    wp, wn, _keep = _scratch(workspace, nbytes, dev, q, stream)
+    ps = KvqPaging(None, None, 0, batch, _dev_ptr(seq_lens, torch.int32, "seq_lens", dev), None, 0)
+    _run(k.device, stream, _lib.kvq_cross_dense_attn, _dev_ptr(k, None, "k", dev), _dev_ptr(v, None, "v", dev),
+         _dev_ptr(cu_kv, torch.int32, "cu_kv", dev), int(k.shape[0]), int(k.shape[1]), int(k.shape[2]),
+         ctypes.byref(ps), _dev_ptr(q, None, "q", dev), _qdtype(q), Hq, _dev_ptr(cu_q, torch.int32, "cu_q", dev), T,
+         int(max_q_per_seq), float(softmax_scale), _dev_ptr(out, torch.float32, "out", dev), wp, wn,
          _dev_ptr(dev_error, torch.int32, "dev_error", dev))
     return out
 

@@ -195,8 +195,8 @@ kvq::RopeArgs rope_args(const kvq_rotary* r, const int32_t* positions) {
   return a;
 }
 
-kvq::DecodeLayout decode_layout(const kvq_cache* c, const kvq_paging* p, int32_t num_q_heads) {
-  const int group = num_q_heads / c->num_kv_heads;
+kvq::DecodeLayout decode_layout(const kvq_cache* c, const kvq_paging* p, int32_t num_q_heads, int slots = 1) {
+  const int group = num_q_heads / c->num_kv_heads * slots;
   return kvq::decode_ws_layout(p->batch, c->num_kv_heads, group, c->head_dim, sm_count(),
                                kvq::decode_shape(kernel_mode(c->mode), c->head_dim, group));
 }
@@ -222,6 +222,12 @@ kvq_status noalloc_scratch(void** out) {
     g_noalloc_ptr[dev] = p;
   }
   *out = g_noalloc_ptr[dev];
+  return KVQ_OK;
+}
+
+kvq_status check_scratch(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need) return fail(KVQ_ERR_WORKSPACE, "workspace missing or too small");
+  if (!aligned(ws, 256)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   return KVQ_OK;
 }
 
@@ -517,9 +523,17 @@ struct FusedWrite {
   const int32_t* positions = nullptr;
 };
 
+// The queries of a cross attention call that the decode kernels serve: up to
+// max_q of a sequence, max_q times the group in the slots of a pair.
+struct CrossQueries {
+  const int32_t* cu_q = nullptr;
+  int32_t total_q = 0, max_q = 0;
+};
+
 kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const void* q, int32_t dtype,
                        int32_t num_q_heads, float softmax_scale, float* out, void* workspace, size_t workspace_bytes,
-                       int32_t num_splits, int32_t* dev_error, void* stream, const FusedWrite& fw) {
+                       int32_t num_splits, int32_t* dev_error, void* stream, const FusedWrite& fw,
+                       const CrossQueries& cq = CrossQueries()) {
   kvq_status st = check_cache(cache);
   if (st != KVQ_OK) return st;
   if ((st = check_paging(paging, cache->num_kv_heads)) != KVQ_OK) return st;
@@ -528,10 +542,18 @@ kvq_status decode_call(const kvq_cache* cache, const kvq_paging* paging, const v
   if ((long long)paging->batch * cache->num_kv_heads + 1 > 0x7FFFFFFFLL)
     return fail(KVQ_ERR_UNSUPPORTED, "batch * num_kv_heads too large");
   if ((st = check_positions(cache, paging)) != KVQ_OK) return st;
-  const kvq::DecodeLayout L = decode_layout(cache, paging, num_q_heads);
+  const kvq::DecodeLayout L = decode_layout(cache, paging, num_q_heads, cq.cu_q ? cq.max_q : 1);
   if (!workspace || workspace_bytes < L.total) return fail(KVQ_ERR_WORKSPACE, "workspace missing or too small");
   if (!aligned(workspace, 256)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   kvq::AttnParams P = attn_params(cache, paging, q, dtype, num_q_heads, softmax_scale, out, dev_error);
+  if (cq.cu_q) {
+    P.cu_q = cq.cu_q;
+    P.total_q = cq.total_q;
+    P.max_q_per_seq = cq.max_q;
+    P.q_group = P.group;
+    P.group *= cq.max_q;
+  }
+  P.exact = cq.cu_q || fw.rope;
   const int rpc = kvq::decode_chunk_rows(P.mode, P.head_dim, P.group);
   if (rpc > 0) {  // the stream kernel's tensor copies: one map per pool
     const int R = kvq_row_bytes(cache->mode, cache->head_dim);
@@ -708,16 +730,16 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 // [rows][Hkv][D] bf16 seen as a 4-D tensor (64, D / 64, Hkv, rows): a box of
-// 64 elements x 1 half x 1 head x 64 rows is one 64-dim half of the tile of
+// 64 elements x 1 half x 1 head x box_rows (64, say) rows is one 64-dim half of the tile of
 // one head, 64 lines of 128 bytes whose 16-byte pieces land XOR-swizzled by
 // the line index (128-byte swizzle), so that the expansion's reads of one
 // column across eight rows fall in eight different banks.
-bool dense_rows_map(CUtensorMap* map, const void* base, int64_t rows, int Hkv, int D) {
+bool dense_rows_map(CUtensorMap* map, const void* base, int64_t rows, int Hkv, int D, int box_rows = 64) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc || D % 64 != 0) return false;
   const cuuint64_t dims[4] = {64, (cuuint64_t)D / 64, (cuuint64_t)Hkv, (cuuint64_t)rows};
   const cuuint64_t strides[3] = {128, (cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2};
-  const cuuint32_t box[4] = {64, 1, 1, 64};
+  const cuuint32_t box[4] = {64, 1, 1, (cuuint32_t)box_rows};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -803,6 +825,233 @@ kvq_status kvq_prefill_dense_attn(const void* k, const void* v, const int32_t* c
   cudaError_t e = kvq::launch_prefill(P, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   return KVQ_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// cross attention
+
+namespace {
+
+// (query, q head) rows of a (sequence, kv head) pair up to which the decode
+// kernels serve a call: they take that many slots, stream the pages once at
+// the decode's rate and split them over every SM.
+constexpr int CROSS_SLOTS = 8;
+
+bool cross_by_decode(int32_t group, int32_t max_q) { return (long long)group * max_q <= CROSS_SLOTS; }
+
+// Parts that a query tile's keys are cut into, for `tiles` query tiles of up to
+// `key_tiles` key tiles each: the number for which the waves of parts over the
+// SMs take the shortest, a part costing its key tiles and four more to start
+// and end, and the join of the parts another four.
+int cross_splits(long long tiles, long long key_tiles) {
+  const int sms = sm_count();
+  int best = 1;
+  long long least = LLONG_MAX;
+  for (int s = 1; s <= 64 && s <= std::max(1LL, key_tiles); ++s) {
+    const long long waves = (tiles * s + sms - 1) / sms;
+    const long long cost = waves * ((key_tiles + s - 1) / s + 4) + (s > 1 ? 4 : 0);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+    if (tiles * s >= 2LL * sms) break;  // every SM has its share
+  }
+  return best;
+}
+
+struct CrossPlan {
+  int group = 0, splits = 1;
+  size_t bytes = 0;
+};
+
+// Parts and scratch of a call by the tensor-core kernels.  The size does not go
+// by the queries' type, so it is that of the form with more of it.
+kvq_status cross_plan(int32_t num_kv_heads, int32_t num_q_heads, int32_t batch, int32_t head_dim, int32_t max_q,
+                      long long most_keys, bool rows16, bool f32, CrossPlan* plan) {
+  plan->group = num_q_heads / num_kv_heads;
+  const long long tiles = kvq::prefill_grid_x(max_q, plan->group), pairs = (long long)num_kv_heads * batch;
+  if (num_kv_heads > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_kv_heads > 65535");
+  size_t most = 0;
+  for (int i = 0; i < 2; ++i) {
+    const bool wide = rows16 && i == 0;  // two row tiles per CTA
+    const long long blocks = wide ? kvq::cross16_blocks(max_q, plan->group, false) : tiles;
+    const int splits = cross_splits(blocks * pairs, (most_keys + (rows16 ? 127 : 63)) / (rows16 ? 128 : 64));
+    if (blocks * splits > 0x7FFFFFFFLL)
+      return fail(KVQ_ERR_UNSUPPORTED, "max_q_per_seq gives more query tiles than one launch can hold");
+    if (splits > 1)
+      most = std::max(most, (size_t)(blocks * (wide ? 2 : 1) * pairs * splits * kvq::split_record_floats(head_dim) * 4));
+    if (rows16 && wide == f32) continue;  // (the other form's)
+    plan->splits = splits;
+  }
+  plan->bytes = most;
+  return KVQ_OK;
+}
+
+kvq_status check_cross_heads(int32_t num_kv_heads, int32_t num_q_heads, int32_t max_q) {
+  if (num_q_heads <= 0 || num_q_heads % num_kv_heads != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (num_q_heads / num_kv_heads > 8) return fail(KVQ_ERR_UNSUPPORTED, "GQA group size above 8");
+  if (max_q < 0) return fail(KVQ_ERR_INVALID_ARG, "max_q_per_seq < 0");
+  return KVQ_OK;
+}
+
+// The bf16 rows of a call: the dense ones, or the pools' (box rows of one chunk).
+kvq_status cross16_maps(kvq::AttnParams& P, const void* k, const void* v, int64_t rows, int heads, int box_rows) {
+  P.chunk_rows_total = (int)rows;
+  if (!dense_rows_map(&P.kv_map[0], k, rows, heads, P.head_dim, box_rows) ||
+      !dense_rows_map(&P.kv_map[1], v, rows, heads, P.head_dim, box_rows))
+    return fail(KVQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the K / V rows");
+  return KVQ_OK;
+}
+
+kvq_status check_no_window(const kvq_paging* p) {
+  if (p->window_per_kv_head) return fail(KVQ_ERR_UNSUPPORTED, "cross attention takes no sliding windows");
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_cross_workspace_size(const kvq_cache* cache, const kvq_paging* paging, int32_t num_q_heads,
+                                    int32_t max_q_per_seq, size_t* bytes) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if ((st = check_paging(paging, cache->num_kv_heads)) != KVQ_OK) return st;
+  if ((st = check_no_window(paging)) != KVQ_OK) return st;
+  if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is NULL");
+  if ((st = check_cross_heads(cache->num_kv_heads, num_q_heads, max_q_per_seq)) != KVQ_OK) return st;
+  *bytes = 0;
+  if (paging->batch == 0 || max_q_per_seq == 0) return KVQ_OK;
+  if (cross_by_decode(num_q_heads / cache->num_kv_heads, max_q_per_seq)) {
+    *bytes = decode_layout(cache, paging, num_q_heads, max_q_per_seq).total;
+    return KVQ_OK;
+  }
+  CrossPlan plan;
+  st = cross_plan(cache->num_kv_heads, num_q_heads, paging->batch, cache->head_dim, max_q_per_seq,
+                  (long long)paging->max_blocks * cache->block_size, cache->mode == KVQ_BF16_CACHE, false, &plan);
+  *bytes = plan.bytes;
+  return st;
+}
+
+kvq_status kvq_cross_attn(const kvq_cache* cache, const kvq_paging* paging, const void* q, int32_t dtype,
+                          int32_t num_q_heads, const int32_t* cu_q, int32_t total_q, int32_t max_q_per_seq,
+                          float softmax_scale, float* out, void* workspace, size_t workspace_bytes,
+                          int32_t* dev_error, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if ((st = check_paging(paging, cache->num_kv_heads)) != KVQ_OK) return st;
+  if ((st = check_no_window(paging)) != KVQ_OK) return st;
+  if (total_q < 0 || max_q_per_seq < 0) return fail(KVQ_ERR_INVALID_ARG, "total_q / max_q_per_seq < 0");
+  if (paging->batch == 0 || total_q == 0 || max_q_per_seq == 0) return KVQ_OK;
+  if ((st = check_q(cache, q, dtype, num_q_heads, out)) != KVQ_OK) return st;
+  if (!cu_q) return fail(KVQ_ERR_INVALID_ARG, "cu_q is NULL");
+  if ((st = check_positions(cache, paging)) != KVQ_OK) return st;
+  if (cross_by_decode(num_q_heads / cache->num_kv_heads, max_q_per_seq)) {
+    CrossQueries cq;
+    cq.cu_q = cu_q;
+    cq.total_q = total_q;
+    cq.max_q = max_q_per_seq;
+    return decode_call(cache, paging, q, dtype, num_q_heads, softmax_scale, out, workspace, workspace_bytes, 0,
+                       dev_error, stream, FusedWrite(), cq);
+  }
+  CrossPlan plan;
+  if ((st = cross_plan(cache->num_kv_heads, num_q_heads, paging->batch, cache->head_dim, max_q_per_seq,
+                       (long long)paging->max_blocks * cache->block_size, cache->mode == KVQ_BF16_CACHE,
+                       dtype == KVQ_F32, &plan)) != KVQ_OK)
+    return st;
+  if (plan.bytes > 0 && (st = check_scratch(workspace, workspace_bytes, plan.bytes)) != KVQ_OK) return st;
+  kvq::AttnParams P = attn_params(cache, paging, q, dtype, num_q_heads, softmax_scale, out, dev_error);
+  P.cu_q = cu_q;
+  P.total_q = total_q;
+  P.max_q_per_seq = max_q_per_seq;
+  P.cross = 1;
+  P.splits = plan.splits;
+  P.part = static_cast<float*>(workspace);
+  cudaError_t e;
+  if (cache->mode == KVQ_BF16_CACHE) {
+    const long long rows = (long long)cache->num_blocks * cache->num_kv_heads * cache->block_size;
+    if (rows > INT_MAX - 64) return fail(KVQ_ERR_UNSUPPORTED, "pool too large for 32-bit row numbers");
+    if ((st = cross16_maps(P, cache->k_pages, cache->v_pages, rows, 1, 16)) != KVQ_OK) return st;
+    e = kvq::launch_cross16(P, static_cast<cudaStream_t>(stream));
+  } else {
+    e = kvq::launch_prefill(P, static_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+kvq_status kvq_cross_dense_workspace_size(int32_t num_kv_rows, int32_t num_kv_heads, int32_t head_dim, int32_t batch,
+                                          int32_t num_q_heads, int32_t max_q_per_seq, size_t* bytes) {
+  if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is NULL");
+  if (head_dim != 64 && head_dim != 128) return fail(KVQ_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (num_kv_heads <= 0 || num_kv_rows < 0 || batch < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_kv_heads <= 0, num_kv_rows < 0 or batch < 0");
+  if (batch > 65535) return fail(KVQ_ERR_UNSUPPORTED, "batch > 65535");
+  kvq_status st = check_cross_heads(num_kv_heads, num_q_heads, max_q_per_seq);
+  if (st != KVQ_OK) return st;
+  *bytes = 0;
+  if (batch == 0 || max_q_per_seq == 0) return KVQ_OK;
+  CrossPlan plan;
+  st = cross_plan(num_kv_heads, num_q_heads, batch, head_dim, max_q_per_seq, num_kv_rows, true, false, &plan);
+  *bytes = plan.bytes;
+  return st;
+}
+
+kvq_status kvq_cross_dense_attn(const void* k, const void* v, const int32_t* cu_kv, int32_t num_kv_rows,
+                                int32_t num_kv_heads, int32_t head_dim, const kvq_paging* paging, const void* q,
+                                int32_t dtype, int32_t num_q_heads, const int32_t* cu_q, int32_t total_q,
+                                int32_t max_q_per_seq, float softmax_scale, float* out, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  if (!paging) return fail(KVQ_ERR_INVALID_ARG, "paging is NULL");
+  if (paging->block_tables || paging->block_tables_headwise)
+    return fail(KVQ_ERR_INVALID_ARG, "dense attention takes no block table");
+  kvq_status st = check_no_window(paging);
+  if (st != KVQ_OK) return st;
+  size_t need = 0;
+  if ((st = kvq_cross_dense_workspace_size(num_kv_rows, num_kv_heads, head_dim, paging->batch, num_q_heads,
+                                           max_q_per_seq, &need)) != KVQ_OK)
+    return st;
+  if (total_q < 0) return fail(KVQ_ERR_INVALID_ARG, "total_q < 0");
+  if (paging->batch == 0 || total_q == 0 || max_q_per_seq == 0) return KVQ_OK;
+  if (num_kv_rows == 0) return fail(KVQ_ERR_INVALID_ARG, "no K / V rows");
+  if (num_kv_rows > INT_MAX - 256) return fail(KVQ_ERR_UNSUPPORTED, "too many K / V rows");
+  if (!k || !v || !cu_kv || !cu_q || !paging->seq_lens) return fail(KVQ_ERR_INVALID_ARG, "k / v / cu_kv / cu_q / seq_lens is NULL");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(KVQ_ERR_INVALID_ARG, "k / v must be 16-byte aligned");
+  if (!q || !out) return fail(KVQ_ERR_INVALID_ARG, "q / out is NULL");
+  if (dtype != KVQ_F32 && dtype != KVQ_BF16) return fail(KVQ_ERR_UNSUPPORTED, "dtype must be KVQ_F32 or KVQ_BF16");
+  if (!aligned(q, 16) || !aligned(out, 16)) return fail(KVQ_ERR_INVALID_ARG, "q / out must be 16-byte aligned");
+  CrossPlan plan;
+  if ((st = cross_plan(num_kv_heads, num_q_heads, paging->batch, head_dim, max_q_per_seq, num_kv_rows, true,
+                       dtype == KVQ_F32, &plan)) != KVQ_OK)
+    return st;
+  if (need > 0 && (st = check_scratch(workspace, workspace_bytes, need)) != KVQ_OK) return st;
+  kvq::AttnParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.num_kv_heads = num_kv_heads;
+  P.block_size = 16;  // (no pages: cu_kv bounds the positions)
+  P.head_dim = head_dim;
+  P.mode = kvq::MODE_DBF16;
+  P.batch = paging->batch;
+  P.seq_lens = paging->seq_lens;
+  P.q = q;
+  P.dtype = dtype;
+  P.num_q_heads = num_q_heads;
+  P.group = num_q_heads / num_kv_heads;
+  P.softmax_scale = softmax_scale;
+  P.out = out;
+  P.dev_error = dev_error;
+  P.cu_q = cu_q;
+  P.total_q = total_q;
+  P.max_q_per_seq = max_q_per_seq;
+  P.cu_kv = cu_kv;
+  P.cross = 1;
+  P.splits = plan.splits;
+  P.part = static_cast<float*>(workspace);
+  if ((st = cross16_maps(P, k, v, num_kv_rows, num_kv_heads, 128)) != KVQ_OK) return st;
+  const cudaError_t e = kvq::launch_cross16(P, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }
 
 }  // extern "C"
@@ -912,12 +1161,6 @@ kvq::PagePlan page_plan(const kvq_cache* c, const kvq_paging* p, int32_t* dev_er
   P.bs_log2 = c->block_size == 16 ? 4 : c->block_size == 32 ? 5 : 6;
   P.dev_error = dev_error;
   return P;
-}
-
-kvq_status check_scratch(const void* ws, size_t have, size_t need) {
-  if (!ws || have < need) return fail(KVQ_ERR_WORKSPACE, "workspace missing or too small");
-  if (!aligned(ws, 256)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  return KVQ_OK;
 }
 
 // Whether n ints at a and m ints at b share memory (NULL shares with nothing).

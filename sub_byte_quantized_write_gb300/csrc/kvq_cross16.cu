@@ -1,0 +1,560 @@
+// kvq_cross16.cu -- cross attention over 16-bit (bf16) rows, dense or in pages,
+// on the 5th-generation tensor cores (tcgen05, TMEM).
+//
+// For every query i of sequence b and q head: out = sum_j p_j v_j / sum_j p_j
+// with p_j = exp(scale q_i . k_j) over all seq_lens[b] rows of the sequence,
+// whatever the number of queries.  4 D flops per (query, q head, key).
+//
+// Design: one CTA of 10 warps per (up to 256 rows, kv head, sequence, part of
+// the keys); a row is a (query, q head of the GQA group) pair, 128 rows make a
+// tile, and the CTA's two tiles share every K and V tile of 128 keys.
+//   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread per row: the row's
+//                   128 logits from TMEM, its maximum, the weights, and those
+//                   back to TMEM over the logits.  While one tile is in its
+//                   softmax the tensor cores work on the other.
+//   warp 8          TMEM; lane 0 issues S = Q K^T (M = 128 rows, N = 128 keys)
+//                   and O += P V (N = D).
+//   warp 9          tensor copies: K and V rows land as they are, 128-byte
+//                   swizzled, ready to be operands: K as K-major, V as MN-major,
+//                   so nothing is converted or transposed.
+// bf16 x bf16 products are exact in the fp32 sums.  An fp32 query is three bf16
+// terms (24 bits), three products into one sum, and one row tile per CTA.  The
+// weights are two bf16 terms (17 bits: 2^-18 of a weight at most, 2e-6 of an
+// output; one term alone would be 1e-3), so P.V takes twice its operations and
+// the whole call 1.5 times 4 D per pair, which bounds it: two thirds of the
+// tensor cores' rate.  The running maximum is a reference that moves, and O is
+// rescaled, only when a logit passes it by 2^8.
+// Rows that are not there (an evicted page, past the sequence's end): chunks of
+// a page without an entry are copied from past the tensor's end, which gives
+// zeros, and masked; value rows past the end of the sequence, which may hold
+// anything, are zeroed in shared memory before the last P.V (a weight 0 does not
+// cancel a NaN).
+// Every wait is bounded; on a timeout the CTA reports KVQ_DEVERR_TIMEOUT,
+// drains, frees its TMEM and returns.
+//
+// Sources: FastDeploy PR #7718 "Optimize AppendAttention for discrete head-wise
+// block_idx" (head-wise tables, -1 sentinel); vllm-ascend-quantized-kv-cache
+// METADATA, 运行机制 (gather, then dense attention).
+
+#include <math_constants.h>
+
+#include "kvq_decode.cuh"
+#include "kvq_internal.h"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int CX_ROWS = PREFILL_ROWS;  // rows of a tile
+constexpr int CX_KT = 128;             // keys of a tile
+constexpr int CX_CHUNK = 16;           // rows of a page copied at a time
+constexpr int CX_THREADS = 320;
+constexpr int CX_MMA_WARP = 8, CX_COPY_WARP = 9;
+constexpr float CX_SLACK = 8.0f;  // log2 units a logit may pass the reference maximum by
+constexpr uint32_t CX_NAP = 20;   // ns between polls of a wait
+
+template <int D, int TERMS>
+struct CxCfg {
+  static constexpr int TILES = TERMS == 1 ? 2 : 1;  // row tiles of a CTA
+  static constexpr int HALF = CX_KT * 128;          // 64 dims of 128 rows: 128 lines of 128 bytes
+  static constexpr int TILE = (D / 64) * HALF;      // 128 rows of Q, K or V
+  static constexpr int NST = 2;                     // K stages, and V stages
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + TILES * TERMS * TILE;
+  static constexpr int OFF_V = OFF_K + NST * TILE;
+  static constexpr int OFF_MASK = OFF_V + NST * TILE;  // [4] chunks of tile v & 3 that hold rows
+  static constexpr int OFF_BAR = OFF_MASK + 16;
+  static constexpr int OFF_MISC = OFF_BAR + 16 * 8;    // TMEM address, abort flag
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  // TMEM columns: S (P over it: high terms, then low terms) and O of each row tile
+  static constexpr int TM_O = 2 * CX_KT;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+enum { CB_KFULL = 0, CB_KEMPTY = 2, CB_VFULL = 4, CB_VEMPTY = 6, CB_SFULL = 8, CB_PFULL = 10, CB_ODONE = 12, CB_DRAIN = 13 };
+
+// kind::f16 with bf16 operands and fp32 sums; B K-major, or MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+// MN-major operand in 128-byte-swizzled lines of 64 elements along MN: groups of
+// 8 lines along K 1024 bytes apart, the next 64 elements `lead` bytes further.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, int lead) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace
+
+// Rows that sequence b's queries see, -1 where the sequence is skipped (its
+// dense rows do not hold them).  `flag`: report what is wrong.
+__device__ __forceinline__ int cross_keys(const AttnParams& P, int b, bool flag) {
+  int L = load_input<false>(P.seq_lens + b);
+  if (L < 0) {
+    if (flag) flag_error(P.dev_error, DEVERR_SEQ_LEN);
+    L = 0;
+  }
+  if (P.cu_kv) {
+    const int c0 = load_input<false>(P.cu_kv + b), rows = load_input<false>(P.cu_kv + b + 1) - c0;
+    if (rows < L || (L > 0 && (c0 < 0 || c0 > P.chunk_rows_total - L))) {
+      if (flag) flag_error(P.dev_error, DEVERR_SEQ_LEN);
+      return -1;
+    }
+  } else if (L > P.max_blocks * P.block_size) {
+    if (flag) flag_error(P.dev_error, DEVERR_TABLE_RANGE);
+    L = P.max_blocks * P.block_size;
+  }
+  return L;
+}
+
+template <int D, int TERMS>
+__global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_constant__ AttnParams P) {
+  using C = CxCfg<D, TERMS>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int sp = blockIdx.x % P.splits, block = blockIdx.x / P.splits;  // part of the keys, group of row tiles
+  const int G = P.group, Hkv = P.num_kv_heads, QB = CX_ROWS / G;
+
+  const int cq0 = __ldg(P.cu_q + b);
+  int n = __ldg(P.cu_q + b + 1) - cq0;
+  const bool first = tid == 0 && block == 0 && h == 0 && sp == 0;
+  if (first && (n > P.max_q_per_seq || (n > 0 && (cq0 < 0 || cq0 > P.total_q - n)))) flag_error(P.dev_error, DEVERR_SEQ_LEN);
+  n = min(n, P.max_q_per_seq);
+  const int q0 = block * C::TILES * QB;
+  if (q0 >= n || cq0 < 0) return;
+  n = min(n, P.total_q - cq0);  // rows past the q that was given are neither read nor written
+  if (q0 >= n) return;
+  const int tiles = min(C::TILES, (n - q0 + QB - 1) / QB);
+  const int L = cross_keys(P, b, first);
+  if (L < 0) return;
+  const int n_total = (L + CX_KT - 1) / CX_KT;
+  const int v0 = (int)((long long)sp * n_total / P.splits);
+  const int nv = (int)((long long)(sp + 1) * n_total / P.splits) - v0;  // this part's key tiles
+
+  volatile int* mask = reinterpret_cast<volatile int*>(sm + C::OFF_MASK);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
+  if (tid == 0) {
+    for (int i = 0; i < 14; ++i) mbar_init(bar + i, i == CB_PFULL || i == CB_PFULL + 1 ? CX_ROWS : 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == CX_MMA_WARP) tc::alloc(tmem_slot, 512);
+
+  // the rows' queries, as bf16 terms in the operand's layout (rows without a query: zeros)
+  const bool negative = P.softmax_scale < 0.0f;  // carried by the queries
+  for (int i = tid; i < tiles * CX_ROWS * (D / 8); i += CX_THREADS) {
+    const int c = i % (D / 8), r = i / (D / 8) % CX_ROWS, t = i / (D / 8) / CX_ROWS;
+    const int qi = q0 + t * QB + r / G;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+    if (r / G < QB && qi < n && KVQ_IN_BOUNDS(cq0 + qi < P.total_q, P.dev_error))
+      load_row_elems<8>(P.q, TERMS == 1 ? DT_BF16 : DT_F32, ((size_t)(cq0 + qi) * P.num_q_heads + h * G + r % G) * D + 8 * c, x);
+    if (negative) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = -x[e];
+    }
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+        x[2 * e] -= __uint_as_float(w[e] << 16);
+        x[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint4*>(sm + C::OFF_Q + (t * TERMS + k) * C::TILE + (c >> 3) * C::HALF + tc::sw128_off(r, c & 7)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  tc::fence_proxy_async();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == CX_COPY_WARP) {
+    // ======================= copies =======================
+    // pages: lane c of the first eight has chunk c of each tile, and looks up its
+    // table entry one tile before it is copied
+    const bool paged = P.cu_kv == nullptr;
+    const int32_t* tbl = P.table + (paged ? (size_t)(P.headwise ? b * Hkv + h : b) * P.max_blocks : 0);
+    const int bs = P.block_size, bs_log2 = __ffs(bs) - 1;
+    const int row0 = paged ? 0 : __ldg(P.cu_kv + b);
+    auto lookup = [&](int v) -> int {
+      const int key = (v0 + v) * CX_KT + CX_CHUNK * lane;
+      return paged && lane < CX_KT / CX_CHUNK && v < nv && key < L ? __ldg(tbl + (key >> bs_log2)) : -1;
+    };
+    int entry = lookup(0), err = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int v = 0; v < nv && ok; ++v) {
+      const int st = v & 1, parity = ((v >> 1) & 1) ^ 1;
+      const int key0 = (v0 + v) * CX_KT;
+      int row = P.chunk_rows_total;  // past the end: zeros
+      if (entry >= P.num_blocks) err |= DEVERR_BLOCK_RANGE;
+      else if (entry >= 0) row = (entry * Hkv + h) * bs + ((key0 + CX_CHUNK * lane) & (bs - 1));
+      const unsigned found = paged ? __ballot_sync(0xffffffffu, row < P.chunk_rows_total) : 0xFFu;
+      entry = lookup(v + 1);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + (kv ? CB_VEMPTY : CB_KEMPTY) + st, parity, CX_NAP)) ||
+            __any_sync(0xffffffffu, *abort_flag != 0)) {
+          ok = false;
+          break;
+        }
+        uint64_t* full = bar + (kv ? CB_VFULL : CB_KFULL) + st;
+        uint8_t* dst = sm + (kv ? C::OFF_V : C::OFF_K) + st * C::TILE;
+        if (lane == 0) {
+          if (kv == 0) mask[v & 3] = (int)found;
+          mbar_arrive_expect_tx(full, C::TILE);
+        }
+        __syncwarp();
+        if (paged) {
+          if (lane < CX_KT / CX_CHUNK) {
+#pragma unroll
+            for (int hh = 0; hh < D / 64; ++hh)
+              tc::tma_load_4d(dst + hh * C::HALF + lane * (CX_CHUNK * 128), &P.kv_map[kv], 0, hh, 0, row, full);
+          }
+        } else if (lane == 0) {
+#pragma unroll
+          for (int hh = 0; hh < D / 64; ++hh)
+            tc::tma_load_4d(dst + hh * C::HALF, &P.kv_map[kv], 0, hh, h, row0 + key0, full);
+        }
+      }
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
+    }
+    err = __reduce_or_sync(0xffffffffu, err);
+    if (err && lane == 0) flag_error(P.dev_error, err);
+  } else if (warp == CX_MMA_WARP) {
+    // ======================= MMA issue =======================
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16(CX_ROWS, CX_KT, false), id_o = idesc_bf16(CX_ROWS, D, true);
+      // S(t, v) goes where P(t, v - 1) was: P.V(t, v - 1) was issued before it, and
+      // this thread's MMAs run in order; its commit tells the softmax of both.
+      auto logits = [&](int t, int st) {
+        const uint32_t a = smem_addr(sm + C::OFF_Q + t * TERMS * C::TILE), k = smem_addr(sm + C::OFF_K + st * C::TILE);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint64_t bd = tc::sw128_desc(k + (s >> 2) * C::HALF + (s & 3) * 32);
+#pragma unroll
+          for (int i = 0; i < TERMS; ++i)
+            tc::mma_f16(tmem + t * CX_KT, tc::sw128_desc(a + i * C::TILE + (s >> 2) * C::HALF + (s & 3) * 32), bd, id_s,
+                        s > 0 || i > 0 ? 1u : 0u);
+        }
+        tc::commit(bar + CB_SFULL + t);
+      };
+      bool ok = true;
+      if (nv > 0) {
+        ok = mbar_wait_bounded(bar + CB_KFULL, 0, CX_NAP);
+        if (ok) {
+          tc::fence_after();
+          for (int t = 0; t < tiles; ++t) logits(t, 0);
+          tc::commit(bar + CB_KEMPTY);
+        }
+      }
+#pragma unroll 1
+      for (int v = 0; v < nv && ok; ++v) {
+        const int st = v & 1;
+        ok = mbar_wait_bounded(bar + CB_VFULL + st, (v >> 1) & 1, CX_NAP);
+#pragma unroll 1
+        for (int t = 0; t < tiles && ok; ++t) {
+          ok = mbar_wait_bounded(bar + CB_PFULL + t, v & 1, CX_NAP) && !*abort_flag;
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t p = tmem + t * CX_KT, o = tmem + C::TM_O + t * D, vt = smem_addr(sm + C::OFF_V + st * C::TILE);
+#pragma unroll
+          for (int kk = 0; kk < CX_KT / 16; ++kk) {
+            const uint64_t bd = mn_desc(vt + kk * 16 * 128, C::HALF);
+            tc::mma_f16_ts(o, p + 8 * kk, bd, id_o, v > 0 || kk > 0 ? 1u : 0u);
+            tc::mma_f16_ts(o, p + CX_KT / 2 + 8 * kk, bd, id_o, 1u);
+          }
+          if (v + 1 < nv) {
+            if (t == 0) {
+              ok = mbar_wait_bounded(bar + CB_KFULL + (st ^ 1), ((v + 1) >> 1) & 1, CX_NAP);
+              if (!ok) break;
+              tc::fence_after();
+            }
+            logits(t, st ^ 1);
+          }
+        }
+        if (!ok) break;
+        tc::commit(bar + CB_VEMPTY + st);
+        if (v + 1 < nv) tc::commit(bar + CB_KEMPTY + (st ^ 1));
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(P.dev_error, DEVERR_TIMEOUT);
+      }
+      tc::commit(bar + CB_ODONE);
+      tc::commit(bar + CB_DRAIN);  // every MMA issued by this thread has completed
+      (void)mbar_wait_bounded(bar + CB_DRAIN, 0);
+    }
+    __syncwarp();
+  } else if (warp / 4 < tiles) {
+    // ======================= softmax =======================
+    const int t = warp / 4, r = tid & (CX_ROWS - 1);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lanes + t * CX_KT, o_tm = tmem + lanes + C::TM_O + t * D;
+    const float sl = fmaxf(fabsf(P.softmax_scale) * 1.4426950408889634f, 1e-30f);
+    float m = -CUDART_INF_F, l = 0.0f;
+    bool ok = true;
+#pragma unroll 1
+    for (int v = 0; v < nv; ++v) {
+      // every decision around a .sync.aligned TMEM access is warp-uniform
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + CB_SFULL + t, v & 1, CX_NAP))) {
+        ok = false;
+        break;
+      }
+      tc::fence_after();
+      uint32_t y[CX_KT];
+#pragma unroll
+      for (int c = 0; c < CX_KT; c += 32) ld32(s_tm + c, y + c);
+      const int left = L - (v0 + v) * CX_KT;  // keys of the sequence from this tile on
+      const int chunks = mask[v & 3];
+      if (t == 0 && left < CX_KT && r >= left) {  // a value row past the end, before the P.V that would read it
+        ok = mbar_wait_bounded(bar + CB_VFULL + (v & 1), (v >> 1) & 1, CX_NAP);
+        uint8_t* row = sm + C::OFF_V + (v & 1) * C::TILE + r * 128;
+        if (ok) {
+#pragma unroll
+          for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(row + hh * C::HALF + 16 * c) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_proxy_async();
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc::wait_ld();
+      tc::regs_after_wait(y);
+      if (left < CX_KT || chunks != 0xFF) {  // (uniform over the CTA)
+#pragma unroll
+        for (int j = 0; j < CX_KT; ++j)
+          if (j >= left || !((chunks >> (j / CX_CHUNK)) & 1)) y[j] = __float_as_uint(-CUDART_INF_F);
+      }
+      float top = -CUDART_INF_F;
+#pragma unroll
+      for (int j = 0; j < CX_KT; ++j) top = fmaxf(top, __uint_as_float(y[j]));
+      const float tmax = sl * top;
+      const bool grow = tmax > m + CX_SLACK;
+      const bool resc = grow && m != -CUDART_INF_F;
+      if (__any_sync(0xffffffffu, resc)) {  // (P.V(v - 1) is done: S(v), committed after it, is)
+        const float f = resc ? ex2(m - tmax) : 1.0f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          tc::ld16(o_tm + c, o);
+          tc::wait_ld();
+          tc::regs_after_wait(o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tc::st16(o_tm + c, o);
+        }
+        l *= f;
+      }
+      m = grow ? tmax : m;
+      const float ref = m == -CUDART_INF_F ? 0.0f : m;
+      float sum = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CX_KT; c += 32) {  // 32 keys: 16 columns of high terms and 16 of low ones
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float p0 = ex2(fmaf(__uint_as_float(y[c + 2 * j]), sl, -ref));
+          const float p1 = ex2(fmaf(__uint_as_float(y[c + 2 * j + 1]), sl, -ref));
+          sum += p0 + p1;
+          hi[j] = pack_bf16x2(p0, p1);
+          lo[j] = pack_bf16x2(p0 - __uint_as_float(hi[j] << 16), p1 - __uint_as_float(hi[j] & 0xFFFF0000u));
+        }
+        tc::st16(s_tm + c / 2, hi);
+        tc::st16(s_tm + CX_KT / 2 + c / 2, lo);
+      }
+      l += sum;
+      tc::wait_st();
+      tc::fence_before();
+      tc::mbar_arrive(bar + CB_PFULL + t);
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+        ok = false;
+        break;
+      }
+    }
+    // ---- the rows out: divided by the sum, or as this part's record
+    if (ok && nv > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + CB_ODONE, 0, CX_NAP))) ok = false;
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
+    } else {
+      tc::fence_after();
+      const int qi = q0 + t * QB + r / G;
+      const bool real = r / G < QB && qi < n;
+      float* to;
+      float w;
+      if (P.splits > 1) {
+        const long long tile = ((long long)b * Hkv + h) * (gridDim.x / P.splits * C::TILES) + block * C::TILES + t;
+        float* rec = P.part + (tile * P.splits + sp) * split_record_floats(D);
+        reinterpret_cast<float2*>(rec + CX_ROWS * D)[r] = make_float2(m, l);
+        to = rec + r * D;
+        w = 1.0f;
+      } else {
+        to = P.out + ((size_t)(cq0 + qi) * P.num_q_heads + h * G + r % G) * D;
+        w = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // (a NaN stays one)
+      }
+      const bool store = real && KVQ_IN_BOUNDS(cq0 + qi < P.total_q, P.dev_error);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        if (nv > 0) {
+          tc::ld16(o_tm + c, o);
+          tc::wait_ld();
+          tc::regs_after_wait(o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = 0;
+        }
+        if (store) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4*>(to + c + j) =
+                make_float4(__uint_as_float(o[j]) * w, __uint_as_float(o[j + 1]) * w, __uint_as_float(o[j + 2]) * w,
+                            __uint_as_float(o[j + 3]) * w);
+        }
+      }
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == CX_MMA_WARP) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of one (query, q head) row: log-sum-exp weights, then the
+// inverse RHT (or the INT8 V channel scales) and 1 / l; one warp per row, lane
+// l dims l * EPL .. + EPL - 1.
+template <int D>
+__global__ void __launch_bounds__(256) split_merge_kernel(const AttnParams P, int qtiles) {
+  constexpr int EPL = D / 32;
+  const int lane = threadIdx.x & 31, G = P.group, Hkv = P.num_kv_heads, QB = PREFILL_ROWS / G;
+  const long long wid = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int row = (int)(wid % PREFILL_ROWS);
+  const long long tile = wid / PREFILL_ROWS;  // (b * Hkv + h) * qtiles + qtile
+  if (tile >= (long long)P.batch * Hkv * qtiles) return;
+  const int qtile = (int)(tile % qtiles), h = (int)(tile / qtiles % Hkv), b = (int)(tile / qtiles / Hkv);
+  grid_dependency_wait();  // every record is written
+  const int cq0 = load_input<false>(P.cu_q + b);
+  const int n = min(load_input<false>(P.cu_q + b + 1) - cq0, P.max_q_per_seq);
+  const int qi = qtile * QB + row / G;
+  if (row / G >= QB || qi >= n || cq0 < 0 || cq0 + qi >= P.total_q) return;
+  if (cross_keys(P, b, false) < 0) return;  // (a skipped sequence has no records)
+  float m = -CUDART_INF_F, l = 0.0f, o[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) o[e] = 0.0f;
+  const float* rec0 = P.part + tile * P.splits * split_record_floats(D);
+  constexpr int U = 4;  // records whose loads are in flight together
+  for (int s0 = 0; s0 < P.splits; s0 += U) {
+    float2 ml[U];
+    float v[U][EPL];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float* rec = rec0 + min(s0 + u, P.splits - 1) * split_record_floats(D);
+      ml[u] = __ldcg(reinterpret_cast<const float2*>(rec + PREFILL_ROWS * D) + row);
+      if constexpr (EPL == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + row * D) + lane);
+        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(rec + row * D) + lane);
+        v[u][0] = x.x; v[u][1] = x.y;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (s0 + u >= P.splits || ml[u].y == 0.0f) continue;  // no visible key in this part
+      const float mn = fmaxf(m, ml[u].x);
+      const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - mn), w = ex2(ml[u].x - mn);
+      m = mn;
+      l = l * f + ml[u].y * w;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = o[e] * f + v[u][e] * w;
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // (a NaN stays one)
+  if (P.mode == MODE_INT8) {
+    const float* am = P.ch_amax + ((size_t)Hkv + h) * D + lane * EPL;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] *= __fdiv_rn(am[e], 127.0f) * inv;
+  } else if (P.signs) {
+    wht_warp<EPL>(o, lane);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] = (__ldg(P.signs + lane * EPL + e) < 0 ? -o[e] : o[e]) * (inv / (float)D);
+  } else {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] *= inv;
+  }
+  float* out = P.out + ((size_t)(cq0 + qi) * P.num_q_heads + h * G + row % G) * D + lane * EPL;
+  if constexpr (EPL == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0], o[1], o[2], o[3]);
+  else *reinterpret_cast<float2*>(out) = make_float2(o[0], o[1]);
+}
+
+cudaError_t launch_split_merge(const AttnParams& P, int qtiles, cudaStream_t stream) {
+  const long long warps = (long long)P.batch * P.num_kv_heads * qtiles * PREFILL_ROWS;
+  const unsigned blocks = (unsigned)((warps + 7) / 8);
+  if (P.head_dim == 128) split_merge_kernel<128><<<blocks, 256, 0, stream>>>(P, qtiles);
+  else split_merge_kernel<64><<<blocks, 256, 0, stream>>>(P, qtiles);
+  return cudaGetLastError();
+}
+
+template <int D, int TERMS>
+static cudaError_t launch_cross16_t(const AttnParams& P, cudaStream_t stream) {
+  using C = CxCfg<D, TERMS>;
+  static bool attr_set[64] = {false};  // once per device, not inside later calls, which may be captured
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(cross16_kernel<D, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const int blocks = (int)cross16_blocks(P.max_q_per_seq, P.group, TERMS > 1);
+  const dim3 grid((unsigned)blocks * P.splits, P.num_kv_heads, P.batch);
+  cross16_kernel<D, TERMS><<<grid, CX_THREADS, C::SMEM, stream>>>(P);
+  if ((e = cudaGetLastError()) != cudaSuccess || P.splits == 1) return e;
+  return launch_split_merge(P, blocks * C::TILES, stream);
+}
+
+cudaError_t launch_cross16(const AttnParams& P, cudaStream_t stream) {
+  const bool f32 = P.dtype == DT_F32;
+  if (P.head_dim == 128) return f32 ? launch_cross16_t<128, 3>(P, stream) : launch_cross16_t<128, 1>(P, stream);
+  return f32 ? launch_cross16_t<64, 3>(P, stream) : launch_cross16_t<64, 1>(P, stream);
+}
+
+}  // namespace kvq

@@ -188,6 +188,20 @@ __host__ __device__ constexpr float kfold_int2(int d) {
   return (d & 7) == 4 || (d & 7) == 7 ? 6.0f : ((d & 7) == 1 || (d & 7) == 3 || (d & 7) == 6) ? 18.0f : 66.0f;
 }
 
+// The same with smaller constants, 16 and 4 (EXACT): the sum of a key's products
+// and their constants is rounded at the size of the constants, so these cost an
+// eighth of the error of 64's, for two more shifts per word.
+template <int P>
+__device__ __forceinline__ uint32_t kpair_int2_fold_exact(uint32_t w) {
+  constexpr int pos = (P == 0 || P == 3 || P == 5) ? 6 : 8;
+  constexpr uint32_t magic = pos == 6 ? 0x4C004C00u : 0x44004400u;  // 16, 4
+  const uint32_t src = P <= 1 ? (w << 6) : P == 2 ? (w << 4) : P <= 4 ? w : P <= 6 ? (w >> 4) : (w >> 6);
+  return lop3_and_or(src, 0x00030003u << pos, magic);
+}
+__host__ __device__ constexpr float kfold_int2_exact(int d) {
+  return ((d & 7) == 0 || (d & 7) == 3 || (d & 7) == 5) ? 18.0f : 6.0f;
+}
+
 template <int MODE>
 __device__ __forceinline__ void kpair_dims(int w, int P, int& d0, int& d1) {
   if (MODE == MODE_INT4) { d0 = 8 * w + P; d1 = d0 + 4; }
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
   constexpr int EPL = D / 32;
   constexpr int NH = 4 * NT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int Hkv = P.num_kv_heads, G = P.group, Hq = P.num_q_heads;
+  const int Hkv = P.num_kv_heads, G = P.group;
   __shared__ __half qh[2][NH][D];
   // This kernel may start while the kernel before it still runs (programmatic
   // launch: the library's own write lets it, and so may a caller's kernel).
@@ -397,9 +411,9 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
   if constexpr (ROPE) turn = rope_lane<EPL, false>(P.rope, query_position(P, b), lane);
   for (int i = warp; i < NH; i += 4) {
     float x[EPL];
-    if (i < G) {
-      const int hq = h * G + i;
-      load_row_elems<EPL, false>(P.q, P.dtype, ((size_t)b * Hq + hq) * D + lane * EPL, x);
+    const long long row = i < G ? slot_row(P, b, h, i, h == 0 && i == 0 && lane == 0) : -1;
+    if (row >= 0) {
+      load_row_elems<EPL, false>(P.q, P.dtype, (size_t)row * D + lane * EPL, x);
       if constexpr (ROPE) rope_row(turn, x);
       if constexpr (MODE == MODE_INT8) {
         const float* am = P.ch_amax + (size_t)h * D + lane * EPL;  // K channel scales
@@ -437,7 +451,9 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
       const __half lo = __float2half_rn(v - __half2float(hi));
       qh[0][i][lane * EPL + e] = hi;
       qh[1][i][lane * EPL + e] = lo;
-      const float kc = MODE == MODE_INT4 ? KFOLD_INT4 : MODE == MODE_INT2 ? kfold_int2(lane * EPL + e) : 0.0f;
+      const float kc = MODE == MODE_INT4   ? KFOLD_INT4
+                       : MODE == MODE_INT2 ? (P.exact ? kfold_int2_exact(lane * EPL + e) : kfold_int2(lane * EPL + e))
+                                           : 0.0f;
       opsum = fmaf(kc, __half2float(hi) + __half2float(lo), opsum);
     }
     opsum = warp_sum(opsum);
@@ -1024,7 +1040,20 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 //    layout through shared memory (the consumed K tile), two 16-byte stores
 //    and four 8-byte loads per lane, bank-conflict free.
 
-template <int MODE, int D, int NT, bool STEGO>
+//
+// EXACT (the calls with rope and cross attention, over 2-bit and 8-bit rows): the
+// same with what made the fp32 outputs lose bits put right, which moves the
+// results by less than 4e-5 of them, so that the calls that had the other form
+// keep it.
+//  * P.V of 16 keys goes to fresh sums that are then added in fp32: the
+//    accumulators truncate, and over a slice of some fifty tiles that was 3e-5
+//    of an output where the values' mean is not zero (2-bit rows, 16384 keys).
+//  * 8-bit rows: the weights p s are multiplied by a power of two that takes the
+//    largest s so far to 2^11, since s of unit-sized rows is below 2^-5 and
+//    p s fell among the fp16 subnormals (2e-5 to 4e-5 of an output).
+//  * 2-bit keys: the fold's smaller constants (1e-5 of an output).
+
+template <int MODE, int D, int NT, bool STEGO, bool EXACT>
 __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE, D, NT>::CTAS))
     decode_tma_kernel(const __grid_constant__ AttnParams P, DecodeWs ws) {
   using C = DecCfg<MODE, D>;
@@ -1186,9 +1215,12 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
   float bet[NT], gam[NT], kap[NT];
   float oacc[NT][C::MT][4];
   float mrun[NT], lrun[NT], pmrun[NT];
+  constexpr bool SCALED = EXACT && TC::BYTES;
+  float vmul = 1.0f;  // SCALED: the value scales' factor, a power of two
   int part_id = 0;
 
   auto begin_seg = [&]() {
+    if constexpr (SCALED) vmul = 0x1p120f;  // above any scale's: the first one sets it
     part_id = gw + cs.bh;  // partial record id: slice index + pair index (unique, see reduce)
     const int qbh = KVQ_IN_BOUNDS(cs.bh >= 0 && cs.bh < BH, P.dev_error) ? cs.bh : 0;
     const uint4* src = reinterpret_cast<const uint4*>(ws.qfrag + ((size_t)qbh * 32 + lane) * PER_LANE);
@@ -1233,8 +1265,13 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
         float* po = ws.part_o + ((size_t)part_id * G + head) * D;
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt) {
-          po[gq * (D / 16) + mt] = oacc[nt][mt][0] + oacc[nt][mt][1] + pm;
-          po[(8 + gq) * (D / 16) + mt] = oacc[nt][mt][2] + oacc[nt][mt][3] + pm;
+          if constexpr (SCALED) {  // (no zero points: pm is 0)
+            po[gq * (D / 16) + mt] = (oacc[nt][mt][0] + oacc[nt][mt][1]) * (1.0f / vmul);
+            po[(8 + gq) * (D / 16) + mt] = (oacc[nt][mt][2] + oacc[nt][mt][3]) * (1.0f / vmul);
+          } else {
+            po[gq * (D / 16) + mt] = oacc[nt][mt][0] + oacc[nt][mt][1] + pm;
+            po[(8 + gq) * (D / 16) + mt] = oacc[nt][mt][2] + oacc[nt][mt][3] + pm;
+          }
         }
         if (gq == 0) ws.part_ml[(size_t)part_id * G + head] = make_float2(mrun[nt], l);
       }
@@ -1285,6 +1322,11 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
               av[1] = kpair_int4_fold<2 * sig>(kw[h2][m][1]);
               av[2] = kpair_int4_fold<2 * sig + 1>(kw[h2][m][0]);
               av[3] = kpair_int4_fold<2 * sig + 1>(kw[h2][m][1]);
+            } else if constexpr (MODE == MODE_INT2 && EXACT) {
+              av[0] = kpair_int2_fold_exact<2 * sig>(kw[h2][m][0]);
+              av[1] = kpair_int2_fold_exact<2 * sig>(kw[h2][m][1]);
+              av[2] = kpair_int2_fold_exact<2 * sig + 1>(kw[h2][m][0]);
+              av[3] = kpair_int2_fold_exact<2 * sig + 1>(kw[h2][m][1]);
             } else if constexpr (MODE == MODE_INT2) {
               av[0] = kpair_int2_fold<2 * sig>(kw[h2][m][0]);
               av[1] = kpair_int2_fold<2 * sig>(kw[h2][m][1]);
@@ -1358,6 +1400,35 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
             lg[h2][m][hh][nt] = FULL ? zz : (ok ? zz : -CUDART_INF_F);
           }
         }
+
+    if constexpr (SCALED) {
+      float most = 0.0f;  // (a masked row's scale may be any bits)
+#pragma unroll
+      for (int h2 = 0; h2 < NH2; ++h2)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) most = fmaxf(most, FULL || vk[h2][m][hh] ? sv_[h2][m][hh] : 0.0f);
+      if (__any_sync(0xffffffffu, most * vmul > 4096.0f)) {
+        most = warp_max(most);
+        const int ex = (int)(__float_as_uint(most) >> 23) - 127;  // (most >= 2^-108)
+        const float to = __uint_as_float((uint32_t)(127 + max(11 - ex, -116)) << 23);
+        const float f = to / vmul;
+        vmul = to;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) oacc[nt][mt][r] *= f;
+      }
+#pragma unroll
+      for (int h2 = 0; h2 < NH2; ++h2)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) sv_[h2][m][hh] *= vmul;
+    }
 
     uint32_t xh[NH2][NT][2], xl[NH2][NT][2];  // packed (P s) hi / lo per (h2, m): (key hh=0, key hh=1)
 #pragma unroll
@@ -1481,7 +1552,16 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
           const uint32_t av[4] = {vpair<MODE, mt>(vl[0][0], vl[0][1]), vpair<MODE, mt>(vh[0][0], vh[0][1]),
                                   vpair<MODE, mt>(vl[1][0], vl[1][1]), vpair<MODE, mt>(vh[1][0], vh[1][1])};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(oacc[nt][mt], av, bw[h2][mp][nt][0], bw[h2][mp][nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (EXACT) {
+              float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma_16816(o, av, bw[h2][mp][nt][0], bw[h2][mp][nt][1]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) oacc[nt][mt][r] += o[r];
+            } else {
+              mma_16816(oacc[nt][mt], av, bw[h2][mp][nt][0], bw[h2][mp][nt][1]);
+            }
+          }
         });
       }
   };
@@ -1542,17 +1622,17 @@ __global__ void __launch_bounds__(256) decode_reduce_kernel(AttnParams P, Decode
   constexpr int EPL = D / 32;
   const int lane = threadIdx.x & 31;
   const long long wid = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int Hq = P.num_q_heads, G = P.group, Hkv = P.num_kv_heads;
-  if (wid >= (long long)P.batch * Hq) return;
-  const int b = (int)(wid / Hq), hq = (int)(wid % Hq);
-  const int h = hq / G, i = hq % G;
-  const int bh = b * Hkv + h;
-  const int BH = P.batch * Hkv;
-  float* out = P.out + (size_t)wid * D;
+  const int G = P.group, Hkv = P.num_kv_heads, BH = P.batch * Hkv;
+  if (wid >= (long long)BH * G) return;
+  const int bh = (int)(wid / G), i = (int)(wid % G);
+  const int b = bh / Hkv, h = bh % Hkv;
   // the output transform's constants do not depend on the kernels before
   float tsign[EPL];
   output_signs<D>(P, h, lane, tsign);
   grid_dependency_wait();  // every partial of the stream kernel is written
+  const long long row = slot_row(P, b, h, i);
+  if (row < 0) return;
+  float* out = P.out + (size_t)row * D;
   const int T = ws.tile_start[BH];
   const int start = ws.tile_start[bh], end = ws.tile_start[bh + 1];
   if (start >= end || !KVQ_IN_BOUNDS(start >= 0 && end <= T, P.dev_error)) {
@@ -1595,7 +1675,7 @@ DecodeShape decode_shape(int mode, int head_dim, int group) {
   return group > 4 ? decode_shape_dnt<128, 2>(mode) : decode_shape_dnt<128, 1>(mode);
 }
 
-template <int MODE, int D, int NT, bool STEGO>
+template <int MODE, int D, int NT, bool STEGO, bool EXACT = false>
 cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
   constexpr bool TMA = MODE != MODE_INT8;
   using TC = TmaCfg<MODE, D, NT>;
@@ -1609,7 +1689,7 @@ cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, c
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     if constexpr (TMA)
-      e = cudaFuncSetAttribute(decode_tma_kernel<MODE, D, NT, STEGO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(decode_tma_kernel<MODE, D, NT, STEGO, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)smem);
     else
       e = cudaFuncSetAttribute(decode_stream_kernel<MODE, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1628,12 +1708,12 @@ cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, c
   // the stream and merge kernels launch programmatically: their CTAs become
   // resident while the previous kernel drains and wait on its completion
   if constexpr (TMA)
-    e = launch_dependent(decode_tma_kernel<MODE, D, NT, STEGO>, dim3(grid), dim3(TC::WARPS * 32), smem, stream, P,
+    e = launch_dependent(decode_tma_kernel<MODE, D, NT, STEGO, EXACT>, dim3(grid), dim3(TC::WARPS * 32), smem, stream, P,
                          ws);
   else
     e = launch_dependent(decode_stream_kernel<MODE, D, NT>, dim3(grid), dim3(128), smem, stream, P, ws);
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)P.batch * P.num_q_heads;
+  const long long warps = (long long)BH * P.group;
   return launch_dependent(decode_reduce_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P, ws);
 }
 
@@ -1644,6 +1724,11 @@ cudaError_t launch_decode_md(const AttnParams& P, const DecodeWs& ws, int grid, 
       if (P.group <= 4) return launch_decode_t<MODE, D, 1, true>(P, ws, grid, stream);
       return launch_decode_t<MODE, D, 2, true>(P, ws, grid, stream);
     }
+  }
+  if constexpr (MODE == MODE_INT2 || byte_token_head(MODE)) {
+    if (P.exact)
+      return P.group <= 4 ? launch_decode_t<MODE, D, 1, false, true>(P, ws, grid, stream)
+                          : launch_decode_t<MODE, D, 2, false, true>(P, ws, grid, stream);
   }
   if (P.group <= 4) return launch_decode_t<MODE, D, 1, false>(P, ws, grid, stream);
   return launch_decode_t<MODE, D, 2, false>(P, ws, grid, stream);

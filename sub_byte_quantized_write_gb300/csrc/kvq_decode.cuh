@@ -182,6 +182,18 @@ __device__ __forceinline__ void merge_records(const AttnParams& P, const DecodeW
   }
 }
 
+// Row of q and out of slot i (< P.group) of pair (b, h): the decode query's head
+// i of the pair, or with P.q_group > 0 query i / q_group of the sequence; -1
+// where it has no such query.  `flag`: report queries that are not served.
+__device__ __forceinline__ long long slot_row(const AttnParams& P, int b, int h, int i, bool flag = false) {
+  if (P.q_group == 0) return (long long)b * P.num_q_heads + h * P.group + i;
+  const int c0 = load_input<false>(P.cu_q + b), n = load_input<false>(P.cu_q + b + 1) - c0;
+  if (flag && (n > P.max_q_per_seq || (n > 0 && (c0 < 0 || c0 > P.total_q - n)))) flag_error(P.dev_error, DEVERR_SEQ_LEN);
+  const int qi = i / P.q_group;
+  if (qi >= n || c0 + qi < 0 || c0 + qi >= P.total_q) return -1;
+  return (long long)(c0 + qi) * P.num_q_heads + h * P.q_group + i % P.q_group;
+}
+
 template <typename Kern, typename... Args>
 cudaError_t launch_dependent(Kern kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};

@@ -269,14 +269,15 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
   float m[2], l[2];
   const float sl = P.softmax_scale * 1.4426950408889634f;
   auto begin_pair = [&](int bh) {
-    const size_t q0 = ((size_t)(bh / Hkv) * P.num_q_heads + (bh % Hkv) * G + g) * D + 8 * c;
+    const long long qrow = g < G ? slot_row(P, bh / Hkv, bh % Hkv, g) : -1;
+    const size_t q0 = (size_t)max(qrow, 0LL) * D + 8 * c;
 #pragma unroll
     for (int j = 0; j < JK; ++j) {
       if constexpr (Q32) {
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-        if (g < G) load_row_elems<8, false>(P.q, DT_F32, q0 + 32 * j, x);
+        if (qrow >= 0) load_row_elems<8, false>(P.q, DT_F32, q0 + 32 * j, x);
         uint32_t t[4][3];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split3(x[2 * i], x[2 * i + 1], t[i]);
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
         for (int k = 0; k < 3; ++k)
           *reinterpret_cast<uint4*>(qw + (k * JK + j) * 512) = make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
       } else {
-        qf[j] = g < G ? load_input<false>(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.q) + 2 * q0) + 4 * j)
+        qf[j] = qrow >= 0 ? load_input<false>(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(P.q) + 2 * q0) + 4 * j)
                       : make_uint4(0, 0, 0, 0);
       }
     }
@@ -456,8 +457,8 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
         o.w = fmaf(f, x.w, o.w);
       }
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // no visible key: zeros
-      const size_t row = (size_t)(blockIdx.x / Hkv) * P.num_q_heads + (blockIdx.x % Hkv) * G + head;
-      *reinterpret_cast<float4*>(P.out + row * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      const long long row = slot_row(P, blockIdx.x / Hkv, blockIdx.x % Hkv, head, blockIdx.x % Hkv == 0 && i == 0);
+      if (row >= 0) *reinterpret_cast<float4*>(P.out + row * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
   }
 }
@@ -491,11 +492,12 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
   const long long wid = (long long)(blockIdx.x / CUTS) * HEADS + warp / W;
   const int d0 = (blockIdx.x % CUTS) * 32 * EPL + EPL * lane;  // the lane's first dim
-  const int Hq = P.num_q_heads, G = P.group, Hkv = P.num_kv_heads;
-  if (wid >= (long long)P.batch * Hq) return;  // (whole CTAs, for W > 1)
-  const int b = (int)(wid / Hq), hq = (int)(wid % Hq), head = hq % G;
-  const int bh = b * Hkv + hq / G, BH = P.batch * Hkv;
+  const int G = P.group, Hkv = P.num_kv_heads, BH = P.batch * Hkv;
+  if (wid >= (long long)BH * G) return;  // (whole CTAs, for W > 1)
+  const int bh = (int)(wid / G), head = (int)(wid % G);
   grid_dependency_wait();  // every record is written
+  const long long row = slot_row(P, bh / Hkv, bh % Hkv, head, bh % Hkv == 0 && head == 0 && d0 == 0 && part == 0);
+  if (row < 0) return;  // (whole CTAs, for W > 1)
   const int T = __ldcg(ws.tile_start + BH);
   const int start = __ldcg(ws.tile_start + bh), end = __ldcg(ws.tile_start + bh + 1);
   float m = -CUDART_INF_F, l = 0.0f, o[EPL];
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) decode16_merge_kernel(co
       for (int e = 0; e < EPL; ++e) o[e] = fmaf(x, sm_o[w][EPL * lane + e], o[e]);
     }
   }
-  float* out = P.out + (size_t)wid * D + d0;
+  float* out = P.out + (size_t)row * D + d0;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   if constexpr (EPL == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
   else if constexpr (EPL == 2) *reinterpret_cast<float2*>(out) = make_float2(o[0] * inv, o[1] * inv);
@@ -608,7 +610,7 @@ cudaError_t launch_decode16_d(const AttnParams& P, const DecodeWs& ws, int grid,
   cudaError_t e = f32 ? launch_decode16_t<D, true, false>(P, ws, grid, stream)
                       : launch_decode16_t<D, false, false>(P, ws, grid, stream);
   if (e != cudaSuccess) return e;
-  const long long heads = (long long)P.batch * P.num_q_heads;
+  const long long heads = (long long)pairs * P.group;
   // a pair is cut into nwall / pairs records on average when the GPU is full
   const long long cuts = chunks < ws.nwall / pairs ? chunks : ws.nwall / pairs;
   if (cuts >= 8 * D16_WIDE_MERGE)

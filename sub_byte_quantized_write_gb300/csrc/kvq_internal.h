@@ -91,6 +91,14 @@ struct AttnParams {
   int new_dtype, num_new;
   const int32_t* cu_new;
   RopeArgs rope;          // the query and the new K rows are turned to their positions
+  // cross attention: the queries of cu_q (at most max_q_per_seq of a sequence)
+  // each see every key.  By the decode kernels: q_group > 0, and `group` counts
+  // the slots of a pair, query i's head g in slot i * q_group + g.  By the
+  // prefill kernel: cross = 1, and each query tile's keys are cut into `splits`
+  // parts, with `part` (splits > 1) their records, as split_record lays them out.
+  int q_group, cross, splits;
+  float* part;
+  int exact;  // decode kernels: the closer sums of decode_tma_kernel's EXACT form
   CUtensorMap kv_map[2];  // 128-byte aligned by its own declaration
 };
 
@@ -105,6 +113,8 @@ struct DecodeWs {
   int nwall;           // stream warps launched
   int fixed_workers;   // > 0: use exactly this many workers
 };
+
+constexpr int PREFILL_ROWS = 128;  // (query, q head) rows of a prefill CTA
 
 // Split-KV geometry shared by the host API and the kernels.
 constexpr int DECODE_KEYS_PER_TILE = 32;
@@ -203,6 +213,12 @@ cudaError_t launch_copy_pages(const PageCopy& C, int sms, cudaStream_t stream);
 cudaError_t launch_fork(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream);
 cudaError_t launch_compact(const PagePlan& P, PageCopy C, int sms, cudaStream_t stream);
 
+// Records of split query tiles: per tile and part the PREFILL_ROWS_PER_CTA rows'
+// unnormalised outputs [rows][D], then their (maximum in log2 units, sum) pairs.
+__host__ __device__ constexpr long long split_record_floats(int head_dim) {
+  return (long long)PREFILL_ROWS * (head_dim + 2);
+}
+
 DecodeShape decode_shape(int mode, int head_dim, int group);
 // Key rows per page chunk that the decode's tensor copies move (16 or 8), or 0
 // when the configuration reads its pages another way (INT8 per channel, bf16).
@@ -225,15 +241,28 @@ cudaError_t launch_decode(const AttnParams& P, const DecodeWs& ws, int grid, cud
 DecodeShape decode16_shape(int head_dim);
 cudaError_t launch_decode16(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream);
 cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream);
+// cross attention over bf16 rows (kvq_cross16.cu): dense (cu_kv, rows by
+// kv_map) or in pages (table; kv_map views the pools as rows); chunk_rows_total
+// counts the maps' rows.
+cudaError_t launch_cross16(const AttnParams& P, cudaStream_t stream);
+// joins the records of split query tiles, qtiles of each (sequence, kv head)
+cudaError_t launch_split_merge(const AttnParams& P, int qtiles, cudaStream_t stream);
 
 // The prefill grid: x = query tiles of the longest chunk (PREFILL_ROWS_PER_CTA
 // (query, q head) rows per CTA), y = kv heads, z = sequences.  Computed in 64
 // bits so that no max_q_per_seq can wrap it; the host checks it against the
 // launch limits before any launch.
-constexpr int PREFILL_ROWS_PER_CTA = 128;
+constexpr int PREFILL_ROWS_PER_CTA = PREFILL_ROWS;
 inline long long prefill_grid_x(int max_q_per_seq, int group) {
   const long long qb = PREFILL_ROWS_PER_CTA / group;
   return ((long long)max_q_per_seq + qb - 1) / qb;
+}
+
+// CTAs of the cross attention over bf16 rows per (sequence, kv head, part): two
+// row tiles each, one with fp32 queries.
+inline long long cross16_blocks(int max_q_per_seq, int group, bool f32) {
+  const long long tiles = prefill_grid_x(max_q_per_seq, group);
+  return f32 ? tiles : (tiles + 1) / 2;
 }
 
 }  // namespace kvq

@@ -40,6 +40,8 @@
 
 #include <math_constants.h>
 
+#include <climits>
+
 #include "kvq_internal.h"
 #include "kvq_tc.cuh"
 
@@ -84,7 +86,8 @@ struct TpCfg {
   static constexpr int OFF_SC = OFF_RAW + NRAW * 2 * RAW;              // [NKV][ks, kz, vs, vz][64] f32
   static constexpr int OFF_KVAL = OFF_SC + NKV * 4 * TP_KT * 4;        // [NKV][4] chunk validity of the expanded tiles
   static constexpr int OFF_RAWVAL = OFF_KVAL + 64;                     // [NRAW][4] chunk validity of the raw tiles
-  static constexpr int OFF_XMAX = OFF_RAWVAL + 64;                     // [2 key halves][128] f32 (epilogue)
+  static constexpr int OFF_VMUL = OFF_RAWVAL + 64;                     // [NKV][2 key halves] value scale factors
+  static constexpr int OFF_XMAX = OFF_VMUL + 32;                       // [2 key halves][128] f32 (epilogue)
   static constexpr int OFF_ROW = OFF_XMAX + 2 * 2 * TP_ROWS * 4;       // beta, gamma [128] f32, pos [128] int
   static constexpr int OFF_BAR = OFF_ROW + 3 * TP_ROWS * 4;            // mbarriers
   static constexpr int NBAR = 32;
@@ -257,16 +260,23 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   }
   __syncthreads();
   const int b = *seq_slot, h = blockIdx.y;
-  const int qtile = gridDim.x - 1 - blockIdx.x;  // later queries (more keys) first
+  // later queries (more keys) first; cross attention: part `sp` of the tile's keys
+  const int sp = P.cross ? blockIdx.x % P.splits : 0;
+  const int qtile = P.cross ? blockIdx.x / P.splits : gridDim.x - 1 - blockIdx.x;
   const int G = P.group, Hq = P.num_q_heads, Hkv = P.num_kv_heads, bs = P.block_size;
   const int QB = TP_ROWS / G;
 
   const int cq0 = __ldg(P.cu_q + b);
-  const int n = __ldg(P.cu_q + b + 1) - cq0;
+  int n = __ldg(P.cu_q + b + 1) - cq0;
   const int q0 = qtile * QB;
+  int L = __ldg(P.seq_lens + b);
+  if (P.cross) {  // any number of queries up to max_q_per_seq, and no keys for a length below 0
+    if ((n > P.max_q_per_seq || L < 0) && tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
+    n = min(n, P.max_q_per_seq);
+    L = max(L, 0);
+  }
   if (q0 >= n) return;
-  const int L = __ldg(P.seq_lens + b);
-  if (n > L || L < 0) {
+  if (!P.cross && (n > L || L < 0)) {
     if (tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
     return;
   }
@@ -285,11 +295,12 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   const int nq = cq0 < 0 ? 0 : min(min(QB, n - q0), P.total_q - cq0 - q0);
   if (nq < min(QB, n - q0) && tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
   if (nq <= 0) return;
-  const int p_min = L - n + q0, p_max = L - n + q0 + nq - 1;
+  const int p_min = L - n + q0, p_max = P.cross ? L - 1 : L - n + q0 + nq - 1;
 
   float* sc = reinterpret_cast<float*>(sm + C::OFF_SC);
   int* kval = reinterpret_cast<int*>(sm + C::OFF_KVAL);
   int* rawval = reinterpret_cast<int*>(sm + C::OFF_RAWVAL);
+  float* vmuls = reinterpret_cast<float*>(sm + C::OFF_VMUL);
   float* rbeta = reinterpret_cast<float*>(sm + C::OFF_ROW);
   float* rgamma = rbeta + TP_ROWS;
   int* rpos = reinterpret_cast<int*>(rgamma + TP_ROWS);
@@ -299,7 +310,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
 
   // ---- key tiles: [0, p_max] or, for a sliding-window head, the sink tiles
   // plus the tiles from the earliest window start of the CTA's rows
-  const int W = P.window ? __ldg(P.window + h) : 0;
+  const int W = P.window ? __ldg(P.window + h) : 0;  // (cross attention has none)
   const int n_total = min(p_max / TP_KT + 1, (Leff + TP_KT - 1) / TP_KT);
   int ns = 0, tw = 0;
   bool gap = false;
@@ -312,7 +323,12 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     }
   }
   // (max: of a length past the table, the windows may start behind the last tile)
-  const int n_virt = gap ? ns + max(n_total - tw, 0) : n_total;
+  int n_virt = gap ? ns + max(n_total - tw, 0) : n_total;
+  if (P.cross) {  // this part's tiles, as a gap before the first of them
+    gap = true;
+    tw = (int)((long long)sp * n_total / P.splits);
+    n_virt = (int)((long long)(sp + 1) * n_total / P.splits) - tw;
+  }
   auto tile_of = [&](int v) { return (gap && v >= ns) ? tw + (v - ns) : v; };
 
   // ---- set-up: barriers, TMEM, query rows
@@ -391,7 +407,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
         const float sabs = fabsf(P.softmax_scale);
         rbeta[r] = fmaxf(sabs * log2e / (dnorm * scl), 1e-30f);
         rgamma[r] = sabs * log2e * sum / dnorm;
-        rpos[r] = rv ? (L - n + q0 + ql) : -1;
+        rpos[r] = rv ? (P.cross ? INT_MAX : L - n + q0 + ql) : -1;
       }
     }
   }
@@ -553,6 +569,11 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     const int pwarp = warp - TP_PROD_WARP0;
     int kvs = 0, kv_phase = 0;  // K/V stage of tile v and its wrap count parity
     int rs = 0, rphase = 0;     // raw stage of tile v
+    // Cross attention: value scales are multiplied by a power of two that takes
+    // the largest so far (of this half of the keys) to 2^10, so that p s (p up
+    // to 2^TP_SLACK) neither overflows fp16 nor falls among its subnormals,
+    // where 8-bit rows of unit size lost 1e-5 to 2e-5 of an output.
+    float vmul = P.cross ? 0x1p100f : 1.0f;
 #pragma unroll 1
     for (int v = 0; v < n_virt; ++v) {
       // raw tile v has landed; the tensor cores are done with this K/V stage
@@ -632,6 +653,13 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
               const uint32_t pad = lds32((isv ? rvp : rk) + key * C::R + C::DATA);
               pad_scale_zero<MODE>(pad, P.stego != 0, s, z);  // z: the value of the signed code 0
             }
+          }
+          if (P.cross && isv) {  // (idx is pt: a whole warp has 32 keys of V)
+            const float most = warp_max(s);
+            if (most * vmul > 2048.0f)
+              vmul = __uint_as_float((uint32_t)(127 + max(10 - ((int)(__float_as_uint(most) >> 23) - 127), -100)) << 23);
+            s *= vmul;
+            if (lane == 0) vmuls[kvs * 2 + (key >> 5)] = vmul;
           }
           float* scs = sc + kvs * 4 * TP_KT;
           scs[(isv ? 2 : 0) * TP_KT + key] = s;
@@ -732,6 +760,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     const uint32_t tmem_oh = hf ? tmem_o1 : tmem_o;  // this half's O
     float* xmax = reinterpret_cast<float*>(sm + C::OFF_XMAX);
     float mrow = -CUDART_INF_F, lrow = 0.0f, pzrow = 0.0f;  // lrow, pzrow: this half's keys
+    float vmul = 1.0f;  // cross attention: the factor of this half's O (of tile v's value scales)
     bool ok = true;
     int kvs = 0;
 #pragma unroll 1
@@ -802,9 +831,15 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
         break;
       }
       const bool resc = v >= 1 && grow && mrow != -CUDART_INF_F;
-      if (__any_sync(0xffffffffu, resc)) {  // this half's O; rows keeping their reference scale by 1
+      float turn = 1.0f;  // cross attention: what the value scales' factor changes by
+      if (MODE != MODE_INT8 && P.cross) {
+        const float to = vmuls[kvs * 2 + hf];
+        if (v >= 1) turn = to / vmul;
+        vmul = to;
+      }
+      if (__any_sync(0xffffffffu, resc || turn != 1.0f)) {  // this half's O; rows keeping their reference scale by 1
         tc::fence_after();
-        const float f = resc ? ex2(mrow - muse) : 1.0f;
+        const float f = resc ? ex2(mrow - muse) : 1.0f, fo = f * turn;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t ra[16], rb2[16];
@@ -815,8 +850,8 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
           tc::regs_after_wait(rb2);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            ra[j] = __float_as_uint(__uint_as_float(ra[j]) * f);
-            rb2[j] = __float_as_uint(__uint_as_float(rb2[j]) * f);
+            ra[j] = __float_as_uint(__uint_as_float(ra[j]) * fo);
+            rb2[j] = __float_as_uint(__uint_as_float(rb2[j]) * fo);
           }
           tc::st16(tmem_oh + lane_base + c0, ra);
           tc::st16(tmem_oh + lane_base + c0 + 16, rb2);
@@ -890,6 +925,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     good = __all_sync(0xffffffffu, ok && good && xsum[(2 + (hf ^ 1)) * TP_ROWS + r] != 0.0f);
     const float mrr = fmaxf(mrow, xmax[(hf ^ 1) * TP_ROWS + r]);
     const float fw = mrow == -CUDART_INF_F ? 0.0f : ex2(mrow - mrr);  // 0 for a half without visible keys
+    const float fwo = fw / vmul;
 #pragma unroll 1
     for (int ph = 0; ph < 2; ++ph) {
       if (good && hf == ph) {  // every P.V is done: the K / V^T stages are free for staging
@@ -910,8 +946,8 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
               const uint32_t* w = j < 4 ? ra + 4 * j : rb2 + 4 * (j - 4);
               float4& dst = stage[r * P4 + ((c0 / 4 + j) ^ (r & 7))];
               const float4 prev = ph ? dst : make_float4(0.f, 0.f, 0.f, 0.f);
-              dst = make_float4(fmaf(fw, __uint_as_float(w[0]), prev.x), fmaf(fw, __uint_as_float(w[1]), prev.y),
-                                fmaf(fw, __uint_as_float(w[2]), prev.z), fmaf(fw, __uint_as_float(w[3]), prev.w));
+              dst = make_float4(fmaf(fwo, __uint_as_float(w[0]), prev.x), fmaf(fwo, __uint_as_float(w[1]), prev.y),
+                                fmaf(fwo, __uint_as_float(w[2]), prev.z), fmaf(fwo, __uint_as_float(w[3]), prev.w));
             }
           }
         } else if (ph == 0) {
@@ -924,6 +960,20 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     if (!good) {
       *abort_flag = 1;
       if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
+    } else if (P.cross && P.splits > 1) {  // this part's record
+      constexpr int EPL = D / 32;
+      float* rec = P.part + ((((long long)b * Hkv + h) * (gridDim.x / P.splits) + qtile) * P.splits + sp) *
+                                split_record_floats(D);
+      float2* ml = reinterpret_cast<float2*>(rec + TP_ROWS * D);
+      if (hf == 0) ml[r] = make_float2(mrr, xsum[r]);
+      for (int k = 16 * hf; k < 16 * hf + 16; ++k) {
+        const int row = quad * 32 + k;
+        const float pz = xsum[TP_ROWS + row];
+        const float* src = reinterpret_cast<const float*>(stage + row * P4 + ((lane * EPL / 4) ^ (row & 7))) +
+                           (lane * EPL) % 4;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) rec[row * D + lane * EPL + e] = src[e] + pz;
+      }
     } else {
       constexpr int EPL = D / 32;  // lane holds dims lane * EPL .. + EPL - 1
       for (int k = 16 * hf; k < 16 * hf + 16; ++k) {
@@ -987,9 +1037,11 @@ cudaError_t launch_prefill_tc_t(const AttnParams& P, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  dim3 grid((unsigned)prefill_grid_x(P.max_q_per_seq, P.group), P.num_kv_heads, P.batch);  // TP_THREADS threads each
+  const int qtiles = (int)prefill_grid_x(P.max_q_per_seq, P.group);
+  dim3 grid((unsigned)qtiles * (P.cross ? P.splits : 1), P.num_kv_heads, P.batch);  // TP_THREADS threads each
   prefill_tc_kernel<MODE, D><<<grid, TP_THREADS, C::SMEM, stream>>>(P);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || !P.cross || P.splits == 1) return e;
+  return launch_split_merge(P, qtiles, stream);
 }
 
 cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream) {
