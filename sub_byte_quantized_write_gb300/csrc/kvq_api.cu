@@ -734,12 +734,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // one head, 64 lines of 128 bytes whose 16-byte pieces land XOR-swizzled by
 // the line index (128-byte swizzle), so that the expansion's reads of one
 // column across eight rows fall in eight different banks.
-bool dense_rows_map(CUtensorMap* map, const void* base, int64_t rows, int Hkv, int D, int box_rows = 64) {
+bool dense_rows_map(CUtensorMap* map, const void* base, int64_t rows, int Hkv, int D, int box_rows = 64,
+                    int box_heads = 1) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc || D % 64 != 0) return false;
   const cuuint64_t dims[4] = {64, (cuuint64_t)D / 64, (cuuint64_t)Hkv, (cuuint64_t)rows};
   const cuuint64_t strides[3] = {128, (cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2};
-  const cuuint32_t box[4] = {64, 1, 1, (cuuint32_t)box_rows};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -897,12 +898,17 @@ kvq_status check_cross_heads(int32_t num_kv_heads, int32_t num_q_heads, int32_t 
   return KVQ_OK;
 }
 
-// The bf16 rows of a call: the dense ones, or the pools' (box rows of one chunk).
+// The bf16 rows of a call: the dense ones, or the pools' (box rows of one chunk),
+// and its queries, where they are bf16 and the scale's sign need not be turned
+// into them.
 kvq_status cross16_maps(kvq::AttnParams& P, const void* k, const void* v, int64_t rows, int heads, int box_rows) {
   P.chunk_rows_total = (int)rows;
   if (!dense_rows_map(&P.kv_map[0], k, rows, heads, P.head_dim, box_rows) ||
       !dense_rows_map(&P.kv_map[1], v, rows, heads, P.head_dim, box_rows))
     return fail(KVQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the K / V rows");
+  P.q_tma = P.dtype == KVQ_BF16 && P.softmax_scale >= 0.0f && P.total_q <= INT_MAX - 256;
+  if (P.q_tma && !dense_rows_map(&P.q_map, P.q, P.total_q, P.num_q_heads, P.head_dim, kvq::PREFILL_ROWS / P.group, P.group))
+    return fail(KVQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the queries");
   return KVQ_OK;
 }
 

@@ -5,25 +5,36 @@
 // with p_j = exp(scale q_i . k_j) over all seq_lens[b] rows of the sequence,
 // whatever the number of queries.  4 D flops per (query, q head, key).
 //
-// Design: one CTA of 10 warps per (up to 256 rows, kv head, sequence, part of
+// Design: one CTA of 12 warps per (up to 256 rows, kv head, sequence, part of
 // the keys); a row is a (query, q head of the GQA group) pair, 128 rows make a
 // tile, and the CTA's two tiles share every K and V tile of 128 keys.
-//   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread per row: the row's
-//                   128 logits from TMEM, its maximum, the weights, and those
-//                   back to TMEM over the logits.  While one tile is in its
-//                   softmax the tensor cores work on the other.
-//   warp 8          TMEM; lane 0 issues S = Q K^T (M = 128 rows, N = 128 keys)
-//                   and O += P V (N = D).
-//   warp 9          tensor copies: K and V rows land as they are, 128-byte
-//                   swizzled, ready to be operands: K as K-major, V as MN-major,
-//                   so nothing is converted or transposed.
+//   warp 0          TMEM, and every tcgen05.mma: S = Q K^T (M = 128 rows, N = 128
+//                   keys) and O += P V (N = D), the first half of the keys when
+//                   its weights are there.  The oldest warp, since an SM's issue
+//                   slots go to the oldest: as the youngest it was late by 300
+//                   cycles at every step.
+//   warps 1 and 2   tensor copies of K and of V (one warp for both held the next K
+//                   back until a V stage was free): the rows land as they are,
+//                   128-byte swizzled, ready to be operands: K as K-major, V as
+//                   MN-major, so nothing is converted or transposed.
+//   warps 4-7, 8-11 softmax of row tile 0 and 1, one thread per row: the row's
+//                   128 logits from TMEM in one trip (a trip costs some 250
+//                   cycles and 4 per column), their maximum, the weights, and
+//                   those back to TMEM over the logits.  While one tile is in
+//                   its softmax the tensor cores work on the other.  (Two threads
+//                   per row, who must agree on the maximum: 8% slower.)
+// A CTA with one row tile (few queries, fp32 ones) takes the other's logits' place
+// for its next key tile: S(v + 1) is there when the softmax of v ends.
 // bf16 x bf16 products are exact in the fp32 sums.  An fp32 query is three bf16
 // terms (24 bits), three products into one sum, and one row tile per CTA.  The
 // weights are two bf16 terms (17 bits: 2^-18 of a weight at most, 2e-6 of an
 // output; one term alone would be 1e-3), so P.V takes twice its operations and
 // the whole call 1.5 times 4 D per pair, which bounds it: two thirds of the
 // tensor cores' rate.  The running maximum is a reference that moves, and O is
-// rescaled, only when a logit passes it by 2^8.
+// rescaled, only when a logit passes it by 2^8.  The accumulators truncate, some
+// 2^-25 of O per step of 16 keys and term (1.3e-5 of an output over 8192 keys):
+// every CX_FLUSH tiles O is added in fp32 to the row where it will end up, and
+// begins anew.
 // Rows that are not there (an evicted page, past the sequence's end): chunks of
 // a page without an entry are copied from past the tensor's end, which gives
 // zeros, and masked; value rows past the end of the sequence, which may hold
@@ -49,8 +60,10 @@ namespace {
 constexpr int CX_ROWS = PREFILL_ROWS;  // rows of a tile
 constexpr int CX_KT = 128;             // keys of a tile
 constexpr int CX_CHUNK = 16;           // rows of a page copied at a time
-constexpr int CX_THREADS = 320;
-constexpr int CX_MMA_WARP = 8, CX_COPY_WARP = 9;
+constexpr int CX_THREADS = 384;
+constexpr int CX_MMA_WARP = 0, CX_COPY_WARP = 1;  // copies of K, and in the next warp of V
+constexpr int CX_SOFTMAX_WARP = 4;                // the first of eight (warp 3 only loads queries)
+constexpr int CX_FLUSH = 16;           // key tiles after which O is added up
 constexpr float CX_SLACK = 8.0f;  // log2 units a logit may pass the reference maximum by
 constexpr uint32_t CX_NAP = 20;   // ns between polls of a wait
 
@@ -64,15 +77,23 @@ struct CxCfg {
   static constexpr int OFF_K = OFF_Q + TILES * TERMS * TILE;
   static constexpr int OFF_V = OFF_K + NST * TILE;
   static constexpr int OFF_MASK = OFF_V + NST * TILE;  // [4] chunks of tile v & 3 that hold rows
-  static constexpr int OFF_BAR = OFF_MASK + 16;
-  static constexpr int OFF_MISC = OFF_BAR + 16 * 8;    // TMEM address, abort flag
+  // [TILES * 4 warps][32 rows][32 dims] fp32 on their way out; three-term queries leave no room for it
+  static constexpr bool STAGED = TERMS == 1;
+  static constexpr int OFF_OUT = OFF_MASK + 16;
+  static constexpr int OUT_WARP = 32 * 32 * 4;
+  static constexpr int OFF_BAR = OFF_OUT + (STAGED ? TILES * 4 * OUT_WARP : 0);
+  static constexpr int NBAR = 18;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // TMEM address, abort flag
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   // TMEM columns: S (P over it: high terms, then low terms) and O of each row tile
   static constexpr int TM_O = 2 * CX_KT;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-enum { CB_KFULL = 0, CB_KEMPTY = 2, CB_VFULL = 4, CB_VEMPTY = 6, CB_SFULL = 8, CB_PFULL = 10, CB_ODONE = 12, CB_DRAIN = 13 };
+// PFULL: of row tile (or, with one, key tile v & 1) t, the weights of half i of
+// the keys, at 2 t + i; PVDONE: with one row tile, P.V of each key tile
+enum { CB_KFULL = 0, CB_KEMPTY = 2, CB_VFULL = 4, CB_VEMPTY = 6, CB_SFULL = 8, CB_PFULL = 10, CB_ODONE = 14, CB_DRAIN = 15, CB_QFULL = 16,
+       CB_PVDONE = 17 };
 
 // kind::f16 with bf16 operands and fp32 sums; B K-major, or MN-major.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
@@ -95,6 +116,87 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// 16 rows (TMEM lanes) x 64 columns: lane 4 i + j gets of columns 8 k + 2 j, + 1
+// those of row i in r[4 k], r[4 k + 1] and of row i + 8 in r[4 k + 2], r[4 k + 3].
+__device__ __forceinline__ void ld_rows16(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Four neighbouring fp32 values of global memory, each added to.
+__device__ __forceinline__ void red_add4(float* p, float4 v) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+// One lane of the warp, the same one each time; every lane calls these.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
+  return is;
+}
+// The MMAs and commits of kvq_tc.cuh issued by the lane whose `on` is set: the
+// warp's control flow stays uniform, and descriptors in uniform registers.
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_addr(bar)),
+      "r"(on)
+      : "memory");
+}
+
+// Two fp32 values at a time.
+__device__ __forceinline__ uint64_t pair32(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair32(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -131,7 +233,26 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, b = blockIdx.z;
+  allow_dependent_launch();  // the join of the parts may launch; it waits for this grid
+  const int h = blockIdx.y;
+  // barriers, TMEM and the sequence of this CTA, then (the copies already begin)
+  // the queries
+  volatile int* mask = reinterpret_cast<volatile int*>(sm + C::OFF_MASK);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
+  int* seq_slot = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
+  if (warp == CX_COPY_WARP) {
+    const int b0 = heavy_first_sequence(P, blockIdx.z);
+    if (lane == 0) *seq_slot = b0;
+  } else if (tid == 0) {
+    for (int i = 0; i < C::NBAR; ++i)
+      mbar_init(bar + i, i >= CB_PFULL && i < CB_PFULL + 4 ? CX_ROWS / 32 : i == CB_QFULL ? CX_THREADS - 63 : 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+  const int b = *seq_slot;
   const int sp = blockIdx.x % P.splits, block = blockIdx.x / P.splits;  // part of the keys, group of row tiles
   const int G = P.group, Hkv = P.num_kv_heads, QB = CX_ROWS / G;
 
@@ -151,52 +272,71 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
   const int v0 = (int)((long long)sp * n_total / P.splits);
   const int nv = (int)((long long)(sp + 1) * n_total / P.splits) - v0;  // this part's key tiles
 
-  volatile int* mask = reinterpret_cast<volatile int*>(sm + C::OFF_MASK);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
-  if (tid == 0) {
-    for (int i = 0; i < 14; ++i) mbar_init(bar + i, i == CB_PFULL || i == CB_PFULL + 1 ? CX_ROWS : 1);
-    *abort_flag = 0;
-    mbar_init_fence();
-  }
-  if (warp == CX_MMA_WARP) tc::alloc(tmem_slot, 512);
-
-  // the rows' queries, as bf16 terms in the operand's layout (rows without a query: zeros)
-  const bool negative = P.softmax_scale < 0.0f;  // carried by the queries
-  for (int i = tid; i < tiles * CX_ROWS * (D / 8); i += CX_THREADS) {
-    const int c = i % (D / 8), r = i / (D / 8) % CX_ROWS, t = i / (D / 8) / CX_ROWS;
-    const int qi = q0 + t * QB + r / G;
-    float x[8];
+  uint32_t tmem = 0;
+  bool started = true;
+  if (warp == CX_COPY_WARP && lane == 0) {
+    if (P.q_tma) {  // (queries of no row of this CTA come along, those past q as zeros: neither is stored)
+      mbar_arrive_expect_tx(bar + CB_QFULL, (uint32_t)(tiles * (D / 64) * G * QB * 128));
+      for (int t = 0; t < tiles; ++t)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-    if (r / G < QB && qi < n && KVQ_IN_BOUNDS(cq0 + qi < P.total_q, P.dev_error))
-      load_row_elems<8>(P.q, TERMS == 1 ? DT_BF16 : DT_F32, ((size_t)(cq0 + qi) * P.num_q_heads + h * G + r % G) * D + 8 * c, x);
-    if (negative) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = -x[e];
+        for (int hh = 0; hh < D / 64; ++hh)
+          tc::tma_load_4d(sm + C::OFF_Q + t * C::TILE + hh * C::HALF, &P.q_map, 0, hh, h * G, cq0 + q0 + t * QB, bar + CB_QFULL);
+    } else {
+      tc::mbar_arrive(bar + CB_QFULL);
     }
+  }
+  const bool copies = warp == CX_COPY_WARP || warp == CX_COPY_WARP + 1;
+  if (!copies) {
+    if (warp == CX_MMA_WARP) tc::alloc(tmem_slot, 512);
+    if (!P.q_tma) {
+      // the rows' queries, as bf16 terms in the operand's layout: a warp per row (rows without a query: zeros)
+      constexpr int EPL = D / 32, RU = 4, NW = CX_THREADS / 32 - 2;  // RU rows in flight
+      const bool negative = P.softmax_scale < 0.0f;                  // carried by the queries
+      const int d0 = lane * EPL, w0 = warp > CX_COPY_WARP ? warp - 2 : warp;
+      for (int i0 = w0; i0 < tiles * CX_ROWS; i0 += RU * NW) {
+        float x[RU][EPL];
 #pragma unroll
-    for (int k = 0; k < TERMS; ++k) {
-      uint32_t w[4];
+        for (int u = 0; u < RU; ++u) {
+          const int i = i0 + u * NW, r = i % CX_ROWS, qi = q0 + i / CX_ROWS * QB + r / G;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-        x[2 * e] -= __uint_as_float(w[e] << 16);
-        x[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+          for (int e = 0; e < EPL; ++e) x[u][e] = 0.0f;
+          if (i < tiles * CX_ROWS && r / G < QB && qi < n && KVQ_IN_BOUNDS(cq0 + qi < P.total_q, P.dev_error))
+            load_row_elems<EPL>(P.q, TERMS == 1 ? DT_BF16 : DT_F32, ((size_t)(cq0 + qi) * P.num_q_heads + h * G + r % G) * D + d0, x[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+          const int i = i0 + u * NW, r = i % CX_ROWS, t = i / CX_ROWS;
+          if (i < tiles * CX_ROWS) {
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) x[u][e] = negative ? -x[u][e] : x[u][e];
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) {
+              uint8_t* at = sm + C::OFF_Q + (t * TERMS + k) * C::TILE + (d0 >> 6) * C::HALF +
+                            tc::sw128_off(r, (d0 & 63) >> 3) + 2 * (d0 & 7);
+#pragma unroll
+              for (int e = 0; e < EPL; e += 2) {
+                const uint32_t w = pack_bf16x2(x[u][e], x[u][e + 1]);
+                *reinterpret_cast<uint32_t*>(at + 2 * e) = w;
+                x[u][e] -= __uint_as_float(w << 16);
+                x[u][e + 1] -= __uint_as_float(w & 0xFFFF0000u);
+              }
+            }
+          }
+        }
       }
-      *reinterpret_cast<uint4*>(sm + C::OFF_Q + (t * TERMS + k) * C::TILE + (c >> 3) * C::HALF + tc::sw128_off(r, c & 7)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
     }
+    tc::fence_proxy_async();
+    tc::fence_before();
+    tc::mbar_arrive(bar + CB_QFULL);
+    started = __all_sync(0xffffffffu, mbar_wait_bounded(bar + CB_QFULL, 0, CX_NAP));
+    tc::fence_after();
+    tmem = *tmem_slot;
+    if (!started) *abort_flag = 1;
   }
-  tc::fence_proxy_async();
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
 
-  if (warp == CX_COPY_WARP) {
+  if (copies) {
     // ======================= copies =======================
+    const int kv = warp - CX_COPY_WARP;
     // pages: lane c of the first eight has chunk c of each tile, and looks up its
     // table entry one tile before it is copied
     const bool paged = P.cu_kv == nullptr;
@@ -218,31 +358,28 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
       else if (entry >= 0) row = (entry * Hkv + h) * bs + ((key0 + CX_CHUNK * lane) & (bs - 1));
       const unsigned found = paged ? __ballot_sync(0xffffffffu, row < P.chunk_rows_total) : 0xFFu;
       entry = lookup(v + 1);
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + (kv ? CB_VEMPTY : CB_KEMPTY) + st, parity, CX_NAP)) ||
-            __any_sync(0xffffffffu, *abort_flag != 0)) {
-          ok = false;
-          break;
-        }
-        uint64_t* full = bar + (kv ? CB_VFULL : CB_KFULL) + st;
-        uint8_t* dst = sm + (kv ? C::OFF_V : C::OFF_K) + st * C::TILE;
-        if (lane == 0) {
-          if (kv == 0) mask[v & 3] = (int)found;
-          mbar_arrive_expect_tx(full, C::TILE);
-        }
-        __syncwarp();
-        if (paged) {
-          if (lane < CX_KT / CX_CHUNK) {
-#pragma unroll
-            for (int hh = 0; hh < D / 64; ++hh)
-              tc::tma_load_4d(dst + hh * C::HALF + lane * (CX_CHUNK * 128), &P.kv_map[kv], 0, hh, 0, row, full);
-          }
-        } else if (lane == 0) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + (kv ? CB_VEMPTY : CB_KEMPTY) + st, parity, CX_NAP)) ||
+          __any_sync(0xffffffffu, *abort_flag != 0)) {
+        ok = false;
+        break;
+      }
+      uint64_t* full = bar + (kv ? CB_VFULL : CB_KFULL) + st;
+      uint8_t* dst = sm + (kv ? C::OFF_V : C::OFF_K) + st * C::TILE;
+      if (lane == 0) {
+        if (kv == 0) mask[v & 3] = (int)found;
+        mbar_arrive_expect_tx(full, C::TILE);
+      }
+      __syncwarp();
+      if (paged) {
+        if (lane < CX_KT / CX_CHUNK) {
 #pragma unroll
           for (int hh = 0; hh < D / 64; ++hh)
-            tc::tma_load_4d(dst + hh * C::HALF, &P.kv_map[kv], 0, hh, h, row0 + key0, full);
+            tc::tma_load_4d(dst + hh * C::HALF + lane * (CX_CHUNK * 128), &P.kv_map[kv], 0, hh, 0, row, full);
         }
+      } else if (lane == 0) {
+#pragma unroll
+        for (int hh = 0; hh < D / 64; ++hh)
+          tc::tma_load_4d(dst + hh * C::HALF, &P.kv_map[kv], 0, hh, h, row0 + key0, full);
       }
     }
     if (!ok) {
@@ -253,85 +390,236 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
     if (err && lane == 0) flag_error(P.dev_error, err);
   } else if (warp == CX_MMA_WARP) {
     // ======================= MMA issue =======================
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16(CX_ROWS, CX_KT, false), id_o = idesc_bf16(CX_ROWS, D, true);
-      // S(t, v) goes where P(t, v - 1) was: P.V(t, v - 1) was issued before it, and
-      // this thread's MMAs run in order; its commit tells the softmax of both.
-      auto logits = [&](int t, int st) {
-        const uint32_t a = smem_addr(sm + C::OFF_Q + t * TERMS * C::TILE), k = smem_addr(sm + C::OFF_K + st * C::TILE);
+    const uint32_t one = elect_one();
+    const uint32_t id_s = idesc_bf16(CX_ROWS, CX_KT, false), id_o = idesc_bf16(CX_ROWS, D, true);
+    const uint64_t q_desc = tc::sw128_desc(smem_addr(sm + C::OFF_Q)), k_desc = tc::sw128_desc(smem_addr(sm + C::OFF_K));
+    const uint64_t v_desc = mn_desc(smem_addr(sm + C::OFF_V), C::HALF);  // (addresses are counted in 16 bytes)
+    auto wait = [&](int i, int parity) -> bool { return __all_sync(0xffffffffu, mbar_wait_bounded(bar + i, parity & 1, CX_NAP)); };
+    // S(t, v) goes where P(t, v - 1) was: P.V(t, v - 1) was issued before it, and
+    // this thread's MMAs run in order; its commit tells the softmax of both.
+    auto logits = [&](int t, int u, int st) {  // row tile t, to place u
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint64_t bd = tc::sw128_desc(k + (s >> 2) * C::HALF + (s & 3) * 32);
+      for (int s = 0; s < D / 16; ++s) {
+        const int at = ((s >> 2) * C::HALF + (s & 3) * 32) >> 4;
 #pragma unroll
-          for (int i = 0; i < TERMS; ++i)
-            tc::mma_f16(tmem + t * CX_KT, tc::sw128_desc(a + i * C::TILE + (s >> 2) * C::HALF + (s & 3) * 32), bd, id_s,
-                        s > 0 || i > 0 ? 1u : 0u);
+        for (int i = 0; i < TERMS; ++i)
+          mma_ss_if(one, tmem + u * CX_KT, q_desc + (uint64_t)((t * TERMS + i) * (C::TILE >> 4) + at),
+                    k_desc + (uint64_t)(st * (C::TILE >> 4) + at), id_s, s > 0 || i > 0 ? 1u : 0u);
+      }
+      commit_if(one, bar + CB_SFULL + u);
+    };
+    // O(t) += P V of key tile v, the weights at place u as they come
+    auto values = [&](int t, int u, int v, int phase) -> bool {
+      const uint32_t p = tmem + u * CX_KT, o = tmem + C::TM_O + t * D;
+      const uint64_t vd = v_desc + (uint64_t)((v & 1) * (C::TILE >> 4));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!wait(CB_PFULL + 2 * u + i, phase)) return false;
+        tc::fence_after();
+#pragma unroll
+        for (int kk = 4 * i; kk < 4 * i + 4; ++kk) {
+          mma_ts_if(one, o, p + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, v % CX_FLUSH > 0 || kk > 0 ? 1u : 0u);
+          mma_ts_if(one, o, p + CX_KT / 2 + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, 1u);
         }
-        tc::commit(bar + CB_SFULL + t);
-      };
-      bool ok = true;
-      if (nv > 0) {
-        ok = mbar_wait_bounded(bar + CB_KFULL, 0, CX_NAP);
-        if (ok) {
-          tc::fence_after();
-          for (int t = 0; t < tiles; ++t) logits(t, 0);
-          tc::commit(bar + CB_KEMPTY);
-        }
+      }
+      return true;
+    };
+    bool ok = started;
+    if (tiles == 1) {
+#pragma unroll 1
+      for (int v = 0; v < min(nv, 2) && ok; ++v) {
+        ok = wait(CB_KFULL + v, 0);
+        if (!ok) break;
+        tc::fence_after();
+        logits(0, v, v);
+        commit_if(one, bar + CB_KEMPTY + v);
       }
 #pragma unroll 1
       for (int v = 0; v < nv && ok; ++v) {
         const int st = v & 1;
-        ok = mbar_wait_bounded(bar + CB_VFULL + st, (v >> 1) & 1, CX_NAP);
-#pragma unroll 1
-        for (int t = 0; t < tiles && ok; ++t) {
-          ok = mbar_wait_bounded(bar + CB_PFULL + t, v & 1, CX_NAP) && !*abort_flag;
+        ok = wait(CB_VFULL + st, v >> 1) && values(0, st, v, v >> 1);
+        if (!ok) break;
+        commit_if(one, bar + CB_VEMPTY + st);
+        commit_if(one, bar + CB_PVDONE);
+        if (v + 2 < nv) {
+          ok = wait(CB_KFULL + st, (v + 2) >> 1);
           if (!ok) break;
           tc::fence_after();
-          const uint32_t p = tmem + t * CX_KT, o = tmem + C::TM_O + t * D, vt = smem_addr(sm + C::OFF_V + st * C::TILE);
+          logits(0, st, st);
+          commit_if(one, bar + CB_KEMPTY + st);
+        }
+        ok = !__any_sync(0xffffffffu, *abort_flag != 0);
+      }
+    } else {
+      if (ok && nv > 0 && (ok = wait(CB_KFULL, 0))) {
+        tc::fence_after();
+        logits(0, 0, 0);
+        logits(1, 1, 0);
+        commit_if(one, bar + CB_KEMPTY);
+      }
+#pragma unroll 1
+      for (int v = 0; v < nv && ok; ++v) {
+        const int st = v & 1;
+        const bool more = v + 1 < nv;
+        ok = wait(CB_VFULL + st, v >> 1) && (!more || wait(CB_KFULL + (st ^ 1), (v + 1) >> 1));
+#pragma unroll 1
+        for (int t = 0; t < 2 && ok; ++t) {
+          ok = values(t, t, v, v);
+          if (ok && more) logits(t, t, st ^ 1);
+        }
+        if (!ok || __any_sync(0xffffffffu, *abort_flag != 0)) {
+          ok = false;
+          break;
+        }
+        commit_if(one, bar + CB_VEMPTY + st);
+        if (more) commit_if(one, bar + CB_KEMPTY + (st ^ 1));
+      }
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
+    }
+    commit_if(one, bar + CB_ODONE);
+    commit_if(one, bar + CB_DRAIN);  // every MMA issued by this warp has completed
+    (void)wait(CB_DRAIN, 0);
+  } else if (warp >= CX_SOFTMAX_WARP && warp / 4 - CX_SOFTMAX_WARP / 4 < tiles) {
+    // ======================= softmax =======================
+    const int t = warp / 4 - CX_SOFTMAX_WARP / 4, r = tid & (CX_ROWS - 1);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t o_tm = tmem + lanes + C::TM_O + t * D;
+    const float sl = fmaxf(fabsf(P.softmax_scale) * 1.4426950408889634f, 1e-30f);
+    // where the row ends up: its output, or this part's record
+    const int qi = q0 + t * QB + r / G;
+    const bool real = r / G < QB && qi < n && KVQ_IN_BOUNDS(cq0 + qi < P.total_q, P.dev_error);
+    float* base = P.out;
+    long long to = ((long long)(cq0 + qi) * P.num_q_heads + h * G + r % G) * D;  // from base
+    if (P.splits > 1) {
+      const long long tile = ((long long)b * Hkv + h) * (gridDim.x / P.splits * C::TILES) + block * C::TILES + t;
+      base = P.part + (tile * P.splits + sp) * split_record_floats(D);
+      to = r * D;
+    }
+    if (!real) to = -1;
+    float m = -CUDART_INF_F, l = 0.0f;
+    float held = -CUDART_INF_F;  // the reference of what `to` holds
+    // The row at `to` = (itself 2^(held - m) + O) w; without `any` O is zeros,
+    // without `more` the row is.
+    auto add_up = [&](bool any, bool more, bool last, float w) {
+      const float f = held == -CUDART_INF_F ? 0.0f : ex2(held - m);
+      held = m;
+      // O is added in memory, unread, while no reference of the warp's rows has moved
+      const bool add = more && !last && __all_sync(0xffffffffu, f == 1.0f);
+      if constexpr (C::STAGED) {
+        // 32 dims at a time through shared memory, so that a warp's stores and adds
+        // are whole 128-byte lines: four rows, eight lanes each
+        uint8_t* stage = sm + C::OFF_OUT + (t * 4 + (warp & 3)) * C::OUT_WARP;
+        long long at[8];
+        float rf[8], rw[8];
 #pragma unroll
-          for (int kk = 0; kk < CX_KT / 16; ++kk) {
-            const uint64_t bd = mn_desc(vt + kk * 16 * 128, C::HALF);
-            tc::mma_f16_ts(o, p + 8 * kk, bd, id_o, v > 0 || kk > 0 ? 1u : 0u);
-            tc::mma_f16_ts(o, p + CX_KT / 2 + 8 * kk, bd, id_o, 1u);
-          }
-          if (v + 1 < nv) {
-            if (t == 0) {
-              ok = mbar_wait_bounded(bar + CB_KFULL + (st ^ 1), ((v + 1) >> 1) & 1, CX_NAP);
-              if (!ok) break;
-              tc::fence_after();
+        for (int k = 0; k < 8; ++k) {
+          const int row = 4 * k + (lane >> 3);
+          at[k] = __shfl_sync(0xffffffffu, to, row);
+          rf[k] = __shfl_sync(0xffffffffu, f, row);
+          rw[k] = __shfl_sync(0xffffffffu, w, row);
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          {
+            uint32_t o[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+            if (any) {
+              ld32(o_tm + c, o);
+              tc::wait_ld();
+              tc::regs_after_wait(o);
             }
-            logits(t, st ^ 1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              sts128(stage + lane * 128 + 16 * ((j ^ lane) & 7), make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+          }
+          __syncwarp();
+          float4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = 4 * k + (lane >> 3);
+            x[k] = *reinterpret_cast<const float4*>(stage + row * 128 + 16 * ((lane ^ row) & 7));
+          }
+          __syncwarp();
+          float* p = base + c + 4 * (lane & 7);
+          if (add) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (at[k] >= 0) red_add4(p + at[k], x[k]);
+          } else {
+            float4 e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              e[k] = more && at[k] >= 0 ? __ldcg(reinterpret_cast<const float4*>(p + at[k])) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (at[k] >= 0)
+                __stcg(reinterpret_cast<float4*>(p + at[k]),
+                       make_float4(fmaf(e[k].x, rf[k], x[k].x) * rw[k], fmaf(e[k].y, rf[k], x[k].y) * rw[k],
+                                   fmaf(e[k].z, rf[k], x[k].z) * rw[k], fmaf(e[k].w, rf[k], x[k].w) * rw[k]));
           }
         }
-        if (!ok) break;
-        tc::commit(bar + CB_VEMPTY + st);
-        if (v + 1 < nv) tc::commit(bar + CB_KEMPTY + (st ^ 1));
+      } else {
+        // in the layout of the 16-row loads: lane 4 i + j has dims 8 k + 2 j, + 1 of
+        // rows i + 8 u, whole sectors
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = 8 * u + (lane >> 2);
+          const long long at = __shfl_sync(0xffffffffu, to, row);
+          const float g = __shfl_sync(0xffffffffu, f, row), x = __shfl_sync(0xffffffffu, w, row);
+          float* p = base + at + 2 * (lane & 3);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 64) {
+            uint32_t o[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+            if (any) {
+              ld_rows16(o_tm + ((uint32_t)(16 * (u >> 1)) << 16) + c, o);
+              tc::wait_ld();
+              tc::regs_after_wait(o);
+            }
+            if (at < 0) continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float o0 = __uint_as_float(o[4 * k + 2 * (u & 1)]), o1 = __uint_as_float(o[4 * k + 2 * (u & 1) + 1]);
+              float2* to2 = reinterpret_cast<float2*>(p + c + 8 * k);
+              const float2 e = more ? __ldcg(to2) : make_float2(0.0f, 0.0f);
+              __stcg(to2, make_float2(fmaf(e.x, g, o0) * x, fmaf(e.y, g, o1) * x));
+            }
+          }
+        }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        flag_error(P.dev_error, DEVERR_TIMEOUT);
-      }
-      tc::commit(bar + CB_ODONE);
-      tc::commit(bar + CB_DRAIN);  // every MMA issued by this thread has completed
-      (void)mbar_wait_bounded(bar + CB_DRAIN, 0);
-    }
-    __syncwarp();
-  } else if (warp / 4 < tiles) {
-    // ======================= softmax =======================
-    const int t = warp / 4, r = tid & (CX_ROWS - 1);
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_tm = tmem + lanes + t * CX_KT, o_tm = tmem + lanes + C::TM_O + t * D;
-    const float sl = fmaxf(fabsf(P.softmax_scale) * 1.4426950408889634f, 1e-30f);
-    float m = -CUDART_INF_F, l = 0.0f;
-    bool ok = true;
+    };
+    const uint64_t sl2 = pair32(sl, sl), minus1 = pair32(-1.0f, -1.0f);
+    bool ok = started;
 #pragma unroll 1
     for (int v = 0; v < nv; ++v) {
       // every decision around a .sync.aligned TMEM access is warp-uniform
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + CB_SFULL + t, v & 1, CX_NAP))) {
+      const int u = tiles == 1 ? v & 1 : t, phase = tiles == 1 ? v >> 1 : v;
+      const uint32_t s_tm = tmem + lanes + u * CX_KT;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + CB_SFULL + u, phase & 1, CX_NAP))) {
         ok = false;
         break;
       }
       tc::fence_after();
+      // O may be touched when P.V(v - 1) is done: with two row tiles it is, since
+      // S(v) was committed after it
+      auto o_is_done = [&]() -> bool {
+        if (tiles > 1 || v == 0) return true;
+        const bool good = __all_sync(0xffffffffu, mbar_wait_bounded(bar + CB_PVDONE, (v - 1) & 1, CX_NAP));
+        tc::fence_after();
+        return good;
+      };
+      if (v > 0 && v % CX_FLUSH == 0) {
+        if (!o_is_done()) {
+          ok = false;
+          break;
+        }
+        add_up(true, v > CX_FLUSH, false, 1.0f);
+      }
       uint32_t y[CX_KT];
 #pragma unroll
       for (int c = 0; c < CX_KT; c += 32) ld32(s_tm + c, y + c);
@@ -348,58 +636,76 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
         }
         tc::fence_proxy_async();
       }
+      tc::wait_ld();
+      tc::regs_after_wait(y);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
-      tc::wait_ld();
-      tc::regs_after_wait(y);
       if (left < CX_KT || chunks != 0xFF) {  // (uniform over the CTA)
 #pragma unroll
         for (int j = 0; j < CX_KT; ++j)
           if (j >= left || !((chunks >> (j / CX_CHUNK)) & 1)) y[j] = __float_as_uint(-CUDART_INF_F);
       }
-      float top = -CUDART_INF_F;
+      float top[4];  // four chains: one is 128 latencies long
 #pragma unroll
-      for (int j = 0; j < CX_KT; ++j) top = fmaxf(top, __uint_as_float(y[j]));
-      const float tmax = sl * top;
+      for (int j = 0; j < 4; ++j) top[j] = fmaxf(__uint_as_float(y[j]), __uint_as_float(y[j + 4]));
+#pragma unroll
+      for (int j = 8; j < CX_KT; j += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(fmaxf(top[i], __uint_as_float(y[j + i])), __uint_as_float(y[j + 4 + i]));
+      const float tmax = sl * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       const bool grow = tmax > m + CX_SLACK;
       const bool resc = grow && m != -CUDART_INF_F;
-      if (__any_sync(0xffffffffu, resc)) {  // (P.V(v - 1) is done: S(v), committed after it, is)
+      if (__any_sync(0xffffffffu, resc)) {
         const float f = resc ? ex2(m - tmax) : 1.0f;
+        if (v % CX_FLUSH > 0) {  // (else O begins anew)
+          if (!o_is_done()) {
+            ok = false;
+            break;
+          }
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tc::ld16(o_tm + c, o);
-          tc::wait_ld();
-          tc::regs_after_wait(o);
+          for (int c = 0; c < D; c += 8) {
+            uint32_t o[8];
+            ld8(o_tm + c, o);
+            tc::wait_ld();
+            tc::regs_after_wait(o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tc::st16(o_tm + c, o);
+            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            st8(o_tm + c, o);
+          }
         }
         l *= f;
       }
       m = grow ? tmax : m;
       const float ref = m == -CUDART_INF_F ? 0.0f : m;
-      float sum = 0.0f;
+      const uint64_t nref2 = pair32(-ref, -ref);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < CX_KT; c += 32) {  // 32 keys: 16 columns of high terms and 16 of low ones
         uint32_t hi[16], lo[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float p0 = ex2(fmaf(__uint_as_float(y[c + 2 * j]), sl, -ref));
-          const float p1 = ex2(fmaf(__uint_as_float(y[c + 2 * j + 1]), sl, -ref));
-          sum += p0 + p1;
+          const float2 x = unpair32(fma_pair(pair32(__uint_as_float(y[c + 2 * j]), __uint_as_float(y[c + 2 * j + 1])), sl2, nref2));
+          const float p0 = ex2(x.x), p1 = ex2(x.y);
+          const uint64_t pp = pair32(p0, p1);
+          sum[j & 1] = add_pair(sum[j & 1], pp);
           hi[j] = pack_bf16x2(p0, p1);
-          lo[j] = pack_bf16x2(p0 - __uint_as_float(hi[j] << 16), p1 - __uint_as_float(hi[j] & 0xFFFF0000u));
+          const float2 d = unpair32(
+              fma_pair(pair32(__uint_as_float(hi[j] << 16), __uint_as_float(hi[j] & 0xFFFF0000u)), minus1, pp));
+          lo[j] = pack_bf16x2(d.x, d.y);
         }
         tc::st16(s_tm + c / 2, hi);
         tc::st16(s_tm + CX_KT / 2 + c / 2, lo);
+        if (c % 64 == 32) {  // a half of the keys: P.V may begin with it
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar + CB_PFULL + 2 * u + c / 64);
+        }
       }
-      l += sum;
-      tc::wait_st();
-      tc::fence_before();
-      tc::mbar_arrive(bar + CB_PFULL + t);
+      const float2 sum2 = unpair32(add_pair(sum[0], sum[1]));
+      l += sum2.x + sum2.y;
       if (__any_sync(0xffffffffu, *abort_flag != 0)) {
         ok = false;
         break;
@@ -412,40 +718,9 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
       if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
     } else {
       tc::fence_after();
-      const int qi = q0 + t * QB + r / G;
-      const bool real = r / G < QB && qi < n;
-      float* to;
-      float w;
-      if (P.splits > 1) {
-        const long long tile = ((long long)b * Hkv + h) * (gridDim.x / P.splits * C::TILES) + block * C::TILES + t;
-        float* rec = P.part + (tile * P.splits + sp) * split_record_floats(D);
-        reinterpret_cast<float2*>(rec + CX_ROWS * D)[r] = make_float2(m, l);
-        to = rec + r * D;
-        w = 1.0f;
-      } else {
-        to = P.out + ((size_t)(cq0 + qi) * P.num_q_heads + h * G + r % G) * D;
-        w = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // (a NaN stays one)
-      }
-      const bool store = real && KVQ_IN_BOUNDS(cq0 + qi < P.total_q, P.dev_error);
-#pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        uint32_t o[16];
-        if (nv > 0) {
-          tc::ld16(o_tm + c, o);
-          tc::wait_ld();
-          tc::regs_after_wait(o);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = 0;
-        }
-        if (store) {
-#pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4*>(to + c + j) =
-                make_float4(__uint_as_float(o[j]) * w, __uint_as_float(o[j + 1]) * w, __uint_as_float(o[j + 2]) * w,
-                            __uint_as_float(o[j + 3]) * w);
-        }
-      }
+      const bool part = P.splits > 1;
+      if (part) reinterpret_cast<float2*>(base + CX_ROWS * D)[r] = make_float2(m, l);
+      add_up(nv > 0, nv > CX_FLUSH, true, part ? 1.0f : l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l));  // (a NaN stays one)
     }
   }
 
@@ -527,9 +802,8 @@ __global__ void __launch_bounds__(256) split_merge_kernel(const AttnParams P, in
 cudaError_t launch_split_merge(const AttnParams& P, int qtiles, cudaStream_t stream) {
   const long long warps = (long long)P.batch * P.num_kv_heads * qtiles * PREFILL_ROWS;
   const unsigned blocks = (unsigned)((warps + 7) / 8);
-  if (P.head_dim == 128) split_merge_kernel<128><<<blocks, 256, 0, stream>>>(P, qtiles);
-  else split_merge_kernel<64><<<blocks, 256, 0, stream>>>(P, qtiles);
-  return cudaGetLastError();
+  return P.head_dim == 128 ? launch_dependent(split_merge_kernel<128>, dim3(blocks), dim3(256), 0, stream, P, qtiles)
+                           : launch_dependent(split_merge_kernel<64>, dim3(blocks), dim3(256), 0, stream, P, qtiles);
 }
 
 template <int D, int TERMS>

@@ -99,7 +99,12 @@ struct AttnParams {
   int q_group, cross, splits;
   float* part;
   int exact;  // decode kernels: the closer sums of decode_tma_kernel's EXACT form
+  // cross attention over bf16 rows with bf16 queries: q_map views them as
+  // [total_q][num_q_heads][D] in boxes of one 64-dim half of `group` heads of as
+  // many queries as a row tile holds (q_tma 0: the kernel loads them itself)
+  int q_tma;
   CUtensorMap kv_map[2];  // 128-byte aligned by its own declaration
+  CUtensorMap q_map;
 };
 
 // Decode workspace (caller-owned scratch), carved by decode_ws_layout.

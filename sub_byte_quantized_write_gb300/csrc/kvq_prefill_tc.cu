@@ -217,35 +217,6 @@ __device__ __forceinline__ uint32_t codes2(const uint8_t* raw_row, int d) {
 
 }  // namespace
 
-// Heaviest sequences first: CTA row z of the grid takes the sequence of
-// rank z by 2 L - n (a proxy for its keys per query), so the long prefixes
-// start in the first wave and the short ones fill the tail.  Batches above
-// 64 sequences keep their order.
-__device__ __forceinline__ int heavy_first_sequence(const AttnParams& P, int z) {
-  if (P.batch > 64) return z;
-  const int lane = threadIdx.x & 31;
-  int key[2], me = -1;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int b = lane + 32 * k;
-    key[k] = b < P.batch ? 2 * __ldg(P.seq_lens + b) - (__ldg(P.cu_q + b + 1) - __ldg(P.cu_q + b)) : INT_MIN;
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int b = lane + 32 * k;
-    int rank = 0;
-    for (int j = 0; j < P.batch; ++j) {
-      const int kj = __shfl_sync(0xffffffffu, key[j >> 5], j & 31);
-      rank += (kj > key[k] || (kj == key[k] && j < b)) ? 1 : 0;
-    }
-    if (b < P.batch && rank == z) me = b;
-  }
-  const unsigned m = __ballot_sync(0xffffffffu, me >= 0);
-  const int src = m ? __ffs(m) - 1 : 0;
-  const int b = __shfl_sync(0xffffffffu, me, src);
-  return m ? b : z;
-}
-
 template <int MODE, int D>
 __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_constant__ AttnParams P) {
   using C = TpCfg<MODE, D>;
