@@ -147,36 +147,6 @@ __device__ __forceinline__ void red_add4(float* p, float4 v) {
                : "memory");
 }
 
-// One lane of the warp, the same one each time; every lane calls these.
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t is;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
-  return is;
-}
-// The MMAs and commits of kvq_tc.cuh issued by the lane whose `on` is set: the
-// warp's control flow stays uniform, and descriptors in uniform registers.
-__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_addr(bar)),
-      "r"(on)
-      : "memory");
-}
-
 // Two fp32 values at a time.
 __device__ __forceinline__ uint64_t pair32(float a, float b) {
   uint64_t r;
@@ -390,7 +360,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
     if (err && lane == 0) flag_error(P.dev_error, err);
   } else if (warp == CX_MMA_WARP) {
     // ======================= MMA issue =======================
-    const uint32_t one = elect_one();
+    const uint32_t one = tc::elect_one();
     const uint32_t id_s = idesc_bf16(CX_ROWS, CX_KT, false), id_o = idesc_bf16(CX_ROWS, D, true);
     const uint64_t q_desc = tc::sw128_desc(smem_addr(sm + C::OFF_Q)), k_desc = tc::sw128_desc(smem_addr(sm + C::OFF_K));
     const uint64_t v_desc = mn_desc(smem_addr(sm + C::OFF_V), C::HALF);  // (addresses are counted in 16 bytes)
@@ -403,10 +373,10 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
         const int at = ((s >> 2) * C::HALF + (s & 3) * 32) >> 4;
 #pragma unroll
         for (int i = 0; i < TERMS; ++i)
-          mma_ss_if(one, tmem + u * CX_KT, q_desc + (uint64_t)((t * TERMS + i) * (C::TILE >> 4) + at),
+          tc::mma_ss_if(one, tmem + u * CX_KT, q_desc + (uint64_t)((t * TERMS + i) * (C::TILE >> 4) + at),
                     k_desc + (uint64_t)(st * (C::TILE >> 4) + at), id_s, s > 0 || i > 0 ? 1u : 0u);
       }
-      commit_if(one, bar + CB_SFULL + u);
+      tc::commit_if(one, bar + CB_SFULL + u);
     };
     // O(t) += P V of key tile v, the weights at place u as they come
     auto values = [&](int t, int u, int v, int phase) -> bool {
@@ -418,8 +388,8 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
         tc::fence_after();
 #pragma unroll
         for (int kk = 4 * i; kk < 4 * i + 4; ++kk) {
-          mma_ts_if(one, o, p + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, v % CX_FLUSH > 0 || kk > 0 ? 1u : 0u);
-          mma_ts_if(one, o, p + CX_KT / 2 + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, 1u);
+          tc::mma_ts_if(one, o, p + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, v % CX_FLUSH > 0 || kk > 0 ? 1u : 0u);
+          tc::mma_ts_if(one, o, p + CX_KT / 2 + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, 1u);
         }
       }
       return true;
@@ -432,21 +402,21 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
         if (!ok) break;
         tc::fence_after();
         logits(0, v, v);
-        commit_if(one, bar + CB_KEMPTY + v);
+        tc::commit_if(one, bar + CB_KEMPTY + v);
       }
 #pragma unroll 1
       for (int v = 0; v < nv && ok; ++v) {
         const int st = v & 1;
         ok = wait(CB_VFULL + st, v >> 1) && values(0, st, v, v >> 1);
         if (!ok) break;
-        commit_if(one, bar + CB_VEMPTY + st);
-        commit_if(one, bar + CB_PVDONE);
+        tc::commit_if(one, bar + CB_VEMPTY + st);
+        tc::commit_if(one, bar + CB_PVDONE);
         if (v + 2 < nv) {
           ok = wait(CB_KFULL + st, (v + 2) >> 1);
           if (!ok) break;
           tc::fence_after();
           logits(0, st, st);
-          commit_if(one, bar + CB_KEMPTY + st);
+          tc::commit_if(one, bar + CB_KEMPTY + st);
         }
         ok = !__any_sync(0xffffffffu, *abort_flag != 0);
       }
@@ -455,7 +425,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
         tc::fence_after();
         logits(0, 0, 0);
         logits(1, 1, 0);
-        commit_if(one, bar + CB_KEMPTY);
+        tc::commit_if(one, bar + CB_KEMPTY);
       }
 #pragma unroll 1
       for (int v = 0; v < nv && ok; ++v) {
@@ -471,16 +441,16 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
           ok = false;
           break;
         }
-        commit_if(one, bar + CB_VEMPTY + st);
-        if (more) commit_if(one, bar + CB_KEMPTY + (st ^ 1));
+        tc::commit_if(one, bar + CB_VEMPTY + st);
+        if (more) tc::commit_if(one, bar + CB_KEMPTY + (st ^ 1));
       }
     }
     if (!ok) {
       *abort_flag = 1;
       if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
     }
-    commit_if(one, bar + CB_ODONE);
-    commit_if(one, bar + CB_DRAIN);  // every MMA issued by this warp has completed
+    tc::commit_if(one, bar + CB_ODONE);
+    tc::commit_if(one, bar + CB_DRAIN);  // every MMA issued by this warp has completed
     (void)wait(CB_DRAIN, 0);
   } else if (warp >= CX_SOFTMAX_WARP && warp / 4 - CX_SOFTMAX_WARP / 4 < tiles) {
     // ======================= softmax =======================
@@ -733,16 +703,19 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
 }
 
 // Joins the parts of one (query, q head) row: log-sum-exp weights, then the
-// inverse RHT (or the INT8 V channel scales) and 1 / l; one warp per row, lane
-// l dims l * EPL .. + EPL - 1.
-template <int D>
+// inverse RHT (or the INT8 V channel scales) and 1 / l.  W warps per row each
+// take every W-th group of eight parts (their loads in flight together) and meet
+// in shared memory: one row of five queries over 38 parts took 16.5 us with one
+// warp and four loads at a time.  Lane l has dims l * EPL .. + EPL - 1.
+template <int D, int W>
 __global__ void __launch_bounds__(256) split_merge_kernel(const AttnParams P, int qtiles) {
-  constexpr int EPL = D / 32;
-  const int lane = threadIdx.x & 31, G = P.group, Hkv = P.num_kv_heads, QB = PREFILL_ROWS / G;
-  const long long wid = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  constexpr int EPL = D / 32, U = 8, ROWS = 8 / W;  // rows of a CTA
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W, G = P.group, Hkv = P.num_kv_heads;
+  const int QB = PREFILL_ROWS / G;
+  const long long wid = (long long)blockIdx.x * ROWS + warp / W;
   const int row = (int)(wid % PREFILL_ROWS);
   const long long tile = wid / PREFILL_ROWS;  // (b * Hkv + h) * qtiles + qtile
-  if (tile >= (long long)P.batch * Hkv * qtiles) return;
+  if (tile >= (long long)P.batch * Hkv * qtiles) return;  // (whole CTAs, for W > 1; so below)
   const int qtile = (int)(tile % qtiles), h = (int)(tile / qtiles % Hkv), b = (int)(tile / qtiles / Hkv);
   grid_dependency_wait();  // every record is written
   const int cq0 = load_input<false>(P.cu_q + b);
@@ -754,8 +727,7 @@ __global__ void __launch_bounds__(256) split_merge_kernel(const AttnParams P, in
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.0f;
   const float* rec0 = P.part + tile * P.splits * split_record_floats(D);
-  constexpr int U = 4;  // records whose loads are in flight together
-  for (int s0 = 0; s0 < P.splits; s0 += U) {
+  for (int s0 = U * part; s0 < P.splits; s0 += U * W) {
     float2 ml[U];
     float v[U][EPL];
 #pragma unroll
@@ -781,6 +753,31 @@ __global__ void __launch_bounds__(256) split_merge_kernel(const AttnParams P, in
       for (int e = 0; e < EPL; ++e) o[e] = o[e] * f + v[u][e] * w;
     }
   }
+  if constexpr (W > 1) {
+    __shared__ float sm_m[W], sm_l[W], sm_o[W][D];
+    if (lane == 0) {
+      sm_m[part] = m;
+      sm_l[part] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) sm_o[part][EPL * lane + e] = o[e];
+    __syncthreads();
+    if (part != 0) return;
+    const float m0 = m;
+#pragma unroll
+    for (int w = 1; w < W; ++w) m = fmaxf(m, sm_m[w]);
+    const float f0 = m0 == -CUDART_INF_F ? 0.0f : ex2(m0 - m);
+    l *= f0;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] *= f0;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float f = sm_m[w] == -CUDART_INF_F ? 0.0f : ex2(sm_m[w] - m);
+      l = fmaf(f, sm_l[w], l);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = fmaf(f, sm_o[w][EPL * lane + e], o[e]);
+    }
+  }
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // (a NaN stays one)
   if (P.mode == MODE_INT8) {
     const float* am = P.ch_amax + ((size_t)Hkv + h) * D + lane * EPL;
@@ -799,11 +796,15 @@ __global__ void __launch_bounds__(256) split_merge_kernel(const AttnParams P, in
   else *reinterpret_cast<float2*>(out) = make_float2(o[0], o[1]);
 }
 
+template <int D>
+static cudaError_t launch_split_merge_d(const AttnParams& P, int qtiles, cudaStream_t stream) {
+  const long long rows = (long long)P.batch * P.num_kv_heads * qtiles * PREFILL_ROWS;
+  if (P.splits > 8)  // more parts than one warp has in flight
+    return launch_dependent(split_merge_kernel<D, 8>, dim3((unsigned)rows), dim3(256), 0, stream, P, qtiles);
+  return launch_dependent(split_merge_kernel<D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, P, qtiles);
+}
 cudaError_t launch_split_merge(const AttnParams& P, int qtiles, cudaStream_t stream) {
-  const long long warps = (long long)P.batch * P.num_kv_heads * qtiles * PREFILL_ROWS;
-  const unsigned blocks = (unsigned)((warps + 7) / 8);
-  return P.head_dim == 128 ? launch_dependent(split_merge_kernel<128>, dim3(blocks), dim3(256), 0, stream, P, qtiles)
-                           : launch_dependent(split_merge_kernel<64>, dim3(blocks), dim3(256), 0, stream, P, qtiles);
+  return P.head_dim == 128 ? launch_split_merge_d<128>(P, qtiles, stream) : launch_split_merge_d<64>(P, qtiles, stream);
 }
 
 template <int D, int TERMS>

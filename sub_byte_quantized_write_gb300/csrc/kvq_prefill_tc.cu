@@ -17,22 +17,24 @@
 // Design: one CTA of 14 warps per (128 rows, kv head, sequence); the 128
 // rows are (query, q head of the GQA group) pairs, so every key tile is
 // expanded once for the whole group.  Roles:
-//   warps 0-7  softmax: row r belongs to warps r / 32 (keys 0-31 of each
-//              tile) and r / 32 + 4 (keys 32-63).  Each half keeps its own
+//   warps 4-11 softmax: row r belongs to warps 4 + r / 32 (keys 0-31 of each
+//              tile) and 8 + r / 32 (keys 32-63).  Each half keeps its own
 //              running maximum, sum and O accumulator (O0, O1 in TMEM), so
 //              the two never wait for each other inside the key loop; it
 //              reads its logits from TMEM, masks them, writes (P s) hi / lo
 //              over them and rescales its O when its maximum grows.  In the
 //              end the halves merge (log-sum-exp weights) and the row gets
 //              the zero-point term, the inverse RHT and 1 / l.
-//   warp 8     TMEM allocation; lane 0 issues every tcgen05.mma:
+//   warp 0     TMEM allocation; issues every tcgen05.mma (the whole warp goes
+//              through the loop and one lane issues: with a loop of that lane
+//              alone, in the ninth warp, the MMAs came a third later):
 //              S_b = Q_hi K^T + Q_lo K^T (M=128, N=64, K=D) into one of two
 //              TMEM buffers, then O0 += P_hi V + P_lo V over keys 0-31 and
 //              O1 over keys 32-63 (M=128, N=D).
-//   warps 9-12 producers: expansion of the codes into fp16 K (K-major) and
+//   warps 2, 3, 12, 13  producers: expansion of the codes into fp16 K (K-major) and
 //              V^T (K-major, transposed with stmatrix) tiles in the 128-byte
 //              swizzle layout.
-//   warp 13    copy issuer: bulk copies of the raw page chunks.
+//   warp 1     copy issuer: bulk copies of the raw page chunks.
 // Codes enter the tensor cores as signed integers (exact in fp16); the
 // query and (P s) are split into fp16 hi + lo terms so fp16 does not limit
 // accuracy.  Every wait on an mbarrier is bounded; on a timeout the CTA
@@ -52,11 +54,11 @@ namespace {
 constexpr int TP_ROWS = PREFILL_ROWS_PER_CTA;
 constexpr int TP_KT = 64;
 constexpr int TP_THREADS = 448;
-constexpr int TP_SOFTMAX = 256;    // warps 0-7: warp w owns rows 32 (w % 4) .. + 31, keys 32 (w / 4) .. + 31 of a tile
-constexpr int TP_MMA_WARP = 8;
-constexpr int TP_PROD_WARP0 = 9;   // warps 9-12 expand codes
-constexpr int TP_PRODUCERS = 128;
-constexpr int TP_ISSUE_WARP = 13;
+constexpr int TP_SOFTMAX = 256;    // warps 4-11: warp 4 + w owns rows 32 (w % 4) .. + 31, keys 32 (w / 4) .. + 31 of a tile
+constexpr int TP_SOFTMAX_WARP0 = 4;
+constexpr int TP_MMA_WARP = 0;     // the oldest: the issue slots go to it first
+constexpr int TP_ISSUE_WARP = 1;
+constexpr int TP_PRODUCERS = 128;  // warps 2, 3, 12 and 13 expand codes
 // O is rescaled only when a row's maximum grows by more than 2^TP_SLACK, so
 // weights p reach at most 2^TP_SLACK and p * s stays inside fp16 for any
 // scale s below 65504 / 2^TP_SLACK (4094).
@@ -217,7 +219,9 @@ __device__ __forceinline__ uint32_t codes2(const uint8_t* raw_row, int d) {
 
 }  // namespace
 
-template <int MODE, int D>
+// CROSS: cross attention (see AttnParams): every key is seen, the key tiles are
+// cut into P.splits parts, and value scales are kept in fp16's range.
+template <int MODE, int D, bool CROSS>
 __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_constant__ AttnParams P) {
   using C = TpCfg<MODE, D>;
   constexpr int NKV = C::NKV;
@@ -232,8 +236,8 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   __syncthreads();
   const int b = *seq_slot, h = blockIdx.y;
   // later queries (more keys) first; cross attention: part `sp` of the tile's keys
-  const int sp = P.cross ? blockIdx.x % P.splits : 0;
-  const int qtile = P.cross ? blockIdx.x / P.splits : gridDim.x - 1 - blockIdx.x;
+  const int sp = CROSS ? blockIdx.x % P.splits : 0;
+  const int qtile = CROSS ? blockIdx.x / P.splits : gridDim.x - 1 - blockIdx.x;
   const int G = P.group, Hq = P.num_q_heads, Hkv = P.num_kv_heads, bs = P.block_size;
   const int QB = TP_ROWS / G;
 
@@ -241,13 +245,13 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   int n = __ldg(P.cu_q + b + 1) - cq0;
   const int q0 = qtile * QB;
   int L = __ldg(P.seq_lens + b);
-  if (P.cross) {  // any number of queries up to max_q_per_seq, and no keys for a length below 0
+  if constexpr (CROSS) {  // any number of queries up to max_q_per_seq, and no keys for a length below 0
     if ((n > P.max_q_per_seq || L < 0) && tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
     n = min(n, P.max_q_per_seq);
     L = max(L, 0);
   }
   if (q0 >= n) return;
-  if (!P.cross && (n > L || L < 0)) {
+  if (!CROSS && (n > L || L < 0)) {
     if (tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
     return;
   }
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   const int nq = cq0 < 0 ? 0 : min(min(QB, n - q0), P.total_q - cq0 - q0);
   if (nq < min(QB, n - q0) && tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
   if (nq <= 0) return;
-  const int p_min = L - n + q0, p_max = P.cross ? L - 1 : L - n + q0 + nq - 1;
+  const int p_min = L - n + q0, p_max = CROSS ? L - 1 : L - n + q0 + nq - 1;
 
   float* sc = reinterpret_cast<float*>(sm + C::OFF_SC);
   int* kval = reinterpret_cast<int*>(sm + C::OFF_KVAL);
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   }
   // (max: of a length past the table, the windows may start behind the last tile)
   int n_virt = gap ? ns + max(n_total - tw, 0) : n_total;
-  if (P.cross) {  // this part's tiles, as a gap before the first of them
+  if constexpr (CROSS) {  // this part's tiles, as a gap before the first of them
     gap = true;
     tw = (int)((long long)sp * n_total / P.splits);
     n_virt = (int)((long long)(sp + 1) * n_total / P.splits) - tw;
@@ -329,12 +333,9 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     constexpr int EPL = D / 32;
     uint8_t* qhi = sm + C::OFF_K;                      // [128 rows][QROW] fp16 hi
     uint8_t* qlo = sm + C::OFF_K + TP_ROWS * C::QROW;  // [128 rows][QROW] fp16 lo
-    for (int r = warp; r < TP_ROWS; r += TP_THREADS / 32) {
-      const int ql = r / G, i = r % G;
-      const bool rv = ql < nq && KVQ_IN_BOUNDS(cq0 + q0 + ql < P.total_q, P.dev_error);  // warp-uniform
-      float x[EPL];
+    auto stage_row = [&](int r, bool rv, float (&x)[EPL]) {
+      const int ql = r / G;
       if (rv) {
-        load_row_elems<EPL>(P.q, P.dtype, ((size_t)(cq0 + q0 + ql) * Hq + h * G + i) * D + lane * EPL, x);
         if constexpr (MODE == MODE_INT8) {
           const float* am = P.ch_amax + (size_t)h * D + lane * EPL;
 #pragma unroll
@@ -345,9 +346,6 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
             if (__ldg(P.signs + lane * EPL + e) < 0) x[e] = -x[e];
           wht_warp<EPL>(x, lane);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) x[e] = 0.0f;
       }
       if (P.softmax_scale < 0.0f) {
 #pragma unroll
@@ -378,8 +376,26 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
         const float sabs = fabsf(P.softmax_scale);
         rbeta[r] = fmaxf(sabs * log2e / (dnorm * scl), 1e-30f);
         rgamma[r] = sabs * log2e * sum / dnorm;
-        rpos[r] = rv ? (P.cross ? INT_MAX : L - n + q0 + ql) : -1;
+        rpos[r] = rv ? (CROSS ? INT_MAX : L - n + q0 + ql) : -1;
       }
+    };
+    // five rows of a warp in flight together: one by one, a CTA's start took 8 us
+    constexpr int NW = TP_THREADS / 32, RU = 5;
+#pragma unroll 1
+    for (int r0 = warp; r0 < TP_ROWS; r0 += RU * NW) {
+      float x[RU][EPL];
+      bool rv[RU];  // warp-uniform
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        const int r = r0 + u * NW, ql = r / G, i = r % G;
+        rv[u] = r < TP_ROWS && ql < nq && KVQ_IN_BOUNDS(cq0 + q0 + ql < P.total_q, P.dev_error);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) x[u][e] = 0.0f;
+        if (rv[u]) load_row_elems<EPL>(P.q, P.dtype, ((size_t)(cq0 + q0 + ql) * Hq + h * G + i) * D + lane * EPL, x[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < RU; ++u)
+        if (r0 + u * NW < TP_ROWS) stage_row(r0 + u * NW, rv[u], x[u]);
     }
   }
   tc::fence_before();
@@ -389,8 +405,8 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     const uint32_t tmem0 = *tmem_slot;
     // the softmax warps move the query rows into TMEM: warp w writes lanes
     // 32 (w % 4) .. + 31, half w / 4 of the columns of Q hi and of Q lo
-    if (warp < TP_SOFTMAX / 32) {
-      const int quad = warp & 3, hf = warp >> 2;
+    if (warp >= TP_SOFTMAX_WARP0 && warp < TP_SOFTMAX_WARP0 + TP_SOFTMAX / 32) {
+      const int quad = warp & 3, hf = (warp - TP_SOFTMAX_WARP0) >> 2;
       const int r = quad * 32 + lane;
       const uint32_t lb = (uint32_t)(quad * 32) << 16;
 #pragma unroll 1
@@ -534,17 +550,17 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
       }
     }
     __syncwarp();
-  } else if (warp >= TP_PROD_WARP0) {
+  } else if (warp != TP_MMA_WARP && (warp < TP_SOFTMAX_WARP0 || warp >= TP_SOFTMAX_WARP0 + TP_SOFTMAX / 32)) {
     // ======================= producers: code expansion =======================
-    const int pt = tid - TP_PROD_WARP0 * 32;  // 0..127
-    const int pwarp = warp - TP_PROD_WARP0;
+    const int pwarp = warp < TP_SOFTMAX_WARP0 ? warp - 2 : warp - (TP_SOFTMAX_WARP0 + TP_SOFTMAX / 32) + 2;  // 0..3
+    const int pt = 32 * pwarp + lane;  // 0..127
     int kvs = 0, kv_phase = 0;  // K/V stage of tile v and its wrap count parity
     int rs = 0, rphase = 0;     // raw stage of tile v
     // Cross attention: value scales are multiplied by a power of two that takes
     // the largest so far (of this half of the keys) to 2^10, so that p s (p up
     // to 2^TP_SLACK) neither overflows fp16 nor falls among its subnormals,
     // where 8-bit rows of unit size lost 1e-5 to 2e-5 of an output.
-    float vmul = P.cross ? 0x1p100f : 1.0f;
+    float vmul = CROSS ? 0x1p100f : 1.0f;
 #pragma unroll 1
     for (int v = 0; v < n_virt; ++v) {
       // raw tile v has landed; the tensor cores are done with this K/V stage
@@ -625,7 +641,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
               pad_scale_zero<MODE>(pad, P.stego != 0, s, z);  // z: the value of the signed code 0
             }
           }
-          if (P.cross && isv) {  // (idx is pt: a whole warp has 32 keys of V)
+          if (CROSS && isv) {  // (idx is pt: a whole warp has 32 keys of V)
             const float most = warp_max(s);
             if (most * vmul > 2048.0f)
               vmul = __uint_as_float((uint32_t)(127 + max(10 - ((int)(__float_as_uint(most) >> 23) - 127), -100)) << 23);
@@ -651,67 +667,65 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     }
   } else if (warp == TP_MMA_WARP) {
     // ======================= MMA issue =======================
-    if (lane == 0) {
-      const uint32_t idesc_qk = tc::idesc_f16(TP_ROWS, TP_KT);
-      const uint32_t idesc_pv = tc::idesc_f16(TP_ROWS, D);
-      // O0 += P V over the tile's keys 0-31 and O1 over keys 32-63, with P
-      // (hi / lo interleaved per 16 keys, where the tile's S was) from TMEM
-      // and V^T from shared memory
-      auto pv = [&](int i, int kvs_i) -> bool {
-        if (!mbar_wait_bounded(bar + B_PFULL, i & 1, TP_NAP_MMA)) return false;
-        tc::fence_after();
-        const uint32_t a_vt = smem_addr(sm + C::OFF_VT + kvs_i * C::VTILE);
-        const uint32_t p_tm = tmem + (i & 1) * TP_KT;
+    const uint32_t one = tc::elect_one();
+    const uint32_t idesc_qk = tc::idesc_f16(TP_ROWS, TP_KT);
+    const uint32_t idesc_pv = tc::idesc_f16(TP_ROWS, D);
+    const uint64_t k_desc = tc::sw128_desc(smem_addr(sm + C::OFF_K)), vt_desc = tc::sw128_desc(smem_addr(sm + C::OFF_VT));
+    auto wait = [&](int i, int parity) -> bool { return __all_sync(0xffffffffu, mbar_wait_bounded(bar + i, parity, TP_NAP_MMA)); };
+    // O0 += P V over the tile's keys 0-31 and O1 over keys 32-63, with P
+    // (hi / lo interleaved per 16 keys, where the tile's S was) from TMEM
+    // and V^T from shared memory
+    auto pv = [&](int i, int kvs_i) -> bool {
+      if (!wait(B_PFULL, i & 1)) return false;
+      tc::fence_after();
+      const uint32_t p_tm = tmem + (i & 1) * TP_KT;
 #pragma unroll
-        for (int kk = 0; kk < TP_KT / 16; ++kk) {
-          const uint64_t bdesc = tc::sw128_desc(a_vt + 32 * kk);
-          const uint32_t o_tm = kk < TP_KT / 32 ? tmem_o : tmem_o1;
-          tc::mma_f16_ts(o_tm, p_tm + 16 * kk, bdesc, idesc_pv, (i > 0 || (kk % (TP_KT / 32)) > 0) ? 1u : 0u);
-          tc::mma_f16_ts(o_tm, p_tm + 16 * kk + 8, bdesc, idesc_pv, 1u);
-        }
-        tc::commit(bar + B_ODONE);
-        tc::commit(bar + B_KVEMPTY + kvs_i);
-        return true;
-      };
-      bool ok = true;
-      int kvs = 0, kv_phase = 0, kvs_prev = 0;
+      for (int kk = 0; kk < TP_KT / 16; ++kk) {
+        const uint64_t bdesc = vt_desc + (uint64_t)((kvs_i * C::VTILE + 32 * kk) >> 4);
+        const uint32_t o_tm = kk < TP_KT / 32 ? tmem_o : tmem_o1;
+        tc::mma_ts_if(one, o_tm, p_tm + 16 * kk, bdesc, idesc_pv, (i > 0 || (kk % (TP_KT / 32)) > 0) ? 1u : 0u);
+        tc::mma_ts_if(one, o_tm, p_tm + 16 * kk + 8, bdesc, idesc_pv, 1u);
+      }
+      tc::commit_if(one, bar + B_ODONE);
+      tc::commit_if(one, bar + B_KVEMPTY + kvs_i);
+      return true;
+    };
+    bool ok = true;
+    int kvs = 0, kv_phase = 0, kvs_prev = 0;
 #pragma unroll 1
-      for (int v = 0; v < n_virt && ok; ++v) {
-        const int st = v & 1;
-        // S(v) goes where P(v - 2) was: P.V(v - 2) was issued before it and
-        // the tensor cores run this thread's MMAs in order
-        if (!mbar_wait_bounded(bar + B_KVFULL + kvs, kv_phase, TP_NAP_MMA)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after();
-        const uint32_t a_k = smem_addr(sm + C::OFF_K + kvs * C::KTILE);
-        const uint32_t s_tm = tmem + st * TP_KT;
+    for (int v = 0; v < n_virt && ok; ++v) {
+      const int st = v & 1;
+      // S(v) goes where P(v - 2) was: P.V(v - 2) was issued before it and
+      // the tensor cores run this warp's MMAs in order
+      if (!wait(B_KVFULL + kvs, kv_phase)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after();
+      const uint32_t s_tm = tmem + st * TP_KT;
 #pragma unroll
-        for (int s = 0; s < C::KSTEPS; ++s) {
-          const uint64_t bdesc = tc::sw128_desc(a_k + (s >> 2) * C::KATOM + (s & 3) * 32);
-          tc::mma_f16_ts(s_tm, tmem + C::TM_QHI + 8 * s, bdesc, idesc_qk, s > 0 ? 1u : 0u);
-          tc::mma_f16_ts(s_tm, tmem + C::TM_QLO + 8 * s, bdesc, idesc_qk, 1u);
-        }
-        tc::commit(bar + B_SFULL + st);
-        if (v >= 1) ok = pv(v - 1, kvs_prev);
-        if (*abort_flag) ok = false;
-        kvs_prev = kvs;
-        if (++kvs == NKV) {
-          kvs = 0;
-          kv_phase ^= 1;
-        }
+      for (int s = 0; s < C::KSTEPS; ++s) {
+        const uint64_t bdesc = k_desc + (uint64_t)((kvs * C::KTILE + (s >> 2) * C::KATOM + (s & 3) * 32) >> 4);
+        tc::mma_ts_if(one, s_tm, tmem + C::TM_QHI + 8 * s, bdesc, idesc_qk, s > 0 ? 1u : 0u);
+        tc::mma_ts_if(one, s_tm, tmem + C::TM_QLO + 8 * s, bdesc, idesc_qk, 1u);
       }
-      if (ok && n_virt >= 1) ok = pv(n_virt - 1, kvs_prev);
-      if (!ok) {
-        *abort_flag = 1;
-        flag_error(P.dev_error, DEVERR_TIMEOUT);
+      tc::commit_if(one, bar + B_SFULL + st);
+      if (v >= 1) ok = pv(v - 1, kvs_prev);
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) ok = false;
+      kvs_prev = kvs;
+      if (++kvs == NKV) {
+        kvs = 0;
+        kv_phase ^= 1;
       }
-      // drain: every MMA issued by this thread has completed
-      tc::commit(bar + B_DRAIN);
-      (void)mbar_wait_bounded(bar + B_DRAIN, 0);
     }
-    __syncwarp();
+    if (ok && n_virt >= 1) ok = pv(n_virt - 1, kvs_prev);
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
+    }
+    // drain: every MMA issued by this warp has completed
+    tc::commit_if(one, bar + B_DRAIN);
+    (void)wait(B_DRAIN, 0);
   } else {
     // ======================= softmax =======================
     // Row r is shared by warps r / 32 (keys 0-31 of each tile) and r / 32 + 4
@@ -722,7 +736,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     // pass 1 forms y = s c.q'' + rho z (rho = gamma / beta), masks it and
     // takes the maximum; pass 2 forms p = 2^(beta y - m) and writes (p s)
     // hi / lo of its 32 keys to P, over the tile's S columns.
-    const int quad = warp & 3, hf = warp >> 2;
+    const int quad = warp & 3, hf = (warp - TP_SOFTMAX_WARP0) >> 2;
     const int r = quad * 32 + lane;
     const float rb = rbeta[r];
     const float rho = rgamma[r] / rb;
@@ -803,7 +817,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
       }
       const bool resc = v >= 1 && grow && mrow != -CUDART_INF_F;
       float turn = 1.0f;  // cross attention: what the value scales' factor changes by
-      if (MODE != MODE_INT8 && P.cross) {
+      if constexpr (MODE != MODE_INT8 && CROSS) {
         const float to = vmuls[kvs * 2 + hf];
         if (v >= 1) turn = to / vmul;
         vmul = to;
@@ -931,7 +945,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     if (!good) {
       *abort_flag = 1;
       if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
-    } else if (P.cross && P.splits > 1) {  // this part's record
+    } else if (CROSS && P.splits > 1) {  // this part's record
       constexpr int EPL = D / 32;
       float* rec = P.part + ((((long long)b * Hkv + h) * (gridDim.x / P.splits) + qtile) * P.splits + sp) *
                                 split_record_floats(D);
@@ -996,7 +1010,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   }
 }
 
-template <int MODE, int D>
+template <int MODE, int D, bool CROSS>
 cudaError_t launch_prefill_tc_t(const AttnParams& P, cudaStream_t stream) {
   using C = TpCfg<MODE, D>;
   static bool attr_set[64] = {false};
@@ -1004,33 +1018,39 @@ cudaError_t launch_prefill_tc_t(const AttnParams& P, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(prefill_tc_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(prefill_tc_kernel<MODE, D, CROSS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   const int qtiles = (int)prefill_grid_x(P.max_q_per_seq, P.group);
-  dim3 grid((unsigned)qtiles * (P.cross ? P.splits : 1), P.num_kv_heads, P.batch);  // TP_THREADS threads each
-  prefill_tc_kernel<MODE, D><<<grid, TP_THREADS, C::SMEM, stream>>>(P);
-  if ((e = cudaGetLastError()) != cudaSuccess || !P.cross || P.splits == 1) return e;
+  dim3 grid((unsigned)qtiles * (CROSS ? P.splits : 1), P.num_kv_heads, P.batch);  // TP_THREADS threads each
+  prefill_tc_kernel<MODE, D, CROSS><<<grid, TP_THREADS, C::SMEM, stream>>>(P);
+  if ((e = cudaGetLastError()) != cudaSuccess || !CROSS || P.splits == 1) return e;
   return launch_split_merge(P, qtiles, stream);
 }
 
-cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream) {
+template <bool CROSS>
+cudaError_t launch_prefill_modes(const AttnParams& P, cudaStream_t stream) {
   switch (P.mode * 1000 + P.head_dim) {
-    case MODE_INT4 * 1000 + 128: return launch_prefill_tc_t<MODE_INT4, 128>(P, stream);
-    case MODE_INT4 * 1000 + 64: return launch_prefill_tc_t<MODE_INT4, 64>(P, stream);
-    case MODE_INT2 * 1000 + 128: return launch_prefill_tc_t<MODE_INT2, 128>(P, stream);
-    case MODE_INT2 * 1000 + 64: return launch_prefill_tc_t<MODE_INT2, 64>(P, stream);
-    case MODE_INT8 * 1000 + 128: return launch_prefill_tc_t<MODE_INT8, 128>(P, stream);
-    case MODE_INT8 * 1000 + 64: return launch_prefill_tc_t<MODE_INT8, 64>(P, stream);
-    case MODE_I8T * 1000 + 128: return launch_prefill_tc_t<MODE_I8T, 128>(P, stream);
-    case MODE_I8T * 1000 + 64: return launch_prefill_tc_t<MODE_I8T, 64>(P, stream);
-    case MODE_F8T * 1000 + 128: return launch_prefill_tc_t<MODE_F8T, 128>(P, stream);
-    case MODE_F8T * 1000 + 64: return launch_prefill_tc_t<MODE_F8T, 64>(P, stream);
-    case MODE_DBF16 * 1000 + 128: return launch_prefill_tc_t<MODE_DBF16, 128>(P, stream);
-    case MODE_DBF16 * 1000 + 64: return launch_prefill_tc_t<MODE_DBF16, 64>(P, stream);
+    case MODE_INT4 * 1000 + 128: return launch_prefill_tc_t<MODE_INT4, 128, CROSS>(P, stream);
+    case MODE_INT4 * 1000 + 64: return launch_prefill_tc_t<MODE_INT4, 64, CROSS>(P, stream);
+    case MODE_INT2 * 1000 + 128: return launch_prefill_tc_t<MODE_INT2, 128, CROSS>(P, stream);
+    case MODE_INT2 * 1000 + 64: return launch_prefill_tc_t<MODE_INT2, 64, CROSS>(P, stream);
+    case MODE_INT8 * 1000 + 128: return launch_prefill_tc_t<MODE_INT8, 128, CROSS>(P, stream);
+    case MODE_INT8 * 1000 + 64: return launch_prefill_tc_t<MODE_INT8, 64, CROSS>(P, stream);
+    case MODE_I8T * 1000 + 128: return launch_prefill_tc_t<MODE_I8T, 128, CROSS>(P, stream);
+    case MODE_I8T * 1000 + 64: return launch_prefill_tc_t<MODE_I8T, 64, CROSS>(P, stream);
+    case MODE_F8T * 1000 + 128: return launch_prefill_tc_t<MODE_F8T, 128, CROSS>(P, stream);
+    case MODE_F8T * 1000 + 64: return launch_prefill_tc_t<MODE_F8T, 64, CROSS>(P, stream);
+    case MODE_DBF16 * 1000 + 128: return launch_prefill_tc_t<MODE_DBF16, 128, false>(P, stream);
+    case MODE_DBF16 * 1000 + 64: return launch_prefill_tc_t<MODE_DBF16, 64, false>(P, stream);
     default: return cudaErrorInvalidValue;
   }
+}
+
+// (cross attention over 16-bit rows is launch_cross16's)
+cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream) {
+  return P.cross ? launch_prefill_modes<true>(P, stream) : launch_prefill_modes<false>(P, stream);
 }
 
 }  // namespace kvq

@@ -124,39 +124,77 @@ __device__ __forceinline__ void fill_tables(const RopeArgs& R, int tokens, const
   }
 }
 
+// Eight elements as they lie in memory: 16 bytes of bf16, 32 of fp32.
+template <bool F32>
+struct Raw8 {
+  uint4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw8(const void* in, long long at) {
+  Raw8<F32> r;
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i)  // (plain loads: the output may be the input)
+    r.w[i] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(in) + at * (F32 ? 4 : 2))[i];
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void store_raw8(void* out, long long at, const Raw8<F32>& r) {
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at * (F32 ? 4 : 2))[i] = r.w[i];
+}
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (F32) {
+        x[4 * i + k] = __uint_as_float(w[k]);
+      } else {
+        x[2 * k] = __uint_as_float(w[k] << 16);
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
 template <int D, bool F32>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeRows R) {
+__global__ void __launch_bounds__(256, 4) rope_kernel(const RopeRows R) {
   constexpr int PPR = D / ROPE_PIECE;  // pieces per row
-  constexpr int U = F32 ? 2 : 4;       // pieces in flight per thread
+  constexpr int U = F32 ? 1 : 2;       // pieces in flight per thread
   __shared__ __align__(16) float2 table[ROPE_TOKENS][D / 2];
   __shared__ int pos[ROPE_TOKENS];
   __shared__ int valid[ROPE_TOKENS];
   const int t0 = blockIdx.x * R.tokens_per_cta, tokens = min(R.tokens_per_cta, R.num_tokens - t0);
   const int heads = R.heads[0] + R.heads[1];
   const int items = tokens * heads * PPR;
+  // item i: piece i % PPR of head i / PPR % heads (q's, then k's) of token i / PPR / heads
   struct Item {
-    int tok, pc, which;
-    long long row;  // elements from the tensor's start, at dim 0
-    float x[2][8];
+    int tok, head, a, b;
   };
-  auto fetch = [&](int i, Item& it) {
-    it.tok = -1;
-    if (i >= items) return;
-    it.pc = i % PPR;
+  auto item = [&](int i) -> Item {
+    Item it;
     const int r = i / PPR;
     it.tok = r / heads;
-    const int h = r % heads;
-    it.which = h >= R.heads[0];
-    it.row = (long long)(h - (it.which ? R.heads[0] : 0)) * D;
-    int a, b;
-    piece_dims(R.rope, it.pc, a, b);
-    const long long at = (long long)(t0 + it.tok) * R.in_stride[it.which] + it.row;
-    load_row_elems<8, false>(R.in[it.which], F32 ? DT_F32 : DT_BF16, at + a, it.x[0]);
-    load_row_elems<8, false>(R.in[it.which], F32 ? DT_F32 : DT_BF16, at + b, it.x[1]);
+    it.head = r % heads;
+    piece_dims(R.rope, i % PPR, it.a, it.b);
+    return it;
   };
-  Item it[U];
+  Raw8<F32> x[U][2];
+  auto fetch = [&](int i0) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) fetch(threadIdx.x + u * 256, it[u]);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 256;
+      if (i >= items) break;
+      const Item it = item(i);
+      const int k = it.head >= R.heads[0];
+      const long long at = (long long)(t0 + it.tok) * R.in_stride[k] + (it.head - (k ? R.heads[0] : 0)) * D;
+      x[u][0] = load_raw8<F32>(R.in[k], at + it.a);
+      x[u][1] = load_raw8<F32>(R.in[k], at + it.b);
+    }
+  };
+  fetch(threadIdx.x);
   if (threadIdx.x < tokens) {
     int p = 0, seq = 0;
     const int t = t0 + threadIdx.x;
@@ -172,17 +210,26 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeRows R) {
   for (int i0 = threadIdx.x;; i0 += U * 256) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (it[u].tok < 0 || !valid[it[u].tok]) continue;
-      turn_piece(R.rope, table[it[u].tok], it[u].pc, it[u].x);
-      int a, b;
-      piece_dims(R.rope, it[u].pc, a, b);
-      const long long at = (long long)(t0 + it[u].tok) * R.out_stride[it[u].which] + it[u].row;
-      store8<F32>(R.out[it[u].which], at + a, it[u].x[0]);
-      store8<F32>(R.out[it[u].which], at + b, it[u].x[1]);
+      const int i = i0 + u * 256;
+      if (i >= items) break;
+      const Item it = item(i);
+      if (!valid[it.tok]) continue;
+      const int k = it.head >= R.heads[0];
+      const long long at = (long long)(t0 + it.tok) * R.out_stride[k] + (it.head - (k ? R.heads[0] : 0)) * D;
+      if (ROPE_PIECE * (i % PPR) < R.rope.rot) {
+        float f[2][8];
+        unpack8<F32>(x[u][0], f[0]);
+        unpack8<F32>(x[u][1], f[1]);
+        turn_piece(R.rope, table[it.tok], i % PPR, f);
+        store8<F32>(R.out[k], at + it.a, f[0]);
+        store8<F32>(R.out[k], at + it.b, f[1]);
+      } else {
+        store_raw8<F32>(R.out[k], at + it.a, x[u][0]);
+        store_raw8<F32>(R.out[k], at + it.b, x[u][1]);
+      }
     }
     if (i0 + U * 256 >= items) break;
-#pragma unroll
-    for (int u = 0; u < U; ++u) fetch(i0 + (U + u) * 256, it[u]);
+    fetch(i0 + U * 256);
   }
 }
 
