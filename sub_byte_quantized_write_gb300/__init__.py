@@ -381,6 +381,9 @@ class Rope(_Handle):
 
     def struct(self) -> KvqRotary:
         """The C struct: built once, and again when an attribute was set or the tensor's memory or shape changed."""
+        kept, t = self._struct, self.inv_freq
+        if kept is not None and t.data_ptr() == kept.pointers[0] and t.shape == kept.shapes[0]:
+            return kept.struct
         return _kept_struct(self, _rope_tensors, True)
 
     def _build(self) -> KvqRotary:
@@ -734,15 +737,13 @@ def kvq_rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = KVQ_RO
 
 
 def _token_rows(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype) -> Tuple[int, int]:
-    """(pointer, elements between tokens) of t [tokens, heads, head_dim], whose tokens may lie apart."""
-    if t.get_device() != dev:
-        raise ValueError("%s must be on the device of inv_freq" % name)
-    if t.dtype is not dtype:
-        raise ValueError("q, k and their outputs must have one dtype")
+    """(pointer, elements between tokens) of t [tokens, heads, head_dim], whose tokens may lie apart (0: they do not)."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError("q, k and their outputs must have one dtype and be on the device of inv_freq: %s" % name)
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     _, H, D = t.shape
     step, head, dim = t.stride()
-    if t.shape[0] <= 1:
-        step = H * D
     if (dim != 1 and D > 1) or (head != D and H > 1) or step < H * D:
         raise ValueError("%s: the heads of a token must lie one after another" % name)
     return t.data_ptr(), step
@@ -758,41 +759,53 @@ def kvq_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], s
     first = q if q is not None else k
     if first is None:
         raise ValueError("neither q nor k is given")
-    device, tokens = first.device, int(first.shape[0])
+    if first.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, head_dim]")
+    tokens, _, D = first.shape
+    device, dtype = first.device, first.dtype
     dev = first.get_device()
     rs = _rope_struct(rope, dev)
-    args, outs = [], []
-    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
-            if out is not None:
-                raise ValueError("%s_out without %s" % (name, name))
-            args += [None, None, 0, 0, 0]
-            outs.append(None)
-            continue
-        if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != first.shape[2]:
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        qp = qop = None
+        Hq = qs = qos = 0
+    else:
+        Hq = q.shape[1]
+        qp, qs = _token_rows(q, "q", dev, dtype)
+        if q_out is None:
+            q_out = _empty(q.shape, dtype, device, stream)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        qop, qos = _token_rows(q_out, "q_out", dev, dtype)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        kp = kop = None
+        Hk = ks = kos = 0
+    else:
+        Hk = k.shape[1]
+        if k.dim() != 3 or k.shape[0] != tokens or k.shape[2] != D:
             raise ValueError("q and k must be [tokens, heads, head_dim] of the same tokens and head_dim")
-        if out is None:
-            out = _empty(t.shape, t.dtype, device, stream)
-        elif out.shape != t.shape:
-            raise ValueError("%s_out must have the shape of %s" % (name, name))
-        p, step = _token_rows(t, name, dev, first.dtype)
-        po, step_out = _token_rows(out, name + "_out", dev, first.dtype)
-        args += [p, po, int(t.shape[1]), step, step_out]
-        outs.append(out)
-    ps = None
+        kp, ks = _token_rows(k, "k", dev, dtype)
+        if k_out is None:
+            k_out = _empty(k.shape, dtype, device, stream)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+        kop, kos = _token_rows(k_out, "k_out", dev, dtype)
     if positions is None:
         if seq_lens is None or cu_tokens is None:
             raise ValueError("seq_lens and cu_tokens, or positions, must be given")
-        _check_cu(cu_tokens, int(seq_lens.shape[0]), "cu_tokens")
-        ps = ctypes.byref(KvqPaging(None, None, 0, int(seq_lens.shape[0]), _dev_ptr(seq_lens, torch.int32, "seq_lens", dev),
-                                    None, 0))
+        batch = seq_lens.shape[0]
+        _check_cu(cu_tokens, batch, "cu_tokens")
+        ps = ctypes.byref(KvqPaging(None, None, 0, batch, _dev_ptr(seq_lens, torch.int32, "seq_lens", dev), None, 0))
+        at, cu = None, _dev_ptr(cu_tokens, torch.int32, "cu_tokens", dev)
     else:
         _check_positions(positions, tokens)
-        cu_tokens = None
-    _run(device, stream, _lib.kvq_rope, ctypes.byref(rs), _dev_ptr(positions, torch.int32, "positions", dev), ps,
-         _dev_ptr(cu_tokens, torch.int32, "cu_tokens", dev), *args, int(first.shape[2]), _qdtype(first), tokens,
-         _dev_ptr(dev_error, torch.int32, "dev_error", dev))
-    return outs[0], outs[1]
+        at, ps, cu = _dev_ptr(positions, torch.int32, "positions", dev), None, None
+    _run(device, stream, _lib.kvq_rope, ctypes.byref(rs), at, ps, cu, qp, qop, Hq, qs, qos, kp, kop, Hk, ks, kos, D,
+         _qdtype(first), tokens, _dev_ptr(dev_error, torch.int32, "dev_error", dev))
+    return q_out, k_out
 
 
 def kvq_rope_write(cache: PagedCache, paging: Paging, rope: Rope, k: torch.Tensor, v: torch.Tensor,

@@ -160,9 +160,9 @@ __device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&x)[8]) {
 }
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(256, 4) rope_kernel(const RopeRows R) {
+__global__ void __launch_bounds__(256, 6) rope_kernel(const RopeRows R) {
   constexpr int PPR = D / ROPE_PIECE;  // pieces per row
-  constexpr int U = F32 ? 1 : 2;       // pieces in flight per thread
+  constexpr int U = 1;                 // pieces in flight per thread
   __shared__ __align__(16) float2 table[ROPE_TOKENS][D / 2];
   __shared__ int pos[ROPE_TOKENS];
   __shared__ int valid[ROPE_TOKENS];
