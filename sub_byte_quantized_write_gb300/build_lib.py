@@ -22,8 +22,9 @@ LIB = os.path.join(HERE, "libkvq.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libkvq_debug.so")
 SOURCES = ["kvq_api.cu", "kvq_write.cu", "kvq_decode.cu", "kvq_decode16.cu", "kvq_pages.cu",
-           "kvq_prefill_tc.cu", "kvq_rope.cu", "kvq_cross16.cu"]
-HEADERS = ["kvq_common.cuh", "kvq_internal.h", "kvq_decode.cuh", "kvq_tc.cuh", "kvq_row.cuh", "kvq_rope.cuh"]
+           "kvq_prefill_tc.cu", "kvq_rope.cu", "kvq_cross16.cu", "kvq_crossq.cu"]
+HEADERS = ["kvq_common.cuh", "kvq_internal.h", "kvq_decode.cuh", "kvq_tc.cuh", "kvq_row.cuh", "kvq_rope.cuh",
+           "kvq_codes.cuh", "kvq_cross.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

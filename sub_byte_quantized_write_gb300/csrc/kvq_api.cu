@@ -878,7 +878,7 @@ kvq_status cross_plan(int32_t num_kv_heads, int32_t num_q_heads, int32_t batch, 
   for (int i = 0; i < 2; ++i) {
     const bool wide = rows16 && i == 0;  // two row tiles per CTA
     const long long blocks = wide ? kvq::cross16_blocks(max_q, plan->group, false) : tiles;
-    const int splits = cross_splits(blocks * pairs, (most_keys + (rows16 ? 127 : 63)) / (rows16 ? 128 : 64));
+    const int splits = cross_splits(blocks * pairs, (most_keys + 127) / 128);
     if (blocks * splits > 0x7FFFFFFFLL)
       return fail(KVQ_ERR_UNSUPPORTED, "max_q_per_seq gives more query tiles than one launch can hold");
     if (splits > 1)
@@ -983,7 +983,7 @@ kvq_status kvq_cross_attn(const kvq_cache* cache, const kvq_paging* paging, cons
     if ((st = cross16_maps(P, cache->k_pages, cache->v_pages, rows, 1, 16)) != KVQ_OK) return st;
     e = kvq::launch_cross16(P, static_cast<cudaStream_t>(stream));
   } else {
-    e = kvq::launch_prefill(P, static_cast<cudaStream_t>(stream));
+    e = kvq::launch_crossq(P, static_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }

@@ -49,9 +49,9 @@
 
 #include <math_constants.h>
 
+#include "kvq_cross.cuh"
 #include "kvq_decode.cuh"
 #include "kvq_internal.h"
-#include "kvq_tc.cuh"
 
 namespace kvq {
 
@@ -80,8 +80,7 @@ struct CxCfg {
   // [TILES * 4 warps][32 rows][32 dims] fp32 on their way out; three-term queries leave no room for it
   static constexpr bool STAGED = TERMS == 1;
   static constexpr int OFF_OUT = OFF_MASK + 16;
-  static constexpr int OUT_WARP = 32 * 32 * 4;
-  static constexpr int OFF_BAR = OFF_OUT + (STAGED ? TILES * 4 * OUT_WARP : 0);
+  static constexpr int OFF_BAR = OFF_OUT + (STAGED ? TILES * 4 * tc::ADD_ROWS_BYTES : 0);
   static constexpr int NBAR = 18;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // TMEM address, abort flag
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
@@ -100,35 +99,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-// MN-major operand in 128-byte-swizzled lines of 64 elements along MN: groups of
-// 8 lines along K 1024 bytes apart, the next 64 elements `lead` bytes further.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, int lead) {
-  return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // 16 rows (TMEM lanes) x 64 columns: lane 4 i + j gets of columns 8 k + 2 j, + 1
 // those of row i in r[4 k], r[4 k + 1] and of row i + 8 in r[4 k + 2], r[4 k + 3].
 __device__ __forceinline__ void ld_rows16(uint32_t taddr, uint32_t (&r)[32]) {
@@ -141,34 +111,6 @@ __device__ __forceinline__ void ld_rows16(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// Four neighbouring fp32 values of global memory, each added to.
-__device__ __forceinline__ void red_add4(float* p, float4 v) {
-  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
-}
-
-// Two fp32 values at a time.
-__device__ __forceinline__ uint64_t pair32(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair32(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -363,7 +305,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
     const uint32_t one = tc::elect_one();
     const uint32_t id_s = idesc_bf16(CX_ROWS, CX_KT, false), id_o = idesc_bf16(CX_ROWS, D, true);
     const uint64_t q_desc = tc::sw128_desc(smem_addr(sm + C::OFF_Q)), k_desc = tc::sw128_desc(smem_addr(sm + C::OFF_K));
-    const uint64_t v_desc = mn_desc(smem_addr(sm + C::OFF_V), C::HALF);  // (addresses are counted in 16 bytes)
+    const uint64_t v_desc = tc::mn_desc(smem_addr(sm + C::OFF_V), C::HALF);  // (addresses are counted in 16 bytes)
     auto wait = [&](int i, int parity) -> bool { return __all_sync(0xffffffffu, mbar_wait_bounded(bar + i, parity & 1, CX_NAP)); };
     // S(t, v) goes where P(t, v - 1) was: P.V(t, v - 1) was issued before it, and
     // this thread's MMAs run in order; its commit tells the softmax of both.
@@ -479,59 +421,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
       // O is added in memory, unread, while no reference of the warp's rows has moved
       const bool add = more && !last && __all_sync(0xffffffffu, f == 1.0f);
       if constexpr (C::STAGED) {
-        // 32 dims at a time through shared memory, so that a warp's stores and adds
-        // are whole 128-byte lines: four rows, eight lanes each
-        uint8_t* stage = sm + C::OFF_OUT + (t * 4 + (warp & 3)) * C::OUT_WARP;
-        long long at[8];
-        float rf[8], rw[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int row = 4 * k + (lane >> 3);
-          at[k] = __shfl_sync(0xffffffffu, to, row);
-          rf[k] = __shfl_sync(0xffffffffu, f, row);
-          rw[k] = __shfl_sync(0xffffffffu, w, row);
-        }
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          {
-            uint32_t o[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0;
-            if (any) {
-              ld32(o_tm + c, o);
-              tc::wait_ld();
-              tc::regs_after_wait(o);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              sts128(stage + lane * 128 + 16 * ((j ^ lane) & 7), make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
-          }
-          __syncwarp();
-          float4 x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int row = 4 * k + (lane >> 3);
-            x[k] = *reinterpret_cast<const float4*>(stage + row * 128 + 16 * ((lane ^ row) & 7));
-          }
-          __syncwarp();
-          float* p = base + c + 4 * (lane & 7);
-          if (add) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (at[k] >= 0) red_add4(p + at[k], x[k]);
-          } else {
-            float4 e[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              e[k] = more && at[k] >= 0 ? __ldcg(reinterpret_cast<const float4*>(p + at[k])) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (at[k] >= 0)
-                __stcg(reinterpret_cast<float4*>(p + at[k]),
-                       make_float4(fmaf(e[k].x, rf[k], x[k].x) * rw[k], fmaf(e[k].y, rf[k], x[k].y) * rw[k],
-                                   fmaf(e[k].z, rf[k], x[k].z) * rw[k], fmaf(e[k].w, rf[k], x[k].w) * rw[k]));
-          }
-        }
+        tc::add_rows<D>(base, to, o_tm, f, w, any, more, add, sm + C::OFF_OUT + (t * 4 + (warp & 3)) * tc::ADD_ROWS_BYTES);
       } else {
         // in the layout of the 16-row loads: lane 4 i + j has dims 8 k + 2 j, + 1 of
         // rows i + 8 u, whole sectors
@@ -563,7 +453,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
         }
       }
     };
-    const uint64_t sl2 = pair32(sl, sl), minus1 = pair32(-1.0f, -1.0f);
+    const uint64_t sl2 = tc::pair32(sl, sl), minus1 = tc::pair32(-1.0f, -1.0f);
     bool ok = started;
 #pragma unroll 1
     for (int v = 0; v < nv; ++v) {
@@ -592,7 +482,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
       }
       uint32_t y[CX_KT];
 #pragma unroll
-      for (int c = 0; c < CX_KT; c += 32) ld32(s_tm + c, y + c);
+      for (int c = 0; c < CX_KT; c += 32) tc::ld32(s_tm + c, y + c);
       const int left = L - (v0 + v) * CX_KT;  // keys of the sequence from this tile on
       const int chunks = mask[v & 3];
       if (t == 0 && left < CX_KT && r >= left) {  // a value row past the end, before the P.V that would read it
@@ -637,32 +527,32 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
 #pragma unroll 1
           for (int c = 0; c < D; c += 8) {
             uint32_t o[8];
-            ld8(o_tm + c, o);
+            tc::ld8(o_tm + c, o);
             tc::wait_ld();
             tc::regs_after_wait(o);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            st8(o_tm + c, o);
+            tc::st8(o_tm + c, o);
           }
         }
         l *= f;
       }
       m = grow ? tmax : m;
       const float ref = m == -CUDART_INF_F ? 0.0f : m;
-      const uint64_t nref2 = pair32(-ref, -ref);
+      const uint64_t nref2 = tc::pair32(-ref, -ref);
       uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < CX_KT; c += 32) {  // 32 keys: 16 columns of high terms and 16 of low ones
         uint32_t hi[16], lo[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float2 x = unpair32(fma_pair(pair32(__uint_as_float(y[c + 2 * j]), __uint_as_float(y[c + 2 * j + 1])), sl2, nref2));
+          const float2 x = tc::unpair32(tc::fma_pair(tc::pair32(__uint_as_float(y[c + 2 * j]), __uint_as_float(y[c + 2 * j + 1])), sl2, nref2));
           const float p0 = ex2(x.x), p1 = ex2(x.y);
-          const uint64_t pp = pair32(p0, p1);
-          sum[j & 1] = add_pair(sum[j & 1], pp);
+          const uint64_t pp = tc::pair32(p0, p1);
+          sum[j & 1] = tc::add_pair(sum[j & 1], pp);
           hi[j] = pack_bf16x2(p0, p1);
-          const float2 d = unpair32(
-              fma_pair(pair32(__uint_as_float(hi[j] << 16), __uint_as_float(hi[j] & 0xFFFF0000u)), minus1, pp));
+          const float2 d = tc::unpair32(
+              tc::fma_pair(tc::pair32(__uint_as_float(hi[j] << 16), __uint_as_float(hi[j] & 0xFFFF0000u)), minus1, pp));
           lo[j] = pack_bf16x2(d.x, d.y);
         }
         tc::st16(s_tm + c / 2, hi);
@@ -674,7 +564,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
           if (lane == 0) tc::mbar_arrive(bar + CB_PFULL + 2 * u + c / 64);
         }
       }
-      const float2 sum2 = unpair32(add_pair(sum[0], sum[1]));
+      const float2 sum2 = tc::unpair32(tc::add_pair(sum[0], sum[1]));
       l += sum2.x + sum2.y;
       if (__any_sync(0xffffffffu, *abort_flag != 0)) {
         ok = false;

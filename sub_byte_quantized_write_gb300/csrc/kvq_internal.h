@@ -94,7 +94,7 @@ struct AttnParams {
   // cross attention: the queries of cu_q (at most max_q_per_seq of a sequence)
   // each see every key.  By the decode kernels: q_group > 0, and `group` counts
   // the slots of a pair, query i's head g in slot i * q_group + g.  By the
-  // prefill kernel: cross = 1, and each query tile's keys are cut into `splits`
+  // tensor-core kernels: cross = 1, and each query tile's keys are cut into `splits`
   // parts, with `part` (splits > 1) their records, as split_record lays them out.
   int q_group, cross, splits;
   float* part;
@@ -250,6 +250,8 @@ cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream);
 // kv_map) or in pages (table; kv_map views the pools as rows); chunk_rows_total
 // counts the maps' rows.
 cudaError_t launch_cross16(const AttnParams& P, cudaStream_t stream);
+// cross attention over quantised pages (kvq_crossq.cu)
+cudaError_t launch_crossq(const AttnParams& P, cudaStream_t stream);
 // joins the records of split query tiles, qtiles of each (sequence, kv head)
 cudaError_t launch_split_merge(const AttnParams& P, int qtiles, cudaStream_t stream);
 

@@ -42,8 +42,7 @@
 
 #include <math_constants.h>
 
-#include <climits>
-
+#include "kvq_codes.cuh"
 #include "kvq_internal.h"
 #include "kvq_tc.cuh"
 
@@ -88,8 +87,7 @@ struct TpCfg {
   static constexpr int OFF_SC = OFF_RAW + NRAW * 2 * RAW;              // [NKV][ks, kz, vs, vz][64] f32
   static constexpr int OFF_KVAL = OFF_SC + NKV * 4 * TP_KT * 4;        // [NKV][4] chunk validity of the expanded tiles
   static constexpr int OFF_RAWVAL = OFF_KVAL + 64;                     // [NRAW][4] chunk validity of the raw tiles
-  static constexpr int OFF_VMUL = OFF_RAWVAL + 64;                     // [NKV][2 key halves] value scale factors
-  static constexpr int OFF_XMAX = OFF_VMUL + 32;                       // [2 key halves][128] f32 (epilogue)
+  static constexpr int OFF_XMAX = OFF_RAWVAL + 64;                     // [2 key halves][128] f32 (epilogue)
   static constexpr int OFF_ROW = OFF_XMAX + 2 * 2 * TP_ROWS * 4;       // beta, gamma [128] f32, pos [128] int
   static constexpr int OFF_BAR = OFF_ROW + 3 * TP_ROWS * 4;            // mbarriers
   static constexpr int NBAR = 32;
@@ -120,62 +118,6 @@ enum {
   B_RAWFULL = 0, B_RAWEMPTY = 3, B_KVFULL = 6, B_KVEMPTY = 9, B_SFULL = 12, B_SEMPTY = 14, B_PFULL = 16, B_ODONE = 17,
   B_DRAIN = 18, B_EPI = 28
 };
-
-// Two bf16 values (low half first) as an fp16 pair, rounded to nearest.  A
-// bf16 value carries 8 significant bits, so the conversion is exact for 0 and
-// for 2^-17 <= |x| <= 65504 (fp16 normals, and the subnormals that are
-// multiples of 2^-24).  Smaller magnitudes round to a multiple of 2^-24
-// (error at most 2^-25); magnitudes above 65504 become 65504 or infinity.
-__device__ __forceinline__ uint32_t bf16x2_to_half2_bits(uint32_t w) {
-  const __half2 hv = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return *reinterpret_cast<const uint32_t*>(&hv);
-}
-
-// Eight consecutive codes (head dims 8c .. 8c+7) of a raw row as four exact
-// fp16 pairs of signed codes u - 2^(b-1) (INT8: as stored; FP8: the E4M3
-// value; dense rows: the bf16 values), in dim order.
-template <int MODE>
-__device__ __forceinline__ uint4 codes8(const uint8_t* raw_row, int c) {
-  uint32_t o[4];
-  if constexpr (MODE == MODE_DBF16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(raw_row + 16 * c);
-    o[0] = bf16x2_to_half2_bits(w.x);
-    o[1] = bf16x2_to_half2_bits(w.y);
-    o[2] = bf16x2_to_half2_bits(w.z);
-    o[3] = bf16x2_to_half2_bits(w.w);
-  } else if constexpr (MODE == MODE_INT4) {
-    const uint32_t w = lds32(raw_row + 4 * c);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t x = prmt(w, 0u, j | (4 << 4) | (j << 8) | (4 << 12));  // byte j in both halves
-      o[j] = hsub2_bits(lop3_and_or(x, 0x00F0000Fu, 0x54006400u), 0x54806408u);
-    }
-  } else if constexpr (MODE == MODE_INT2) {
-    const uint32_t w = *reinterpret_cast<const uint16_t*>(raw_row + 2 * c);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t x = prmt(w, 0u, j | (4 << 4) | (j << 8) | (4 << 12));
-      o[2 * j] = hsub2_bits(lop3_and_or(x, 0x000C0003u, 0x5C006400u), 0x5C086402u);
-      o[2 * j + 1] = hsub2_bits(lop3_and_or(x, 0x00C00030u, 0x4C005400u), 0x4C805420u);
-    }
-  } else if constexpr (MODE == MODE_F8T) {
-    const uint2 w = make_uint2(lds32(raw_row + 8 * c), lds32(raw_row + 8 * c + 4));  // rows are D + 4 bytes
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = e4m3x2_to_half2_bits((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
-  } else {
-    // INT8 channel rows (D bytes) are 8-byte aligned, token-head rows (D + 4) are not
-    const uint2 w = MODE == MODE_INT8 ? lds64(raw_row + 8 * c)
-                                      : make_uint2(lds32(raw_row + 8 * c), lds32(raw_row + 8 * c + 4));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t src = j < 2 ? w.x : w.y;
-      const int bb = 2 * (j & 1);
-      const uint32_t x = prmt(src, 0u, bb | (4 << 4) | ((bb + 1) << 8) | (4 << 12));
-      o[j] = hsub2_bits(lop3_and_xor(x, 0x00FF00FFu, 0x64806480u), 0x64806480u);
-    }
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
 
 // Dense raw tiles: D / 64 halves of DENSE_HALF bytes, each 64 rows of 128
 // bytes (64 bf16 dims) with the 128-byte swizzle of the tensor copy.
@@ -219,9 +161,7 @@ __device__ __forceinline__ uint32_t codes2(const uint8_t* raw_row, int d) {
 
 }  // namespace
 
-// CROSS: cross attention (see AttnParams): every key is seen, the key tiles are
-// cut into P.splits parts, and value scales are kept in fp16's range.
-template <int MODE, int D, bool CROSS>
+template <int MODE, int D>
 __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_constant__ AttnParams P) {
   using C = TpCfg<MODE, D>;
   constexpr int NKV = C::NKV;
@@ -235,23 +175,16 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   }
   __syncthreads();
   const int b = *seq_slot, h = blockIdx.y;
-  // later queries (more keys) first; cross attention: part `sp` of the tile's keys
-  const int sp = CROSS ? blockIdx.x % P.splits : 0;
-  const int qtile = CROSS ? blockIdx.x / P.splits : gridDim.x - 1 - blockIdx.x;
+  const int qtile = gridDim.x - 1 - blockIdx.x;  // later queries (more keys) first
   const int G = P.group, Hq = P.num_q_heads, Hkv = P.num_kv_heads, bs = P.block_size;
   const int QB = TP_ROWS / G;
 
   const int cq0 = __ldg(P.cu_q + b);
-  int n = __ldg(P.cu_q + b + 1) - cq0;
+  const int n = __ldg(P.cu_q + b + 1) - cq0;
   const int q0 = qtile * QB;
-  int L = __ldg(P.seq_lens + b);
-  if constexpr (CROSS) {  // any number of queries up to max_q_per_seq, and no keys for a length below 0
-    if ((n > P.max_q_per_seq || L < 0) && tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
-    n = min(n, P.max_q_per_seq);
-    L = max(L, 0);
-  }
   if (q0 >= n) return;
-  if (!CROSS && (n > L || L < 0)) {
+  const int L = __ldg(P.seq_lens + b);
+  if (n > L || L < 0) {
     if (tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
     return;
   }
@@ -270,12 +203,11 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   const int nq = cq0 < 0 ? 0 : min(min(QB, n - q0), P.total_q - cq0 - q0);
   if (nq < min(QB, n - q0) && tid == 0) flag_error(P.dev_error, DEVERR_SEQ_LEN);
   if (nq <= 0) return;
-  const int p_min = L - n + q0, p_max = CROSS ? L - 1 : L - n + q0 + nq - 1;
+  const int p_min = L - n + q0, p_max = L - n + q0 + nq - 1;
 
   float* sc = reinterpret_cast<float*>(sm + C::OFF_SC);
   int* kval = reinterpret_cast<int*>(sm + C::OFF_KVAL);
   int* rawval = reinterpret_cast<int*>(sm + C::OFF_RAWVAL);
-  float* vmuls = reinterpret_cast<float*>(sm + C::OFF_VMUL);
   float* rbeta = reinterpret_cast<float*>(sm + C::OFF_ROW);
   float* rgamma = rbeta + TP_ROWS;
   int* rpos = reinterpret_cast<int*>(rgamma + TP_ROWS);
@@ -285,7 +217,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
 
   // ---- key tiles: [0, p_max] or, for a sliding-window head, the sink tiles
   // plus the tiles from the earliest window start of the CTA's rows
-  const int W = P.window ? __ldg(P.window + h) : 0;  // (cross attention has none)
+  const int W = P.window ? __ldg(P.window + h) : 0;
   const int n_total = min(p_max / TP_KT + 1, (Leff + TP_KT - 1) / TP_KT);
   int ns = 0, tw = 0;
   bool gap = false;
@@ -298,12 +230,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     }
   }
   // (max: of a length past the table, the windows may start behind the last tile)
-  int n_virt = gap ? ns + max(n_total - tw, 0) : n_total;
-  if constexpr (CROSS) {  // this part's tiles, as a gap before the first of them
-    gap = true;
-    tw = (int)((long long)sp * n_total / P.splits);
-    n_virt = (int)((long long)(sp + 1) * n_total / P.splits) - tw;
-  }
+  const int n_virt = gap ? ns + max(n_total - tw, 0) : n_total;
   auto tile_of = [&](int v) { return (gap && v >= ns) ? tw + (v - ns) : v; };
 
   // ---- set-up: barriers, TMEM, query rows
@@ -376,7 +303,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
         const float sabs = fabsf(P.softmax_scale);
         rbeta[r] = fmaxf(sabs * log2e / (dnorm * scl), 1e-30f);
         rgamma[r] = sabs * log2e * sum / dnorm;
-        rpos[r] = rv ? (CROSS ? INT_MAX : L - n + q0 + ql) : -1;
+        rpos[r] = rv ? (L - n + q0 + ql) : -1;
       }
     };
     // five rows of a warp in flight together: one by one, a CTA's start took 8 us
@@ -556,11 +483,6 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     const int pt = 32 * pwarp + lane;  // 0..127
     int kvs = 0, kv_phase = 0;  // K/V stage of tile v and its wrap count parity
     int rs = 0, rphase = 0;     // raw stage of tile v
-    // Cross attention: value scales are multiplied by a power of two that takes
-    // the largest so far (of this half of the keys) to 2^10, so that p s (p up
-    // to 2^TP_SLACK) neither overflows fp16 nor falls among its subnormals,
-    // where 8-bit rows of unit size lost 1e-5 to 2e-5 of an output.
-    float vmul = CROSS ? 0x1p100f : 1.0f;
 #pragma unroll 1
     for (int v = 0; v < n_virt; ++v) {
       // raw tile v has landed; the tensor cores are done with this K/V stage
@@ -640,13 +562,6 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
               const uint32_t pad = lds32((isv ? rvp : rk) + key * C::R + C::DATA);
               pad_scale_zero<MODE>(pad, P.stego != 0, s, z);  // z: the value of the signed code 0
             }
-          }
-          if (CROSS && isv) {  // (idx is pt: a whole warp has 32 keys of V)
-            const float most = warp_max(s);
-            if (most * vmul > 2048.0f)
-              vmul = __uint_as_float((uint32_t)(127 + max(10 - ((int)(__float_as_uint(most) >> 23) - 127), -100)) << 23);
-            s *= vmul;
-            if (lane == 0) vmuls[kvs * 2 + (key >> 5)] = vmul;
           }
           float* scs = sc + kvs * 4 * TP_KT;
           scs[(isv ? 2 : 0) * TP_KT + key] = s;
@@ -745,7 +660,6 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     const uint32_t tmem_oh = hf ? tmem_o1 : tmem_o;  // this half's O
     float* xmax = reinterpret_cast<float*>(sm + C::OFF_XMAX);
     float mrow = -CUDART_INF_F, lrow = 0.0f, pzrow = 0.0f;  // lrow, pzrow: this half's keys
-    float vmul = 1.0f;  // cross attention: the factor of this half's O (of tile v's value scales)
     bool ok = true;
     int kvs = 0;
 #pragma unroll 1
@@ -816,15 +730,9 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
         break;
       }
       const bool resc = v >= 1 && grow && mrow != -CUDART_INF_F;
-      float turn = 1.0f;  // cross attention: what the value scales' factor changes by
-      if constexpr (MODE != MODE_INT8 && CROSS) {
-        const float to = vmuls[kvs * 2 + hf];
-        if (v >= 1) turn = to / vmul;
-        vmul = to;
-      }
-      if (__any_sync(0xffffffffu, resc || turn != 1.0f)) {  // this half's O; rows keeping their reference scale by 1
+      if (__any_sync(0xffffffffu, resc)) {  // this half's O; rows keeping their reference scale by 1
         tc::fence_after();
-        const float f = resc ? ex2(mrow - muse) : 1.0f, fo = f * turn;
+        const float f = resc ? ex2(mrow - muse) : 1.0f;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t ra[16], rb2[16];
@@ -835,8 +743,8 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
           tc::regs_after_wait(rb2);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            ra[j] = __float_as_uint(__uint_as_float(ra[j]) * fo);
-            rb2[j] = __float_as_uint(__uint_as_float(rb2[j]) * fo);
+            ra[j] = __float_as_uint(__uint_as_float(ra[j]) * f);
+            rb2[j] = __float_as_uint(__uint_as_float(rb2[j]) * f);
           }
           tc::st16(tmem_oh + lane_base + c0, ra);
           tc::st16(tmem_oh + lane_base + c0 + 16, rb2);
@@ -910,7 +818,6 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     good = __all_sync(0xffffffffu, ok && good && xsum[(2 + (hf ^ 1)) * TP_ROWS + r] != 0.0f);
     const float mrr = fmaxf(mrow, xmax[(hf ^ 1) * TP_ROWS + r]);
     const float fw = mrow == -CUDART_INF_F ? 0.0f : ex2(mrow - mrr);  // 0 for a half without visible keys
-    const float fwo = fw / vmul;
 #pragma unroll 1
     for (int ph = 0; ph < 2; ++ph) {
       if (good && hf == ph) {  // every P.V is done: the K / V^T stages are free for staging
@@ -931,8 +838,8 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
               const uint32_t* w = j < 4 ? ra + 4 * j : rb2 + 4 * (j - 4);
               float4& dst = stage[r * P4 + ((c0 / 4 + j) ^ (r & 7))];
               const float4 prev = ph ? dst : make_float4(0.f, 0.f, 0.f, 0.f);
-              dst = make_float4(fmaf(fwo, __uint_as_float(w[0]), prev.x), fmaf(fwo, __uint_as_float(w[1]), prev.y),
-                                fmaf(fwo, __uint_as_float(w[2]), prev.z), fmaf(fwo, __uint_as_float(w[3]), prev.w));
+              dst = make_float4(fmaf(fw, __uint_as_float(w[0]), prev.x), fmaf(fw, __uint_as_float(w[1]), prev.y),
+                                fmaf(fw, __uint_as_float(w[2]), prev.z), fmaf(fw, __uint_as_float(w[3]), prev.w));
             }
           }
         } else if (ph == 0) {
@@ -945,20 +852,6 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
     if (!good) {
       *abort_flag = 1;
       if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
-    } else if (CROSS && P.splits > 1) {  // this part's record
-      constexpr int EPL = D / 32;
-      float* rec = P.part + ((((long long)b * Hkv + h) * (gridDim.x / P.splits) + qtile) * P.splits + sp) *
-                                split_record_floats(D);
-      float2* ml = reinterpret_cast<float2*>(rec + TP_ROWS * D);
-      if (hf == 0) ml[r] = make_float2(mrr, xsum[r]);
-      for (int k = 16 * hf; k < 16 * hf + 16; ++k) {
-        const int row = quad * 32 + k;
-        const float pz = xsum[TP_ROWS + row];
-        const float* src = reinterpret_cast<const float*>(stage + row * P4 + ((lane * EPL / 4) ^ (row & 7))) +
-                           (lane * EPL) % 4;
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) rec[row * D + lane * EPL + e] = src[e] + pz;
-      }
     } else {
       constexpr int EPL = D / 32;  // lane holds dims lane * EPL .. + EPL - 1
       for (int k = 16 * hf; k < 16 * hf + 16; ++k) {
@@ -1010,7 +903,7 @@ __global__ void __launch_bounds__(TP_THREADS, 1) prefill_tc_kernel(const __grid_
   }
 }
 
-template <int MODE, int D, bool CROSS>
+template <int MODE, int D>
 cudaError_t launch_prefill_tc_t(const AttnParams& P, cudaStream_t stream) {
   using C = TpCfg<MODE, D>;
   static bool attr_set[64] = {false};
@@ -1018,39 +911,31 @@ cudaError_t launch_prefill_tc_t(const AttnParams& P, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(prefill_tc_kernel<MODE, D, CROSS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(prefill_tc_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const int qtiles = (int)prefill_grid_x(P.max_q_per_seq, P.group);
-  dim3 grid((unsigned)qtiles * (CROSS ? P.splits : 1), P.num_kv_heads, P.batch);  // TP_THREADS threads each
-  prefill_tc_kernel<MODE, D, CROSS><<<grid, TP_THREADS, C::SMEM, stream>>>(P);
-  if ((e = cudaGetLastError()) != cudaSuccess || !CROSS || P.splits == 1) return e;
-  return launch_split_merge(P, qtiles, stream);
+  dim3 grid((unsigned)prefill_grid_x(P.max_q_per_seq, P.group), P.num_kv_heads, P.batch);  // TP_THREADS threads each
+  prefill_tc_kernel<MODE, D><<<grid, TP_THREADS, C::SMEM, stream>>>(P);
+  return cudaGetLastError();
 }
 
-template <bool CROSS>
-cudaError_t launch_prefill_modes(const AttnParams& P, cudaStream_t stream) {
+cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream) {
   switch (P.mode * 1000 + P.head_dim) {
-    case MODE_INT4 * 1000 + 128: return launch_prefill_tc_t<MODE_INT4, 128, CROSS>(P, stream);
-    case MODE_INT4 * 1000 + 64: return launch_prefill_tc_t<MODE_INT4, 64, CROSS>(P, stream);
-    case MODE_INT2 * 1000 + 128: return launch_prefill_tc_t<MODE_INT2, 128, CROSS>(P, stream);
-    case MODE_INT2 * 1000 + 64: return launch_prefill_tc_t<MODE_INT2, 64, CROSS>(P, stream);
-    case MODE_INT8 * 1000 + 128: return launch_prefill_tc_t<MODE_INT8, 128, CROSS>(P, stream);
-    case MODE_INT8 * 1000 + 64: return launch_prefill_tc_t<MODE_INT8, 64, CROSS>(P, stream);
-    case MODE_I8T * 1000 + 128: return launch_prefill_tc_t<MODE_I8T, 128, CROSS>(P, stream);
-    case MODE_I8T * 1000 + 64: return launch_prefill_tc_t<MODE_I8T, 64, CROSS>(P, stream);
-    case MODE_F8T * 1000 + 128: return launch_prefill_tc_t<MODE_F8T, 128, CROSS>(P, stream);
-    case MODE_F8T * 1000 + 64: return launch_prefill_tc_t<MODE_F8T, 64, CROSS>(P, stream);
-    case MODE_DBF16 * 1000 + 128: return launch_prefill_tc_t<MODE_DBF16, 128, false>(P, stream);
-    case MODE_DBF16 * 1000 + 64: return launch_prefill_tc_t<MODE_DBF16, 64, false>(P, stream);
+    case MODE_INT4 * 1000 + 128: return launch_prefill_tc_t<MODE_INT4, 128>(P, stream);
+    case MODE_INT4 * 1000 + 64: return launch_prefill_tc_t<MODE_INT4, 64>(P, stream);
+    case MODE_INT2 * 1000 + 128: return launch_prefill_tc_t<MODE_INT2, 128>(P, stream);
+    case MODE_INT2 * 1000 + 64: return launch_prefill_tc_t<MODE_INT2, 64>(P, stream);
+    case MODE_INT8 * 1000 + 128: return launch_prefill_tc_t<MODE_INT8, 128>(P, stream);
+    case MODE_INT8 * 1000 + 64: return launch_prefill_tc_t<MODE_INT8, 64>(P, stream);
+    case MODE_I8T * 1000 + 128: return launch_prefill_tc_t<MODE_I8T, 128>(P, stream);
+    case MODE_I8T * 1000 + 64: return launch_prefill_tc_t<MODE_I8T, 64>(P, stream);
+    case MODE_F8T * 1000 + 128: return launch_prefill_tc_t<MODE_F8T, 128>(P, stream);
+    case MODE_F8T * 1000 + 64: return launch_prefill_tc_t<MODE_F8T, 64>(P, stream);
+    case MODE_DBF16 * 1000 + 128: return launch_prefill_tc_t<MODE_DBF16, 128>(P, stream);
+    case MODE_DBF16 * 1000 + 64: return launch_prefill_tc_t<MODE_DBF16, 64>(P, stream);
     default: return cudaErrorInvalidValue;
   }
-}
-
-// (cross attention over 16-bit rows is launch_cross16's)
-cudaError_t launch_prefill(const AttnParams& P, cudaStream_t stream) {
-  return P.cross ? launch_prefill_modes<true>(P, stream) : launch_prefill_modes<false>(P, stream);
 }
 
 }  // namespace kvq

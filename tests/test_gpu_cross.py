@@ -77,6 +77,18 @@ def test_cross_evicted_pages(mode, G, n):
     assert not out[n[0]:n[0] + n[1], :G].any()
 
 
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_cross_ragged_batch(mode, D):
+    """More query tiles than the card runs at once, sources of many key tiles whose last is partly filled."""
+    H, G, bs, lens, n = 4, 4, 32, [1500, 900, 33, 4500, 700, 1281, 2305], [330, 70, 300, 128, 64, 401, 95]
+    c, pag, k, v = filled(mode, lens, H, D, bs, False, seed=31)
+    q = rows(32, sum(n), H * G, D)
+    out, err = run(c, pag, q, n, D ** -0.5)
+    ref.check(out, q, k, v, n, lens, D ** -0.5)
+    assert err == 0
+
+
 @pytest.mark.parametrize("mode", ["INT4_TOKEN_HEAD", "INT2_TOKEN_HEAD", "FP8_TOKEN_HEAD", "BF16_CACHE"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("n", [(2,), (40,), (300,)])
