@@ -35,6 +35,9 @@
 // 2^-25 of O per step of 16 keys and term (1.3e-5 of an output over 8192 keys):
 // every CX_FLUSH tiles O is added in fp32 to the row where it will end up, and
 // begins anew.
+// Measured: 8 prompts of 1024 queries over 2048 .. 8192 rows (32 q and 8 kv heads
+// of 128) 750 us, 958 TFLOP/s of 4 D per pair and 1437 of the operations done; 5
+// queries over 131071 rows 62 us with the join, 4.3 TB/s.
 // Rows that are not there (an evicted page, past the sequence's end): chunks of
 // a page without an entry are copied from past the tensor's end, which gives
 // zeros, and masked; value rows past the end of the sequence, which may hold
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  allow_dependent_launch();  // the join of the parts may launch; it waits for this grid
+  if (P.splits > 1) allow_dependent_launch();  // the join of the parts may launch; it waits for this grid
   const int h = blockIdx.y;
   // barriers, TMEM and the sequence of this CTA, then (the copies already begin)
   // the queries

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  allow_dependent_launch();  // the join of the parts may launch; it waits for this grid
+  if (P.splits > 1) allow_dependent_launch();  // the join of the parts may launch; it waits for this grid
   const int h = blockIdx.y;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
