@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
   const int tiles = min(C::TILES, (n - q0 + QB - 1) / QB);
   const int L = cross_keys(P, b, first);
   if (L < 0) return;
-  const int n_total = (L + CX_KT - 1) / CX_KT;
+  const int n_total = L / CX_KT + (L % CX_KT ? 1 : 0);  // (L may be next to 2^31)
   const int v0 = (int)((long long)sp * n_total / P.splits);
   const int nv = (int)((long long)(sp + 1) * n_total / P.splits) - v0;  // this part's key tiles
 

@@ -41,6 +41,7 @@
 // the tensor cores' rate counting the doubled products.  What bounds it is the
 // chain of a tile: logits from TMEM, maximum, weights, back, P.V, next S, some
 // 8500 cycles with two tiles in flight (TMEM is full: S twice, O and Q).
+// (S half by half, each right after the P.V that frees its place: 721 us.)
 // Every wait is bounded; on a timeout the CTA reports KVQ_DEVERR_TIMEOUT, drains,
 // frees its TMEM and returns.
 //
@@ -71,6 +72,7 @@ constexpr uint32_t CQ_NAP = 20;
 template <int MODE, int D>
 struct CqCfg {
   static constexpr int DATA = data_bytes(MODE, D);  // (scale and zero point follow)
+  static_assert(DATA <= row_bytes_of(MODE, D), "the pad follows the codes");
   static constexpr int R = row_bytes_of(MODE, D);
   static constexpr int CHUNK = 16 * R;
   static constexpr int RAW = CQ_KT * R;           // raw rows of K (or V) of a tile
@@ -142,7 +144,8 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   int* seq_slot = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
   volatile float* vmuls = reinterpret_cast<volatile float*>(sm + C::OFF_MISC + 16);  // [8], of tile v & 7
-  volatile int* mask = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 48);  if (warp == CQ_COPY_WARP) {
+  volatile int* mask = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 48);     // [8], of tile v & 7
+  if (warp == CQ_COPY_WARP) {
     const int b0 = heavy_first_sequence(P, blockIdx.z);
     if (lane == 0) *seq_slot = b0;
   } else if (tid == 0) {
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
     if (first) flag_error(P.dev_error, L < 0 ? DEVERR_SEQ_LEN : DEVERR_TABLE_RANGE);
     L = L < 0 ? 0 : P.max_blocks * bs;
   }
-  const int n_total = (L + CQ_KT - 1) / CQ_KT;
+  const int n_total = L / CQ_KT + (L % CQ_KT ? 1 : 0);  // (L may be next to 2^31)
   const int v0 = (int)((long long)sp * n_total / P.splits);
   const int nv = (int)((long long)(sp + 1) * n_total / P.splits) - v0;
 

@@ -273,6 +273,63 @@ def test_encoder_decoder_as_used():
         assert torch.equal(res[0], res[1])
 
 
+@pytest.mark.parametrize("mode", ["INT4_TOKEN_HEAD", "INT8_CHANNEL", "BF16_CACHE"])
+@pytest.mark.parametrize("n", [(2, 1), (90, 33)])
+def test_cross_captured_over_a_cache_that_changes(mode, n):
+    """A captured call answers with the lengths, tables, rows and queries of each replay, its parts' records in a
+    workspace of its own; the step after it writes into the pages that it reads."""
+    K = kvq()
+    H, G, D, lens = 2, 4, 128, [1500, 700]
+    c, pag, k, v = filled(mode, lens, H, D, 16, False, seed=12)
+    q = rows(3, sum(n), H * G, D, dtype=torch.bfloat16)
+    cu = cu_of(n)
+    ws = torch.empty(max(1, K.kvq_cross_workspace_size(c, pag, H * G, max(n))), dtype=torch.uint8, device="cuda")
+    res = torch.empty((sum(n), H * G, D), device="cuda")
+    K.kvq_cross_attn(c, pag, q, cu, max(n), D ** -0.5, out=res, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        K.kvq_cross_attn(c, pag, q, cu, max(n), D ** -0.5, out=res, workspace=ws)
+    for step in range(3):
+        now = [lens[0] - 129 * step, lens[1] - 333 * step]
+        pag.seq_lens.copy_(i32(now))
+        q.copy_(rows(40 + step, sum(n), H * G, D, dtype=torch.bfloat16))
+        kk, vv = K.kvq_gather(c, pag, cu_of(now), sum(now))
+        g.replay()
+        if mode != "INT8_CHANNEL":  # behind it, into its last rows
+            one = rows(50 + step, 2, H, D), rows(60 + step, 2, H, D)
+            K.kvq_write_decode_attn(c, pag, *one, i32([0, 1, 2]), rows(70, 2, H * G, D), D ** -0.5)
+        torch.cuda.synchronize()
+        ref.check(res, q, kk, vv, n, now, D ** -0.5)
+
+
+def test_dense_captured_beside_itself():
+    """Two captured calls, each with its own workspace, on two streams at once, over lengths that change."""
+    K = kvq()
+    H, G, D, n, lens = 2, 4, 64, (70, 5), [900, 1400]
+    k, v = (rows(5 + i, sum(lens), H, D, dtype=torch.bfloat16) for i in range(2))
+    q, cu, ck = rows(9, sum(n), H * G, D, dtype=torch.bfloat16), cu_of(n), cu_of(lens)
+    L = i32(lens)
+    ws = [torch.empty(max(1, K.kvq_cross_dense_workspace_size(k, L, H * G, max(n))), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    res = [torch.empty((sum(n), H * G, D), device="cuda") for _ in range(2)]
+    K.kvq_cross_dense_attn(k, v, ck, L, q, cu, max(n), D ** -0.5, out=res[0], workspace=ws[0])
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            K.kvq_cross_dense_attn(k, v, ck, L, q, cu, max(n), D ** -0.5, out=res[i], workspace=ws[i])
+    s = torch.cuda.Stream()
+    for step in range(3):
+        now = [lens[0] - 300 * step, lens[1] - 17 * step]
+        L.copy_(i32(now))
+        s.wait_stream(torch.cuda.current_stream())
+        graphs[0].replay()
+        with torch.cuda.stream(s):
+            graphs[1].replay()
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        ref.check(res[0], q, k, v, n, now, D ** -0.5, start=[0, lens[0]])
+        assert torch.equal(res[0], res[1])
+
+
 def test_cross_binding_refusals():
     K = kvq()
     c, pag, _, _ = filled("BF16_CACHE", [20], 1, 64, 16, False)
