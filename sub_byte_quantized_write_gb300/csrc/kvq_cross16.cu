@@ -313,14 +313,15 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
     // S(t, v) goes where P(t, v - 1) was: P.V(t, v - 1) was issued before it, and
     // this thread's MMAs run in order; its commit tells the softmax of both.
     auto logits = [&](int t, int u, int st) {  // row tile t, to place u
+      // the low terms first, while the sums that each step truncates are small
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const int at = ((s >> 2) * C::HALF + (s & 3) * 32) >> 4;
+      for (int i = TERMS - 1; i >= 0; --i)
 #pragma unroll
-        for (int i = 0; i < TERMS; ++i)
+        for (int s = 0; s < D / 16; ++s) {
+          const int at = ((s >> 2) * C::HALF + (s & 3) * 32) >> 4;
           tc::mma_ss_if(one, tmem + u * CX_KT, q_desc + (uint64_t)((t * TERMS + i) * (C::TILE >> 4) + at),
-                    k_desc + (uint64_t)(st * (C::TILE >> 4) + at), id_s, s > 0 || i > 0 ? 1u : 0u);
-      }
+                        k_desc + (uint64_t)(st * (C::TILE >> 4) + at), id_s, s > 0 || i < TERMS - 1 ? 1u : 0u);
+        }
       tc::commit_if(one, bar + CB_SFULL + u);
     };
     // O(t) += P V of key tile v, the weights at place u as they come

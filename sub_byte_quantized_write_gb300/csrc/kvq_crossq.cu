@@ -437,12 +437,14 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
     const uint32_t id_s = idesc_f16_mn(CQ_ROWS, CQ_KT, false), id_o = idesc_f16_mn(CQ_ROWS, D, true);
     const uint64_t k_desc = tc::sw128_desc(smem_addr(sm + C::OFF_K)), v_desc = tc::mn_desc(smem_addr(sm + C::OFF_V), C::HALF);
     auto logits = [&](int u) {  // of the tile in stage u, to place u
+      // the low terms first, while the sums that each step truncates are small
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint64_t bd = k_desc + (uint64_t)((u * C::TILE + (s >> 2) * C::HALF + (s & 3) * 32) >> 4);
-        tc::mma_ts_if(one, tmem + u * CQ_KT, tmem + C::TM_QHI + 8 * s, bd, id_s, s > 0 ? 1u : 0u);
-        tc::mma_ts_if(one, tmem + u * CQ_KT, tmem + C::TM_QLO + 8 * s, bd, id_s, 1u);
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint64_t bd = k_desc + (uint64_t)((u * C::TILE + (s >> 2) * C::HALF + (s & 3) * 32) >> 4);
+          tc::mma_ts_if(one, tmem + u * CQ_KT, tmem + (i ? C::TM_QHI : C::TM_QLO) + 8 * s, bd, id_s, s > 0 || i > 0 ? 1u : 0u);
+        }
       tc::commit_if(one, bar + QB_SFULL + u);
       tc::commit_if(one, bar + QB_KEMPTY + u);
     };
