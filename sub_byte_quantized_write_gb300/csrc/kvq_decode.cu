@@ -57,6 +57,7 @@
 
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kvq_decode.cuh"
@@ -186,20 +187,6 @@ __device__ __forceinline__ uint32_t kpair_int2_fold(uint32_t w) {
 // adds to the signed code u - 2.
 __host__ __device__ constexpr float kfold_int2(int d) {
   return (d & 7) == 4 || (d & 7) == 7 ? 6.0f : ((d & 7) == 1 || (d & 7) == 3 || (d & 7) == 6) ? 18.0f : 66.0f;
-}
-
-// The same with smaller constants, 16 and 4 (EXACT): the sum of a key's products
-// and their constants is rounded at the size of the constants, so these cost an
-// eighth of the error of 64's, for two more shifts per word.
-template <int P>
-__device__ __forceinline__ uint32_t kpair_int2_fold_exact(uint32_t w) {
-  constexpr int pos = (P == 0 || P == 3 || P == 5) ? 6 : 8;
-  constexpr uint32_t magic = pos == 6 ? 0x4C004C00u : 0x44004400u;  // 16, 4
-  const uint32_t src = P <= 1 ? (w << 6) : P == 2 ? (w << 4) : P <= 4 ? w : P <= 6 ? (w >> 4) : (w >> 6);
-  return lop3_and_or(src, 0x00030003u << pos, magic);
-}
-__host__ __device__ constexpr float kfold_int2_exact(int d) {
-  return ((d & 7) == 0 || (d & 7) == 3 || (d & 7) == 5) ? 18.0f : 6.0f;
 }
 
 template <int MODE>
@@ -374,6 +361,29 @@ __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int
   }
 }
 
+// Whether a query's high terms lie on a grid that makes their sums with the
+// folded codes exact (the calls with rope and cross attention).  Every folded
+// code is an integer of 80 at most and a query's elements end below 2048, so high
+// terms that are multiples of D / 64 have sums of multiples of it below 2^24 times
+// it: nothing is truncated, whatever the order.  The low terms are below 1, and
+// their constants' part is cut at 2^-11 of a unit.  Without the grid the sums hold
+// the constants times sum(q''), D times one element of the query before its
+// transform, and what they lose at that size: 1.2e-5 (4-bit rows) and 3e-5 (2-bit)
+// of an output where the query lies in that element alone; on the grid 2e-6.
+// A step over 4-bit rows (exact 1) keeps the older calls' terms, so
+// that it is to the bit what turned rows give there, unless that element is four
+// times the others' root mean square: up to there the sums lose 2e-6 of an output
+// at most, of logits below 12.
+template <int MODE, int EPL>
+__device__ __forceinline__ bool fold_on_grid(const AttnParams& P, float sum, const float (&x)[EPL]) {
+  if constexpr (MODE != MODE_INT4 && MODE != MODE_INT2) return false;
+  if (P.exact != 1 || MODE != MODE_INT4) return P.exact != 0;
+  float ss = 0.0f;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) ss = fmaf(x[e], x[e], ss);
+  return sum * sum > 16.0f * warp_sum(ss);
+}
+
 // The position a decode query turns to: its sequence's last token's.
 __device__ __forceinline__ int query_position(const AttnParams& P, int b) {
   if (P.rope.positions && P.num_new > 0) {
@@ -441,27 +451,28 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
     amx = warp_max(amx);
     const int ex = amx > 0.0f ? ilogbf(amx) : 0;
     const float sc = ldexpf(1.0f, 10 - ex);  // max |q''| in [1024, 2048)
+    const bool grid = fold_on_grid<MODE>(P, sum, x);
     // the folded key offset: sum over dims of the exact operand value (hi +
-    // lo) times the constant the folded key unpack adds to the signed code
-    float opsum = 0.0f;
+    // lo, or apart) times the constant the folded key unpack adds to the signed code
+    float opsum = 0.0f, ophi = 0.0f;
 #pragma unroll
     for (int e = 0; e < EPL; ++e) {
       const float v = x[e] * sc;
-      const __half hi = __float2half_rn(v);
+      const __half hi = __float2half_rn(grid ? rintf(v * (64.0f / D)) * (D / 64.0f) : v);
       const __half lo = __float2half_rn(v - __half2float(hi));
       qh[0][i][lane * EPL + e] = hi;
       qh[1][i][lane * EPL + e] = lo;
-      const float kc = MODE == MODE_INT4   ? KFOLD_INT4
-                       : MODE == MODE_INT2 ? (P.exact ? kfold_int2_exact(lane * EPL + e) : kfold_int2(lane * EPL + e))
-                                           : 0.0f;
-      opsum = fmaf(kc, __half2float(hi) + __half2float(lo), opsum);
+      const float kc = MODE == MODE_INT4 ? KFOLD_INT4 : MODE == MODE_INT2 ? kfold_int2(lane * EPL + e) : 0.0f;
+      ophi = fmaf(kc, grid ? __half2float(hi) : 0.0f, ophi);
+      opsum = fmaf(kc, grid ? __half2float(lo) : __half2float(hi) + __half2float(lo), opsum);
     }
     opsum = warp_sum(opsum);
+    ophi = warp_sum(ophi);
     if (lane == 0) {
       const float beta = i < G ? P.softmax_scale * log2e / (dnorm * sc) : 0.0f;
       const float gamma = i < G ? P.softmax_scale * log2e * sum / dnorm : 0.0f;
       const float corr = opsum;
-      ws.qbg[(size_t)bh * NH + i] = make_float4(beta, gamma, corr, 0.0f);
+      ws.qbg[(size_t)bh * NH + i] = make_float4(beta, gamma, corr, ophi);
     }
   }
   __syncthreads();
@@ -515,7 +526,9 @@ __device__ __forceinline__ void load_seg(const AttnParams& P, int bh, int start,
   s.tbl = P.table + (size_t)(P.headwise ? bh : b) * P.max_blocks;
 }
 
-template <int MODE, int D, int NT>
+// CLOSER (cross attention): products of 16 keys start from zero, as in
+// decode_tma_kernel's FORM 2.
+template <int MODE, int D, int NT, bool CLOSER>
 __global__ void __launch_bounds__(128, (StreamCfg<MODE, D, NT>::CTAS)) decode_stream_kernel(AttnParams P, DecodeWs ws) {
   using C = DecCfg<MODE, D>;
   using SC = StreamCfg<MODE, D, NT>;
@@ -992,7 +1005,16 @@ __global__ void __launch_bounds__(128, (StreamCfg<MODE, D, NT>::CTAS)) decode_st
           const uint32_t a[4] = {vpair<MODE, mt>(vl[0][0], vl[0][1]), vpair<MODE, mt>(vh[0][0], vh[0][1]),
                                  vpair<MODE, mt>(vl[1][0], vl[1][1]), vpair<MODE, mt>(vh[1][0], vh[1][1])};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(oacc[nt][mt], a, bw[nt][0], bw[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (CLOSER) {
+              float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma_16816(o, a, bw[nt][0], bw[nt][1]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) oacc[nt][mt][r] += o[r];
+            } else {
+              mma_16816(oacc[nt][mt], a, bw[nt][0], bw[nt][1]);
+            }
+          }
         });
       }
   }
@@ -1041,19 +1063,21 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 //    and four 8-byte loads per lane, bank-conflict free.
 
 //
-// EXACT (the calls with rope and cross attention, over 2-bit and 8-bit rows): the
-// same with what made the fp32 outputs lose bits put right, which moves the
-// results by less than 4e-5 of them, so that the calls that had the other form
-// keep it.
-//  * P.V of 16 keys goes to fresh sums that are then added in fp32: the
-//    accumulators truncate, and over a slice of some fifty tiles that was 3e-5
-//    of an output where the values' mean is not zero (2-bit rows, 16384 keys).
-//  * 8-bit rows: the weights p s are multiplied by a power of two that takes the
-//    largest s so far to 2^11, since s of unit-sized rows is below 2^-5 and
-//    p s fell among the fp16 subnormals (2e-5 to 4e-5 of an output).
-//  * 2-bit keys: the fold's smaller constants (1e-5 of an output).
+// FORM 0: the calls that had this kernel first keep their results.  The calls with
+// rope and cross attention take
+//  * for queries on fold_on_grid's grid the constants' part of the high terms off
+//    their own sum, which is exact, and a row's middle (its value of code 2^(b-1))
+//    in one product, since its two parts cancel.
+//  * 8-bit rows: the weights p s times a power of two that takes the largest s so
+//    far to 2^11, since s of unit-sized rows is below 2^-5 and p s fell among the
+//    fp16 subnormals (2e-5 to 4e-5 of an output).
+// FORM 2: and products of 16 keys start from zero and join the running sums in fp32,
+// since the accumulators truncate: over a slice of some fifty tiles that was 3e-5
+// of an output where the values' mean is not zero (2-bit rows, 16384 keys).
+// FORM 1, a step over 4-bit rows: without FORM 2's sums, so that the results are those
+// of FORM 0 to the bit where that is as close.
 
-template <int MODE, int D, int NT, bool STEGO, bool EXACT>
+template <int MODE, int D, int NT, bool STEGO, int FORM>
 __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE, D, NT>::CTAS))
     decode_tma_kernel(const __grid_constant__ AttnParams P, DecodeWs ws) {
   using C = DecCfg<MODE, D>;
@@ -1215,7 +1239,9 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
   float bet[NT], gam[NT], kap[NT];
   float oacc[NT][C::MT][4];
   float mrun[NT], lrun[NT], pmrun[NT];
-  constexpr bool SCALED = EXACT && TC::BYTES;
+  constexpr bool NEWER = FORM > 0, CLOSER = FORM == 2;
+  [[maybe_unused]] float fhi[NT], gmid[NT];     // NEWER: the constants' part of the high terms' sums; gamma of the rows' middles
+  constexpr bool SCALED = NEWER && TC::BYTES;
   float vmul = 1.0f;  // SCALED: the value scales' factor, a power of two
   int part_id = 0;
 
@@ -1241,6 +1267,15 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
       bet[nt] = bg.x;
       gam[nt] = TC::BYTES ? 0.0f : bg.y;
       kap[nt] = TC::BYTES ? 0.0f : fmaf(-bg.x, bg.z, HR * bg.y);  // 2^(b-1) gamma - beta fold
+      if constexpr (NEWER) {
+        fhi[nt] = bg.w;
+        gmid[nt] = 0.0f;
+        if (!TC::BYTES && (CLOSER || bg.w != 0.0f)) {  // on the grid
+          kap[nt] = -bg.x * bg.z;
+          gmid[nt] = gam[nt];
+          gam[nt] = 0.0f;
+        }
+      }
       mrun[nt] = -CUDART_INF_F;
       lrun[nt] = 0.0f;
       pmrun[nt] = 0.0f;
@@ -1322,11 +1357,6 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
               av[1] = kpair_int4_fold<2 * sig>(kw[h2][m][1]);
               av[2] = kpair_int4_fold<2 * sig + 1>(kw[h2][m][0]);
               av[3] = kpair_int4_fold<2 * sig + 1>(kw[h2][m][1]);
-            } else if constexpr (MODE == MODE_INT2 && EXACT) {
-              av[0] = kpair_int2_fold_exact<2 * sig>(kw[h2][m][0]);
-              av[1] = kpair_int2_fold_exact<2 * sig>(kw[h2][m][1]);
-              av[2] = kpair_int2_fold_exact<2 * sig + 1>(kw[h2][m][0]);
-              av[3] = kpair_int2_fold_exact<2 * sig + 1>(kw[h2][m][1]);
             } else if constexpr (MODE == MODE_INT2) {
               av[0] = kpair_int2_fold<2 * sig>(kw[h2][m][0]);
               av[1] = kpair_int2_fold<2 * sig>(kw[h2][m][1]);
@@ -1386,17 +1416,23 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
             sv_[h2][m][hh] = fv.x;
             zv_[h2][m][hh] = fmaf(HR, fv.x, fv.y);
           }
+          [[maybe_unused]] const float mid = STEGO ? sk * (HR - zst) : fmaf(HR, sk, mk);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float cdot = sacc[h2][m][nt][2 * hh] + sacc[h2][m][nt][2 * hh + 1];  // hi + lo slots
+            float shi = sacc[h2][m][nt][2 * hh];
+            if constexpr (NEWER && !TC::BYTES) shi -= fhi[nt];
+            const float cdot = shi + sacc[h2][m][nt][2 * hh + 1];  // hi + lo slots
             float zz;
             if constexpr (TC::BYTES) {
               zz = sk * (bet[nt] * cdot);
+            } else if constexpr (CLOSER) {
+              zz = fmaf(gmid[nt], mid, sk * fmaf(bet[nt], cdot, kap[nt]));
             } else if constexpr (STEGO) {
               zz = sk * fmaf(-gam[nt], zst, fmaf(bet[nt], cdot, kap[nt]));
             } else {
               zz = fmaf(sk, fmaf(bet[nt], cdot, kap[nt]), gam[nt] * mk);
             }
+            if constexpr (FORM == 1) zz = fmaf(gmid[nt], mid, zz);
             lg[h2][m][hh][nt] = FULL ? zz : (ok ? zz : -CUDART_INF_F);
           }
         }
@@ -1553,7 +1589,7 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
                                   vpair<MODE, mt>(vl[1][0], vl[1][1]), vpair<MODE, mt>(vh[1][0], vh[1][1])};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (EXACT) {
+            if constexpr (CLOSER) {
               float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
               mma_16816(o, av, bw[h2][mp][nt][0], bw[h2][mp][nt][1]);
 #pragma unroll
@@ -1675,7 +1711,7 @@ DecodeShape decode_shape(int mode, int head_dim, int group) {
   return group > 4 ? decode_shape_dnt<128, 2>(mode) : decode_shape_dnt<128, 1>(mode);
 }
 
-template <int MODE, int D, int NT, bool STEGO, bool EXACT = false>
+template <int MODE, int D, int NT, bool STEGO, int FORM>
 cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
   constexpr bool TMA = MODE != MODE_INT8;
   using TC = TmaCfg<MODE, D, NT>;
@@ -1689,10 +1725,10 @@ cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, c
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     if constexpr (TMA)
-      e = cudaFuncSetAttribute(decode_tma_kernel<MODE, D, NT, STEGO, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(decode_tma_kernel<MODE, D, NT, STEGO, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)smem);
     else
-      e = cudaFuncSetAttribute(decode_stream_kernel<MODE, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(decode_stream_kernel<MODE, D, NT, FORM == 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
@@ -1708,30 +1744,39 @@ cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, c
   // the stream and merge kernels launch programmatically: their CTAs become
   // resident while the previous kernel drains and wait on its completion
   if constexpr (TMA)
-    e = launch_dependent(decode_tma_kernel<MODE, D, NT, STEGO, EXACT>, dim3(grid), dim3(TC::WARPS * 32), smem, stream, P,
+    e = launch_dependent(decode_tma_kernel<MODE, D, NT, STEGO, FORM>, dim3(grid), dim3(TC::WARPS * 32), smem, stream, P,
                          ws);
   else
-    e = launch_dependent(decode_stream_kernel<MODE, D, NT>, dim3(grid), dim3(128), smem, stream, P, ws);
+    e = launch_dependent(decode_stream_kernel<MODE, D, NT, FORM == 2>, dim3(grid), dim3(128), smem, stream, P, ws);
   if (e != cudaSuccess) return e;
   const long long warps = (long long)BH * P.group;
   return launch_dependent(decode_reduce_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P, ws);
 }
 
+template <int MODE, int D, int NT, bool STEGO>
+cudaError_t launch_decode_form(AttnParams P, const DecodeWs& ws, int grid, cudaStream_t stream) {
+  if constexpr (MODE == MODE_INT4) {
+    if (P.exact && P.q_group == 0) {
+      P.exact = 1;
+      return launch_decode_t<MODE, D, NT, STEGO, 1>(P, ws, grid, stream);
+    }
+  }
+  if (P.exact) {
+    P.exact = 2;
+    return launch_decode_t<MODE, D, NT, STEGO, 2>(P, ws, grid, stream);
+  }
+  return launch_decode_t<MODE, D, NT, STEGO, 0>(P, ws, grid, stream);
+}
+
 template <int MODE, int D>
 cudaError_t launch_decode_md(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {
   if constexpr (MODE == MODE_INT4) {
-    if (P.stego) {
-      if (P.group <= 4) return launch_decode_t<MODE, D, 1, true>(P, ws, grid, stream);
-      return launch_decode_t<MODE, D, 2, true>(P, ws, grid, stream);
-    }
+    if (P.stego)
+      return P.group <= 4 ? launch_decode_form<MODE, D, 1, true>(P, ws, grid, stream)
+                          : launch_decode_form<MODE, D, 2, true>(P, ws, grid, stream);
   }
-  if constexpr (MODE == MODE_INT2 || byte_token_head(MODE)) {
-    if (P.exact)
-      return P.group <= 4 ? launch_decode_t<MODE, D, 1, false, true>(P, ws, grid, stream)
-                          : launch_decode_t<MODE, D, 2, false, true>(P, ws, grid, stream);
-  }
-  if (P.group <= 4) return launch_decode_t<MODE, D, 1, false>(P, ws, grid, stream);
-  return launch_decode_t<MODE, D, 2, false>(P, ws, grid, stream);
+  return P.group <= 4 ? launch_decode_form<MODE, D, 1, false>(P, ws, grid, stream)
+                      : launch_decode_form<MODE, D, 2, false>(P, ws, grid, stream);
 }
 
 cudaError_t launch_decode(const AttnParams& P, const DecodeWs& ws, int grid, cudaStream_t stream) {

@@ -98,7 +98,7 @@ struct AttnParams {
   // parts, with `part` (splits > 1) their records, as split_record lays them out.
   int q_group, cross, splits;
   float* part;
-  int exact;  // decode kernels: the closer sums of decode_tma_kernel's EXACT form
+  int exact;  // decode kernels: not 0 for the calls with rope and cross attention (decode_tma_kernel's FORM)
   // cross attention over bf16 rows with bf16 queries: q_map views them as
   // [total_q][num_q_heads][D] in boxes of one 64-dim half of `group` heads of as
   // many queries as a row tile holds (q_tma 0: the kernel loads them itself)
