@@ -196,9 +196,15 @@ __device__ __forceinline__ void kpair_dims(int w, int P, int& d0, int& d1) {
   else { d0 = 4 * w + 2 * P; d1 = d0 + 1; }
 }
 
+// magic_minus whose high half is one less.
+__host__ __device__ constexpr uint32_t magic_minus_alt(uint32_t magic_half, int pos, int bias) {
+  return magic_minus(magic_half, pos, bias) - (1u << (16 + pos));
+}
+
 // Code C of the lane ranges of two keys (A: key e=0, B: key e=1) as an exact
-// fp16 pair of signed codes (A's code in the low half).
-template <int MODE, int C>
+// fp16 pair of signed codes (A's code in the low half).  ALT: B's code is
+// u - 2^(b-1) + 1, so that the means of even and odd keys, -1/2 and 1/2, cancel.
+template <int MODE, int C, bool ALT = false>
 __device__ __forceinline__ uint32_t vpair(uint2 A, uint2 B) {
   if constexpr (MODE == MODE_INT4) {
     constexpr int byte = C / 2;
@@ -207,14 +213,16 @@ __device__ __forceinline__ uint32_t vpair(uint2 A, uint2 B) {
     constexpr int pos = (C & 1) ? 4 : 0;
     constexpr uint32_t mask = 0x000F000Fu << pos;
     constexpr uint32_t magic = (C & 1) ? 0x54005400u : 0x64006400u;
-    return hsub2_bits(lop3_and_or(x, mask, magic), magic_minus(magic & 0xFFFF, pos, 8));
+    return hsub2_bits(lop3_and_or(x, mask, magic), ALT ? magic_minus_alt(magic & 0xFFFF, pos, 8)
+                                                       : magic_minus(magic & 0xFFFF, pos, 8));
   } else if constexpr (MODE == MODE_INT2) {
     constexpr int byte = C / 4, q = C % 4;
     constexpr uint32_t sel = byte | (byte << 4) | ((4 + byte) << 8) | ((4 + byte) << 12);
     const uint32_t x = prmt(A.x, B.x, sel);
     constexpr uint32_t mask = 0x00030003u << (2 * q);
     constexpr uint32_t magic = q == 0 ? 0x64006400u : q == 1 ? 0x5C005C00u : q == 2 ? 0x54005400u : 0x4C004C00u;
-    return hsub2_bits(lop3_and_or(x, mask, magic), magic_minus(magic & 0xFFFF, 2 * q, 2));
+    return hsub2_bits(lop3_and_or(x, mask, magic), ALT ? magic_minus_alt(magic & 0xFFFF, 2 * q, 2)
+                                                       : magic_minus(magic & 0xFFFF, 2 * q, 2));
   } else if constexpr (MODE == MODE_F8T) {
     constexpr int b = C & 3;
     return e4m3x2_to_half2_bits((C < 4) ? prmt(A.x, B.x, b | ((4 + b) << 4)) : prmt(A.y, B.y, b | ((4 + b) << 4)));
@@ -370,7 +378,7 @@ __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int
 // the constants times sum(q''), D times one element of the query before its
 // transform, and what they lose at that size: 1.2e-5 (4-bit rows) and 3e-5 (2-bit)
 // of an output where the query lies in that element alone; on the grid 2e-6.
-// A step over 4-bit rows (exact 1) keeps the older calls' terms, so
+// A step over 4-bit rows in short slices (exact 1) keeps the older calls' terms, so
 // that it is to the bit what turned rows give there, unless that element is four
 // times the others' root mean square: up to there the sums lose 2e-6 of an output
 // at most, of logits below 12.
@@ -1073,9 +1081,13 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 //    fp16 subnormals (2e-5 to 4e-5 of an output).
 // FORM 2: and products of 16 keys start from zero and join the running sums in fp32,
 // since the accumulators truncate: over a slice of some fifty tiles that was 3e-5
-// of an output where the values' mean is not zero (2-bit rows, 16384 keys).
-// FORM 1, a step over 4-bit rows: without FORM 2's sums, so that the results are those
-// of FORM 0 to the bit where that is as close.
+// of an output where the values' mean is not zero (2-bit rows, 16384 keys), and
+// over twenty 7e-6 (4-bit rows).  Codes of odd keys are counted from 2^(b-1) - 1, of
+// even ones from 2^(b-1): from one value alone the codes' mean is half a code, and
+// its sum, which the zero points' then cancels, came to 79 times the output's own
+// over 30011 keys of 2-bit rows in one slice, 1.1e-5 of it in fp32's roundings.
+// FORM 1, a step over 4-bit rows in slices of at most 15 tiles: without FORM 2's sums,
+// so that the results are those of FORM 0 to the bit where that is as close.
 
 template <int MODE, int D, int NT, bool STEGO, int FORM>
 __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE, D, NT>::CTAS))
@@ -1407,14 +1419,14 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
             zst = (float)(int)(pk & 15u);
             const float s_v = __uint_as_float(pv & ~15u);
             sv_[h2][m][hh] = s_v;
-            zv_[h2][m][hh] = s_v * (float)(8 - (int)(pv & 15u));
+            zv_[h2][m][hh] = s_v * (float)((CLOSER ? 8 - hh : 8) - (int)(pv & 15u));
           } else {
             const float2 fk = __half22float2(*reinterpret_cast<const __half2*>(&pk));
             const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&pv));
             sk = fk.x;
             mk = fk.y;
             sv_[h2][m][hh] = fv.x;
-            zv_[h2][m][hh] = fmaf(HR, fv.x, fv.y);
+            zv_[h2][m][hh] = fmaf(CLOSER ? HR - hh : HR, fv.x, fv.y);
           }
           [[maybe_unused]] const float mid = STEGO ? sk * (HR - zst) : fmaf(HR, sk, mk);
 #pragma unroll
@@ -1585,8 +1597,8 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
         }
         Unroll<C::MT, MODE>::run([&](auto mt_c) {
           constexpr int mt = decltype(mt_c)::value;
-          const uint32_t av[4] = {vpair<MODE, mt>(vl[0][0], vl[0][1]), vpair<MODE, mt>(vh[0][0], vh[0][1]),
-                                  vpair<MODE, mt>(vl[1][0], vl[1][1]), vpair<MODE, mt>(vh[1][0], vh[1][1])};
+          const uint32_t av[4] = {vpair<MODE, mt, CLOSER>(vl[0][0], vl[0][1]), vpair<MODE, mt, CLOSER>(vh[0][0], vh[0][1]),
+                                  vpair<MODE, mt, CLOSER>(vl[1][0], vl[1][1]), vpair<MODE, mt, CLOSER>(vh[1][0], vh[1][1])};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if constexpr (CLOSER) {
@@ -1753,10 +1765,19 @@ cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, c
   return launch_dependent(decode_reduce_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P, ws);
 }
 
+// Whether no warp of a call has more than 15 tiles, by the width of its table.
+template <int MODE, int D, int NT>
+bool short_slices(const AttnParams& P, const DecodeWs& ws, int grid) {
+  using TC = TmaCfg<MODE, D, NT>;
+  const long long tiles = ((long long)P.max_blocks * P.block_size + TC::KT - 1) / TC::KT * P.batch * P.num_kv_heads;
+  const long long warps = ws.fixed_workers > 0 ? std::min(ws.fixed_workers, grid * TC::WARPS) : grid * TC::WARPS;
+  return tiles <= DECODE_MIN_TILES_PER_WARP * warps;
+}
+
 template <int MODE, int D, int NT, bool STEGO>
 cudaError_t launch_decode_form(AttnParams P, const DecodeWs& ws, int grid, cudaStream_t stream) {
   if constexpr (MODE == MODE_INT4) {
-    if (P.exact && P.q_group == 0) {
+    if (P.exact && P.q_group == 0 && short_slices<MODE, D, NT>(P, ws, grid)) {
       P.exact = 1;
       return launch_decode_t<MODE, D, NT, STEGO, 1>(P, ws, grid, stream);
     }
