@@ -222,9 +222,10 @@ kvq_status kvq_write(const kvq_cache* cache, const kvq_paging* paging,
 /* Rotary positions.  Pair i of a row at position p turns by the angle p f_i:
  * (a, b) becomes scale * (a cos - b sin, b cos + a sin).  The pairs are dims
  * (i, i + rot_dim / 2), or (2i, 2i + 1) where interleaved; dims from rot_dim on
- * stay as they are.  Angles are counted in 64-bit fixed point (exact to 2^-33
- * of a turn at any 32-bit position, beside inv_freq's own rounding), the rest
- * in fp32; rows are rounded once, where they are stored.
+ * stay as they are.  Angles are counted in 64-bit fixed point (exact to 2^-31
+ * of a turn at any 32-bit position for |inv_freq| below 2, and to 2^-24 below 2^16,
+ * beside inv_freq's own rounding), the rest in fp32; rows are rounded once, where
+ * they are stored.
  * inv_freq : fp32 [rot_dim / 2] (device): f_i, radians per position, below 2^16 in size.
  * rot_dim  : a multiple of 16, up to head_dim.
  * scale    : on cosine and sine; 1 unless a scaled context asks for another.

@@ -9,8 +9,9 @@
 // positions, and fp64 runs at a small fraction of fp32's rate here.  So angles
 // are counted in fixed point: u = f / (2 pi) turns as a 64-bit fraction, whole
 // turns dropped; p u modulo 2^64 is the angle's fraction of a turn, exact but
-// for p times u's own rounding (2^-64: below 2^-33 of a turn for any 32-bit
-// p).  Its top 32 bits give the quadrant and what is left of it, at most an
+// for p times u's own rounding (2^-64 for f below 2: below 2^-33 of a turn for
+// any 32-bit p; 248 times that for the largest f, 2^16).  Its top 32 bits (cut at
+// 2^-32 of a turn) give the quadrant and what is left of it, at most an
 // eighth of a turn either way, where the Taylor series of sine (to y^9, the
 // next term below 2e-9) and cosine (to y^10, below 2e-10) are as exact as
 // fp32.
@@ -29,8 +30,9 @@ struct RopeArgs {
 };
 
 // f radians as a 64-bit fraction of a turn.  f = m 2^e with a 24-bit m, and
-// 2^66 / (2 pi) as an integer (rounded): m times it is off by 2^23 at most,
-// which the shift by 2 - e >= 2 + 22 (f < 2) takes below one unit.
+// 2^66 / (2 pi) as an integer (0.0151 above it): m times it is off by 2^24 *
+// 0.0151 at most, which the shift by 2 - e (25 or more for f < 2) takes below one
+// unit and that of the largest f, 2^16, to 247.
 __device__ __forceinline__ uint64_t rope_turns(float f) {
   constexpr uint64_t C = 0xA2F9836E4E44152AULL;  // 2^66 / (2 pi) = 2^65 / pi
   const uint32_t bits = __float_as_uint(f);
