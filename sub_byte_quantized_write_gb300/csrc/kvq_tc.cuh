@@ -94,40 +94,15 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// D[tmem] (+)= A[smem] . B[smem]^T, issued by one thread.
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] . B[smem]^T, issued by one thread: A is M rows in TMEM
-// lanes 0 .. M-1, each k-step of 16 fp16 elements in 8 consecutive 32-bit
-// columns from `a_tmem` (element 2j in the low half of column j).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on `bar` once all previously issued tcgen05 operations of this thread complete.
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
-}
-
 // One lane of the warp, the same one each time; every lane calls these.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t is;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
   return is;
 }
-// The MMAs and commits above issued by the lane whose `on` is set: the
-// warp's control flow stays uniform, and descriptors in uniform registers.
+// MMAs and commits issued by the lane whose `on` is set: the warp's control flow
+// stays uniform, and descriptors in uniform registers.
+// D[tmem] (+)= A[smem] . B[smem]^T.
 __device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
@@ -135,6 +110,9 @@ __device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, u
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
 }
+// D[tmem] (+)= A[tmem] . B[smem]^T: A is M rows in TMEM lanes 0 .. M-1, each k-step
+// of 16 elements in 8 consecutive 32-bit columns from `a` (element 2j in the low
+// half of column j).
 __device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
@@ -142,6 +120,7 @@ __device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, u
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
 }
+// Arrive on `bar` once all tcgen05 operations issued before by this lane complete.
 __device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
