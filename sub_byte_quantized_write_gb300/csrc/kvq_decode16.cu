@@ -147,9 +147,11 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
   const int G = P.group, Hkv = P.num_kv_heads, bs = P.block_size, BH = P.batch * Hkv;
   const int bs_log2 = __ffs(bs) - 1;
   // The kernel before may still run (programmatic launch).  The write of the
-  // same call touches neither queries, tables and lengths nor the workspace,
-  // so only the pages wait for it; another may be writing the former or
-  // reading memory that has since become the latter.
+  // same call touches neither tables and lengths nor the workspace's records, so
+  // only the pages wait for it, and with rope the queries, which it then writes
+  // turned into the workspace (P.q): neither is read, and nothing is written
+  // there, before the second wait below.  Another kernel may be writing the former
+  // or reading memory that has since become the latter.
   if (P.new_k == nullptr) grid_dependency_wait();
   int lo, hi, gw = 0, items = 1, nruns = 1;
   if constexpr (DIRECT) {
@@ -325,7 +327,8 @@ __global__ void __launch_bounds__(d16_warps(D) * 32, 1) decode16_kernel(const At
   };
 
   Chunk cur = look_up(lane), nxt = look_up(32 + lane);
-  grid_dependency_wait();  // the pages: the write of this step's tokens may still run
+  // the pages, and with rope the queries that begin_pair reads: the write of this step's tokens may still run
+  grid_dependency_wait();
   int row = __shfl_sync(0xffffffffu, cur.row, 0);
   load_k(row);
   load_v(row);
