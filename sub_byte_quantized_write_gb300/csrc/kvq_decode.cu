@@ -1076,9 +1076,12 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 //  * for queries on fold_on_grid's grid the constants' part of the high terms off
 //    their own sum, which is exact, and a row's middle (its value of code 2^(b-1))
 //    in one product, since its two parts cancel.
-//  * 8-bit rows: the weights p s times a power of two that takes the largest s so
-//    far to 2^11, since s of unit-sized rows is below 2^-5 and p s fell among the
-//    fp16 subnormals (2e-5 to 4e-5 of an output).
+//  * scales in fp32: the weights p s times a power of two for each head, which
+//    follows the largest of them so far and keeps it at 2^4 .. 2^12: fp16 holds
+//    nothing below 2^-24, and s of unit-sized 8-bit rows is below 2^-5 (2e-5 to
+//    4e-5 of an output).  It goes by p s and not by s: a row of large values that
+//    no query looks at does not push the others' weights down.  (By s alone 64
+//    sources with 2 queries each took 141 us in place of 149.)
 // FORM 2: and products of 16 keys start from zero and join the running sums in fp32,
 // since the accumulators truncate: over a slice of some fifty tiles that was 3e-5
 // of an output where the values' mean is not zero (2-bit rows, 16384 keys), and
@@ -1087,7 +1090,8 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 // its sum, which the zero points' then cancels, came to 79 times the output's own
 // over 30011 keys of 2-bit rows in one slice, 1.1e-5 of it in fp32's roundings.
 // FORM 1, a step over 4-bit rows in slices of at most 15 tiles: without FORM 2's sums,
-// so that the results are those of FORM 0 to the bit where that is as close.
+// and with the weights' factor 1 while the largest is 2^-2 .. 2^12, so that the
+// results are those of FORM 0 to the bit where that is as close.
 
 template <int MODE, int D, int NT, bool STEGO, int FORM>
 __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE, D, NT>::CTAS))
@@ -1253,12 +1257,11 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
   float mrun[NT], lrun[NT], pmrun[NT];
   constexpr bool NEWER = FORM > 0, CLOSER = FORM == 2;
   [[maybe_unused]] float fhi[NT], gmid[NT];     // NEWER: the constants' part of the high terms' sums; gamma of the rows' middles
-  constexpr bool SCALED = NEWER && TC::BYTES;
-  float vmul = 1.0f;  // SCALED: the value scales' factor, a power of two
+  constexpr bool SCALED = NEWER && (TC::BYTES || STEGO);
+  [[maybe_unused]] float vmul[NT], wtop[NT];    // SCALED: the weights' factor, a power of two, and this lane's largest
   int part_id = 0;
 
   auto begin_seg = [&]() {
-    if constexpr (SCALED) vmul = 0x1p120f;  // above any scale's: the first one sets it
     part_id = gw + cs.bh;  // partial record id: slice index + pair index (unique, see reduce)
     const int qbh = KVQ_IN_BOUNDS(cs.bh >= 0 && cs.bh < BH, P.dev_error) ? cs.bh : 0;
     const uint4* src = reinterpret_cast<const uint4*>(ws.qfrag + ((size_t)qbh * 32 + lane) * PER_LANE);
@@ -1288,6 +1291,10 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
           gam[nt] = 0.0f;
         }
       }
+      if constexpr (SCALED) {
+        vmul[nt] = 1.0f;
+        wtop[nt] = 0.0f;
+      }
       mrun[nt] = -CUDART_INF_F;
       lrun[nt] = 0.0f;
       pmrun[nt] = 0.0f;
@@ -1312,9 +1319,10 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
         float* po = ws.part_o + ((size_t)part_id * G + head) * D;
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt) {
-          if constexpr (SCALED) {  // (no zero points: pm is 0)
-            po[gq * (D / 16) + mt] = (oacc[nt][mt][0] + oacc[nt][mt][1]) * (1.0f / vmul);
-            po[(8 + gq) * (D / 16) + mt] = (oacc[nt][mt][2] + oacc[nt][mt][3]) * (1.0f / vmul);
+          if constexpr (SCALED) {
+            const float unmul = 1.0f / vmul[nt];  // (a power of two)
+            po[gq * (D / 16) + mt] = fmaf(oacc[nt][mt][0] + oacc[nt][mt][1], unmul, pm);
+            po[(8 + gq) * (D / 16) + mt] = fmaf(oacc[nt][mt][2] + oacc[nt][mt][3], unmul, pm);
           } else {
             po[gq * (D / 16) + mt] = oacc[nt][mt][0] + oacc[nt][mt][1] + pm;
             po[(8 + gq) * (D / 16) + mt] = oacc[nt][mt][2] + oacc[nt][mt][3] + pm;
@@ -1449,35 +1457,6 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
           }
         }
 
-    if constexpr (SCALED) {
-      float most = 0.0f;  // (a masked row's scale may be any bits)
-#pragma unroll
-      for (int h2 = 0; h2 < NH2; ++h2)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) most = fmaxf(most, FULL || vk[h2][m][hh] ? sv_[h2][m][hh] : 0.0f);
-      if (__any_sync(0xffffffffu, most * vmul > 4096.0f)) {
-        most = warp_max(most);
-        const int ex = (int)(__float_as_uint(most) >> 23) - 127;  // (most >= 2^-108)
-        const float to = __uint_as_float((uint32_t)(127 + max(11 - ex, -116)) << 23);
-        const float f = to / vmul;
-        vmul = to;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) oacc[nt][mt][r] *= f;
-      }
-#pragma unroll
-      for (int h2 = 0; h2 < NH2; ++h2)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) sv_[h2][m][hh] *= vmul;
-    }
-
     uint32_t xh[NH2][NT][2], xl[NH2][NT][2];  // packed (P s) hi / lo per (h2, m): (key hh=0, key hh=1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -1495,35 +1474,70 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
       if (__any_sync(0xffffffffu, f != 1.0f)) {
         lrun[nt] *= f;
         pmrun[nt] *= f;
+        if constexpr (SCALED) wtop[nt] *= f;
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 4; ++r) oacc[nt][mt][r] *= f;
       }
       float tl = 0.0f, tpm = 0.0f;  // tile-local sums, added once per tile
+      float wv[NH2][2][2];
 #pragma unroll
       for (int h2 = 0; h2 < NH2; ++h2)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float wv[2];
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const float p = ex2(lg[h2][m][hh][nt] - muse);
             if constexpr (FULL) {
               tl += p;
               if constexpr (!TC::BYTES) tpm = fmaf(p, zv_[h2][m][hh], tpm);
-              wv[hh] = p * sv_[h2][m][hh];
+              wv[h2][m][hh] = p * sv_[h2][m][hh];
             } else {
               // select after the product: a masked row's scale may be any bits
               const bool ok = vk[h2][m][hh];
               tl += ok ? p : 0.0f;
               if constexpr (!TC::BYTES) tpm += ok ? p * zv_[h2][m][hh] : 0.0f;
-              wv[hh] = ok ? p * sv_[h2][m][hh] : 0.0f;
+              wv[h2][m][hh] = ok ? p * sv_[h2][m][hh] : 0.0f;
             }
           }
-          const __half2 hp = __floats2half2_rn(wv[0], wv[1]);
+      if constexpr (SCALED) {
+        constexpr float LOW = CLOSER ? 16.0f : 0.25f, HIGH = 4096.0f;
+#pragma unroll
+        for (int h2 = 0; h2 < NH2; ++h2)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) wtop[nt] = fmaxf(wtop[nt], fmaxf(wv[h2][m][0], wv[h2][m][1]));
+        const float now = wtop[nt] * vmul[nt];
+        const uint32_t below = __ballot_sync(0xffffffffu, now < LOW) >> tq;  // (a head's lanes are four apart)
+        if (__any_sync(0xffffffffu, now > HIGH || (below & 0x11111111u) == 0x11111111u)) {
+          float top = wtop[nt];
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const bool adjust = top * vmul[nt] > HIGH || (top > 0.0f && top * vmul[nt] < LOW);
+          const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+          const float to = adjust ? __uint_as_float((uint32_t)(127 + min(max(11 - ex, -116), 116)) << 23) : vmul[nt];
+          const float r = to / vmul[nt];
+          vmul[nt] = to;
+#pragma unroll
+          for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) oacc[nt][mt][i] *= r;
+        }
+#pragma unroll
+        for (int h2 = 0; h2 < NH2; ++h2)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) wv[h2][m][hh] *= vmul[nt];
+      }
+#pragma unroll
+      for (int h2 = 0; h2 < NH2; ++h2)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const __half2 hp = __floats2half2_rn(wv[h2][m][0], wv[h2][m][1]);
           const float2 hf = __half22float2(hp);
-          const __half2 lp = __floats2half2_rn(wv[0] - hf.x, wv[1] - hf.y);
+          const __half2 lp = __floats2half2_rn(wv[h2][m][0] - hf.x, wv[h2][m][1] - hf.y);
           xh[h2][nt][m] = *reinterpret_cast<const uint32_t*>(&hp);
           xl[h2][nt][m] = *reinterpret_cast<const uint32_t*>(&lp);
         }
