@@ -18,9 +18,10 @@ __device__ __forceinline__ uint32_t bf16x2_to_half2_bits(uint32_t w) {
 
 // Eight consecutive codes (head dims 8c .. 8c+7) of a raw row as four exact
 // fp16 pairs of signed codes u - 2^(b-1) (INT8: as stored; FP8: the E4M3
-// value; dense rows: the bf16 values), in dim order.
+// value; dense rows: the bf16 values), in dim order.  `one` 1: INT4 and INT2 codes
+// one larger, u - 2^(b-1) + 1.
 template <int MODE>
-__device__ __forceinline__ uint4 codes8(const uint8_t* raw_row, int c) {
+__device__ __forceinline__ uint4 codes8(const uint8_t* raw_row, int c, uint32_t one = 0) {
   uint32_t o[4];
   if constexpr (MODE == MODE_DBF16) {
     const uint4 w = *reinterpret_cast<const uint4*>(raw_row + 16 * c);
@@ -33,15 +34,15 @@ __device__ __forceinline__ uint4 codes8(const uint8_t* raw_row, int c) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t x = prmt(w, 0u, j | (4 << 4) | (j << 8) | (4 << 12));  // byte j in both halves
-      o[j] = hsub2_bits(lop3_and_or(x, 0x00F0000Fu, 0x54006400u), 0x54806408u);
+      o[j] = hsub2_bits(lop3_and_or(x, 0x00F0000Fu, 0x54006400u), 0x54806408u - one * 0x00100001u);
     }
   } else if constexpr (MODE == MODE_INT2) {
     const uint32_t w = *reinterpret_cast<const uint16_t*>(raw_row + 2 * c);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t x = prmt(w, 0u, j | (4 << 4) | (j << 8) | (4 << 12));
-      o[2 * j] = hsub2_bits(lop3_and_or(x, 0x000C0003u, 0x5C006400u), 0x5C086402u);
-      o[2 * j + 1] = hsub2_bits(lop3_and_or(x, 0x00C00030u, 0x4C005400u), 0x4C805420u);
+      o[2 * j] = hsub2_bits(lop3_and_or(x, 0x000C0003u, 0x5C006400u), 0x5C086402u - one * 0x00040001u);
+      o[2 * j + 1] = hsub2_bits(lop3_and_or(x, 0x00C00030u, 0x4C005400u), 0x4C805420u - one * 0x00400010u);
     }
   } else if constexpr (MODE == MODE_F8T) {
     const uint2 w = make_uint2(lds32(raw_row + 8 * c), lds32(raw_row + 8 * c + 4));  // rows are D + 4 bytes

@@ -35,7 +35,11 @@
 // within fp16's range; O is rescaled when either moves, which with a slack of 2^4
 // was 8% of the call.  Every CQ_FLUSH tiles O is added in fp32 to the row where
 // it will end up, since the accumulators truncate (kvq_cross16.cu): an error of
-// 7e-6 of an output at 16 tiles; 8 would halve it for 8% of the time.
+// 7e-6 of an output at 16 tiles; 8 would halve it for 8% of the time.  For the same
+// reason value codes of odd keys are counted from 2^(b-1) - 1 and of even ones from
+// 2^(b-1): from 2^(b-1) alone their mean is half a code, whose sum, which the zero
+// points' then cancels, was many times the output's own and what it lost 1.2e-4
+// (2-bit) and 1.6e-5 (4-bit) of an output over 8192 keys.
 // (Added by the last group, beside the next tile's softmax: 746 us for 713.)
 // Measured: 16 prompts of 101 .. 700 queries over 500 .. 4000 keys (4-bit, 32 q
 // and 8 kv heads of 128): 713 us (the prefill kernel's form of it: 1024), 35% of
@@ -363,6 +367,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
             float ks, kz, vz;  // (a pad of zeros: both are 0)
             pad_scale_zero<MODE>(pads[0][i], P.stego != 0, ks, kz);
             pad_scale_zero<MODE>(pads[1][i], P.stego != 0, vs[i], vz);
+            if (ZEROS && (lane & 1)) vz -= vs[i];  // (odd keys' codes are one larger)
             sc[32 * i + lane] = ks;
             sc[CQ_KT + 32 * i + lane] = kz;
             sc[3 * CQ_KT + 32 * i + lane] = vz;
@@ -393,17 +398,19 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
     constexpr int PER = D / 8, STEP = 32 * CQ_PRODUCERS / PER;  // pieces of 8 dims per row; rows per pass of the threads
     const int c8 = pt % PER, row0 = pt / PER;
     // stores of rows row0 + STEP j: the swizzle takes 8 / STEP forms
+    static_assert(STEP % 2 == 0, "a thread's rows are all even or all odd");
     constexpr int FORMS = STEP < 8 ? 8 / STEP : 1;
     int at[FORMS];
 #pragma unroll
     for (int j = 0; j < FORMS; ++j) at[j] = (c8 >> 3) * C::HALF + tc::sw128_off(row0 + STEP * j, c8 & 7) - STEP * j * 128;
     auto expand = [&](const uint8_t* raw, uint8_t* tile, bool is_v) {
       constexpr int U = 8;  // pieces in flight
+      const uint32_t one = is_v ? row0 & 1 : 0;
 #pragma unroll 1
       for (int j0 = 0; j0 < CQ_KT / STEP; j0 += U) {
         uint4 x[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) x[j] = codes8<MODE>(raw + row0 * C::R + STEP * (j0 + j) * C::R, c8);
+        for (int j = 0; j < U; ++j) x[j] = codes8<MODE>(raw + row0 * C::R + STEP * (j0 + j) * C::R, c8, one);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
           if (MODE == MODE_F8T && is_v) {  // stale NaN codes of rows without data
