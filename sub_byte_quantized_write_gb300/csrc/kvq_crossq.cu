@@ -30,9 +30,11 @@
 // dims of a row each, in registers: by a warp to a row a CTA's start and end took
 // 26 us of it.  The start and the end are fetched from L2 as instructions, some 5
 // us each: they are written for few instructions.
-// p may pass the reference by 2^CQ_SLACK, and value scales are multiplied by a
-// power of two that takes the largest so far to 2^5 .. 2^7, so that p s stays
-// within fp16's range; O is rescaled when either moves, which with a slack of 2^4
+// The reference that p is counted from follows the largest p s of the row so far
+// (the running maximum of the logit plus the scale's exponent) and keeps it at
+// 2^CQ_BASE .. 2^(CQ_BASE + CQ_SLACK), within fp16's range: a row of large values
+// does not push the weights of others that the query looks at among the
+// subnormals.  O is rescaled when the reference moves, which with a slack of 2^4
 // was 8% of the call.  Every CQ_FLUSH tiles O is added in fp32 to the row where
 // it will end up, since the accumulators truncate (kvq_cross16.cu): an error of
 // 7e-6 of an output at 16 tiles; 8 would halve it for 8% of the time.  For the same
@@ -70,7 +72,7 @@ constexpr int CQ_KT = 128, CQ_HALF = CQ_KT / 2;  // keys of a tile, and of a sof
 constexpr int CQ_THREADS = 640;
 constexpr int CQ_GROUPS = 4;  // of four softmax warps
 constexpr int CQ_MMA_WARP = 0, CQ_COPY_WARP = 1, CQ_PROD_WARP = 2, CQ_PRODUCERS = 2, CQ_SOFTMAX_WARP = 4;
-constexpr float CQ_SLACK = 8.0f;
+constexpr float CQ_BASE = 6.0f, CQ_SLACK = 8.0f;
 constexpr int CQ_FLUSH = 16;  // (even: the same softmax group does it each time)
 constexpr uint32_t CQ_NAP = 20;
 
@@ -86,16 +88,16 @@ struct CqCfg {
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + 2 * TILE;
   static constexpr int OFF_RAW = OFF_V + 2 * TILE;           // [2][K, V][RAW]
-  static constexpr int OFF_SC = OFF_RAW + 4 * RAW;           // [4, of tile v & 3][ks, kz, vs, vz][128] f32
+  static constexpr int OFF_SC = OFF_RAW + 4 * RAW;           // [4, of tile v & 3][ks, kz, vs, vz, exponent of vs][128] f32
   // at the start [4 groups][128] sum, largest; at the end [4 groups][reference, l, pz][128] and what the rows hold
-  static constexpr int OFF_SUM = OFF_SC + 4 * 4 * CQ_KT * 4;
+  static constexpr int OFF_SUM = OFF_SC + 4 * 5 * CQ_KT * 4;
   static constexpr int OFF_FAC = OFF_SUM + (3 * CQ_GROUPS + 1) * CQ_ROWS * 4;  // factors of a query's and of an output's dims [D] f32
   static constexpr int OFF_M = OFF_FAC + 2 * D * 4;          // [4 groups][128] published references
   static constexpr int OFF_BAR = OFF_M + CQ_GROUPS * CQ_ROWS * 4;
   static constexpr int NBAR = 48;
   static constexpr int PIECES = D / 32;  // of a row at the start and at the end: 32 dims, one thread
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;        // TMEM address, abort, sequence, [8] factors, [8] masks
-  static constexpr int SMEM = OFF_MISC + 80 + 1024;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;        // TMEM address, abort, sequence, [8] masks
+  static constexpr int SMEM = OFF_MISC + 48 + 1024;
   // TMEM columns: S of tiles v & 1 (P over it: high terms, then low terms), O, Q high, Q low
   static constexpr int TM_O = 2 * CQ_KT, TM_QHI = TM_O + D, TM_QLO = TM_QHI + D / 2;
   static_assert(CQ_ROWS * D * 4 <= 4 * TILE, "the rows fit the K / V stages");
@@ -148,8 +150,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   int* seq_slot = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
-  volatile float* vmuls = reinterpret_cast<volatile float*>(sm + C::OFF_MISC + 16);  // [8], of tile v & 7
-  volatile int* mask = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 48);     // [8], of tile v & 7
+  volatile int* mask = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 16);  // [8], of tile v & 7
   if (warp == CQ_COPY_WARP) {
     const int b0 = heavy_first_sequence(P, blockIdx.z);
     if (lane == 0) *seq_slot = b0;
@@ -312,7 +313,6 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
       return lane < CQ_KT / 16 && v < nv && key < L ? __ldg(tbl + (key >> bs_log2)) : -1;
     };
     int entry = lookup(0), err = 0, v = 0;
-    float vmul = 0x1p100f;
 #pragma unroll 1
     for (; v < nv + 1 && ok; ++v) {
       const int st = v & 1;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
           }
           const uint8_t* rk = sm + C::OFF_RAW + su * 2 * C::RAW + C::DATA;
           const int chunks = mask[u & 7], left = L - (v0 + u) * CQ_KT;
-          float* sc = reinterpret_cast<float*>(sm + C::OFF_SC) + (u & 3) * 4 * CQ_KT;
+          float* sc = reinterpret_cast<float*>(sm + C::OFF_SC) + (u & 3) * 5 * CQ_KT;
           uint32_t pads[2][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -361,23 +361,21 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
             pads[0][i] = has ? lds32(rk + j * C::R) : 0u;
             pads[1][i] = has ? lds32(rk + C::RAW + j * C::R) : 0u;
           }
-          float vs[4], most = 0.0f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float ks, kz, vz;  // (a pad of zeros: both are 0)
+            float ks, kz, vs, vz;  // (a pad of zeros: both are 0)
             pad_scale_zero<MODE>(pads[0][i], P.stego != 0, ks, kz);
-            pad_scale_zero<MODE>(pads[1][i], P.stego != 0, vs[i], vz);
-            if (ZEROS && (lane & 1)) vz -= vs[i];  // (odd keys' codes are one larger)
+            pad_scale_zero<MODE>(pads[1][i], P.stego != 0, vs, vz);
+            if (ZEROS && (lane & 1)) vz -= vs;  // (odd keys' codes are one larger)
             sc[32 * i + lane] = ks;
             sc[CQ_KT + 32 * i + lane] = kz;
+            sc[2 * CQ_KT + 32 * i + lane] = vs;
             sc[3 * CQ_KT + 32 * i + lane] = vz;
-            most = fmaxf(most, vs[i]);
+            // (not far below the zero point's, whose product with p is summed in fp32, and
+            // not below -90: p, of values however small, stays below 2^104)
+            const int es = (__float_as_uint(vs) >> 23) & 255, ez = ZEROS ? (int)((__float_as_uint(vz) >> 23) & 255) - 12 : 0;
+            sc[4 * CQ_KT + 32 * i + lane] = (float)max(max(es, ez) - 126, -90);
           }
-          most = warp_max(most);
-          if (most * vmul > 128.0f) vmul = pow2(max(5 - ((int)(__float_as_uint(most) >> 23) - 127), -100));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[2 * CQ_KT + 32 * i + lane] = vs[i] * vmul;
-          if (lane == 0) vmuls[u & 7] = vmul;
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(bar + QB_KFULL + su);
         }
@@ -518,7 +516,6 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
         break;
       }
       tc::fence_after();
-      const float vmul = SCALES ? vmuls[v & 7] : 1.0f, vmul0 = SCALES && v > 0 ? vmuls[(v - 1) & 7] : vmul;
       const bool anew = half == 0 && v % CQ_FLUSH == 0;
       if (anew && v > 0) {  // (group 0) O so far is added to the rows
         if (!wait(QB_PUB + 4 * (CQ_GROUPS - 1) + quad, (t - 1) >> 2) || !wait(QB_PVDONE + ((t - 1) & 3), (t - 1) >> 2)) {
@@ -528,7 +525,6 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
         tc::fence_after();
         m = pub[(CQ_GROUPS - 1) * CQ_ROWS + r];
         const float f = held == -CUDART_INF_F ? 0.0f : ex2(held - m);
-        const float w = 1.0f / vmul0;
         const bool more = v > CQ_FLUSH, add = more && __all_sync(0xffffffffu, f == 1.0f);
         // (a thread its own row: few instructions, and they are fetched anew each time)
 #pragma unroll 1
@@ -544,8 +540,8 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
           if (to >= 0) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float4 x = make_float4(fmaf(__uint_as_float(o[4 * j]), w, e[j].x * f), fmaf(__uint_as_float(o[4 * j + 1]), w, e[j].y * f),
-                                           fmaf(__uint_as_float(o[4 * j + 2]), w, e[j].z * f), fmaf(__uint_as_float(o[4 * j + 3]), w, e[j].w * f));
+              const float4 x = make_float4(fmaf(e[j].x, f, __uint_as_float(o[4 * j])), fmaf(e[j].y, f, __uint_as_float(o[4 * j + 1])),
+                                           fmaf(e[j].z, f, __uint_as_float(o[4 * j + 2])), fmaf(e[j].w, f, __uint_as_float(o[4 * j + 3])));
               if (add) tc::red_add4(reinterpret_cast<float*>(p + j), x);
               else __stcg(p + j, x);
             }
@@ -558,7 +554,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
       tc::ld32(s_tm, y);
       tc::ld32(s_tm + 32, y + 32);
       const int left = L - (v0 + v) * CQ_KT - half * CQ_HALF, chunks = (mask[v & 7] >> (4 * half)) & 15;
-      const float4* s4 = reinterpret_cast<const float4*>(sm + C::OFF_SC) + (v & 3) * CQ_KT + half * (CQ_HALF / 4);  // ks, kz, vs, vz: 32 apart
+      const float4* s4 = reinterpret_cast<const float4*>(sm + C::OFF_SC) + (v & 3) * (5 * CQ_KT / 4) + half * (CQ_HALF / 4);  // ks, kz, vs, vz, exponents: 32 apart
       tc::wait_ld();
       tc::regs_after_wait(y);
       float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
@@ -586,11 +582,27 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
         for (int j = 0; j < CQ_HALF; ++j)
           if (j >= left || !((chunks >> (j / 16)) & 1)) y[j] = __float_as_uint(-CUDART_INF_F);
       }
+      const uint64_t rb2 = tc::pair32(rb, rb);
+      // the largest p s, as a power of two
 #pragma unroll
-      for (int j = 0; j < CQ_HALF; j += 8)
+      for (int j = 0; j < CQ_HALF; j += 8) {
+        float t[8];
+        if constexpr (SCALES) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top[i] = fmaxf(fmaxf(top[i], __uint_as_float(y[j + i])), __uint_as_float(y[j + 4 + i]));
-      const float tmax = rb * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          for (int i = 0; i < 8; i += 4) {
+            const float4 ex = s4[128 + (j + i) / 4];
+            const float2 a = tc::unpair32(tc::fma_pair(tc::pair32(__uint_as_float(y[j + i]), __uint_as_float(y[j + i + 1])), rb2, tc::pair32(ex.x, ex.y)));
+            const float2 c = tc::unpair32(tc::fma_pair(tc::pair32(__uint_as_float(y[j + i + 2]), __uint_as_float(y[j + i + 3])), rb2, tc::pair32(ex.z, ex.w)));
+            t[i] = a.x; t[i + 1] = a.y; t[i + 2] = c.x; t[i + 3] = c.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = __uint_as_float(y[j + i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(fmaxf(top[i], t[i]), t[4 + i]);
+      }
+      const float tmax = (SCALES ? 1.0f : rb) * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) - CQ_BASE;
       if (t > 0) {  // the reference so far, from the group before
         if (!wait(QB_PUB + 4 * ((g - 1) & 3) + quad, (t - 1) >> 2)) {
           ok = false;
@@ -604,15 +616,13 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
       pub[g * CQ_ROWS + r] = m;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar + QB_PUB + 4 * g + quad);
-      // what the value scales' factor changes by with the tile (1 almost always)
-      const float turn = v > 0 && half == 0 ? vmul / vmul0 : 1.0f;
-      if (!anew && __any_sync(0xffffffffu, (grow && m0 != -CUDART_INF_F) || turn != 1.0f)) {
+      if (!anew && __any_sync(0xffffffffu, grow && m0 != -CUDART_INF_F)) {
         if (!wait(QB_PVDONE + ((t - 1) & 3), (t - 1) >> 2)) {
           ok = false;
           break;
         }
         tc::fence_after();
-        const float f = (m0 == -CUDART_INF_F ? 1.0f : ex2(m0 - m)) * turn;
+        const float f = m0 == -CUDART_INF_F ? 1.0f : ex2(m0 - m);
 #pragma unroll 1
         for (int c = 0; c < D; c += 8) {
           uint32_t o[8];
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
         pz *= f;
         mine = m;
       }
-      const uint64_t rb2 = tc::pair32(rb, rb), nref2 = tc::pair32(-ref, -ref);
+      const uint64_t nref2 = tc::pair32(-ref, -ref);
       uint64_t sum[2] = {0, 0}, zsum[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < CQ_HALF; c += 32) {
@@ -708,7 +718,6 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
         pzt = fmaf(f, sums[(3 * k + 2) * CQ_ROWS + r], pzt);
       }
       const float fh = hm == -CUDART_INF_F ? 0.0f : ex2(hm - mt);
-      const float inv_mul = SCALES && nv > 0 ? 1.0f / vmuls[(nv - 1) & 7] : 1.0f;
       const bool part = P.splits > 1, both = rht && !part;
       float x[32];
       uint8_t* row = sm + C::OFF_K + r * (D * 4);  // whole rows (K and V are done with), 16-byte pieces XOR-swizzled by row
@@ -725,10 +734,10 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
         tc::regs_after_wait(o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          x[4 * j] = fmaf(e[j].x, fh, fmaf(__uint_as_float(o[4 * j]), inv_mul, pzt));
-          x[4 * j + 1] = fmaf(e[j].y, fh, fmaf(__uint_as_float(o[4 * j + 1]), inv_mul, pzt));
-          x[4 * j + 2] = fmaf(e[j].z, fh, fmaf(__uint_as_float(o[4 * j + 2]), inv_mul, pzt));
-          x[4 * j + 3] = fmaf(e[j].w, fh, fmaf(__uint_as_float(o[4 * j + 3]), inv_mul, pzt));
+          x[4 * j] = fmaf(e[j].x, fh, __uint_as_float(o[4 * j]) + pzt);
+          x[4 * j + 1] = fmaf(e[j].y, fh, __uint_as_float(o[4 * j + 1]) + pzt);
+          x[4 * j + 2] = fmaf(e[j].z, fh, __uint_as_float(o[4 * j + 2]) + pzt);
+          x[4 * j + 3] = fmaf(e[j].w, fh, __uint_as_float(o[4 * j + 3]) + pzt);
         }
         if (both) {
 #pragma unroll

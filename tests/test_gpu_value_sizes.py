@@ -40,7 +40,7 @@ def check(mode, D, n, lens, k, v, unseen=()):
 
 @pytest.mark.parametrize("mode", ["INT8_TOKEN_HEAD", "FP8_TOKEN_HEAD", "INT4_TOKEN_HEAD", "INT4_STEGO", "INT2_TOKEN_HEAD"])
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("n", [(2, 1)])
+@pytest.mark.parametrize("n", [(2, 1), (40, 5)])
 @pytest.mark.parametrize("at", [0, 60, 300])
 def test_a_large_row_that_no_query_looks_at(mode, D, n, at):
     """Its scale is a million times the others' (fp16 scales: 2^14 times), its weight 2^-40 or less."""
@@ -54,7 +54,7 @@ def test_a_large_row_that_no_query_looks_at(mode, D, n, at):
 
 @pytest.mark.parametrize("mode,decades", [("INT8_TOKEN_HEAD", 8), ("FP8_TOKEN_HEAD", 8), ("INT4_STEGO", 8), ("INT4_TOKEN_HEAD", 4), ("INT2_TOKEN_HEAD", 4)])
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("n", [(2, 1)])
+@pytest.mark.parametrize("n", [(2, 1), (40, 5)])
 def test_values_that_shrink_along_the_sequence(mode, decades, D, n):
     """Weights grow as values shrink, so that each row's part of an output is of one size."""
     H, lens = 1, [700, 97]
