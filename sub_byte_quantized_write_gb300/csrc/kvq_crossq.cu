@@ -111,12 +111,6 @@ enum { QB_RAWKFULL = 0, QB_RAWKEMPTY = 2, QB_KFULL = 4, QB_KEMPTY = 6, QB_VFULL 
        QB_RAWVFULL = 44, QB_RAWVEMPTY = 46 };
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
-// Two fp16 values of E4M3 codes, NaNs (all ones in the exponent: no code is infinite) as zeros.
-__device__ __forceinline__ uint32_t nan_to_zero(uint32_t p) {
-  if ((p & 0x7C00u) == 0x7C00u) p &= 0xFFFF0000u;
-  if ((p & 0x7C000000u) == 0x7C000000u) p &= 0x0000FFFFu;
-  return p;
-}
 // Hadamard transform of a thread's values.
 template <int N>
 __device__ __forceinline__ void wht_regs(float (&x)[N]) {
@@ -401,9 +395,10 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
     int at[FORMS];
 #pragma unroll
     for (int j = 0; j < FORMS; ++j) at[j] = (c8 >> 3) * C::HALF + tc::sw128_off(row0 + STEP * j, c8 & 7) - STEP * j * 128;
-    auto expand = [&](const uint8_t* raw, uint8_t* tile, bool is_v) {
+    auto expand = [&](const uint8_t* raw, uint8_t* tile, bool is_v, int v) {
       constexpr int U = 8;  // pieces in flight
       const uint32_t one = is_v ? row0 & 1 : 0;
+      const int chunks = mask[v & 7], left = L - (v0 + v) * CQ_KT;
 #pragma unroll 1
       for (int j0 = 0; j0 < CQ_KT / STEP; j0 += U) {
         uint4 x[U];
@@ -411,8 +406,9 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
         for (int j = 0; j < U; ++j) x[j] = codes8<MODE>(raw + row0 * C::R + STEP * (j0 + j) * C::R, c8, one);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-          if (MODE == MODE_F8T && is_v) {  // stale NaN codes of rows without data
-            x[j] = make_uint4(nan_to_zero(x[j].x), nan_to_zero(x[j].y), nan_to_zero(x[j].z), nan_to_zero(x[j].w));
+          if (MODE == MODE_F8T && is_v) {  // rows without data may hold NaN codes, which a weight 0 does not cancel
+            const int row = row0 + STEP * (j0 + j);
+            if (row >= left || !((chunks >> (row >> 4)) & 1)) x[j] = make_uint4(0u, 0u, 0u, 0u);
           }
           *reinterpret_cast<uint4*>(tile + at[j % FORMS] + STEP * (j0 + j) * 128) = x[j];
         }
@@ -429,7 +425,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
         ok = false;
         break;
       }
-      expand(sm + C::OFF_RAW + (2 * st + (is_v ? 1 : 0)) * C::RAW, sm + (is_v ? C::OFF_V : C::OFF_K) + st * C::TILE, is_v);
+      expand(sm + C::OFF_RAW + (2 * st + (is_v ? 1 : 0)) * C::RAW, sm + (is_v ? C::OFF_V : C::OFF_K) + st * C::TILE, is_v, v);
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) {

@@ -1082,6 +1082,8 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 //    4e-5 of an output).  It goes by p s and not by s: a row of large values that
 //    no query looks at does not push the others' weights down.  (By s alone 64
 //    sources with 2 queries each took 141 us in place of 149.)
+//  * zeros for the value rows that are not there, and NaN codes of visible ones as
+//    they are (8-bit floats).
 // FORM 2: and products of 16 keys start from zero and join the running sums in fp32,
 // since the accumulators truncate: over a slice of some fifty tiles that was 3e-5
 // of an output where the values' mean is not zero (2-bit rows, 16384 keys), and
@@ -1605,6 +1607,12 @@ __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE,
           for (int hp = 0; hp < 2; ++hp)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+              if constexpr (NEWER) {
+                const int kappa = 32 * h2 + 8 * tq + 4 * mp + 2 * hp + e, j = key0 + kappa;
+                if (!((cur >> (kappa / TC::RPC)) & 1) || j >= Leff || (W > 0 && j >= P.sink && j <= p_q - W))
+                  vl[hp][e] = vh[hp][e] = make_uint2(0u, 0u);
+                continue;
+              }
               vl[hp][e] = make_uint2(e4m3x4_no_nan(vl[hp][e].x), e4m3x4_no_nan(vl[hp][e].y));
               vh[hp][e] = make_uint2(e4m3x4_no_nan(vh[hp][e].x), e4m3x4_no_nan(vh[hp][e].y));
             }
