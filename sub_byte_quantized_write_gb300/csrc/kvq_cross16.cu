@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
       const int key = (v0 + v) * CX_KT + CX_CHUNK * lane;
       return paged && lane < CX_KT / CX_CHUNK && v < nv && key < L ? __ldg(tbl + (key >> bs_log2)) : -1;
     };
-    int entry = lookup(0), err = 0;
+    int entry = lookup(0), err = 0, issued = 0;  // tiles copied
     bool ok = true;
 #pragma unroll 1
     for (int v = 0; v < nv && ok; ++v) {
@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
         mbar_arrive_expect_tx(full, C::TILE);
       }
       __syncwarp();
+      issued = v + 1;
       if (paged) {
         if (lane < CX_KT / CX_CHUNK) {
 #pragma unroll
@@ -301,6 +302,9 @@ __global__ void __launch_bounds__(CX_THREADS, 1) cross16_kernel(const __grid_con
       *abort_flag = 1;
       if (lane == 0) flag_error(P.dev_error, DEVERR_TIMEOUT);
     }
+    // the copies in flight land before the CTA ends, whoever gave up (there is nothing to wait for otherwise)
+    for (int u = max(issued - 2, 0); u < issued; ++u)
+      (void)__all_sync(0xffffffffu, mbar_wait_bounded(bar + (kv ? CB_VFULL : CB_KFULL) + (u & 1), (u >> 1) & 1, CX_NAP));
     err = __reduce_or_sync(0xffffffffu, err);
     if (err && lane == 0) flag_error(P.dev_error, err);
   } else if (warp == CX_MMA_WARP) {

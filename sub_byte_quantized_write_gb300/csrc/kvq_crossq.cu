@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
       const int key = (v0 + v) * CQ_KT + 16 * lane;
       return lane < CQ_KT / 16 && v < nv && key < L ? __ldg(tbl + (key >> bs_log2)) : -1;
     };
-    int entry = lookup(0), err = 0, v = 0;
+    int entry = lookup(0), err = 0, v = 0, issued[2] = {0, 0};  // tiles whose K, and V, was copied
 #pragma unroll 1
     for (; v < nv + 1 && ok; ++v) {
       const int st = v & 1;
@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
           mbar_arrive_expect_tx(full, (uint32_t)(__popc(found) * C::CHUNK));
         }
         __syncwarp();
+        issued[i] = v + 1;
         if (off >= 0)
           bulk_g2s(sm + C::OFF_RAW + (2 * st + i) * C::RAW + lane * C::CHUNK, (i ? P.v_pages : P.k_pages) + off, C::CHUNK, full);
         return true;
@@ -376,12 +377,9 @@ __global__ void __launch_bounds__(CQ_THREADS, 1) crossq_kernel(const __grid_cons
       }
       if (v < nv) ok = copy(1);
     }
-    if (!ok) {  // the copies in flight land before the CTA ends
-      for (int u = max(min(v, nv - 1) - 1, 0); u <= min(v, nv - 1); ++u) {
-        (void)wait(QB_RAWKFULL + (u & 1), u >> 1);
-        (void)wait(QB_RAWVFULL + (u & 1), u >> 1);
-      }
-    }
+    // the copies in flight land before the CTA ends, whoever gave up (there is nothing to wait for otherwise)
+    for (int u = max(issued[0] - 2, 0); u < issued[0]; ++u) (void)wait(QB_RAWKFULL + (u & 1), u >> 1);
+    for (int u = max(issued[1] - 2, 0); u < issued[1]; ++u) (void)wait(QB_RAWVFULL + (u & 1), u >> 1);
     err = __reduce_or_sync(0xffffffffu, err);
     if (err && lane == 0) flag_error(P.dev_error, err);
   } else if (warp >= CQ_PROD_WARP && warp < CQ_PROD_WARP + CQ_PRODUCERS) {
