@@ -378,18 +378,19 @@ __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int
 // the constants times sum(q''), D times one element of the query before its
 // transform, and what they lose at that size: 1.2e-5 (4-bit rows) and 3e-5 (2-bit)
 // of an output where the query lies in that element alone; on the grid 2e-6.
-// A step over 4-bit rows in short slices (exact 1) keeps the older calls' terms, so
-// that it is to the bit what turned rows give there, unless that element is four
-// times the others' root mean square: up to there the sums lose 2e-6 of an output
-// at most, of logits below 12.
+// A small step over 4-bit rows (exact 1) keeps the older calls' terms, so
+// that it is to the bit what turned rows give there, up to queries that give rows of
+// size 1 logits of 2 powers of two (their root mean square), 1/2 of it from that
+// element: the sums lose 2e-6 of an output there, and more in proportion.
+// `unit`: a logit, in powers of two, per unit of the transformed query.
 template <int MODE, int EPL>
-__device__ __forceinline__ bool fold_on_grid(const AttnParams& P, float sum, const float (&x)[EPL]) {
+__device__ __forceinline__ bool fold_on_grid(const AttnParams& P, float sum, float unit, float dnorm, const float (&x)[EPL]) {
   if constexpr (MODE != MODE_INT4 && MODE != MODE_INT2) return false;
   if (P.exact != 1 || MODE != MODE_INT4) return P.exact != 0;
   float ss = 0.0f;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) ss = fmaf(x[e], x[e], ss);
-  return sum * sum > 16.0f * warp_sum(ss);
+  return fabsf(unit * sum) > 0.5f || unit * unit * dnorm * warp_sum(ss) > 4.0f;
 }
 
 // The position a decode query turns to: its sequence's last token's.
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(AttnParams P, DecodeWs
     amx = warp_max(amx);
     const int ex = amx > 0.0f ? ilogbf(amx) : 0;
     const float sc = ldexpf(1.0f, 10 - ex);  // max |q''| in [1024, 2048)
-    const bool grid = fold_on_grid<MODE>(P, sum, x);
+    const bool grid = fold_on_grid<MODE>(P, sum, P.softmax_scale * log2e / dnorm, dnorm, x);
     // the folded key offset: sum over dims of the exact operand value (hi +
     // lo, or apart) times the constant the folded key unpack adds to the signed code
     float opsum = 0.0f, ophi = 0.0f;
@@ -1091,7 +1092,7 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 // even ones from 2^(b-1): from one value alone the codes' mean is half a code, and
 // its sum, which the zero points' then cancels, came to 79 times the output's own
 // over 30011 keys of 2-bit rows in one slice, 1.1e-5 of it in fp32's roundings.
-// FORM 1, a step over 4-bit rows in slices of at most 15 tiles: without FORM 2's sums,
+// FORM 1, a small step over 4-bit rows (small_call): without FORM 2's sums,
 // and with the weights' factor 1 while the largest is 2^-2 .. 2^12, so that the
 // results are those of FORM 0 to the bit where that is as close.
 
@@ -1787,19 +1788,22 @@ cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, c
   return launch_dependent(decode_reduce_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P, ws);
 }
 
-// Whether no warp of a call has more than 15 tiles, by the width of its table.
+// FORM 1's calls, by the width of the table: a few thousand keys in all, no warp with
+// more than 15 tiles.  Their time is the launches' (7 sequences of 401 keys 21 us
+// with either form); a call of 64 sequences pays 2% for FORM 2.
+constexpr int DECODE_SMALL_TILES = 512;
 template <int MODE, int D, int NT>
-bool short_slices(const AttnParams& P, const DecodeWs& ws, int grid) {
+bool small_call(const AttnParams& P, const DecodeWs& ws, int grid) {
   using TC = TmaCfg<MODE, D, NT>;
   const long long tiles = ((long long)P.max_blocks * P.block_size + TC::KT - 1) / TC::KT * P.batch * P.num_kv_heads;
   const long long warps = ws.fixed_workers > 0 ? std::min(ws.fixed_workers, grid * TC::WARPS) : grid * TC::WARPS;
-  return tiles <= DECODE_MIN_TILES_PER_WARP * warps;
+  return tiles <= DECODE_SMALL_TILES && tiles <= DECODE_MIN_TILES_PER_WARP * warps;
 }
 
 template <int MODE, int D, int NT, bool STEGO>
 cudaError_t launch_decode_form(AttnParams P, const DecodeWs& ws, int grid, cudaStream_t stream) {
   if constexpr (MODE == MODE_INT4) {
-    if (P.exact && P.q_group == 0 && short_slices<MODE, D, NT>(P, ws, grid)) {
+    if (P.exact && P.q_group == 0 && small_call<MODE, D, NT>(P, ws, grid)) {
       P.exact = 1;
       return launch_decode_t<MODE, D, NT, STEGO, 1>(P, ws, grid, stream);
     }

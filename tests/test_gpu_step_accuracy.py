@@ -52,3 +52,23 @@ def test_query_in_one_element(mode, D, G, dim):
     assert most < 16 and ref.off(out, want) < BOUND
     out = K.kvq_cross_attn(c, pag, q, cu_of([1] * B), 1, D ** -0.5)
     assert ref.off(out, want) < BOUND
+
+
+@pytest.mark.parametrize("mode", ["INT4_TOKEN_HEAD", "INT4_STEGO", "INT2_TOKEN_HEAD"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 5, 8])
+def test_query_in_eight_elements(mode, D, G):
+    """One of the eight is the element whose transform is the same in every dim.  The bound, for logits below 24: no part of
+    one is above 28 here (a row's middle adds gamma, below 1.5, times less than 3), so the three operations' errors, as root
+    mean squares and squares added, are 2^-24 28 = 1.7e-6, the query's 24 / 16 of 0.8e-6, the rest 0.3e-6: 2.1e-6."""
+    K = kvq()
+    H, lens = 2, [1500, 700, 33, 1]
+    c, pag, _, _ = filled(mode, lens, H, D)
+    B = len(lens)
+    q = rows(3, B, H * G, D)
+    q[:, :, [0, 9, 17, 30, 33, 41, 50, 58]] = 0.7 * math.sqrt(D)
+    out = K.kvq_rope_write_decode_attn(c, pag, make_rope(D), rows(4, B, H, D), rows(5, B, H, D), cu_of([1] * B), q, D ** -0.5,
+                                       positions=i32([0] * B))
+    k, v = K.kvq_gather(c, pag, cu_of(lens), sum(lens))
+    want, most = ref.attention64(q, k, v, [1] * B, lens, D ** -0.5)
+    assert most < 24 and ref.off(out, want) < BOUND
