@@ -34,10 +34,11 @@
 // rescaled, only when a logit passes it by 2^8.  The accumulators truncate, some
 // 2^-25 of O per step of 16 keys and term (1.3e-5 of an output over 8192 keys):
 // every CX_FLUSH tiles O is added in fp32 to the row where it will end up, and
-// begins anew.
+// begins anew: 4e-6 to 6e-6.  (Every 8 tiles: half of that, 6% of the time.)
 // Measured: 8 prompts of 1024 queries over 2048 .. 8192 rows (32 q and 8 kv heads
-// of 128) 750 us, 958 TFLOP/s of 4 D per pair and 1437 of the operations done; 5
-// queries over 131071 rows 62 us with the join, 4.3 TB/s.
+// of 128) 795 us in a loop of calls, 905 TFLOP/s of 4 D per pair and 1360 of the
+// operations done (750 us alone, before the power cap lowers the clock); 5 queries
+// over 131071 rows 62 us with the join, 4.3 TB/s.
 // Rows that are not there (an evicted page, past the sequence's end): chunks of
 // a page without an entry are copied from past the tensor's end, which gives
 // zeros, and masked; value rows past the end of the sequence, which may hold

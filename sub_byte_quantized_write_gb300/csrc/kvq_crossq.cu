@@ -37,18 +37,21 @@
 // subnormals.  O is rescaled when the reference moves, which with a slack of 2^4
 // was 8% of the call.  Every CQ_FLUSH tiles O is added in fp32 to the row where
 // it will end up, since the accumulators truncate (kvq_cross16.cu): an error of
-// 7e-6 of an output at 16 tiles; 8 would halve it for 8% of the time.  For the same
+// 3e-6 to 8e-6 of an output over 8192 keys at 16 tiles; 8 would halve it for 7% of
+// the time.  (Added by the last group, beside the next tile's softmax: 746 us for
+// 713, measured before the reference went by p s.)  For the same
 // reason value codes of odd keys are counted from 2^(b-1) - 1 and of even ones from
 // 2^(b-1): from 2^(b-1) alone their mean is half a code, whose sum, which the zero
 // points' then cancels, was many times the output's own and what it lost 1.2e-4
 // (2-bit) and 1.6e-5 (4-bit) of an output over 8192 keys.
-// (Added by the last group, beside the next tile's softmax: 746 us for 713.)
 // Measured: 16 prompts of 101 .. 700 queries over 500 .. 4000 keys (4-bit, 32 q
-// and 8 kv heads of 128): 713 us (the prefill kernel's form of it: 1024), 35% of
-// the tensor cores' rate counting the doubled products.  What bounds it is the
+// and 8 kv heads of 128): 737 us (the prefill kernel's form of it: 1024; with a
+// factor by the largest scale so far: 713), 36% of the tensor cores' rate counting
+// the doubled products.  What bounds it is the
 // chain of a tile: logits from TMEM, maximum, weights, back, P.V, next S, some
-// 8500 cycles with two tiles in flight (TMEM is full: S twice, O and Q).
-// (S half by half, each right after the P.V that frees its place: 721 us.)
+// 8500 cycles with two tiles in flight (TMEM is full: S twice, O and Q; Q's terms
+// in shared memory would make room for a third, which was not tried).
+// (S half by half, each right after the P.V that frees its place: 721 us for 713.)
 // Every wait is bounded; on a timeout the CTA reports KVQ_DEVERR_TIMEOUT, drains,
 // frees its TMEM and returns.
 //

@@ -1087,8 +1087,8 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 //    they are (8-bit floats).
 // FORM 2: and products of 16 keys start from zero and join the running sums in fp32,
 // since the accumulators truncate: over a slice of some fifty tiles that was 3e-5
-// of an output where the values' mean is not zero (2-bit rows, 16384 keys), and
-// over twenty 7e-6 (4-bit rows).  Codes of odd keys are counted from 2^(b-1) - 1, of
+// of an output where the values' mean is not zero (2-bit rows, 16384 keys), over
+// twenty 7e-6 and over 30011 keys 1.2e-4 (4-bit rows).  Codes of odd keys are counted from 2^(b-1) - 1, of
 // even ones from 2^(b-1): from one value alone the codes' mean is half a code, and
 // its sum, which the zero points' then cancels, came to 79 times the output's own
 // over 30011 keys of 2-bit rows in one slice, 1.1e-5 of it in fp32's roundings.
