@@ -449,8 +449,8 @@ kvq_status kvq_cross_attn(const kvq_cache* cache, const kvq_paging* paging, cons
 
 /* kvq_cross_dense_attn -- kvq_cross_attn over dense bf16 rows, as an encoder
  * leaves them.
- * k, v        : bf16 [num_kv_rows][num_kv_heads][head_dim], 16-byte aligned;
- *               sequence b's row j is row cu_kv[b] + j.
+ * k, v        : bf16 [num_kv_rows][num_kv_heads][head_dim], one row at least,
+ *               16-byte aligned; sequence b's row j is row cu_kv[b] + j.
  * cu_kv       : int32 [batch + 1] (device); a sequence with cu_kv[b + 1] - cu_kv[b]
  *               < seq_lens[b], or with rows outside k and v, is skipped (its
  *               outputs are left as they were) and sets KVQ_DEVERR_SEQ_LEN.

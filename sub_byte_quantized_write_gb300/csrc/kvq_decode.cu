@@ -378,10 +378,10 @@ __device__ __forceinline__ void fused_write_pair(const AttnParams& P, int b, int
 // the constants times sum(q''), D times one element of the query before its
 // transform, and what they lose at that size: 1.2e-5 (4-bit rows) and 3e-5 (2-bit)
 // of an output where the query lies in that element alone; on the grid 2e-6.
-// A small step over 4-bit rows (exact 1) keeps the older calls' terms, so
-// that it is to the bit what turned rows give there, up to queries that give rows of
-// size 1 logits of 2 powers of two (their root mean square), 1/2 of it from that
-// element: the sums lose 2e-6 of an output there, and more in proportion.
+// A small step over 4-bit rows (exact 1) keeps the older calls' terms, so that it is
+// to the bit what turned rows give there, up to queries that give rows of size 1
+// logits of 2 powers of two (their root mean square), 1/2 of it from that element:
+// the sums lose 2e-6 of an output there, and more in proportion.
 // `unit`: a logit, in powers of two, per unit of the transformed query.
 template <int MODE, int EPL>
 __device__ __forceinline__ bool fold_on_grid(const AttnParams& P, float sum, float unit, float dnorm, const float (&x)[EPL]) {
@@ -1082,19 +1082,20 @@ __device__ __forceinline__ void output_signs(const AttnParams& P, int h, int lan
 //    nothing below 2^-24, and s of unit-sized 8-bit rows is below 2^-5 (2e-5 to
 //    4e-5 of an output).  It goes by p s and not by s: a row of large values that
 //    no query looks at does not push the others' weights down.  (By s alone 64
-//    sources with 2 queries each took 141 us in place of 149.)
+//    sources with 2 queries each took 141 us in place of 150.)
 //  * zeros for the value rows that are not there, and NaN codes of visible ones as
 //    they are (8-bit floats).
 // FORM 2: and products of 16 keys start from zero and join the running sums in fp32,
 // since the accumulators truncate: over a slice of some fifty tiles that was 3e-5
 // of an output where the values' mean is not zero (2-bit rows, 16384 keys), over
-// twenty 7e-6 and over 30011 keys 1.2e-4 (4-bit rows).  Codes of odd keys are counted from 2^(b-1) - 1, of
-// even ones from 2^(b-1): from one value alone the codes' mean is half a code, and
-// its sum, which the zero points' then cancels, came to 79 times the output's own
-// over 30011 keys of 2-bit rows in one slice, 1.1e-5 of it in fp32's roundings.
-// FORM 1, a small step over 4-bit rows (small_call): without FORM 2's sums,
-// and with the weights' factor 1 while the largest is 2^-2 .. 2^12, so that the
-// results are those of FORM 0 to the bit where that is as close.
+// twenty 7e-6 and over 30011 keys 1.2e-4 (4-bit rows).  Codes of odd keys are counted
+// from 2^(b-1) - 1, of even ones from 2^(b-1): from one value alone the codes' mean
+// is half a code, and its sum, which the zero points' then cancels, came to 79 times
+// the output's own over 30011 keys of 2-bit rows in one slice, 1.1e-5 of it in fp32's
+// roundings.
+// FORM 1, a small step over 4-bit rows (small_call): without FORM 2's sums, and with
+// the weights' factor 1 while the largest is 2^-2 .. 2^12, so that the results are
+// those of FORM 0 to the bit where that is as close.
 
 template <int MODE, int D, int NT, bool STEGO, int FORM>
 __global__ void __launch_bounds__(TmaCfg<MODE, D, NT>::WARPS * 32, (TmaCfg<MODE, D, NT>::CTAS))
@@ -1788,9 +1789,10 @@ cudaError_t launch_decode_t(const AttnParams& P, const DecodeWs& ws, int grid, c
   return launch_dependent(decode_reduce_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P, ws);
 }
 
-// FORM 1's calls, by the width of the table: a few thousand keys in all, no warp with
-// more than 15 tiles.  Their time is the launches' (7 sequences of 401 keys 21 us
-// with either form); a call of 64 sequences pays 2% for FORM 2.
+// FORM 1's calls, by the width of the table: a few ten thousand (key, kv head) rows in
+// all, no warp with more than 15 tiles.  Their time is a warp's chain (7 sequences of
+// 401 keys, 8 kv heads: 33.2 us on the GPU in either form); a call of 64 sequences pays
+// 3% for FORM 2.
 constexpr int DECODE_SMALL_TILES = 512;
 template <int MODE, int D, int NT>
 bool small_call(const AttnParams& P, const DecodeWs& ws, int grid) {
